@@ -42,7 +42,9 @@ typedef enum {
     ATTN_ERR_DEVICE_TIMEOUT = -7, /* a bounded device-side wait expired */
     ATTN_ERR_SEQLENS = -8,        /* cu_seqlens not increasing from 0, or a length > N */
     ATTN_ERR_ARCH = -9,           /* current device is not sm_103 */
-    ATTN_ERR_SCRATCH = -10        /* attn_fwd_noalloc: problem larger than its fixed scratch */
+    ATTN_ERR_SCRATCH = -10,       /* attn_fwd_noalloc: problem larger than its fixed scratch;
+                                     a caller's workspace missing or too small */
+    ATTN_ERR_INDEX = -11          /* a position or page outside its table (device) */
 } attn_status;
 
 /*
@@ -198,8 +200,9 @@ int attn_fwd_ex(const void *q, const void *k, const void *v, void *o, float *lse
 /*
  * Synchronises `stream`, then returns and clears the device-side error word
  * of the current device: ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (a bounded wait
- * expired; the kernel stopped early and its outputs are incomplete) or
- * ATTN_ERR_SEQLENS (invalid cu_seqlens; nothing was computed).  Returns
+ * expired; the kernel stopped early and its outputs are incomplete),
+ * ATTN_ERR_SEQLENS (invalid cu_seqlens; nothing was computed) or
+ * ATTN_ERR_INDEX (attn_norm.h, attn_cache.h).  Returns
  * ATTN_ERR_CUDA if the synchronisation itself fails.
  */
 int attn_last_device_error(attn_stream_t stream);

@@ -1,8 +1,9 @@
 """GB300 (sm_103a) fused exact attention: forward and backward.
 
 A thin ctypes binding of the C ABI in ``include/attn_fwd.h``,
-``include/attn_bwd.h`` and ``include/attn_fp8.h`` (the library
-``_build/libattn_fwd.so``, built by ``build.py``).  The functions here only
+``include/attn_bwd.h``, ``include/attn_fp8.h``, ``include/attn_norm.h`` and
+``include/attn_cache.h`` (the library ``_build/libattn_fwd.so``, built by
+``build.py``).  The functions here only
 marshal arguments: every step of the computation runs in the library's CUDA
 kernels.  There is no CPU path: calling the library without it built, or on a
 device other than sm_103, raises.
@@ -18,7 +19,10 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_window", "attn_fwd_fp8", "attn_fwd_
            "attn_fwd_ex", "attn_fwd_host", "attn_fwd_noalloc", "attn_fwd_noalloc_ex",
            "attn_fwd_noalloc_last_device_error", "attn_device_bytes", "attn_fwd_window", "attn_fwd_kvsplit", "attn_fwd_decode", "attn_last_device_error", "attn_last_error_site",
            "attn_status_string", "AttnError", "AttnFwdOptions", "lib", "forward", "backward", "decode",
-           "EXPORTED_SYMBOLS"]
+           "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace",
+           "attn_cache_write", "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace",
+           "AttnRotary", "AttnPagedCache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write",
+           "cache_read", "tree_decode", "EXPORTED_SYMBOLS"]
 
 # Every symbol the headers under include/ declare.
 EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_decode", "attn_last_device_error", "attn_last_error_site",
@@ -26,7 +30,9 @@ EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_decode
                     "attn_fwd_noalloc_ex", "attn_fwd_noalloc_last_device_error", "attn_device_bytes",
                     "attn_fwd_window", "attn_fwd_kvsplit", "attn_bwd", "attn_bwd_window",
                     "attn_fwd_fp8", "attn_fwd_fp8_codes",
-                    "attn_fp8_quantize_qk", "attn_fp8_quantize_v")
+                    "attn_fp8_quantize_qk", "attn_fp8_quantize_v",
+                    "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace",
+                    "attn_cache_write", "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace")
 
 ATTN_OK = 0
 
@@ -43,6 +49,21 @@ class AttnFwdOptions(ctypes.Structure):
                 ("fault_inject", ctypes.c_int),
                 ("max_ctas", ctypes.c_int),
                 ("kernel", ctypes.c_int)]
+
+
+class AttnRotary(ctypes.Structure):
+    """attn_rotary of include/attn_norm.h."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("table_len", ctypes.c_int), ("rot", ctypes.c_int), ("axes", ctypes.c_int),
+                ("section", ctypes.c_int * 3), ("interleaved", ctypes.c_int)]
+
+
+class AttnPagedCache(ctypes.Structure):
+    """attn_paged_cache of include/attn_cache.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("page_table_stride", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int)]
 
 
 _lib = None
@@ -91,6 +112,23 @@ def lib() -> ctypes.CDLL:
         L.attn_device_bytes.restype = ctypes.c_size_t
         L.attn_fwd_host.argtypes = sig
         L.attn_fwd_host.restype = i
+        i64, f = ctypes.c_int64, ctypes.c_float
+        L.attn_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i, i, i, i, f, vp, vp]
+        L.attn_qk_norm_rope.restype = i
+        L.attn_qk_norm_rope_bwd.argtypes = ([vp, i64, vp, i64, vp, vp] + [vp, i64] * 4 +
+                                            [vp, vp, i, i, i, i, f, vp, vp, ctypes.c_size_t, vp])
+        L.attn_qk_norm_rope_bwd.restype = i
+        L.attn_qk_norm_rope_bwd_workspace.argtypes = [i, i, i, i]
+        L.attn_qk_norm_rope_bwd_workspace.restype = ctypes.c_size_t
+        L.attn_cache_write.argtypes = [vp, vp, i64, vp, i64, vp, vp, i, i, vp]
+        L.attn_cache_write.restype = i
+        L.attn_cache_read.argtypes = [vp, vp, vp, vp, i, i, vp]
+        L.attn_cache_read.restype = i
+        L.attn_fwd_tree.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp,
+                                    ctypes.c_size_t, vp]
+        L.attn_fwd_tree.restype = i
+        L.attn_fwd_tree_workspace.argtypes = [i] * 8
+        L.attn_fwd_tree_workspace.restype = ctypes.c_size_t
         L.attn_last_device_error.argtypes = [vp]
         L.attn_last_device_error.restype = i
         L.attn_last_error_site.restype = i
@@ -312,6 +350,84 @@ def attn_fp8_quantize_v(v, codes_t, scale, B: int, H: int, N: int, d: int, cu_se
     return st
 
 
+def _struct(x):
+    """The address of a structure (kept alive by the caller), or None."""
+    return None if x is None else ctypes.addressof(x)
+
+
+def attn_qk_norm_rope(q, q_stride: int, k, k_stride: int, wq, wk, q_out, q_out_stride: int, k_out,
+                      k_out_stride: int, T: int, Hq: int, Hk: int, d: int, eps: float,
+                      rotary: AttnRotary, stream=None) -> int:
+    """The C call ``attn_qk_norm_rope`` (tensors or addresses; strides in elements)."""
+    st = lib().attn_qk_norm_rope(_ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(wq), _ptr(wk),
+                                 _ptr(q_out), int(q_out_stride), _ptr(k_out), int(k_out_stride),
+                                 int(T), int(Hq), int(Hk), int(d), float(eps), _struct(rotary),
+                                 _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope")
+    return st
+
+
+def attn_qk_norm_rope_bwd_workspace(T: int, Hq: int, Hk: int, d: int) -> int:
+    """Bytes of workspace attn_qk_norm_rope_bwd needs."""
+    return int(lib().attn_qk_norm_rope_bwd_workspace(int(T), int(Hq), int(Hk), int(d)))
+
+
+def attn_qk_norm_rope_bwd(q, q_stride: int, k, k_stride: int, wq, wk, dq_out, dq_out_stride: int,
+                          dk_out, dk_out_stride: int, dq, dq_stride: int, dk, dk_stride: int, dwq,
+                          dwk, T: int, Hq: int, Hk: int, d: int, eps: float, rotary: AttnRotary,
+                          workspace, workspace_bytes: int, stream=None) -> int:
+    """The C call ``attn_qk_norm_rope_bwd``."""
+    st = lib().attn_qk_norm_rope_bwd(_ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(wq),
+                                     _ptr(wk), _ptr(dq_out), int(dq_out_stride), _ptr(dk_out),
+                                     int(dk_out_stride), _ptr(dq), int(dq_stride), _ptr(dk),
+                                     int(dk_stride), _ptr(dwq), _ptr(dwk), int(T), int(Hq), int(Hk),
+                                     int(d), float(eps), _struct(rotary), _ptr(workspace),
+                                     int(workspace_bytes), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope_bwd")
+    return st
+
+
+def attn_cache_write(cache: AttnPagedCache, k, k_stride: int, v, v_stride: int, seqlens, cu_seqlens,
+                     B: int, total: int, stream=None) -> int:
+    """The C call ``attn_cache_write``."""
+    st = lib().attn_cache_write(_struct(cache), _ptr(k), int(k_stride), _ptr(v), int(v_stride),
+                                _ptr(seqlens), _ptr(cu_seqlens), int(B), int(total), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_write")
+    return st
+
+
+def attn_cache_read(cache: AttnPagedCache, k, v, cu_seqlens, B: int, total: int, stream=None) -> int:
+    """The C call ``attn_cache_read``."""
+    st = lib().attn_cache_read(_struct(cache), _ptr(k), _ptr(v), _ptr(cu_seqlens), int(B), int(total),
+                               _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_read")
+    return st
+
+
+def attn_fwd_tree_workspace(B: int, total: int, Hq: int, H: int, d: int, max_new: int, max_len: int,
+                            num_splits: int = 0) -> int:
+    """Bytes of workspace attn_fwd_tree needs."""
+    return int(lib().attn_fwd_tree_workspace(int(B), int(total), int(Hq), int(H), int(d), int(max_new),
+                                             int(max_len), int(num_splits)))
+
+
+def attn_fwd_tree(q, q_stride: int, cache: AttnPagedCache, seqlens, cu_seqlens, mask, o, lse, B: int,
+                  total: int, Hq: int, max_new: int, max_len: int, scale: float, num_splits: int = 0,
+                  workspace=None, workspace_bytes: int = 0, stream=None) -> int:
+    """The C call ``attn_fwd_tree``."""
+    st = lib().attn_fwd_tree(_ptr(q), int(q_stride), _struct(cache), _ptr(seqlens), _ptr(cu_seqlens),
+                             _ptr(mask), _ptr(o), _ptr(lse), int(B), int(total), int(Hq),
+                             int(max_new), int(max_len), float(scale), int(num_splits),
+                             _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_tree")
+    return st
+
+
 def attn_last_device_error(stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device error status."""
     return lib().attn_last_device_error(_stream(stream))
@@ -410,3 +526,250 @@ def decode(q, k, v, cu_seqlens_k, max_seqlen_k: int, scale: float | None = None,
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     attn_fwd_decode(q, k, v, o, lse, B, H, d, scale, cu_seqlens_k, max_seqlen_k, num_splits, stream)
     return o, lse
+
+
+# ------------------------------------------- the step before attention, the paged cache --
+# Torch conveniences.  They check what the C calls cannot see (types, shapes,
+# devices), allocate outputs and workspaces, and launch on `stream` (default:
+# the current stream of the tensors' device).
+
+class _Launch:
+    """Makes the tensors' device current, and allocations belong to the launching
+    stream, so that torch hands a workspace out again only behind the call's work."""
+    __slots__ = ("handle", "contexts")
+
+    def __init__(self, device, stream):
+        import torch
+        self.contexts = ()
+        if device.index != torch.cuda.current_device():
+            self.contexts = (torch.cuda.device(device),)
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.handle = stream.cuda_stream
+            self.contexts += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, not {t.device}")
+
+
+def _rows_of(name, t, T=None, H=None, d=None):
+    """(T, H, d, token stride) of bf16 rows [T, H, d] whose tokens may be apart."""
+    import torch
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d]")
+    (t0, t1, t2), (s0, s1, s2) = t.shape, t.stride()
+    if (T is not None and t0 != T) or (H is not None and t1 != H) or (d is not None and t2 != d):
+        want = [n if n is not None else "any" for n in (T, H, d)]
+        raise ValueError(f"{name} must have the shape {want}, not {[t0, t1, t2]}")
+    if s2 != 1 or (t1 > 1 and s1 != t2) or (t0 > 1 and s0 < t1 * t2):
+        raise ValueError(f"{name}: the heads of a token must be contiguous and tokens must not overlap")
+    return t0, t1, t2, s0 if t0 > 1 else t1 * t2
+
+
+def _plain(name, t, dtype, shape):
+    """A contiguous CUDA tensor of the given type and shape (None: any extent)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)}, not {list(t.shape)}")
+
+
+def _rotary(cos, sin, positions, T, sections, interleaved):
+    import torch
+    _plain("cos", cos, torch.float32, (None, None))
+    _plain("sin", sin, torch.float32, cos.shape)
+    if positions.dim() == 1:
+        positions = positions[None]
+    _plain("positions", positions, torch.int32, (None, T))
+    axes, half = positions.shape[0], cos.shape[1]
+    if not 1 <= axes <= 3:
+        raise ValueError("positions must have one to three axes")
+    if sections is None:
+        if axes > 1:
+            raise ValueError("positions with several axes need sections")
+        sections = (half,)
+    if len(sections) != axes or sum(sections) != half or min(sections) < 0:
+        raise ValueError(f"sections must be {axes} counts of pairs that add up to {half}")
+    return AttnRotary(cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), cos.shape[0], 2 * half, axes,
+                      (ctypes.c_int * 3)(*sections), int(bool(interleaved)))
+
+
+def qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps: float = 1e-6, sections=None,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """The norm of every query and key head and the rotary rotation, in one pass.
+
+    q [T, Hq, d], k [T, Hk, d] bf16 (slices of a fused projection are fine: the
+    heads of a token contiguous, tokens any multiple of 8 elements apart), wq,
+    wk bf16 [d], cos, sin fp32 [table length, rot / 2], positions int32 [T], or
+    [axes, T] with `sections` giving each axis its pairs of channels.
+    interleaved: pairs are neighbouring channels instead of halves.  Channels
+    from rot on are normed only.  Returns (q_out, k_out), allocated by torch
+    (contiguous) when not given; q_out may be q and k_out k.
+    """
+    import torch
+    T, Hq, d, qs = _rows_of("q", q)
+    _, Hk, _, ks = _rows_of("k", k, T, None, d)
+    _plain("wq", wq, torch.bfloat16, (d,))
+    _plain("wk", wk, torch.bfloat16, (d,))
+    rotary = _rotary(cos, sin, positions, T, sections, interleaved)
+    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions, q_out=q_out, k_out=k_out)
+    with _Launch(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, d), dtype=torch.bfloat16, device=q.device)
+        qos, kos = _rows_of("q_out", q_out, T, Hq, d)[3], _rows_of("k_out", k_out, T, Hk, d)[3]
+        attn_qk_norm_rope(q, qs, k, ks, wq, wk, q_out, qos, k_out, kos, T, Hq, Hk, d, eps, rotary, s)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, wq, wk, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
+                          sections=None, interleaved: bool = False, stream=None):
+    """The gradient of qk_norm_rope: q, k and the rest as given to it, dq_out and
+    dk_out the gradients of what it returned.  Returns (dq, dk) in bf16 and
+    (dwq, dwk) in fp32, allocated by torch; results repeat bit for bit."""
+    import torch
+    T, Hq, d, qs = _rows_of("q", q)
+    _, Hk, _, ks = _rows_of("k", k, T, None, d)
+    gqs = _rows_of("dq_out", dq_out, T, Hq, d)[3]
+    gks = _rows_of("dk_out", dk_out, T, Hk, d)[3]
+    _plain("wq", wq, torch.bfloat16, (d,))
+    _plain("wk", wk, torch.bfloat16, (d,))
+    rotary = _rotary(cos, sin, positions, T, sections, interleaved)
+    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions, dq_out=dq_out,
+                 dk_out=dk_out)
+    with _Launch(q.device, stream) as s:
+        dq = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        dk = torch.empty((T, Hk, d), dtype=torch.bfloat16, device=q.device)
+        dwq = torch.empty((d,), dtype=torch.float32, device=q.device)
+        dwk = torch.empty((d,), dtype=torch.float32, device=q.device)
+        n = attn_qk_norm_rope_bwd_workspace(T, Hq, Hk, d)
+        ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        attn_qk_norm_rope_bwd(q, qs, k, ks, wq, wk, dq_out, gqs, dk_out, gks, dq, Hq * d, dk, Hk * d, dwq,
+                              dwk, T, Hq, Hk, d, eps, rotary, ws, n, s)
+    return dq, dk, dwq, dwk
+
+
+def _cache(k_cache, v_cache, page_table, B, k_scale, v_scale):
+    """The AttnPagedCache of cache tensors [pages, page size, H, d]."""
+    import torch
+    codes = k_scale is not None
+    if codes != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go together")
+    dtype = k_cache.dtype
+    if codes and dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("a cache with scales holds e4m3 codes (float8_e4m3fn or uint8)")
+    if not codes and dtype is not torch.bfloat16:
+        raise TypeError("a cache without scales must be bf16")
+    _plain("k_cache", k_cache, dtype, (None, None, None, None))
+    pages, page, H, d = k_cache.shape
+    _plain("v_cache", v_cache, dtype, k_cache.shape)
+    if codes:
+        _plain("k_scale", k_scale, torch.float32, (pages, H, page))
+        _plain("v_scale", v_scale, torch.float32, (pages, H, page))
+    _plain("page_table", page_table, torch.int32, (B, None))
+    _same_device(k_cache.device, v_cache=v_cache, page_table=page_table, k_scale=k_scale, v_scale=v_scale)
+    return AttnPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                          page_table.data_ptr(), page_table.shape[1], pages, page, H, d)
+
+
+def cache_write(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, k_scale=None, v_scale=None,
+                stream=None) -> None:
+    """Writes packed new keys and values [total, H, d] bf16 at the last positions of
+    their sequences into a paged cache.
+
+    k_cache, v_cache: [pages, page size, H, d], bf16, or float8_e4m3fn (uint8)
+    with k_scale, v_scale fp32 [pages, H, page size].  page_table int32
+    [B, width], seqlens int32 [B] (the new tokens included), cu_seqlens int32
+    [B+1] (new tokens of sequence b: cu_seqlens[b] .. cu_seqlens[b+1]-1; rows
+    behind the last are padding).  All on the device, where they are checked
+    (attn_last_device_error).
+    """
+    import torch
+    B = seqlens.shape[0]
+    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
+    total, _, _, ks = _rows_of("k", k, None, cache.H, cache.d)
+    vs = _rows_of("v", v, total, cache.H, cache.d)[3]
+    _plain("seqlens", seqlens, torch.int32, (B,))
+    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _same_device(k.device, v=v, k_cache=k_cache, seqlens=seqlens, cu_seqlens=cu_seqlens)
+    with _Launch(k.device, stream) as s:
+        attn_cache_write(cache, k, ks, v, vs, seqlens, cu_seqlens, B, total, s)
+
+
+def cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k_scale=None, v_scale=None,
+               stream=None):
+    """Reads a paged cache (as for cache_write) back: positions 0 .. of every
+    sequence b into the rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of packed bf16
+    k, v [total, H, d], the layout forward() and decode() take.  `total` rows
+    are allocated by torch; rows behind the last sequence are not written."""
+    import torch
+    B = cu_seqlens.shape[0] - 1
+    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
+    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _same_device(k_cache.device, cu_seqlens=cu_seqlens)
+    with _Launch(k_cache.device, stream) as s:
+        k = torch.empty((int(total), cache.H, cache.d), dtype=torch.bfloat16, device=k_cache.device)
+        v = torch.empty_like(k)
+        attn_cache_read(cache, k, v, cu_seqlens, B, total, s)
+    return k, v
+
+
+def tree_decode(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, max_new: int, max_len: int,
+                mask=None, scale: float | None = None, k_scale=None, v_scale=None, num_splits: int = 0,
+                out=None, lse=None, stream=None):
+    """Attention of every sequence's new tokens (one, or a tree of up to 64 drafted
+    ones) over its paged cache (as for cache_write, the new tokens written).
+
+    q [total, Hq, d] bf16, Hq a multiple of the cache's heads; mask int64 [total]:
+    bit t of a token's word lets it see new token t of its sequence (None: itself
+    and those before it); every token sees all older positions.  max_new (at most
+    64) and max_len bound the new tokens and lengths of every sequence.
+    Returns (o [total, Hq, d] bf16, lse [total, Hq] fp32), allocated by torch when
+    not given; rows behind the last sequence are not written.
+    """
+    import torch
+    B = seqlens.shape[0]
+    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
+    total, Hq, d, qs = _rows_of("q", q, None, None, cache.d)
+    if Hq < 1 or cache.H < 1 or Hq % cache.H:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    _plain("seqlens", seqlens, torch.int32, (B,))
+    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    if mask is not None:
+        _plain("mask", mask, torch.int64, (total,))
+    if scale is None:
+        scale = d ** -0.5
+    if out is not None:
+        _plain("out", out, torch.bfloat16, (total, Hq, d))
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (total, Hq))
+    _same_device(q.device, k_cache=k_cache, seqlens=seqlens, cu_seqlens=cu_seqlens, mask=mask, out=out, lse=lse)
+    with _Launch(q.device, stream) as s:
+        if out is None:
+            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+        n = attn_fwd_tree_workspace(B, total, Hq, cache.H, d, max_new, max_len, num_splits)
+        ws = torch.empty((n,), dtype=torch.uint8, device=q.device) if n else None
+        attn_fwd_tree(q, qs, cache, seqlens, cu_seqlens, mask, out, lse, B, total, Hq, max_new, max_len,
+                      scale, num_splits, ws, n, s)
+    return out, lse

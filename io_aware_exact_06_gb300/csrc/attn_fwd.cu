@@ -23,6 +23,7 @@
 #include "attn_fwd_row_kernel.cuh"
 #include "attn_fp8_row_kernel.cuh"
 #include "attn_host.h"
+#include "attn_rows.cuh"
 
 namespace {
 
@@ -167,6 +168,29 @@ cudaError_t pair_cluster_count(int sms, int* out) {
   return cudaSuccess;
 }
 
+// The device's error word, zero.  Also while a stream of this process is being
+// captured: the allocation and the clearing (on a stream of its own) stay out
+// of the capture.
+cudaError_t make_error_word(int** out) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  cudaStream_t s = nullptr;
+  int* p = nullptr;
+  e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = attn_host::lib_malloc(&p, 4 * sizeof(int));
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, 4 * sizeof(int), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (s) cudaStreamDestroy(s);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) {
+    attn_host::lib_free(p);
+    return e;
+  }
+  *out = p;
+  return cudaSuccess;
+}
+
 int device_state(int dev, DeviceState** out) {
   DeviceState& st = g_dev[dev];
   if (!st.ready) {
@@ -180,8 +204,7 @@ int device_state(int dev, DeviceState** out) {
     if (st.major != 10 || st.minor != 3) return ATTN_ERR_ARCH;
     if ((e = set_smem_attributes()) != cudaSuccess) return cuda_fail(e);
     if ((e = pair_cluster_count(st.sms, &st.pair_clusters)) != cudaSuccess) return cuda_fail(e);
-    if ((e = attn_host::lib_malloc(&st.err, 4 * sizeof(int))) != cudaSuccess) return cuda_fail(e);
-    if ((e = cudaMemset(st.err, 0, 4 * sizeof(int))) != cudaSuccess) return cuda_fail(e);
+    if ((e = make_error_word(&st.err)) != cudaSuccess) return cuda_fail(e);
     st.ready = true;
   }
   *out = &st;
@@ -654,6 +677,7 @@ extern "C" int attn_last_device_error(attn_stream_t stream) {
   if (h[0] & attn::kErrTimeout) return ATTN_ERR_DEVICE_TIMEOUT;
   if (h[0] & attn::kErrSeqlens) return ATTN_ERR_SEQLENS;
   if (h[0] & attn::kErrWorklist) return ATTN_ERR_SHAPE;
+  if (h[0] & attn::rows::kBadIndex) return ATTN_ERR_INDEX;
   return ATTN_OK;
 }
 
@@ -673,7 +697,8 @@ extern "C" const char* attn_status_string(int status) {
     case ATTN_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
     case ATTN_ERR_SEQLENS: return "invalid cu_seqlens";
     case ATTN_ERR_ARCH: return "device is not sm_103";
-    case ATTN_ERR_SCRATCH: return "problem larger than the fixed scratch of attn_fwd_noalloc";
+    case ATTN_ERR_SCRATCH: return "problem larger than the scratch it was given (attn_fwd_noalloc's fixed one, or a workspace)";
+    case ATTN_ERR_INDEX: return "a position or page outside its table";
     default: return "unknown status";
   }
 }
@@ -1144,6 +1169,24 @@ int lib_make_map(CUtensorMap* map, const void* ptr, int64_t tokens, int H, int d
   const int st = get_encode(&enc);
   if (st != ATTN_OK) return st;
   return make_map(enc, map, ptr, tokens, H, d);
+}
+
+int lib_make_cache_map(CUtensorMap* map, const void* ptr, int64_t rows, int H, int d, bool codes,
+                       int box_rows) {
+  EncodeTiledFn enc = nullptr;
+  const int st = get_encode(&enc);
+  if (st != ATTN_OK) return st;
+  const int elt = codes ? 1 : 2, box_bytes = std::min(128, d * elt);
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)d * elt, (cuuint64_t)H * d * elt};
+  cuuint32_t box[3] = {(cuuint32_t)(box_bytes / elt), 1, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+  return ATTN_OK;
 }
 
 }  // namespace attn_host

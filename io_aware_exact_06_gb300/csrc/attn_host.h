@@ -37,4 +37,10 @@ int lib_device(int* dev, int* sms, int** err);
 // 128 tokens, 128-byte swizzle.  Call with the lock held.
 int lib_make_map(CUtensorMap* map, const void* ptr, int64_t tokens, int H, int d);
 
+// 3-D TMA view [rows, H, d] of a paged cache's keys or values (bf16, or e4m3
+// codes): box of up to 128 bytes x 1 head x box_rows rows, swizzled to the
+// box's width.  Call with the lock held.
+int lib_make_cache_map(CUtensorMap* map, const void* ptr, int64_t rows, int H, int d, bool codes,
+                       int box_rows);
+
 }  // namespace attn_host

@@ -1,0 +1,472 @@
+// Host side of include/attn_norm.h and include/attn_cache.h: argument checks,
+// TMA descriptors and launches.  These entry points keep no workspace in the
+// library (where they need one it is the caller's), so calls on any streams and
+// captured graphs share nothing but the error word.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "../../include/attn_cache.h"
+#include "../../include/attn_norm.h"
+#include "attn_cache_kernel.cuh"
+#include "attn_host.h"
+#include "attn_norm_kernel.cuh"
+#include "attn_tree_kernel.cuh"
+
+namespace {
+
+constexpr int kPlanSms = 152;  // GB300: the split rules need no device
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int error_word(int** err) {
+  std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
+  int dev = 0, sms = 0;
+  return attn_host::lib_device(&dev, &sms, err);
+}
+
+// Launch that may overlap the end of the stream's previous kernel (every
+// kernel here waits for it before its first global access).
+template <typename... KArgs, typename... Args>
+int launch(void (*kernel)(KArgs...), int64_t grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? ATTN_OK : attn_host::lib_cuda_fail(e);
+}
+
+// ------------------------------------------------------------ norm, rotation --
+int check_rows(const void* x, int64_t stride, int H, int d) {
+  if (H == 0) return ATTN_OK;
+  if (!x) return ATTN_ERR_NULL;
+  if (stride < (int64_t)H * d) return ATTN_ERR_SHAPE;
+  if (!aligned(x, 16) || stride % 8) return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+int check_rotary(const attn_rotary* r, int T, int d, attn::norm::Rotary* out) {
+  if (!r) return ATTN_ERR_NULL;
+  if (r->rot < 0 || r->rot > d || r->rot % 16) return ATTN_ERR_SHAPE;
+  *out = attn::norm::Rotary{};
+  out->half = r->rot / 2;
+  out->edge0 = out->edge1 = INT_MAX;
+  if (r->rot == 0) return ATTN_OK;
+  if (r->axes < 1 || r->axes > 3 || r->table_len < 1) return ATTN_ERR_SHAPE;
+  if (r->axes > 1) {
+    int sum = 0;
+    for (int a = 0; a < r->axes; ++a) {
+      if (r->section[a] < 0 || r->section[a] > out->half) return ATTN_ERR_SHAPE;
+      sum += r->section[a];
+    }
+    if (sum != out->half) return ATTN_ERR_SHAPE;
+    out->edge0 = r->section[0];
+    if (r->axes == 3) out->edge1 = r->section[0] + r->section[1];
+  }
+  if (T == 0) return ATTN_OK;
+  if (!r->cos || !r->sin || !r->positions) return ATTN_ERR_NULL;
+  if (!aligned(r->cos, 16) || !aligned(r->sin, 16) || !aligned(r->positions, 4)) return ATTN_ERR_ALIGN;
+  out->cos = r->cos;
+  out->sin = r->sin;
+  out->pos = r->positions;
+  out->P = r->table_len;
+  out->axes = r->axes;
+  return ATTN_OK;
+}
+
+int check_norm(int T, int Hq, int Hk, int d, float eps) {
+  if (T < 0 || Hq < 0 || Hk < 0) return ATTN_ERR_SHAPE;
+  if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
+  if (!std::isfinite(eps) || eps < 0.f) return ATTN_ERR_SCALE;
+  if (((int64_t)Hq + Hk) * d > (1 << 20)) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+int64_t norm_chunk(int d) { return (int64_t)(32 / (d / 8)) * attn::norm::kSteps; }
+
+// CTAs of the gradient: two an SM, what the kernel's registers allow; fewer
+// when there is less to do.  The order of the weight sums depends on it alone.
+int64_t bwd_ctas(int T, int Hq, int Hk, int d) {
+  const int64_t c = norm_chunk(d);
+  const int64_t items = (int64_t)T * ((Hq + c - 1) / c + (Hk + c - 1) / c);
+  return std::min<int64_t>((items + attn::norm::kWarps - 1) / attn::norm::kWarps, 2 * kPlanSms);
+}
+
+// --------------------------------------------------------------------- cache --
+int check_cache(const attn_paged_cache* c) {
+  if (!c) return ATTN_ERR_NULL;
+  if (c->d != 64 && c->d != 128) return ATTN_ERR_HEADDIM;
+  if (c->H < 1 || (int64_t)c->H * c->d > (1 << 20) || c->num_pages < 1 || c->page_table_stride < 1)
+    return ATTN_ERR_SHAPE;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 &&
+      c->page_size != 256)
+    return ATTN_ERR_SHAPE;
+  // rows, and positions of a sequence, are 32-bit numbers
+  if ((int64_t)c->num_pages * c->page_size > INT32_MAX ||
+      (int64_t)c->page_table_stride * c->page_size > INT32_MAX)
+    return ATTN_ERR_SHAPE;
+  if (!c->k || !c->v || !c->page_table || !c->k_scale != !c->v_scale) return ATTN_ERR_NULL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
+      !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+attn::cache::Pages pages_of(const attn_paged_cache* c) {
+  attn::cache::Pages p{};
+  p.k = c->k;
+  p.v = c->v;
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.table = c->page_table;
+  p.stride = c->page_table_stride;
+  p.pages = c->num_pages;
+  p.log_page = 4;
+  while ((1 << p.log_page) < c->page_size) ++p.log_page;
+  p.H = c->H;
+  return p;
+}
+
+// ---------------------------------------------------------------------- tree --
+struct Plan {
+  int wm, mtiles, chunk, S;
+};
+
+// Row tiles of 16, 32 or 64 rows (the smallest that holds max_new * G), and key
+// ranges: about three rounds of two CTAs per SM, so that ragged lengths even
+// out, but at least 128 keys a range, below which starting a CTA and merging
+// its part cost more than its reading.
+Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
+  Plan pl;
+  const int64_t M = (int64_t)max_new * (Hq / H);
+  pl.wm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  pl.mtiles = (int)((M + 16 * pl.wm - 1) / (16 * pl.wm));
+  const int64_t T = attn::tree::kTile, len = std::max(max_len, 1);
+  const int64_t items = (int64_t)B * H * pl.mtiles;
+  int64_t chunk;
+  if (num_splits > 0)
+    chunk = (len + num_splits - 1) / num_splits;
+  else
+    chunk = std::max<int64_t>(
+        {128, (int64_t)std::min(1e9, (double)len * (double)items / (kPlanSms * 6)), (len + 255) / 256});
+  chunk = std::min((chunk + T - 1) / T * T, (len + T - 1) / T * T);
+  pl.chunk = (int)chunk;
+  pl.S = (int)((len + chunk - 1) / chunk);
+  return pl;
+}
+
+size_t tree_bytes(const Plan& pl, int total, int Hq, int d) {
+  return pl.S == 1 ? 0 : (size_t)pl.S * total * Hq * (d + 1) * sizeof(float);
+}
+
+int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
+  if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
+  if (B < 0 || total < 0 || Hq < 1 || H < 1 || Hq % H || (int64_t)Hq * d > (1 << 20)) return ATTN_ERR_SHAPE;
+  if (max_new < 0 || max_new > attn::tree::kMaxNew || max_len < max_new || num_splits < 0 || num_splits > 256)
+    return ATTN_ERR_SHAPE;
+  if (max_len > INT32_MAX - 256) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+// Raises the dynamic shared-memory limit of a kernel, once per device.  Call
+// with the library lock held.
+int allow_smem(const void* kernel, int bytes) {
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  if (done.count({dev, kernel})) return ATTN_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  done.insert({dev, kernel});
+  return ATTN_OK;
+}
+
+template <int D, bool kCodes, int kWM>
+int launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p, int64_t grid,
+                cudaStream_t s) {
+  auto kernel = attn::tree::tree_kernel<D, kCodes, kWM>;
+  constexpr int kSmem = attn::tree::Cfg<D, kCodes>::kSmem;
+  const int st = allow_smem(reinterpret_cast<const void*>(kernel), kSmem);
+  return st != ATTN_OK ? st : launch(kernel, grid, attn::tree::kThreads, kSmem, s, mk, mv, p);
+}
+
+template <int D, bool kCodes>
+int launch_tree(int wm, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
+                int64_t grid, cudaStream_t s) {
+  return wm == 1   ? launch_tree<D, kCodes, 1>(mk, mv, p, grid, s)
+         : wm == 2 ? launch_tree<D, kCodes, 2>(mk, mv, p, grid, s)
+                   : launch_tree<D, kCodes, 4>(mk, mv, p, grid, s);
+}
+
+}  // namespace
+
+extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* wq, const void* wk, void* q_out, int64_t q_out_stride,
+                                 void* k_out, int64_t k_out_stride, int T, int Hq, int Hk, int d,
+                                 float eps, const attn_rotary* rotary, attn_stream_t stream) {
+  int st = check_norm(T, Hq, Hk, d, eps);
+  if (st != ATTN_OK) return st;
+  attn::norm::Fwd p{};
+  if ((st = check_rotary(rotary, T, d, &p.rot)) != ATTN_OK) return st;
+  if (T == 0 || Hq + Hk == 0) return ATTN_OK;
+  if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
+  if ((st = check_rows(k, k_stride, Hk, d)) != ATTN_OK) return st;
+  if ((st = check_rows(q_out, q_out_stride, Hq, d)) != ATTN_OK) return st;
+  if ((st = check_rows(k_out, k_out_stride, Hk, d)) != ATTN_OK) return st;
+  if ((Hq && !wq) || (Hk && !wk)) return ATTN_ERR_NULL;
+  if (!aligned(wq, 16) || !aligned(wk, 16)) return ATTN_ERR_ALIGN;
+  const int64_t c = norm_chunk(d);
+  const int64_t items = (int64_t)T * ((Hq + Hk + c - 1) / c);
+  const int64_t grid = (items + attn::norm::kWarps - 1) / attn::norm::kWarps;
+  if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
+  if ((st = error_word(&p.err)) != ATTN_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.wq = static_cast<const __nv_bfloat16*>(wq);
+  p.wk = static_cast<const __nv_bfloat16*>(wk);
+  p.qo = static_cast<__nv_bfloat16*>(q_out);
+  p.ko = static_cast<__nv_bfloat16*>(k_out);
+  p.q_ts = q_stride;
+  p.k_ts = k_stride;
+  p.qo_ts = q_out_stride;
+  p.ko_ts = k_out_stride;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.eps = eps;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto kernel = d == 64 ? rotary->interleaved ? attn::norm::norm_rope_kernel<64, true>
+                                              : attn::norm::norm_rope_kernel<64, false>
+                : rotary->interleaved ? attn::norm::norm_rope_kernel<128, true>
+                                      : attn::norm::norm_rope_kernel<128, false>;
+  return launch(kernel, grid, attn::norm::kThreads, 0, s, p);
+}
+
+extern "C" size_t attn_qk_norm_rope_bwd_workspace(int T, int Hq, int Hk, int d) {
+  if (check_norm(T, Hq, Hk, d, 0.f) != ATTN_OK) return 0;
+  return (size_t)bwd_ctas(T, Hq, Hk, d) * 2 * d * sizeof(float);
+}
+
+extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* wq, const void* wk, const void* dq_out,
+                                     int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride,
+                                     void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                                     float* dwq, float* dwk, int T, int Hq, int Hk, int d, float eps,
+                                     const attn_rotary* rotary, void* workspace,
+                                     size_t workspace_bytes, attn_stream_t stream) {
+  int st = check_norm(T, Hq, Hk, d, eps);
+  if (st != ATTN_OK) return st;
+  attn::norm::Bwd p{};
+  if ((st = check_rotary(rotary, T, d, &p.rot)) != ATTN_OK) return st;
+  if (Hq + Hk == 0) return ATTN_OK;
+  if ((Hq && !dwq) || (Hk && !dwk)) return ATTN_ERR_NULL;
+  if (!aligned(dwq, 4) || !aligned(dwk, 4)) return ATTN_ERR_ALIGN;
+  const int64_t grid = bwd_ctas(T, Hq, Hk, d);
+  if (T > 0) {
+    if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
+    if ((st = check_rows(k, k_stride, Hk, d)) != ATTN_OK) return st;
+    if ((st = check_rows(dq_out, dq_out_stride, Hq, d)) != ATTN_OK) return st;
+    if ((st = check_rows(dk_out, dk_out_stride, Hk, d)) != ATTN_OK) return st;
+    if ((st = check_rows(dq, dq_stride, Hq, d)) != ATTN_OK) return st;
+    if ((st = check_rows(dk, dk_stride, Hk, d)) != ATTN_OK) return st;
+    if ((Hq && !wq) || (Hk && !wk)) return ATTN_ERR_NULL;
+    if (!aligned(wq, 16) || !aligned(wk, 16)) return ATTN_ERR_ALIGN;
+    if (!workspace || workspace_bytes < (size_t)grid * 2 * d * sizeof(float)) return ATTN_ERR_SCRATCH;
+    if (!aligned(workspace, 16)) return ATTN_ERR_ALIGN;
+  }
+  if ((st = error_word(&p.err)) != ATTN_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T > 0) {
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.wq = static_cast<const __nv_bfloat16*>(wq);
+    p.wk = static_cast<const __nv_bfloat16*>(wk);
+    p.gq = static_cast<const __nv_bfloat16*>(dq_out);
+    p.gk = static_cast<const __nv_bfloat16*>(dk_out);
+    p.dq = static_cast<__nv_bfloat16*>(dq);
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.q_ts = q_stride;
+    p.k_ts = k_stride;
+    p.gq_ts = dq_out_stride;
+    p.gk_ts = dk_out_stride;
+    p.dq_ts = dq_stride;
+    p.dk_ts = dk_stride;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.eps = eps;
+    p.part = static_cast<float*>(workspace);
+    auto kernel = d == 64 ? rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<64, true>
+                                                : attn::norm::norm_rope_bwd_kernel<64, false>
+                  : rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<128, true>
+                                        : attn::norm::norm_rope_bwd_kernel<128, false>;
+    if ((st = launch(kernel, grid, attn::norm::kThreads, 0, s, p)) != ATTN_OK) return st;
+  }
+  const attn::norm::WeightSum w{static_cast<const float*>(workspace), Hq ? dwq : nullptr,
+                                Hk ? dwk : nullptr, T > 0 ? (int)grid : 0, d};
+  return launch(attn::norm::norm_weight_kernel, 2 * d / 32, 1024, 0, s, w);
+}
+
+extern "C" int attn_cache_write(const attn_paged_cache* cache, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* seqlens,
+                                const int32_t* cu_seqlens, int B, int total, attn_stream_t stream) {
+  if (B < 0 || total < 0) return ATTN_ERR_SHAPE;
+  if (B == 0 || total == 0) return ATTN_OK;
+  int st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  if ((st = check_rows(k, k_stride, cache->H, cache->d)) != ATTN_OK) return st;
+  if ((st = check_rows(v, v_stride, cache->H, cache->d)) != ATTN_OK) return st;
+  if (!seqlens || !cu_seqlens) return ATTN_ERR_NULL;
+  if (!aligned(seqlens, 4) || !aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
+  const int64_t c = (int64_t)(32 / (cache->d / 8)) * attn::cache::kSteps;
+  const int64_t items = (int64_t)total * ((2 * cache->H + c - 1) / c);
+  const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
+  if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
+  attn::cache::Write p{};
+  if ((st = error_word(&p.err)) != ATTN_OK) return st;
+  p.c = pages_of(cache);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_ts = k_stride;
+  p.v_ts = v_stride;
+  p.lens = seqlens;
+  p.cu = cu_seqlens;
+  p.B = B;
+  p.total = total;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool codes = cache->k_scale != nullptr;
+  auto kernel = cache->d == 64 ? codes ? attn::cache::cache_write_kernel<64, true>
+                                       : attn::cache::cache_write_kernel<64, false>
+                : codes ? attn::cache::cache_write_kernel<128, true>
+                        : attn::cache::cache_write_kernel<128, false>;
+  return launch(kernel, grid, attn::cache::kThreads, 0, s, p);
+}
+
+extern "C" int attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
+                               const int32_t* cu_seqlens, int B, int total, attn_stream_t stream) {
+  if (B < 0 || total < 0) return ATTN_ERR_SHAPE;
+  if (B == 0 || total == 0) return ATTN_OK;
+  int st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  const int64_t hd = (int64_t)cache->H * cache->d;
+  if ((st = check_rows(k, hd, cache->H, cache->d)) != ATTN_OK) return st;
+  if ((st = check_rows(v, hd, cache->H, cache->d)) != ATTN_OK) return st;
+  if (!cu_seqlens) return ATTN_ERR_NULL;
+  if (!aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
+  const bool codes = cache->k_scale != nullptr;
+  const int64_t c = (int64_t)(32 / (cache->d / (codes ? 16 : 8))) * attn::cache::kSteps;
+  const int64_t items = (int64_t)total * ((2 * cache->H + c - 1) / c);
+  const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
+  if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
+  attn::cache::Read p{};
+  if ((st = error_word(&p.err)) != ATTN_OK) return st;
+  p.c = pages_of(cache);
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.cu = cu_seqlens;
+  p.B = B;
+  p.total = total;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto kernel = cache->d == 64 ? codes ? attn::cache::cache_read_kernel<64, true>
+                                       : attn::cache::cache_read_kernel<64, false>
+                : codes ? attn::cache::cache_read_kernel<128, true>
+                        : attn::cache::cache_read_kernel<128, false>;
+  return launch(kernel, grid, attn::cache::kThreads, 0, s, p);
+}
+
+extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_new,
+                                          int max_len, int num_splits) {
+  if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
+  if (B == 0 || total == 0 || max_new == 0) return 0;
+  return tree_bytes(tree_plan(B, Hq, H, max_new, max_len, num_splits), total, Hq, d);
+}
+
+extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
+                             const int32_t* seqlens, const int32_t* cu_seqlens, const int64_t* mask,
+                             void* o, float* lse, int B, int total, int Hq, int max_new, int max_len,
+                             float scale, int num_splits, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream) {
+  if (!cache) return ATTN_ERR_NULL;
+  const int d = cache->d;
+  int st = check_tree(B, total, Hq, cache->H, d, max_new, max_len, num_splits);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f) return ATTN_ERR_SCALE;
+  if (B == 0 || total == 0 || max_new == 0) return ATTN_OK;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
+  if (!o || !lse || !seqlens || !cu_seqlens) return ATTN_ERR_NULL;
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) ||
+      !aligned(mask, 8) || !aligned(workspace, 16))
+    return ATTN_ERR_ALIGN;
+  const Plan pl = tree_plan(B, Hq, cache->H, max_new, max_len, num_splits);
+  const size_t need = tree_bytes(pl, total, Hq, d);
+  if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_SCRATCH;
+  const double ctas = (double)B * pl.S * cache->H * pl.mtiles;
+  const int64_t combine = ((int64_t)total * Hq + 7) / 8;
+  if (ctas > INT32_MAX || combine > INT32_MAX) return ATTN_ERR_SHAPE;
+  const int64_t grid = (int64_t)B * pl.S * cache->H * pl.mtiles;
+  const bool codes = cache->k_scale != nullptr;
+  const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
+  const int box = std::min(cache->page_size, (int)attn::tree::kTile);
+
+  const attn::cache::Pages pg = pages_of(cache);
+  attn::tree::Params p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_ts = q_stride;
+  p.lens = seqlens;
+  p.cu = cu_seqlens;
+  p.table = cache->page_table;
+  p.mask = mask;
+  p.v = cache->v;
+  p.kscale = cache->k_scale;
+  p.vscale = cache->v_scale;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = need ? p.o_part + (size_t)pl.S * total * Hq * d : nullptr;
+  p.B = B;
+  p.total = total;
+  p.Hq = Hq;
+  p.H = cache->H;
+  p.G = Hq / cache->H;
+  p.stride = cache->page_table_stride;
+  p.pages = cache->num_pages;
+  p.log_page = pg.log_page;
+  p.max_new = max_new;
+  p.max_len = max_len;
+  p.chunk = pl.chunk;
+  p.S = pl.S;
+  p.mtiles = pl.mtiles;
+  // scale 0 weighs every key alike; the smallest normal factor does, without 0 * inf
+  p.c = (float)std::max((double)scale * 1.4426950408889634, (double)FLT_MIN);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
+  int dev = 0, sms = 0;
+  if ((st = attn_host::lib_device(&dev, &sms, &p.err)) != ATTN_OK) return st;
+  CUtensorMap mk, mv;
+  if ((st = attn_host::lib_make_cache_map(&mk, cache->k, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
+  if ((st = attn_host::lib_make_cache_map(&mv, cache->v, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
+  st = d == 64 ? codes ? launch_tree<64, true>(pl.wm, mk, mv, p, grid, s)
+                       : launch_tree<64, false>(pl.wm, mk, mv, p, grid, s)
+       : codes ? launch_tree<128, true>(pl.wm, mk, mv, p, grid, s)
+               : launch_tree<128, false>(pl.wm, mk, mv, p, grid, s);
+  if (st != ATTN_OK || pl.S == 1) return st;
+  return launch(d == 64 ? attn::tree::tree_combine_kernel<64> : attn::tree::tree_combine_kernel<128>,
+                combine, 256, 0, s, p);
+}
