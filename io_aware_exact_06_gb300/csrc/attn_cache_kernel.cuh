@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   const int b = rows::find_sequence(p.cu, p.B, t);
   if (b >= p.B) return;  // behind the last sequence
   const int start = p.cu[b], end = p.cu[b + 1], len = p.lens[b];
-  if (start < 0 || t < start || t >= end || len < end - start) {
+  // the whole sequence is refused when it is longer than its table
+  if (start < 0 || t < start || t >= end || len < end - start || len > (int64_t)p.c.stride << p.c.log_page) {
     if (lane == 0) atomicOr(p.err, rows::kBadSeqlens);
     return;
   }
@@ -165,8 +166,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const int h0 = (int)(item - (int64_t)t * chunks) * kChunk;
   const int b = rows::find_sequence(p.cu, p.B, t);
   if (b >= p.B) return;
-  const int start = p.cu[b];
-  if (start < 0 || t < start || t >= p.cu[b + 1]) {
+  const int start = p.cu[b], end = p.cu[b + 1];
+  if (start < 0 || t < start || t >= end || end - start > (int64_t)p.c.stride << p.c.log_page) {
     if (lane == 0) atomicOr(p.err, rows::kBadSeqlens);
     return;
   }
