@@ -529,87 +529,51 @@ def decode(q, k, v, cu_seqlens_k, max_seqlen_k: int, scale: float | None = None,
 
 
 # ------------------------------------------- the step before attention, the paged cache --
-# Torch conveniences.  They check what the C calls cannot see (types, shapes,
-# devices), allocate outputs and workspaces, and launch on `stream` (default:
-# the current stream of the tensors' device).
+# Torch conveniences.  The compiled module checks what the C calls cannot see
+# (types, shapes, strides, devices), allocates outputs and workspaces, and
+# launches on the current stream of the tensors' device; `stream` names another.
 
-class _Launch:
-    """Makes the tensors' device current, and allocations belong to the launching
-    stream, so that torch hands a workspace out again only behind the call's work."""
-    __slots__ = ("handle", "contexts")
+_serve = None
 
-    def __init__(self, device, stream):
+
+def _native():
+    """The compiled conveniences, bound to the library; raises if they have not been built."""
+    global _serve
+    if _serve is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module links against it)
+        L = lib()
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError(f"CPython module not built: {path} is missing "
+                               "(run `python -m io_aware_exact_06_gb300.build`)")
+        loader = importlib.machinery.ExtensionFileLoader("_serve", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve", loader))
+        loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace", "attn_cache_write",
+            "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace")])
+        _serve = module
+    return _serve
+
+
+def _call(name: str, stream, device, *args):
+    """_native().name(*args) with `stream` current: outputs and workspaces then
+    belong to it, and torch hands a workspace out again only behind the call."""
+    f = getattr(_native(), name)
+    if stream is None:
+        got = f(*args)
+    else:
         import torch
-        self.contexts = ()
-        if device.index != torch.cuda.current_device():
-            self.contexts = (torch.cuda.device(device),)
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.handle = stream.cuda_stream
-            self.contexts += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-
-
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, not {t.device}")
-
-
-def _rows_of(name, t, T=None, H=None, d=None):
-    """(T, H, d, token stride) of bf16 rows [T, H, d] whose tokens may be apart."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be bf16")
-    if not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d]")
-    (t0, t1, t2), (s0, s1, s2) = t.shape, t.stride()
-    if (T is not None and t0 != T) or (H is not None and t1 != H) or (d is not None and t2 != d):
-        want = [n if n is not None else "any" for n in (T, H, d)]
-        raise ValueError(f"{name} must have the shape {want}, not {[t0, t1, t2]}")
-    if s2 != 1 or (t1 > 1 and s1 != t2) or (t0 > 1 and s0 < t1 * t2):
-        raise ValueError(f"{name}: the heads of a token must be contiguous and tokens must not overlap")
-    return t0, t1, t2, s0 if t0 > 1 else t1 * t2
-
-
-def _plain(name, t, dtype, shape):
-    """A contiguous CUDA tensor of the given type and shape (None: any extent)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)}, not {list(t.shape)}")
-
-
-def _rotary(cos, sin, positions, T, sections, interleaved):
-    import torch
-    _plain("cos", cos, torch.float32, (None, None))
-    _plain("sin", sin, torch.float32, cos.shape)
-    if positions.dim() == 1:
-        positions = positions[None]
-    _plain("positions", positions, torch.int32, (None, T))
-    axes, half = positions.shape[0], cos.shape[1]
-    if not 1 <= axes <= 3:
-        raise ValueError("positions must have one to three axes")
-    if sections is None:
-        if axes > 1:
-            raise ValueError("positions with several axes need sections")
-        sections = (half,)
-    if len(sections) != axes or sum(sections) != half or min(sections) < 0:
-        raise ValueError(f"sections must be {axes} counts of pairs that add up to {half}")
-    return AttnRotary(cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), cos.shape[0], 2 * half, axes,
-                      (ctypes.c_int * 3)(*sections), int(bool(interleaved)))
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            got = f(*args)
+    if type(got) is int and got != ATTN_OK:
+        raise AttnError(got, name)
+    return got
 
 
 def qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps: float = 1e-6, sections=None,
@@ -624,21 +588,8 @@ def qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps: float = 1e-6, sections=
     from rot on are normed only.  Returns (q_out, k_out), allocated by torch
     (contiguous) when not given; q_out may be q and k_out k.
     """
-    import torch
-    T, Hq, d, qs = _rows_of("q", q)
-    _, Hk, _, ks = _rows_of("k", k, T, None, d)
-    _plain("wq", wq, torch.bfloat16, (d,))
-    _plain("wk", wk, torch.bfloat16, (d,))
-    rotary = _rotary(cos, sin, positions, T, sections, interleaved)
-    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions, q_out=q_out, k_out=k_out)
-    with _Launch(q.device, stream) as s:
-        if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-        if k_out is None:
-            k_out = torch.empty((T, Hk, d), dtype=torch.bfloat16, device=q.device)
-        qos, kos = _rows_of("q_out", q_out, T, Hq, d)[3], _rows_of("k_out", k_out, T, Hk, d)[3]
-        attn_qk_norm_rope(q, qs, k, ks, wq, wk, q_out, qos, k_out, kos, T, Hq, Hk, d, eps, rotary, s)
-    return q_out, k_out
+    return _call("norm_rope", stream, q.device, q, k, wq, wk, cos, sin, positions, eps, sections, interleaved,
+                 q_out, k_out)
 
 
 def qk_norm_rope_backward(q, k, wq, wk, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
@@ -646,49 +597,8 @@ def qk_norm_rope_backward(q, k, wq, wk, cos, sin, positions, dq_out, dk_out, eps
     """The gradient of qk_norm_rope: q, k and the rest as given to it, dq_out and
     dk_out the gradients of what it returned.  Returns (dq, dk) in bf16 and
     (dwq, dwk) in fp32, allocated by torch; results repeat bit for bit."""
-    import torch
-    T, Hq, d, qs = _rows_of("q", q)
-    _, Hk, _, ks = _rows_of("k", k, T, None, d)
-    gqs = _rows_of("dq_out", dq_out, T, Hq, d)[3]
-    gks = _rows_of("dk_out", dk_out, T, Hk, d)[3]
-    _plain("wq", wq, torch.bfloat16, (d,))
-    _plain("wk", wk, torch.bfloat16, (d,))
-    rotary = _rotary(cos, sin, positions, T, sections, interleaved)
-    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions, dq_out=dq_out,
-                 dk_out=dk_out)
-    with _Launch(q.device, stream) as s:
-        dq = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-        dk = torch.empty((T, Hk, d), dtype=torch.bfloat16, device=q.device)
-        dwq = torch.empty((d,), dtype=torch.float32, device=q.device)
-        dwk = torch.empty((d,), dtype=torch.float32, device=q.device)
-        n = attn_qk_norm_rope_bwd_workspace(T, Hq, Hk, d)
-        ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
-        attn_qk_norm_rope_bwd(q, qs, k, ks, wq, wk, dq_out, gqs, dk_out, gks, dq, Hq * d, dk, Hk * d, dwq,
-                              dwk, T, Hq, Hk, d, eps, rotary, ws, n, s)
-    return dq, dk, dwq, dwk
-
-
-def _cache(k_cache, v_cache, page_table, B, k_scale, v_scale):
-    """The AttnPagedCache of cache tensors [pages, page size, H, d]."""
-    import torch
-    codes = k_scale is not None
-    if codes != (v_scale is not None):
-        raise ValueError("k_scale and v_scale go together")
-    dtype = k_cache.dtype
-    if codes and dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError("a cache with scales holds e4m3 codes (float8_e4m3fn or uint8)")
-    if not codes and dtype is not torch.bfloat16:
-        raise TypeError("a cache without scales must be bf16")
-    _plain("k_cache", k_cache, dtype, (None, None, None, None))
-    pages, page, H, d = k_cache.shape
-    _plain("v_cache", v_cache, dtype, k_cache.shape)
-    if codes:
-        _plain("k_scale", k_scale, torch.float32, (pages, H, page))
-        _plain("v_scale", v_scale, torch.float32, (pages, H, page))
-    _plain("page_table", page_table, torch.int32, (B, None))
-    _same_device(k_cache.device, v_cache=v_cache, page_table=page_table, k_scale=k_scale, v_scale=v_scale)
-    return AttnPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-                          page_table.data_ptr(), page_table.shape[1], pages, page, H, d)
+    return _call("norm_rope_bwd", stream, q.device, q, k, wq, wk, cos, sin, positions, dq_out, dk_out, eps,
+                 sections, interleaved)
 
 
 def cache_write(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, k_scale=None, v_scale=None,
@@ -703,16 +613,7 @@ def cache_write(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, k_scale
     behind the last are padding).  All on the device, where they are checked
     (attn_last_device_error).
     """
-    import torch
-    B = seqlens.shape[0]
-    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
-    total, _, _, ks = _rows_of("k", k, None, cache.H, cache.d)
-    vs = _rows_of("v", v, total, cache.H, cache.d)[3]
-    _plain("seqlens", seqlens, torch.int32, (B,))
-    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    _same_device(k.device, v=v, k_cache=k_cache, seqlens=seqlens, cu_seqlens=cu_seqlens)
-    with _Launch(k.device, stream) as s:
-        attn_cache_write(cache, k, ks, v, vs, seqlens, cu_seqlens, B, total, s)
+    _call("cache_write", stream, k.device, k, v, k_cache, v_cache, page_table, k_scale, v_scale, seqlens, cu_seqlens)
 
 
 def cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k_scale=None, v_scale=None,
@@ -721,16 +622,8 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k_scale=Non
     sequence b into the rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of packed bf16
     k, v [total, H, d], the layout forward() and decode() take.  `total` rows
     are allocated by torch; rows behind the last sequence are not written."""
-    import torch
-    B = cu_seqlens.shape[0] - 1
-    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
-    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    _same_device(k_cache.device, cu_seqlens=cu_seqlens)
-    with _Launch(k_cache.device, stream) as s:
-        k = torch.empty((int(total), cache.H, cache.d), dtype=torch.bfloat16, device=k_cache.device)
-        v = torch.empty_like(k)
-        attn_cache_read(cache, k, v, cu_seqlens, B, total, s)
-    return k, v
+    return _call("cache_read", stream, k_cache.device, k_cache, v_cache, page_table, k_scale, v_scale, cu_seqlens,
+                 total)
 
 
 def tree_decode(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, max_new: int, max_len: int,
@@ -746,30 +639,5 @@ def tree_decode(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, max_new: i
     Returns (o [total, Hq, d] bf16, lse [total, Hq] fp32), allocated by torch when
     not given; rows behind the last sequence are not written.
     """
-    import torch
-    B = seqlens.shape[0]
-    cache = _cache(k_cache, v_cache, page_table, B, k_scale, v_scale)
-    total, Hq, d, qs = _rows_of("q", q, None, None, cache.d)
-    if Hq < 1 or cache.H < 1 or Hq % cache.H:
-        raise ValueError("the query heads must be a multiple of the cache's heads")
-    _plain("seqlens", seqlens, torch.int32, (B,))
-    _plain("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    if mask is not None:
-        _plain("mask", mask, torch.int64, (total,))
-    if scale is None:
-        scale = d ** -0.5
-    if out is not None:
-        _plain("out", out, torch.bfloat16, (total, Hq, d))
-    if lse is not None:
-        _plain("lse", lse, torch.float32, (total, Hq))
-    _same_device(q.device, k_cache=k_cache, seqlens=seqlens, cu_seqlens=cu_seqlens, mask=mask, out=out, lse=lse)
-    with _Launch(q.device, stream) as s:
-        if out is None:
-            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
-        n = attn_fwd_tree_workspace(B, total, Hq, cache.H, d, max_new, max_len, num_splits)
-        ws = torch.empty((n,), dtype=torch.uint8, device=q.device) if n else None
-        attn_fwd_tree(q, qs, cache, seqlens, cu_seqlens, mask, out, lse, B, total, Hq, max_new, max_len,
-                      scale, num_splits, ws, n, s)
-    return out, lse
+    return _call("tree_decode", stream, q.device, q, k_cache, v_cache, page_table, k_scale, v_scale, seqlens,
+                 cu_seqlens, max_new, max_len, mask, scale, num_splits, out, lse)

@@ -1,4 +1,5 @@
-"""Builds the sm_103a attention library in-tree: _build/libattn_fwd.so.
+"""Builds the sm_103a attention library in-tree: _build/libattn_fwd.so, and the
+CPython module of its norm and cache conveniences: _build/_serve.so.
 
 nvcc compiles the CUDA sources for sm_103a only and links the CUDA runtime
 statically, so the library loads on a machine without a GPU (every CUDA call
@@ -18,6 +19,9 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libattn_fwd.so")
 SOURCES = [os.path.join(CSRC, "attn_fwd.cu"), os.path.join(CSRC, "attn_bwd.cu"),
            os.path.join(CSRC, "attn_serve.cu")]
+# the torch conveniences of the norm and cache calls, as a CPython module
+BINDING = os.path.join(OUT_DIR, "_serve.so")
+BINDING_SOURCE = os.path.join(CSRC, "serve_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,11 +39,49 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _binding_command(out: str) -> list[str]:
+    """g++ on the binding, with the headers and libraries of this interpreter and torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), BINDING_SOURCE, "-o", out,
+            "-L", os.path.join(root, "lib"), "-Wl,-rpath," + os.path.join(root, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
+def _binding_fresh() -> bool:
+    deps = [BINDING_SOURCE, __file__] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in deps)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is missing or older than its sources; returns the library's path."""
+    os.makedirs(OUT_DIR, exist_ok=True)
+    binding = None
+    if force or not _binding_fresh():
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = _binding_command(tmp)
+        binding = (cmd, tmp, subprocess.Popen(cmd))  # beside the kernels
+    try:
+        return _build_library(force, verbose)
+    finally:
+        if binding:
+            cmd, tmp, pr = binding
+            if pr.wait() != 0:
+                raise subprocess.CalledProcessError(pr.returncode, cmd)
+            os.replace(tmp, BINDING)
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and os.path.exists(LIB):
         if os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps()):
             return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
     tag = f".tmp{os.getpid()}"
     # one translation unit per source, compiled in parallel, then one link
     objs, procs = [], []

@@ -1,12 +1,16 @@
 // Writing packed keys and values into a paged cache, and reading it back.
 //
 // The rows of a token (its H key heads, then its H value heads) are cut into
-// chunks; a warp takes one chunk of one token.  Writing: d / 8 lanes hold a
-// row's bf16 channels, 16 bytes each; the row maximum is a shuffle reduction
-// and the codes leave 8 bytes a lane.  Reading: d / 16 lanes hold a row's
-// codes, 16 bytes each (bf16 caches: d / 8 lanes), and write 32 bytes a lane.
-// Every byte moves once, so HBM bounds both (launch latency for a few tokens).
+// chunks; a warp takes one chunk of a run of consecutive tokens, the next
+// token's rows on their way while it works on the current ones.  Writing: d / 8
+// lanes hold a row's bf16 channels, 16 bytes each; the row maximum is a shuffle
+// reduction and the codes leave 8 bytes a lane.  Reading: d / 16 lanes hold a
+// row's codes, 16 bytes each (bf16 caches: d / 8 lanes), and write 32 bytes a
+// lane.  Every byte moves once, so HBM bounds both (launch latency for a few
+// tokens: runs of one).
 #pragma once
+
+#include <climits>
 
 #include "attn_rows.cuh"
 
@@ -30,6 +34,7 @@ struct Write {
   int64_t k_ts, v_ts;
   const int *lens, *cu;
   int B, total;
+  int run;  // tokens of a warp
   int* err;
 };
 
@@ -38,24 +43,54 @@ struct Read {
   __nv_bfloat16 *k, *v;
   const int* cu;
   int B, total;
+  int run;  // tokens of a warp
   int* err;
 };
 
-// Row of position pos of sequence b in the cache, or -1 with the error bit set
-// if the table or its page is out of range.
-__device__ __forceinline__ int64_t cache_row(const Pages& c, int b, int pos, int* err) {
+// Where a warp's tokens lie in the cache.  Tokens come in packed order, so the
+// search and the loads that depend on it happen once per sequence and page, not
+// once per token.
+struct Cursor {
+  int b = -1, start = 0, end = 0, shift = 0;  // packed tokens start .. end-1 sit at positions t + shift
+  int page_at = -1;                           // index of the page in the sequence
+  int64_t row0 = -1;                          // first row of that page, or -1
+  bool ok = false;                            // the sequence's lengths are possible
+};
+
+// Row of packed token t, or -1 (behind the last sequence, or reported).  lens
+// null: the packed tokens are the whole sequences.  For the whole warp.
+__device__ __forceinline__ int64_t find_row(Cursor& c, const Pages& pg, const int* __restrict__ cu,
+                                            const int* __restrict__ lens, int B, int t, int* err) {
   const int lane = threadIdx.x % 32;
-  const int at = pos >> c.log_page;
-  if (pos < 0 || at >= c.stride) {
-    if (lane == 0) atomicOr(err, rows::kBadSeqlens);
-    return -1;
+  if (c.b < 0 || t < c.start || t >= c.end) {
+    c.b = rows::find_sequence(cu, B, t);
+    c.page_at = -1;
+    c.ok = false;
+    if (c.b >= B) {
+      c.start = t, c.end = INT_MAX;  // nor do the tokens behind it
+      return -1;
+    }
+    c.start = cu[c.b], c.end = cu[c.b + 1];
+    // 64-bit differences: the offsets may hold anything
+    const int64_t n = (int64_t)c.end - c.start, len = lens ? lens[c.b] : n;
+    c.ok = c.start >= 0 && t >= c.start && t < c.end && len >= n && len <= (int64_t)pg.stride << pg.log_page;
+    if (!c.ok) {
+      if (lane == 0) atomicOr(err, rows::kBadSeqlens);
+      c.start = t, c.end = t < INT_MAX ? t + 1 : t;  // the next token is looked up again
+      return -1;
+    }
+    c.shift = (int)(len - n) - c.start;
   }
-  const int page = c.table[(int64_t)b * c.stride + at];
-  if ((unsigned)page >= (unsigned)c.pages) {
-    if (lane == 0) atomicOr(err, rows::kBadIndex);
-    return -1;
+  if (!c.ok) return -1;
+  const int pos = t + c.shift, at = pos >> pg.log_page;
+  if (at != c.page_at) {
+    c.page_at = at;
+    const int page = pg.table[(int64_t)c.b * pg.stride + at];
+    const bool in = (unsigned)page < (unsigned)pg.pages;
+    if (!in && lane == 0) atomicOr(err, rows::kBadIndex);
+    c.row0 = in ? (int64_t)page << pg.log_page : -1;
   }
-  return ((int64_t)page << c.log_page) + (pos & ((1 << c.log_page) - 1));
+  return c.row0 < 0 ? -1 : c.row0 + (pos & ((1 << pg.log_page) - 1));
 }
 
 __device__ __forceinline__ int64_t scale_at(const Pages& c, int64_t r, int h) {
@@ -86,7 +121,7 @@ __device__ __forceinline__ void from_e4m3x2(uint16_t w, float& lo, float& hi) {
 }
 
 template <int D, bool kCodes>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ Write p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_constant__ Write p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
@@ -95,63 +130,65 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
   const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item >= (int64_t)p.total * chunks) return;
-  const int t = (int)(item / chunks);
-  const int h0 = (int)(item - (int64_t)t * chunks) * kChunk;
-  uint4 x[kSteps];  // on their way while the token's place is looked up
+  const int64_t first = item / chunks * p.run;
+  if (first >= p.total) return;
+  const int h0 = (int)(item % chunks) * kChunk;
+  const int t0 = (int)first, t1 = (int)min((int64_t)p.total, first + p.run);
+  auto load = [&](int t, uint4 (&x)[kSteps]) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (h < 2 * H) {
-      const __nv_bfloat16* src = h < H ? p.k + t * p.k_ts + (int64_t)h * D
-                                       : p.v + t * p.v_ts + (int64_t)(h - H) * D;
-      x[u] = *reinterpret_cast<const uint4*>(src + 8 * slice);
+    for (int u = 0; u < kSteps; ++u) {
+      const int h = h0 + u * kRows + row;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (h < 2 * H)
+        x[u] = *reinterpret_cast<const uint4*>((h < H ? p.k + t * p.k_ts + (int64_t)h * D
+                                                      : p.v + t * p.v_ts + (int64_t)(h - H) * D) + 8 * slice);
     }
-  }
-  const int b = rows::find_sequence(p.cu, p.B, t);
-  if (b >= p.B) return;  // behind the last sequence
-  const int start = p.cu[b], end = p.cu[b + 1], len = p.lens[b];
-  // the whole sequence is refused when it is longer than its table
-  if (start < 0 || t < start || t >= end || len < end - start || len > (int64_t)p.c.stride << p.c.log_page) {
-    if (lane == 0) atomicOr(p.err, rows::kBadSeqlens);
-    return;
-  }
-  const int64_t r = cache_row(p.c, b, len - (end - t), p.err);
-  if (r < 0) return;
+  };
+  uint4 x[kSteps];
+  load(t0, x);  // on its way while the token's place is looked up
+  Cursor cur;
+  for (int t = t0; t < t1; ++t) {
+    uint4 next[kSteps];
+    if (t + 1 < t1) load(t + 1, next);
+    const int64_t r = find_row(cur, p.c, p.cu, p.lens, p.B, t, p.err);
+    if (r >= 0) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    const int hh = h < H ? h : h - H;
-    void* base = h < H ? p.c.k : p.c.v;
-    const int64_t at = (r * H + hh) * D + 8 * slice;
-    if (!kCodes) {
-      if (h < 2 * H) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at) = x[u];
-      continue;
+      for (int u = 0; u < kSteps; ++u) {
+        const int h = h0 + u * kRows + row;
+        const int hh = h < H ? h : h - H;
+        void* base = h < H ? p.c.k : p.c.v;
+        const int64_t at = (r * H + hh) * D + 8 * slice;
+        if (!kCodes) {
+          if (h < 2 * H) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at) = x[u];
+          continue;
+        }
+        float f[8], top = 0.f;
+        rows::unpack(x[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1)
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
+        // the floor keeps 1 / scale finite; a NaN passes it
+        float scale = __fdiv_rn(top, 448.f);
+        if (scale < 0x1p-64f) scale = 0x1p-64f;
+        const float inv = __frcp_rn(scale);
+        if (h < 2 * H) {
+          uint2 codes;
+          codes.x = e4m3x2(f[0] * inv, f[1] * inv) | e4m3x2(f[2] * inv, f[3] * inv) << 16;
+          codes.y = e4m3x2(f[4] * inv, f[5] * inv) | e4m3x2(f[6] * inv, f[7] * inv) << 16;
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(base) + at) = codes;
+          if (slice == 0) (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)] = scale;
+        }
+      }
     }
-    float f[8], top = 0.f;
-    rows::unpack(x[u], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
-#pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1)
-      top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    // the floor keeps 1 / scale finite; a NaN passes it
-    float scale = __fdiv_rn(top, 448.f);
-    if (scale < 0x1p-64f) scale = 0x1p-64f;
-    const float inv = __frcp_rn(scale);
-    if (h < 2 * H) {
-      uint2 codes;
-      codes.x = e4m3x2(f[0] * inv, f[1] * inv) | e4m3x2(f[2] * inv, f[3] * inv) << 16;
-      codes.y = e4m3x2(f[4] * inv, f[5] * inv) | e4m3x2(f[6] * inv, f[7] * inv) << 16;
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(base) + at) = codes;
-      if (slice == 0) (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)] = scale;
-    }
+    for (int u = 0; u < kSteps; ++u) x[u] = next[u];
   }
 }
 
 template <int D, bool kCodes>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ Read p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_constant__ Read p) {
   constexpr int kPer = kCodes ? 16 : 8;  // channels a lane holds
   constexpr int kLanes = D / kPer, kRows = 32 / kLanes, kChunk = kRows * kSteps;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -161,53 +198,64 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
   const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item >= (int64_t)p.total * chunks) return;
-  const int t = (int)(item / chunks);
-  const int h0 = (int)(item - (int64_t)t * chunks) * kChunk;
-  const int b = rows::find_sequence(p.cu, p.B, t);
-  if (b >= p.B) return;
-  const int start = p.cu[b], end = p.cu[b + 1];
-  if (start < 0 || t < start || t >= end || end - start > (int64_t)p.c.stride << p.c.log_page) {
-    if (lane == 0) atomicOr(p.err, rows::kBadSeqlens);
-    return;
-  }
-  const int64_t r = cache_row(p.c, b, t - start, p.err);
-  if (r < 0) return;
+  const int64_t first = item / chunks * p.run;
+  if (first >= p.total) return;
+  const int h0 = (int)(item % chunks) * kChunk;
+  const int t0 = (int)first, t1 = (int)min((int64_t)p.total, first + p.run);
+  Cursor cur;
+  auto load = [&](int64_t r, uint4 (&x)[kSteps], float (&sc)[kSteps]) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int h = h0 + u * kRows + row;
+      const int hh = h < H ? h : h - H;
+      x[u] = make_uint4(0, 0, 0, 0);
+      sc[u] = 0.f;
+      if (r >= 0 && h < 2 * H) {
+        const char* base = reinterpret_cast<const char*>(h < H ? p.c.k : p.c.v);
+        x[u] = *reinterpret_cast<const uint4*>(base + ((r * H + hh) * D + kPer * slice) * (kCodes ? 1 : 2));
+        if (kCodes) sc[u] = (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)];
+      }
+    }
+  };
   uint4 x[kSteps];
   float sc[kSteps];
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    const int hh = h < H ? h : h - H;
-    x[u] = make_uint4(0, 0, 0, 0);
-    sc[u] = 0.f;
-    if (h < 2 * H) {
-      const char* base = reinterpret_cast<const char*>(h < H ? p.c.k : p.c.v);
-      x[u] = *reinterpret_cast<const uint4*>(base + ((r * H + hh) * D + kPer * slice) * (kCodes ? 1 : 2));
-      if (kCodes) sc[u] = (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)];
+  int64_t r = find_row(cur, p.c, p.cu, nullptr, p.B, t0, p.err);
+  load(r, x, sc);
+  for (int t = t0; t < t1; ++t) {
+    uint4 next[kSteps];
+    float nsc[kSteps];
+    int64_t rn = -1;
+    if (t + 1 < t1) {
+      rn = find_row(cur, p.c, p.cu, nullptr, p.B, t + 1, p.err);
+      load(rn, next, nsc);
     }
-  }
+    if (r >= 0) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    if (h >= 2 * H) continue;
-    __nv_bfloat16* dst =
-        (h < H ? p.k + ((int64_t)t * H + h) * D : p.v + ((int64_t)t * H + h - H) * D) + kPer * slice;
-    if (!kCodes) {
-      *reinterpret_cast<uint4*>(dst) = x[u];
-      continue;
+      for (int u = 0; u < kSteps; ++u) {
+        const int h = h0 + u * kRows + row;
+        if (h >= 2 * H) continue;
+        __nv_bfloat16* dst =
+            (h < H ? p.k + ((int64_t)t * H + h) * D : p.v + ((int64_t)t * H + h - H) * D) + kPer * slice;
+        if (!kCodes) {
+          *reinterpret_cast<uint4*>(dst) = x[u];
+          continue;
+        }
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            from_e4m3x2((uint16_t)(w[2 * i + j / 2] >> (16 * (j & 1))), f[2 * j], f[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= sc[u];
+          *reinterpret_cast<uint4*>(dst + 8 * i) = rows::pack(f);
+        }
+      }
     }
-    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+    r = rn;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        from_e4m3x2((uint16_t)(w[2 * i + j / 2] >> (16 * (j & 1))), f[2 * j], f[2 * j + 1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= sc[u];
-      *reinterpret_cast<uint4*>(dst + 8 * i) = rows::pack(f);
-    }
+    for (int u = 0; u < kSteps; ++u) x[u] = next[u], sc[u] = nsc[u];
   }
 }
 

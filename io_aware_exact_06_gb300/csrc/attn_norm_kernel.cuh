@@ -1,12 +1,18 @@
 // Norm of every query and key head with the rotary rotation, and its gradient.
 //
 // A row (token, head) of d channels is held by d / 8 lanes, 16 bytes each, so
-// a warp holds 32 / (d / 8) rows (2 at d = 128, 4 at d = 64) and takes kSteps
-// such groups of one token's heads.  The row's sum of squares is a shuffle
-// reduction; the partner channel of a half-split pair sits rot / 16 lanes away
-// in the same register, that of an interleaved pair in the same lane.  Nothing
-// goes through shared memory in the forward; each element is read and written
-// once, so HBM bounds it (and launch latency for a few tokens).
+// a warp holds 32 / (d / 8) rows (2 at d = 128, 4 at d = 64) at a time.  The
+// row's sum of squares is a shuffle reduction; the partner channel of a
+// half-split pair sits rot / 16 lanes away in the same register, that of an
+// interleaved pair in the same lane.  Nothing goes through shared memory in the
+// forward; each element is read and written once, so HBM bounds it (and launch
+// latency for a few tokens).
+//
+// The heads of a token are cut into chunks of kSteps (forward) or kBwdSteps row
+// groups, and a warp takes a run of a token's chunks: it loads the next chunk
+// before it works on the current one, and the token's position and angles, two
+// dependent loads, once per run.  The run is the whole token when there are
+// tokens enough to fill the GPU four times over, one chunk when there are few.
 #pragma once
 
 #include "attn_rows.cuh"
@@ -16,7 +22,8 @@ namespace norm {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSteps = 4;  // row groups a warp loads before it uses the first
+constexpr int kSteps = 4;     // row groups of a chunk, forward
+constexpr int kBwdSteps = 2;  // gradient: two tensors are loaded
 
 struct Rotary {
   const float *cos, *sin;  // [P, half]
@@ -30,19 +37,22 @@ struct Fwd {
   __nv_bfloat16 *qo, *ko;
   int64_t q_ts, k_ts, qo_ts, ko_ts;
   int T, Hq, Hk;
+  int run;  // chunks of a warp
   float eps;
   Rotary rot;
   int* err;
 };
 
 struct Bwd {
-  const __nv_bfloat16 *q, *k, *wq, *wk, *gq, *gk;
-  __nv_bfloat16 *dq, *dk;
-  int64_t q_ts, k_ts, gq_ts, gk_ts, dq_ts, dk_ts;
-  int T, Hq, Hk;
+  const __nv_bfloat16 *x[2], *w[2], *g[2];  // queries, keys
+  __nv_bfloat16* dx[2];
+  int64_t x_ts[2], g_ts[2], dx_ts[2];
+  int H[2], run[2];
+  int T;
+  int ctas_q;  // CTAs 0 .. ctas_q - 1 take the queries, the others the keys
   float eps;
   Rotary rot;
-  float* part;  // [gridDim.x][2][D]
+  float* part;  // [gridDim.x][D]
   int* err;
 };
 
@@ -115,7 +125,7 @@ __device__ __forceinline__ void rotate(float (&y)[8], const float (&c)[8], const
 }
 
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ Fwd p) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ Fwd p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
@@ -123,167 +133,202 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   grid_dep_launch();
   const int H = p.Hq + p.Hk;
   const int chunks = (H + kChunk - 1) / kChunk;
+  const int runs = (chunks + p.run - 1) / p.run;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item >= (int64_t)p.T * chunks) return;
-  const int t = (int)(item / chunks);
-  const int h0 = (int)(item - (int64_t)t * chunks) * kChunk;
-  uint4 x[kSteps];
+  if (item >= (int64_t)p.T * runs) return;
+  const int t = (int)(item / runs);
+  const int c0 = (int)(item - (int64_t)t * runs) * p.run, c1 = min(chunks, c0 + p.run);
+  const __nv_bfloat16* qs = p.q + t * p.q_ts + row * D + 8 * slice;
+  const __nv_bfloat16* ks = p.k + t * p.k_ts + row * D + 8 * slice;
+  __nv_bfloat16* qd = p.qo + t * p.qo_ts + row * D + 8 * slice;
+  __nv_bfloat16* kd = p.ko + t * p.ko_ts + row * D + 8 * slice;
+  auto load = [&](int chunk, uint4 (&x)[kSteps]) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (h < H) {
-      const __nv_bfloat16* src = h < p.Hq ? p.q + t * p.q_ts + (int64_t)h * D
-                                          : p.k + t * p.k_ts + (int64_t)(h - p.Hq) * D;
-      x[u] = *reinterpret_cast<const uint4*>(src + 8 * slice);
+    for (int u = 0; u < kSteps; ++u) {
+      const int h = chunk * kChunk + u * kRows;  // of the group's first row
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (h + row < H)
+        x[u] = *reinterpret_cast<const uint4*>(h + row < p.Hq ? qs + (int64_t)h * D
+                                                              : ks + (int64_t)(h - p.Hq) * D);
     }
-  }
-  float c[8], s[8], w[2][8];
+  };
+  uint4 x[kSteps];
+  load(c0, x);
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (p.Hq) wq = *reinterpret_cast<const uint4*>(p.wq + 8 * slice);
+  if (p.Hk) wk = *reinterpret_cast<const uint4*>(p.wk + 8 * slice);
+  float c[8], s[8];
   bool rotates;
-  const bool ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates);
-  if (!ok) {  // the same for the whole warp: one token
+  if (!load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates)) {  // the same for the whole warp: one token
     if (lane == 0) atomicOr(p.err, rows::kBadIndex);
     return;
   }
-  if (p.Hq) rows::unpack(*reinterpret_cast<const uint4*>(p.wq + 8 * slice), w[0]);
-  if (p.Hk) rows::unpack(*reinterpret_cast<const uint4*>(p.wk + 8 * slice), w[1]);
+  for (int ch = c0; ch < c1; ++ch) {
+    uint4 next[kSteps];
+    if (ch + 1 < c1) load(ch + 1, next);
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int h = h0 + u * kRows + row;
-    float y[8];
-    rows::unpack(x[u], y);
-    float sq = 0.f;
+    for (int u = 0; u < kSteps; ++u) {
+      const int h = ch * kChunk + u * kRows;
+      const bool isq = h + row < p.Hq;
+      float y[8], w[8];
+      rows::unpack(x[u], y);
+      rows::unpack(isq ? wq : wk, w);
+      float sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-    const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
+      for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
+      const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * r * (h < p.Hq ? w[0][i] : w[1][i]);
-    rotate<kInter, false>(y, c, s, rotates, p.rot.half, slice);
-    if (h < H) {
-      __nv_bfloat16* dst = h < p.Hq ? p.qo + t * p.qo_ts + (int64_t)h * D
-                                    : p.ko + t * p.ko_ts + (int64_t)(h - p.Hq) * D;
-      *reinterpret_cast<uint4*>(dst + 8 * slice) = rows::pack(y);
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+      rotate<kInter, false>(y, c, s, rotates, p.rot.half, slice);
+      if (h + row < H)
+        *reinterpret_cast<uint4*>(isq ? qd + (int64_t)h * D : kd + (int64_t)(h - p.Hq) * D) = rows::pack(y);
     }
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) x[u] = next[u];
   }
 }
 
 // Gradient.  With n = x r and g the output's gradient rotated back:
 //   dw = sum over rows of g n,   dn = g w,   dx = r (dn - n mean(dn n)),
-// both row sums (x^2 and g w x) in one reduction.  Persistent CTAs; a lane
-// keeps its 8 channels of dwq and dwk in registers over all its rows, the CTA
-// adds its warps' through shared memory and writes one partial row, and
-// norm_weight_kernel adds the CTAs' in a fixed order: no atomics, so results
-// repeat bit for bit.
+// both row sums (x^2 and g w x) in one reduction.  Persistent CTAs, each for
+// queries or for keys alone (in proportion to their heads), so that a lane
+// carries one weight and the 8 channels of one weight gradient in registers over
+// all its rows; the CTA adds its warps' through shared memory and writes one
+// partial row, and norm_weight_kernel adds the CTAs' in a fixed order: no
+// atomics, so results repeat bit for bit.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ Bwd p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ Bwd p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kBwdSteps;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
-  __shared__ float sm[kWarps][2][D];
+  __shared__ float sm[kWarps][D];
   grid_dep_wait();
   grid_dep_launch();
-  // a chunk holds heads of one kind, so that its weight gradient has one home
-  const int cq = (p.Hq + kChunk - 1) / kChunk, ck = (p.Hk + kChunk - 1) / kChunk;
-  const int chunks = cq + ck;
-  float acc[2][8], w[2][8];
+  const int kind = (int)blockIdx.x >= p.ctas_q;
+  const int cta = blockIdx.x - (kind ? p.ctas_q : 0), ctas = kind ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int H = p.H[kind], run = p.run[kind];
+  const int chunks = (H + kChunk - 1) / kChunk, runs = (chunks + run - 1) / run;
+  const int64_t items = (int64_t)p.T * runs, stride = (int64_t)ctas * kWarps;
+  const __nv_bfloat16* xb = p.x[kind] + row * D + 8 * slice;
+  const __nv_bfloat16* gb = p.g[kind] + row * D + 8 * slice;
+  __nv_bfloat16* db = p.dx[kind] + row * D + 8 * slice;
+  const int64_t x_ts = p.x_ts[kind], g_ts = p.g_ts[kind], dx_ts = p.dx_ts[kind];
+  float acc[8], w[8];
+  rows::unpack(*reinterpret_cast<const uint4*>(p.w[kind] + 8 * slice), w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = w[0][i] = w[1][i] = 0.f;
-  if (p.Hq) rows::unpack(*reinterpret_cast<const uint4*>(p.wq + 8 * slice), w[0]);
-  if (p.Hk) rows::unpack(*reinterpret_cast<const uint4*>(p.wk + 8 * slice), w[1]);
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)p.T * chunks;
-       item += (int64_t)gridDim.x * kWarps) {
-    const int t = (int)(item / chunks);
-    const int ch = (int)(item - (int64_t)t * chunks);
-    const bool isk = ch >= cq;
-    const int h0 = (isk ? ch - cq : ch) * kChunk, H = isk ? p.Hk : p.Hq;
-    const __nv_bfloat16* xs = isk ? p.k + t * p.k_ts : p.q + t * p.q_ts;
-    const __nv_bfloat16* gs = isk ? p.gk + t * p.gk_ts : p.gq + t * p.gq_ts;
-    __nv_bfloat16* ds = isk ? p.dk + t * p.dk_ts : p.dq + t * p.dq_ts;
-    uint4 xv[kSteps], gv[kSteps];
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  auto load = [&](int t, int chunk, uint4 (&xv)[kBwdSteps], uint4 (&gv)[kBwdSteps]) {
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int h = h0 + u * kRows + row;
+    for (int u = 0; u < kBwdSteps; ++u) {
+      const int h = chunk * kChunk + u * kRows;
       xv[u] = gv[u] = make_uint4(0, 0, 0, 0);
-      if (h < H) {
-        xv[u] = *reinterpret_cast<const uint4*>(xs + (int64_t)h * D + 8 * slice);
-        gv[u] = *reinterpret_cast<const uint4*>(gs + (int64_t)h * D + 8 * slice);
+      if (h + row < H) {
+        xv[u] = *reinterpret_cast<const uint4*>(xb + t * x_ts + (int64_t)h * D);
+        gv[u] = *reinterpret_cast<const uint4*>(gb + t * g_ts + (int64_t)h * D);
       }
     }
+  };
+  int64_t item = (int64_t)cta * kWarps + warp;
+  uint4 xv[kBwdSteps], gv[kBwdSteps];
+  int t = 0, ch = 0, c1 = 0;
+  auto place = [&](int64_t it) {
+    t = (int)(it / runs);
+    ch = (int)(it - (int64_t)t * runs) * run;
+    c1 = min(chunks, ch + run);
+  };
+  if (item < items) {
+    place(item);
+    load(t, ch, xv, gv);
+  }
+  while (item < items) {
     float c[8], s[8];
     bool rotates;
-    if (!load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates)) {
-      if (lane == 0) atomicOr(p.err, rows::kBadIndex);
-      continue;
-    }
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int h = h0 + u * kRows + row;
-      float x[8], g[8];
-      rows::unpack(xv[u], x);
-      rows::unpack(gv[u], g);
-      rotate<kInter, true>(g, c, s, rotates, p.rot.half, slice);
-      float sq = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sq = fmaf(x[i], x[i], sq);
-        dot = fmaf(g[i] * (isk ? w[1][i] : w[0][i]), x[i], dot);
+    const bool ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates);
+    if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
+    while (true) {  // the run's chunks; the next one, of this run or the next, is on its way
+      const int ct = t, cc = ch;
+      const bool last = ++ch == c1;
+      if (last) {
+        item += stride;
+        if (item < items) place(item);
       }
-      sq = rows::row_sum<kLanes>(sq);
-      dot = rows::row_sum<kLanes>(dot);
-      const float r = rsqrtf(sq * (1.0f / D) + p.eps);
-      const float coef = dot * (1.0f / D) * r * r;
-      float dx[8];
+      uint4 nx[kBwdSteps], ng[kBwdSteps];
+      if (item < items) load(t, ch, nx, ng);
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dx[i] = r * (g[i] * (isk ? w[1][i] : w[0][i]) - x[i] * coef);
-        const float dw = h < H ? g[i] * (x[i] * r) : 0.f;
-        acc[0][i] += isk ? 0.f : dw;
-        acc[1][i] += isk ? dw : 0.f;
+        for (int u = 0; u < kBwdSteps; ++u) {
+          const int h = cc * kChunk + u * kRows;
+          float x[8], g[8];
+          rows::unpack(xv[u], x);
+          rows::unpack(gv[u], g);
+          rotate<kInter, true>(g, c, s, rotates, p.rot.half, slice);
+          float sq = 0.f, dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sq = fmaf(x[i], x[i], sq);
+            dot = fmaf(g[i] * w[i], x[i], dot);
+          }
+          sq = rows::row_sum<kLanes>(sq);
+          dot = rows::row_sum<kLanes>(dot);
+          const float r = rsqrtf(sq * (1.0f / D) + p.eps);
+          const float coef = dot * (1.0f / D) * r * r;
+          float dx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dx[i] = r * (g[i] * w[i] - x[i] * coef);
+            if (h + row < H) acc[i] += g[i] * (x[i] * r);
+          }
+          if (h + row < H) *reinterpret_cast<uint4*>(db + ct * dx_ts + (int64_t)h * D) = rows::pack(dx);
+        }
       }
-      if (h < H) *reinterpret_cast<uint4*>(ds + (int64_t)h * D + 8 * slice) = rows::pack(dx);
+#pragma unroll
+      for (int u = 0; u < kBwdSteps; ++u) xv[u] = nx[u], gv[u] = ng[u];
+      if (last) break;
     }
   }
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int i = 0; i < 8; ++i) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int off = kLanes; off < 32; off <<= 1)
-        acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], off);
-      if (row == 0) sm[warp][m][8 * slice + i] = acc[m][i];
-    }
+    for (int off = kLanes; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    if (row == 0) sm[warp][8 * slice + i] = acc[i];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int wp = 0; wp < kWarps; ++wp) v += sm[wp][i / D][i % D];
-    p.part[(int64_t)blockIdx.x * 2 * D + i] = v;
+    for (int wp = 0; wp < kWarps; ++wp) v += sm[wp][i];
+    p.part[(int64_t)blockIdx.x * D + i] = v;
   }
 }
 
 struct WeightSum {
-  const float* part;  // [G][2][D]
+  const float* part;  // [Gq + Gk][D]
   float *dwq, *dwk;
-  int G, D;
+  int Gq, Gk, D;
 };
 
-// dwq and dwk: the G partial rows of 2 D floats added up.  32 columns a CTA,
-// 32 slices of rows each, then the slices in shared memory.
+// dwq and dwk: the partial rows of their CTAs added up.  32 columns a CTA, 32
+// slices of rows each, then the slices in shared memory.
 __global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ WeightSum p) {
   __shared__ float sm[32][33];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, sl = threadIdx.x / 32;
+  const int per = p.D / 32, lane = threadIdx.x % 32, sl = threadIdx.x / 32;
+  const bool isk = (int)blockIdx.x >= per;
+  const int col = (blockIdx.x - (isk ? per : 0)) * 32 + lane;
+  const float* part = p.part + (isk ? (int64_t)p.Gq * p.D : 0) + col;
+  const int G = isk ? p.Gk : p.Gq;
   grid_dep_wait();
   grid_dep_launch();
   float v = 0.f;
-  for (int g = sl; g < p.G; g += 32) v += p.part[(int64_t)g * 2 * p.D + col];
-  sm[sl][threadIdx.x % 32] = v;
+#pragma unroll 4
+  for (int g = sl; g < G; g += 32) v += part[(int64_t)g * p.D];
+  sm[sl][lane] = v;
   __syncthreads();
   if (sl == 0) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += sm[i][threadIdx.x];
-    float* dst = col < p.D ? p.dwq : p.dwk;
-    if (dst) dst[col % p.D] = v;
+    for (int i = 0; i < 32; ++i) v += sm[i][lane];
+    float* dst = isk ? p.dwk : p.dwq;
+    if (dst) dst[col] = v;
   }
 }
 

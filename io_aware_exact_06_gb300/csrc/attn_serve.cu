@@ -97,14 +97,39 @@ int check_norm(int T, int Hq, int Hk, int d, float eps) {
   return ATTN_OK;
 }
 
-int64_t norm_chunk(int d) { return (int64_t)(32 / (d / 8)) * attn::norm::kSteps; }
+// Chunks of H heads of d channels when a warp holds `steps` row groups.
+int64_t chunks_of(int H, int d, int steps) {
+  const int64_t c = (int64_t)(32 / (d / 8)) * steps;
+  return (H + c - 1) / c;
+}
 
-// CTAs of the gradient: two an SM, what the kernel's registers allow; fewer
-// when there is less to do.  The order of the weight sums depends on it alone.
-int64_t bwd_ctas(int T, int Hq, int Hk, int d) {
-  const int64_t c = norm_chunk(d);
-  const int64_t items = (int64_t)T * ((Hq + c - 1) / c + (Hk + c - 1) / c);
-  return std::min<int64_t>((items + attn::norm::kWarps - 1) / attn::norm::kWarps, 2 * kPlanSms);
+// How many of `most` pieces (chunks of a token, tokens) a warp takes one after
+// the other: as many as leave the GPU's resident warps about four rounds, so
+// that loads run ahead without an uneven end.
+int run_of(int64_t pieces, int64_t most, int warps_per_sm) {
+  return (int)std::clamp<int64_t>(pieces / (4 * (int64_t)kPlanSms * warps_per_sm), 1, most);
+}
+
+// CTAs of the gradient for queries and for keys: two an SM in all, what the
+// kernel's registers allow, in proportion to the heads; fewer when there is
+// less to do.  The order of the weight sums depends on these alone.
+struct BwdPlan {
+  int64_t ctas[2];
+  int run[2];
+};
+BwdPlan bwd_plan(int T, int Hq, int Hk, int d) {
+  BwdPlan pl{};
+  const int H[2] = {Hq, Hk};
+  int64_t share = 2 * kPlanSms;
+  for (int i = 0; i < 2; ++i) {
+    if (H[i] == 0 || T == 0) continue;
+    const int64_t chunks = chunks_of(H[i], d, attn::norm::kBwdSteps);
+    const int64_t mine = std::max<int64_t>(1, share * H[i] / (Hq + Hk));
+    pl.run[i] = (int)std::clamp<int64_t>((int64_t)T * chunks / (4 * mine * attn::norm::kWarps), 1, chunks);
+    const int64_t items = (int64_t)T * ((chunks + pl.run[i] - 1) / pl.run[i]);
+    pl.ctas[i] = std::min((items + attn::norm::kWarps - 1) / attn::norm::kWarps, mine);
+  }
+  return pl;
 }
 
 // --------------------------------------------------------------------- cache --
@@ -126,6 +151,8 @@ int check_cache(const attn_paged_cache* c) {
     return ATTN_ERR_ALIGN;
   return ATTN_OK;
 }
+
+constexpr int kMaxRun = 16;  // tokens a warp writes or reads one after the other, at most
 
 attn::cache::Pages pages_of(const attn_paged_cache* c) {
   attn::cache::Pages p{};
@@ -231,8 +258,9 @@ extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
   if ((st = check_rows(k_out, k_out_stride, Hk, d)) != ATTN_OK) return st;
   if ((Hq && !wq) || (Hk && !wk)) return ATTN_ERR_NULL;
   if (!aligned(wq, 16) || !aligned(wk, 16)) return ATTN_ERR_ALIGN;
-  const int64_t c = norm_chunk(d);
-  const int64_t items = (int64_t)T * ((Hq + Hk + c - 1) / c);
+  const int64_t chunks = chunks_of(Hq + Hk, d, attn::norm::kSteps);
+  p.run = run_of(T * chunks, chunks, 3 * attn::norm::kWarps);
+  const int64_t items = T * ((chunks + p.run - 1) / p.run);
   const int64_t grid = (items + attn::norm::kWarps - 1) / attn::norm::kWarps;
   if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
@@ -260,7 +288,8 @@ extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
 
 extern "C" size_t attn_qk_norm_rope_bwd_workspace(int T, int Hq, int Hk, int d) {
   if (check_norm(T, Hq, Hk, d, 0.f) != ATTN_OK) return 0;
-  return (size_t)bwd_ctas(T, Hq, Hk, d) * 2 * d * sizeof(float);
+  const BwdPlan pl = bwd_plan(T, Hq, Hk, d);
+  return (size_t)(pl.ctas[0] + pl.ctas[1]) * d * sizeof(float);
 }
 
 extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -277,7 +306,8 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
   if (Hq + Hk == 0) return ATTN_OK;
   if ((Hq && !dwq) || (Hk && !dwk)) return ATTN_ERR_NULL;
   if (!aligned(dwq, 4) || !aligned(dwk, 4)) return ATTN_ERR_ALIGN;
-  const int64_t grid = bwd_ctas(T, Hq, Hk, d);
+  const BwdPlan pl = bwd_plan(T, Hq, Hk, d);
+  const int64_t grid = pl.ctas[0] + pl.ctas[1];
   if (T > 0) {
     if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
     if ((st = check_rows(k, k_stride, Hk, d)) != ATTN_OK) return st;
@@ -287,29 +317,29 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
     if ((st = check_rows(dk, dk_stride, Hk, d)) != ATTN_OK) return st;
     if ((Hq && !wq) || (Hk && !wk)) return ATTN_ERR_NULL;
     if (!aligned(wq, 16) || !aligned(wk, 16)) return ATTN_ERR_ALIGN;
-    if (!workspace || workspace_bytes < (size_t)grid * 2 * d * sizeof(float)) return ATTN_ERR_SCRATCH;
+    if (!workspace || workspace_bytes < (size_t)grid * d * sizeof(float)) return ATTN_ERR_SCRATCH;
     if (!aligned(workspace, 16)) return ATTN_ERR_ALIGN;
   }
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T > 0) {
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k = static_cast<const __nv_bfloat16*>(k);
-    p.wq = static_cast<const __nv_bfloat16*>(wq);
-    p.wk = static_cast<const __nv_bfloat16*>(wk);
-    p.gq = static_cast<const __nv_bfloat16*>(dq_out);
-    p.gk = static_cast<const __nv_bfloat16*>(dk_out);
-    p.dq = static_cast<__nv_bfloat16*>(dq);
-    p.dk = static_cast<__nv_bfloat16*>(dk);
-    p.q_ts = q_stride;
-    p.k_ts = k_stride;
-    p.gq_ts = dq_out_stride;
-    p.gk_ts = dk_out_stride;
-    p.dq_ts = dq_stride;
-    p.dk_ts = dk_stride;
+    const void *x[2] = {q, k}, *w[2] = {wq, wk}, *g[2] = {dq_out, dk_out};
+    void* dx[2] = {dq, dk};
+    const int64_t x_ts[2] = {q_stride, k_stride}, g_ts[2] = {dq_out_stride, dk_out_stride},
+                  dx_ts[2] = {dq_stride, dk_stride};
+    for (int i = 0; i < 2; ++i) {
+      p.x[i] = static_cast<const __nv_bfloat16*>(x[i]);
+      p.w[i] = static_cast<const __nv_bfloat16*>(w[i]);
+      p.g[i] = static_cast<const __nv_bfloat16*>(g[i]);
+      p.dx[i] = static_cast<__nv_bfloat16*>(dx[i]);
+      p.x_ts[i] = x_ts[i];
+      p.g_ts[i] = g_ts[i];
+      p.dx_ts[i] = dx_ts[i];
+      p.H[i] = i ? Hk : Hq;
+      p.run[i] = pl.run[i];
+    }
     p.T = T;
-    p.Hq = Hq;
-    p.Hk = Hk;
+    p.ctas_q = (int)pl.ctas[0];
     p.eps = eps;
     p.part = static_cast<float*>(workspace);
     auto kernel = d == 64 ? rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<64, true>
@@ -319,7 +349,7 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
     if ((st = launch(kernel, grid, attn::norm::kThreads, 0, s, p)) != ATTN_OK) return st;
   }
   const attn::norm::WeightSum w{static_cast<const float*>(workspace), Hq ? dwq : nullptr,
-                                Hk ? dwk : nullptr, T > 0 ? (int)grid : 0, d};
+                                Hk ? dwk : nullptr, (int)pl.ctas[0], (int)pl.ctas[1], d};
   return launch(attn::norm::norm_weight_kernel, 2 * d / 32, 1024, 0, s, w);
 }
 
@@ -334,11 +364,12 @@ extern "C" int attn_cache_write(const attn_paged_cache* cache, const void* k, in
   if ((st = check_rows(v, v_stride, cache->H, cache->d)) != ATTN_OK) return st;
   if (!seqlens || !cu_seqlens) return ATTN_ERR_NULL;
   if (!aligned(seqlens, 4) || !aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
-  const int64_t c = (int64_t)(32 / (cache->d / 8)) * attn::cache::kSteps;
-  const int64_t items = (int64_t)total * ((2 * cache->H + c - 1) / c);
+  attn::cache::Write p{};
+  const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps);
+  p.run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
+  const int64_t items = ((int64_t)total + p.run - 1) / p.run * chunks;
   const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
   if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
-  attn::cache::Write p{};
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
   p.c = pages_of(cache);
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -370,11 +401,12 @@ extern "C" int attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
   if (!cu_seqlens) return ATTN_ERR_NULL;
   if (!aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
   const bool codes = cache->k_scale != nullptr;
-  const int64_t c = (int64_t)(32 / (cache->d / (codes ? 16 : 8))) * attn::cache::kSteps;
-  const int64_t items = (int64_t)total * ((2 * cache->H + c - 1) / c);
+  attn::cache::Read p{};
+  const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps * (codes ? 2 : 1));
+  p.run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
+  const int64_t items = ((int64_t)total + p.run - 1) / p.run * chunks;
   const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
   if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
-  attn::cache::Read p{};
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
   p.c = pages_of(cache);
   p.k = static_cast<__nv_bfloat16*>(k);

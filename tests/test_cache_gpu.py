@@ -122,7 +122,9 @@ def test_read_ragged_and_padded(dev, codes):
     put(dev, c, kv[:, :H], kv[:, H:], lens, lens)
     k = torch.full((total + 9, H, d), 3.0, dtype=torch.bfloat16, device=dev)
     v = torch.full_like(k, 3.0)
-    cache = fa._cache(c["k_cache"], c["v_cache"], c["page_table"], len(lens), c["k_scale"], c["v_scale"])
+    ptr = lambda t: None if t is None else t.data_ptr()
+    cache = fa.AttnPagedCache(ptr(c["k_cache"]), ptr(c["v_cache"]), ptr(c["k_scale"]), ptr(c["v_scale"]),
+                              ptr(c["page_table"]), c["page_table"].shape[1], c["k_cache"].shape[0], page, H, d)
     fa.attn_cache_read(cache, k, v, cu_of(dev, lens), len(lens), total + 9)
     assert fa.attn_last_device_error() == 0
     assert (k[total:] == 3).all() and (v[total:] == 3).all()
