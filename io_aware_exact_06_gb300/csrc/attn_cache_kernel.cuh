@@ -1,8 +1,10 @@
 // Writing packed keys and values into a paged cache, and reading it back.
 //
 // The rows of a token (its H key heads, then its H value heads) are cut into
-// chunks; a warp takes one chunk of a run of consecutive tokens, the next
-// token's rows on their way while it works on the current ones.  Writing: d / 8
+// chunks; a warp takes one chunk of `run` tokens, `step` tokens apart, the next
+// token's rows on their way while it works on the current ones; all warps
+// together so sweep the packed rows in order, which DRAM serves faster than as
+// many streams as there are warps.  Writing: d / 8
 // lanes hold a row's bf16 channels, 16 bytes each; the row maximum is a shuffle
 // reduction and the codes leave 8 bytes a lane.  Reading: d / 16 lanes hold a
 // row's codes, 16 bytes each (bf16 caches: d / 8 lanes), and write 32 bytes a
@@ -34,7 +36,7 @@ struct Write {
   int64_t k_ts, v_ts;
   const int *lens, *cu;
   int B, total;
-  int run;  // tokens of a warp
+  int step;  // a warp takes tokens t, t + step, ..
   int* err;
 };
 
@@ -43,13 +45,12 @@ struct Read {
   __nv_bfloat16 *k, *v;
   const int* cu;
   int B, total;
-  int run;  // tokens of a warp
+  int step;  // a warp takes tokens t, t + step, ..
   int* err;
 };
 
-// Where a warp's tokens lie in the cache.  Tokens come in packed order, so the
-// search and the loads that depend on it happen once per sequence and page, not
-// once per token.
+// Where a warp's tokens lie in the cache.  The search and the loads that depend
+// on it happen once per sequence and page that its tokens fall in.
 struct Cursor {
   int b = -1, start = 0, end = 0, shift = 0;  // packed tokens start .. end-1 sit at positions t + shift
   int page_at = -1;                           // index of the page in the sequence
@@ -130,10 +131,9 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_c
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
   const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t first = item / chunks * p.run;
-  if (first >= p.total) return;
+  if (item / chunks >= p.step) return;
+  const int t0 = (int)(item / chunks);
   const int h0 = (int)(item % chunks) * kChunk;
-  const int t0 = (int)first, t1 = (int)min((int64_t)p.total, first + p.run);
   auto load = [&](int t, uint4 (&x)[kSteps]) {
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
@@ -147,9 +147,10 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_c
   uint4 x[kSteps];
   load(t0, x);  // on its way while the token's place is looked up
   Cursor cur;
-  for (int t = t0; t < t1; ++t) {
+  for (int64_t tt = t0; tt < p.total; tt += p.step) {
+    const int t = (int)tt;
     uint4 next[kSteps];
-    if (t + 1 < t1) load(t + 1, next);
+    if (tt + p.step < p.total) load(t + p.step, next);
     const int64_t r = find_row(cur, p.c, p.cu, p.lens, p.B, t, p.err);
     if (r >= 0) {
 #pragma unroll
@@ -198,10 +199,9 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
   const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t first = item / chunks * p.run;
-  if (first >= p.total) return;
+  if (item / chunks >= p.step) return;
+  const int t0 = (int)(item / chunks);
   const int h0 = (int)(item % chunks) * kChunk;
-  const int t0 = (int)first, t1 = (int)min((int64_t)p.total, first + p.run);
   Cursor cur;
   auto load = [&](int64_t r, uint4 (&x)[kSteps], float (&sc)[kSteps]) {
 #pragma unroll
@@ -221,12 +221,13 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
   float sc[kSteps];
   int64_t r = find_row(cur, p.c, p.cu, nullptr, p.B, t0, p.err);
   load(r, x, sc);
-  for (int t = t0; t < t1; ++t) {
+  for (int64_t tt = t0; tt < p.total; tt += p.step) {
+    const int t = (int)tt;
     uint4 next[kSteps];
     float nsc[kSteps];
     int64_t rn = -1;
-    if (t + 1 < t1) {
-      rn = find_row(cur, p.c, p.cu, nullptr, p.B, t + 1, p.err);
+    if (tt + p.step < p.total) {
+      rn = find_row(cur, p.c, p.cu, nullptr, p.B, t + p.step, p.err);
       load(rn, next, nsc);
     }
     if (r >= 0) {

@@ -171,26 +171,28 @@ attn::cache::Pages pages_of(const attn_paged_cache* c) {
 
 // ---------------------------------------------------------------------- tree --
 struct Plan {
-  int wm, mtiles, chunk, S;
+  int rows;  // query rows of a CTA: 8 or 16 (few rows), 32 or 64
+  int mtiles, chunk, S;
 };
 
-// Row tiles of 16, 32 or 64 rows (the smallest that holds max_new * G), and key
-// ranges: about three rounds of two CTAs per SM, so that ragged lengths even
-// out, but at least 128 keys a range, below which starting a CTA and merging
+// Query rows of a CTA: the smallest tile that holds max_new * G of them, and key
+// ranges: about three rounds of the CTAs that fit the SMs, so that ragged lengths
+// even out, but at least 128 keys a range, below which starting a CTA and merging
 // its part cost more than its reading.
 Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
   Plan pl;
   const int64_t M = (int64_t)max_new * (Hq / H);
-  pl.wm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  pl.mtiles = (int)((M + 16 * pl.wm - 1) / (16 * pl.wm));
+  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  pl.mtiles = (int)((M + pl.rows - 1) / pl.rows);
   const int64_t T = attn::tree::kTile, len = std::max(max_len, 1);
   const int64_t items = (int64_t)B * H * pl.mtiles;
+  const int slots = kPlanSms * (pl.rows == 8 ? 3 : 2);
   int64_t chunk;
   if (num_splits > 0)
     chunk = (len + num_splits - 1) / num_splits;
   else
     chunk = std::max<int64_t>(
-        {128, (int64_t)std::min(1e9, (double)len * (double)items / (kPlanSms * 6)), (len + 255) / 256});
+        {128, (int64_t)std::min(1e9, (double)len * (double)items / (slots * 3)), (len + 255) / 256});
   chunk = std::min((chunk + T - 1) / T * T, (len + T - 1) / T * T);
   pl.chunk = (int)chunk;
   pl.S = (int)((len + chunk - 1) / chunk);
@@ -224,21 +226,17 @@ int allow_smem(const void* kernel, int bytes) {
   return ATTN_OK;
 }
 
-template <int D, bool kCodes, int kWM>
-int launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p, int64_t grid,
-                cudaStream_t s) {
-  auto kernel = attn::tree::tree_kernel<D, kCodes, kWM>;
-  constexpr int kSmem = attn::tree::Cfg<D, kCodes>::kSmem;
-  const int st = allow_smem(reinterpret_cast<const void*>(kernel), kSmem);
-  return st != ATTN_OK ? st : launch(kernel, grid, attn::tree::kThreads, kSmem, s, mk, mv, p);
-}
-
 template <int D, bool kCodes>
-int launch_tree(int wm, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
+int launch_tree(int rows, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                 int64_t grid, cudaStream_t s) {
-  return wm == 1   ? launch_tree<D, kCodes, 1>(mk, mv, p, grid, s)
-         : wm == 2 ? launch_tree<D, kCodes, 2>(mk, mv, p, grid, s)
-                   : launch_tree<D, kCodes, 4>(mk, mv, p, grid, s);
+  using namespace attn::tree;
+  auto kernel = rows == 8    ? tree_few_kernel<D, kCodes, 1>
+                : rows == 16 ? tree_few_kernel<D, kCodes, 2>
+                : rows == 32 ? tree_kernel<D, kCodes, 2>
+                             : tree_kernel<D, kCodes, 4>;
+  const int smem = rows <= 16 ? FewCfg<D, kCodes>::kSmem : Cfg<D, kCodes>::kSmem;
+  const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  return st != ATTN_OK ? st : launch(kernel, grid, kThreads, smem, s, mk, mv, p);
 }
 
 }  // namespace
@@ -366,8 +364,9 @@ extern "C" int attn_cache_write(const attn_paged_cache* cache, const void* k, in
   if (!aligned(seqlens, 4) || !aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
   attn::cache::Write p{};
   const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps);
-  p.run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
-  const int64_t items = ((int64_t)total + p.run - 1) / p.run * chunks;
+  const int run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
+  p.step = (total - 1) / run + 1;
+  const int64_t items = p.step * chunks;
   const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
   if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
@@ -403,8 +402,9 @@ extern "C" int attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
   const bool codes = cache->k_scale != nullptr;
   attn::cache::Read p{};
   const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps * (codes ? 2 : 1));
-  p.run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
-  const int64_t items = ((int64_t)total + p.run - 1) / p.run * chunks;
+  const int run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
+  p.step = (total - 1) / run + 1;
+  const int64_t items = p.step * chunks;
   const int64_t grid = (items + attn::cache::kWarps - 1) / attn::cache::kWarps;
   if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
@@ -455,7 +455,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   const int64_t grid = (int64_t)B * pl.S * cache->H * pl.mtiles;
   const bool codes = cache->k_scale != nullptr;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
-  const int box = std::min(cache->page_size, (int)attn::tree::kTile);
+  const int box = std::min(cache->page_size, pl.rows <= 16 ? attn::tree::kFewTile : attn::tree::kTile);
 
   const attn::cache::Pages pg = pages_of(cache);
   attn::tree::Params p{};
@@ -494,10 +494,10 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   CUtensorMap mk, mv;
   if ((st = attn_host::lib_make_cache_map(&mk, cache->k, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
   if ((st = attn_host::lib_make_cache_map(&mv, cache->v, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
-  st = d == 64 ? codes ? launch_tree<64, true>(pl.wm, mk, mv, p, grid, s)
-                       : launch_tree<64, false>(pl.wm, mk, mv, p, grid, s)
-       : codes ? launch_tree<128, true>(pl.wm, mk, mv, p, grid, s)
-               : launch_tree<128, false>(pl.wm, mk, mv, p, grid, s);
+  st = d == 64 ? codes ? launch_tree<64, true>(pl.rows, mk, mv, p, grid, s)
+                       : launch_tree<64, false>(pl.rows, mk, mv, p, grid, s)
+       : codes ? launch_tree<128, true>(pl.rows, mk, mv, p, grid, s)
+               : launch_tree<128, false>(pl.rows, mk, mv, p, grid, s);
   if (st != ATTN_OK || pl.S == 1) return st;
   return launch(d == 64 ? attn::tree::tree_combine_kernel<64> : attn::tree::tree_combine_kernel<128>,
                 combine, 256, 0, s, p);
