@@ -19,6 +19,7 @@
 #include "attn_cache_kernel.cuh"
 #include "attn_host.h"
 #include "attn_norm_kernel.cuh"
+#include "attn_tree_few_kernel.cuh"
 #include "attn_tree_kernel.cuh"
 
 namespace {
@@ -171,36 +172,53 @@ attn::cache::Pages pages_of(const attn_paged_cache* c) {
 
 // ---------------------------------------------------------------------- tree --
 struct Plan {
-  int rows;  // query rows of a CTA: 8 or 16 (few rows), 32 or 64
-  int mtiles, chunk, S;
+  int rows;               // query rows of a CTA: 8 or 16 (few rows), 32 or 64
+  int mtiles, chunk, S;   // 32 or 64: key ranges
+  attn::tree::Work work;  // 8 or 16: the line of tiles
+  int64_t slots;          // parts in the workspace, `rows` rows each
 };
 
-// Query rows of a CTA: the smallest tile that holds max_new * G of them, and key
-// ranges: about three rounds of the CTAs that fit the SMs, so that ragged lengths
-// even out, but at least 128 keys a range, below which starting a CTA and merging
-// its part cost more than its reading.
+bool few(const Plan& pl) { return pl.rows <= 16; }
+
+// Query rows of a CTA: the smallest tile that holds max_new * G of them.  Few
+// rows: as many persistent CTAs as fit the SMs (num_splits caps the pieces of a
+// segment instead), at least four tiles (128 keys) each, below which starting a
+// CTA and merging its part cost more than its reading.  More rows: key ranges.
 Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
-  Plan pl;
+  Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
   pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
   pl.mtiles = (int)((M + pl.rows - 1) / pl.rows);
-  const int64_t T = attn::tree::kTile, len = std::max(max_len, 1);
-  const int64_t items = (int64_t)B * H * pl.mtiles;
-  const int slots = kPlanSms * (pl.rows == 8 ? 3 : 2);
+  const int64_t len = std::max(max_len, 1);
+  const int64_t segments = (int64_t)B * H * pl.mtiles;
+  if (few(pl)) {
+    const int64_t T = attn::tree::kFewTile, tiles = (len + T - 1) / T;
+    pl.work.rows = pl.rows;
+    pl.work.log_tile = attn::tree::kLogFewTile;
+    pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 4;
+    const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
+    pl.work.ctas = (int)std::min<int64_t>(most, kPlanSms * attn::tree::kFewCtas);
+    pl.slots = 2 * (int64_t)pl.work.ctas;
+    return pl;
+  }
+  const int64_t T = attn::tree::kTile;
   int64_t chunk;
   if (num_splits > 0)
     chunk = (len + num_splits - 1) / num_splits;
   else
     chunk = std::max<int64_t>(
-        {128, (int64_t)std::min(1e9, (double)len * (double)items / (slots * 3)), (len + 255) / 256});
+        {128, (int64_t)std::min(1e9, (double)len * (double)segments / (kPlanSms * 6)), (len + 255) / 256});
   chunk = std::min((chunk + T - 1) / T * T, (len + T - 1) / T * T);
   pl.chunk = (int)chunk;
   pl.S = (int)((len + chunk - 1) / chunk);
   return pl;
 }
 
+size_t tree_rows(const Plan& pl, int total, int Hq) {
+  return few(pl) ? (size_t)pl.slots * pl.rows : pl.S == 1 ? 0 : (size_t)pl.S * total * Hq;
+}
 size_t tree_bytes(const Plan& pl, int total, int Hq, int d) {
-  return pl.S == 1 ? 0 : (size_t)pl.S * total * Hq * (d + 1) * sizeof(float);
+  return tree_rows(pl, total, Hq) * (d + 1) * sizeof(float);
 }
 
 int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
@@ -227,16 +245,22 @@ int allow_smem(const void* kernel, int bytes) {
 }
 
 template <int D, bool kCodes>
-int launch_tree(int rows, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
-                int64_t grid, cudaStream_t s) {
+int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
+                int64_t grid, int64_t join, cudaStream_t s) {
   using namespace attn::tree;
-  auto kernel = rows == 8    ? tree_few_kernel<D, kCodes, 1>
-                : rows == 16 ? tree_few_kernel<D, kCodes, 2>
-                : rows == 32 ? tree_kernel<D, kCodes, 2>
-                             : tree_kernel<D, kCodes, 4>;
-  const int smem = rows <= 16 ? FewCfg<D, kCodes>::kSmem : Cfg<D, kCodes>::kSmem;
-  const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
-  return st != ATTN_OK ? st : launch(kernel, grid, kThreads, smem, s, mk, mv, p);
+  int st;
+  if (few(pl)) {
+    auto kernel = pl.rows == 8 ? tree_few_kernel<D, kCodes, 1> : tree_few_kernel<D, kCodes, 2>;
+    const int smem = pl.rows == 8 ? FewCfg<D, kCodes, 1>::kSmem : FewCfg<D, kCodes, 2>::kSmem;
+    if ((st = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != ATTN_OK) return st;
+    if ((st = launch(kernel, pl.work.ctas, kFewThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK) return st;
+    return launch(tree_join_kernel<D>, join, 256, 0, s, p, pl.work);
+  }
+  auto kernel = pl.rows == 32 ? tree_kernel<D, kCodes, 2> : tree_kernel<D, kCodes, 4>;
+  constexpr int kSmem = Cfg<D, kCodes>::kSmem;
+  if ((st = allow_smem(reinterpret_cast<const void*>(kernel), kSmem)) != ATTN_OK) return st;
+  if ((st = launch(kernel, grid, kThreads, kSmem, s, mk, mv, p)) != ATTN_OK || pl.S == 1) return st;
+  return launch(tree_combine_kernel<D>, join, 256, 0, s, p);
 }
 
 }  // namespace
@@ -449,13 +473,13 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   const Plan pl = tree_plan(B, Hq, cache->H, max_new, max_len, num_splits);
   const size_t need = tree_bytes(pl, total, Hq, d);
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_SCRATCH;
-  const double ctas = (double)B * pl.S * cache->H * pl.mtiles;
+  const double ctas = (double)B * std::max(pl.S, 1) * cache->H * pl.mtiles;
   const int64_t combine = ((int64_t)total * Hq + 7) / 8;
   if (ctas > INT32_MAX || combine > INT32_MAX) return ATTN_ERR_SHAPE;
   const int64_t grid = (int64_t)B * pl.S * cache->H * pl.mtiles;
   const bool codes = cache->k_scale != nullptr;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
-  const int box = std::min(cache->page_size, pl.rows <= 16 ? attn::tree::kFewTile : attn::tree::kTile);
+  const int box = std::min(cache->page_size, few(pl) ? attn::tree::kFewTile : attn::tree::kTile);
 
   const attn::cache::Pages pg = pages_of(cache);
   attn::tree::Params p{};
@@ -471,7 +495,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = need ? p.o_part + (size_t)pl.S * total * Hq * d : nullptr;
+  p.lse_part = need ? p.o_part + tree_rows(pl, total, Hq) * d : nullptr;
   p.B = B;
   p.total = total;
   p.Hq = Hq;
@@ -494,11 +518,8 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   CUtensorMap mk, mv;
   if ((st = attn_host::lib_make_cache_map(&mk, cache->k, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
   if ((st = attn_host::lib_make_cache_map(&mv, cache->v, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
-  st = d == 64 ? codes ? launch_tree<64, true>(pl.rows, mk, mv, p, grid, s)
-                       : launch_tree<64, false>(pl.rows, mk, mv, p, grid, s)
-       : codes ? launch_tree<128, true>(pl.rows, mk, mv, p, grid, s)
-               : launch_tree<128, false>(pl.rows, mk, mv, p, grid, s);
-  if (st != ATTN_OK || pl.S == 1) return st;
-  return launch(d == 64 ? attn::tree::tree_combine_kernel<64> : attn::tree::tree_combine_kernel<128>,
-                combine, 256, 0, s, p);
+  return d == 64 ? codes ? launch_tree<64, true>(pl, mk, mv, p, grid, combine, s)
+                         : launch_tree<64, false>(pl, mk, mv, p, grid, combine, s)
+         : codes ? launch_tree<128, true>(pl, mk, mv, p, grid, combine, s)
+                 : launch_tree<128, false>(pl, mk, mv, p, grid, combine, s);
 }

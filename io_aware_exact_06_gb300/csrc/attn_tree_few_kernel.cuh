@@ -1,0 +1,452 @@
+// Attention of the newest tokens over the paged cache for few query rows of a key
+// head, on the warp-level tensor instructions (see attn_tree_kernel.cuh for what
+// is computed and how codes and scales enter).
+#pragma once
+
+#include "attn_tree_work.cuh"
+
+namespace attn {
+namespace tree {
+
+// Up to 8 kNT rows (one token, or a few drafts, of a key head's group): keys
+// take the 16-row side of the products and queries the 8-column side,
+//   S^T = K Q^T,   O^T += V^T P^T,
+// so a fragment holds 8 queries, not 16, and every warp takes whole tiles of
+// its own (tile i of the CTA's share goes to warp i mod 4): no key or value is
+// read or converted twice, and the warps meet only at the end of a piece.  P^T
+// is the score fragment transposed in registers (movmatrix).
+//
+// Persistent CTAs, three an SM.  Each warp owns its stages of the ring: when it
+// is done with a tile it issues the copies of a later one into the same stage
+// itself, across the ends of segments.  (A producer warp for the CTA spent about
+// 1000 cycles a 32-key tile on issue, against 365 that HBM needs for e4m3 tiles
+// of three CTAs; four warps share that work and need no barrier to hand a stage
+// back.)
+constexpr int kFewTile = 32;  // keys per stage
+constexpr int kLogFewTile = 5;
+constexpr int kFewThreads = 32 * kWarps;
+constexpr int kFewCtas = 3;  // per SM
+
+template <int D, bool kCodes, int kNT>
+struct FewCfg : Row<D, kCodes> {
+  using Row<D, kCodes>::kRowBytes;
+  static constexpr int kMatBytes = kFewTile * kRowBytes;
+  static constexpr int kScaleBytes = kCodes ? kFewTile * 4 : 0;
+  static constexpr int kStage = 2 * kMatBytes;
+  static constexpr int kOwn = 16384 / kStage < 3 ? 16384 / kStage : 3;  // stages of a warp
+  static constexpr int kStages = kOwn * kWarps;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kMergeCols = 32;  // the warps' sums meet 32 columns at a time
+  static constexpr int kPad = kMergeCols + 4;
+  static constexpr int kMerge = kWarps * 8 * kNT * kPad * 4;
+  static constexpr int kSmem = kRing + kStages * 2 * kScaleBytes + kMerge + 1024;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrive on the barrier once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, bool kCodes, int kNT>
+__global__ void __launch_bounds__(kFewThreads, kFewCtas)
+tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                const __grid_constant__ Params p, const __grid_constant__ Work w) {
+  using C = FewCfg<D, kCodes, kNT>;
+  constexpr int kQ = D / 16;  // k-steps of the score product
+  constexpr int kMT = D / 16;  // 16-column tiles of the output
+  constexpr int kHH = D / 64;  // 16-byte chunks of a lane's codes
+  constexpr int kRows = 8 * kNT;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[C::kStages];
+  __shared__ int64_t scratch[kWarps];
+  __shared__ Walk place;
+  __shared__ uint32_t hidden[2][2];    // by the segment's parity
+  __shared__ int expired;              // a wait ran out
+  __shared__ int sm_bad[kWarps];
+  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+  float* merge = reinterpret_cast<float*>(ring_ptr + C::kRing + C::kStages * 2 * C::kScaleBytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto full = [&](int s) { return smem_u32(&bars[s]); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), kCodes ? 17 : 1);  // the copies' bytes, and 16 lanes' scales
+    }
+    fence_mbar_init();
+    hidden[0][0] = hidden[0][1] = hidden[1][0] = hidden[1][1] = 0;
+    expired = 0;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  Walk wk;
+  if (!find_place<kFewThreads>(p, w, scratch, &place, wk)) return;
+  volatile int* vexpired = &expired;
+
+  // ------------------------------------------------------- the warp's copies --
+  const int page = 1 << p.log_page;
+  const int box = min(page, kFewTile);  // rows of one copy
+  const int per = kFewTile / box;       // copies per tile (of each matrix)
+  const int batch = 32 / per;           // tiles whose page numbers one load fetches
+  Walk fw = wk;                         // runs ahead of wk
+  int f_tile, f_end, f_base = 0, f_at = 0, f_head, f_ids, f_next, f_stage = 0;
+  bool f_more = true;
+  uint32_t bad = 0;  // bit s: the tile in the warp's stage s reads a page outside the cache
+  auto fetch = [&](int tile) {  // this lane's copy of the warp's `batch` tiles from `tile` on
+    const int64_t pos = (tile + (int64_t)(lane / per) * kWarps) * kFewTile + lane % per * box;
+    return pos < fw.s.len ? p.table[(int64_t)fw.b * p.stride + (pos >> p.log_page)] : 0;
+  };
+  auto enter = [&]() {  // the first tile of the warp in fw's segment
+    f_tile = fw.tile + ((warp - f_base) & (kWarps - 1));
+    f_end = fw.tile + fw.piece();
+    f_head = fw.seg / (fw.segs / p.H);
+    f_at = 0;
+    if (f_tile < f_end) {
+      f_ids = fetch(f_tile);
+      f_next = fetch(f_tile + batch * kWarps);
+    }
+  };
+  auto feed = [&]() {  // copies of the warp's next tile into its stage f_stage
+    while (f_more && f_tile >= f_end) {
+      f_base += fw.piece();
+      f_more = fw.next(p, w);
+      if (f_more) enter();
+    }
+    if (!f_more || __any_sync(0xffffffffu, *vexpired)) return;
+    const int s = warp * C::kOwn + f_stage, key0 = f_tile * kFewTile, len = fw.s.len;
+    int id = __shfl_sync(0xffffffffu, f_ids, f_at * per + lane % per);
+    const bool wrong = (unsigned)id >= (unsigned)p.pages;
+    if (wrong) id = 0;
+    const int n = min(per, (len - key0 + box - 1) / box);
+    bad &= ~(1u << f_stage);
+    if (__any_sync(0xffffffffu, wrong)) {
+      bad |= 1u << f_stage;
+      if (lane == 0) atomicOr(p.err, rows::kBadIndex);
+    }
+    if (lane == 0) mbar_arrive_expect_tx(full(s), n * box * 2 * C::kRowBytes);
+    __syncwarp();
+    if (lane < n) {
+      const int row = (id << p.log_page) + ((key0 + lane * box) & (page - 1));
+      const uint32_t dst = ring + s * C::kStage + lane * box * C::kBox;
+      constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
+#pragma unroll
+      for (int f = 0; f < C::kHalves; ++f) {
+        tma_load_3d(dst + f * kFewTile * C::kBox, &map_k, full(s), f * kElems, f_head, row);
+        tma_load_3d(dst + C::kMatBytes + f * kFewTile * C::kBox, &map_v, full(s), f * kElems, f_head, row);
+      }
+    }
+    if (kCodes) {  // lanes 0-7: four key scales each, 8-15: value scales
+      const int key = (lane & 7) * 4;
+      const int sid = __shfl_sync(0xffffffffu, id, per == 1 ? 0 : key / 16);
+      if (lane < 16) {
+        if (key0 + key < len) {
+          const int64_t at = (((int64_t)sid * p.H + f_head) << p.log_page) + ((key0 + key) & (page - 1));
+          cp_async16(ring + C::kRing + (2 * s + lane / 8) * C::kScaleBytes + key * 4,
+                     (lane < 8 ? p.kscale : p.vscale) + at);
+        }
+        cp_async_arrive(full(s));
+      }
+    }
+    if (++f_stage == C::kOwn) f_stage = 0;
+    f_tile += kWarps;
+    if (++f_at == batch) {
+      f_at = 0;
+      f_ids = f_next;
+      f_next = fetch(f_tile + batch * kWarps);
+    }
+  };
+  enter();
+#pragma unroll 1
+  for (int i = 0; i < C::kOwn; ++i) feed();
+
+  // --------------------------------------------------------------- compute --
+    const int c = lane % 4, n = lane / 4;
+    int base = 0, stage = 0, parity = 0, seg_parity = 0;  // tiles before this piece; the warp's stage and its phase
+    bool first = true;
+    do {
+    const Seq sq = wk.s;
+    const int M = sq.n * p.G, ctx = sq.len - sq.n;
+    const int mtiles = wk.segs / p.H, h = wk.seg / mtiles, row0 = (wk.seg - h * mtiles) * kRows;
+    const int t_begin = wk.tile, t_end = wk.tile + wk.piece();
+    int poison = 0;
+    uint64_t word[kNT][2];  // masks and score factors (log2 units) of queries 2c, 2c + 1
+    float rc[kNT][2];
+    uint32_t qb[kNT][kQ][2];  // query n's channels
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int r = row0 + 8 * nt + n;
+      const bool live = r < M;
+      const int tok = live ? r / p.G : 0, g = live ? r % p.G : 0;
+      const __nv_bfloat16* q = p.q + (int64_t)(sq.q0 + tok) * p.q_ts + (int64_t)(h * p.G + g) * D;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ri = row0 + 8 * nt + 2 * c + i;
+        word[nt][i] = ri < M ? mask_word(p.mask, sq.q0 + ri / p.G, ri / p.G) : 0;
+        rc[nt][i] = p.c;
+      }
+      if (!kCodes) {
+#pragma unroll
+        for (int s = 0; s < kQ; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qb[nt][s][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8 * i) : 0u;
+      } else {
+        // lane c's channels of k-step s: the four that its 16 bytes of a key's
+        // codes (chunk kHH c + s / 4) hold at 4 (s % 4)
+        float amax = 0.f;
+#pragma unroll
+        for (int s = 0; s < kQ; ++s) {
+          const int ch = 16 * (kHH * c + s / 4) + 4 * (s % 4);
+          const uint2 raw = live ? *reinterpret_cast<const uint2*>(q + ch) : make_uint2(0, 0);
+          qb[nt][s][0] = raw.x, qb[nt][s][1] = raw.y;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qb[nt][s][k] << 16)),
+                                     fabsf(__uint_as_float(qb[nt][s][k] & 0xffff0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int e = (int)(__float_as_uint(amax) >> 23) - 127;
+        e = amax == 0.f ? 0 : min(max(e, -126), 126);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float up = p.c * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rc[nt][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * c + i));
+#pragma unroll
+        for (int s = 0; s < kQ; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            qb[nt][s][k] = pack_half(__uint_as_float(qb[nt][s][k] << 16) * down,
+                                     __uint_as_float(qb[nt][s][k] & 0xffff0000u) * down);
+      }
+    }
+    float o[kMT][kNT][4], m[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
+    }
+
+    for (int t = t_begin + ((warp - base) & (kWarps - 1)); t < t_end; t += kWarps) {
+      const int mine = warp * C::kOwn + stage;
+      if (!*vexpired && !mbar_wait(full(mine), parity, kWaitNs)) {
+        *vexpired = 1;
+        atomicOr(p.err, kTimedOut);
+      }
+      __syncwarp();
+      poison |= bad >> stage & 1;
+      const int key0 = t * kFewTile;
+      const uint32_t kt = ring + mine * C::kStage, vt = kt + C::kMatBytes;
+      const uint32_t ks = ring + C::kRing + mine * 2 * C::kScaleBytes, vs = ks + C::kScaleBytes;
+      const bool edge = key0 + kFewTile > ctx;
+      if (edge) {
+        clean_values<D, kCodes, kFewTile, 32>(ring_ptr + mine * C::kStage + C::kMatBytes, lane, key0, ctx, sq.len,
+                                              hidden[seg_parity]);
+        __syncwarp();
+      }
+      float sc[2][kNT][4];  // [16-key half][query tile]: keys n, n + 8 x queries 2c, 2c + 1
+#pragma unroll
+      for (int ksub = 0; ksub < 2; ++ksub) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) sc[ksub][nt][0] = sc[ksub][nt][1] = sc[ksub][nt][2] = sc[ksub][nt][3] = 0.f;
+        if (!kCodes) {
+#pragma unroll
+          for (int q2 = 0; q2 < kQ; ++q2) {
+            uint32_t ka[4];
+            const int ch = 2 * q2 + lane / 16;  // 16-byte chunk of the key row
+            ldsm4(ka, kt + (ch / 8) * (kFewTile * 128) + swz<128>(16 * ksub + lane % 16, ch % 8));
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mma<false>(sc[ksub][nt], ka, qb[nt][q2][0], qb[nt][q2][1]);
+          }
+        } else {
+#pragma unroll
+          for (int hh = 0; hh < kHH; ++hh) {
+            const uint4 w0 = lds128(kt + swz<C::kBox>(16 * ksub + n, kHH * c + hh));
+            const uint4 w1 = lds128(kt + swz<C::kBox>(16 * ksub + n + 8, kHH * c + hh));
+            const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t ka[4] = {codes_lo(x0[j]), codes_lo(x1[j]), codes_hi(x0[j]), codes_hi(x1[j])};
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+                mma<true>(sc[ksub][nt], ka, qb[nt][4 * hh + j][0], qb[nt][4 * hh + j][1]);
+            }
+          }
+        }
+      }
+      // log2 scores, masked; their maxima (with the value scale for codes)
+      float vsc[2][2];
+      float top[kNT][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+      for (int ksub = 0; ksub < 2; ++ksub)
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+          const int key = 16 * ksub + 8 * kh + n;
+          float ksc = 1.f, lg = 0.f;
+          if (kCodes) {
+            ksc = __uint_as_float(lds32(ks + key * 4));
+            vsc[ksub][kh] = __uint_as_float(lds32(vs + key * 4));
+            lg = lg2(fmaxf(vsc[ksub][kh], 0x1p-64f));
+          }
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = sc[ksub][nt][2 * kh + i] * rc[nt][i];
+              if (kCodes) x *= ksc;
+              if (edge) {
+                const int d = key0 + key - ctx;
+                if (d >= sq.n || (d >= 0 && !sees(word[nt][i], d))) x = -INFINITY;
+              }
+              sc[ksub][nt][2 * kh + i] = x;
+              // a masked score stays -inf whatever the scale of its key holds
+              top[nt][i] = fmaxf(top[nt][i], kCodes && x != -INFINITY ? x + lg : x);
+            }
+        }
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], off));
+          grow |= top[nt][i] > m[nt][i] + kLazy;  // also the first finite one: m is -inf
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[nt][i], top[nt][i]);
+            const float a = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - mn);
+            m[nt][i] = mn;
+            l[nt][i] *= a;
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+              o[mt][nt][i] *= a;
+              o[mt][nt][2 + i] *= a;
+            }
+          }
+      }
+#pragma unroll
+      for (int ksub = 0; ksub < 2; ++ksub) {
+        uint32_t pb[kNT][2];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = sc[ksub][nt][2 * kh + i];
+              const float pr = ex2(x - (m[nt][i] == -INFINITY ? 0.f : m[nt][i]));
+              l[nt][i] += pr;
+              w[i] = kCodes ? (x == -INFINITY ? 0.f : pr * vsc[ksub][kh]) : pr;
+            }
+            pb[nt][kh] = transposed(kCodes ? pack_half(w[0], w[1]) : rows::pack2(w[0], w[1]));
+          }
+        if (!kCodes) {
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) {
+            uint32_t va[4];
+            const int ch = 2 * mt + ((lane / 8) & 1);
+            ldsm4t(va, vt + (ch / 8) * (kFewTile * 128) + swz<128>(16 * ksub + lane % 8 + 8 * (lane / 16), ch % 8));
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mma<false>(o[mt][nt], va, pb[nt][0], pb[nt][1]);
+          }
+        } else {
+          // lane (n, c): columns 32 g + 4 n .. + 3 of keys 2c, 2c+1, 2c+8, 2c+9; the
+          // first two are rows n, n + 8 of output tile 2 g, the others of 2 g + 1
+#pragma unroll
+          for (int g = 0; g < D / 32; ++g) {
+            const int ch = 2 * g + n / 4, in = 4 * (n % 4), key = 16 * ksub + 2 * c;
+            const uint32_t w0 = lds32(vt + swz<C::kBox>(key, ch) + in);
+            const uint32_t w1 = lds32(vt + swz<C::kBox>(key + 1, ch) + in);
+            const uint32_t w2 = lds32(vt + swz<C::kBox>(key + 8, ch) + in);
+            const uint32_t w3 = lds32(vt + swz<C::kBox>(key + 9, ch) + in);
+            const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
+            const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+            const uint32_t va[4] = {codes_lo(a01), codes_hi(a01), codes_lo(a23), codes_hi(a23)};
+            const uint32_t vb[4] = {codes_lo(b01), codes_hi(b01), codes_lo(b23), codes_hi(b23)};
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              mma<true>(o[2 * g][nt], va, pb[nt][0], pb[nt][1]);
+              mma<true>(o[2 * g + 1][nt], vb, pb[nt][0], pb[nt][1]);
+            }
+          }
+        }
+      }
+      if (edge) fence_async_smem();  // this thread wrote to the stage; a copy follows
+      __syncwarp();
+      feed();
+      if (++stage == C::kOwn) stage = 0, parity ^= 1;
+    }
+    base += t_end - t_begin;
+
+    // ---------------------------------------------------- merge the warps --
+    compute_sync();  // the last piece's sums have been read
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
+        if (l[nt][i] != l[nt][i] && m[nt][i] == -INFINITY) m[nt][i] = 0.f;  // NaN scores alone: not an empty row
+        if (n == 0) {
+          sm_m[warp][8 * nt + 2 * c + i] = m[nt][i];
+          sm_l[warp][8 * nt + 2 * c + i] = l[nt][i];
+        }
+      }
+    if (lane == 0) sm_bad[warp] = poison;
+    if (threadIdx.x == 0) hidden[seg_parity ^ 1][0] = hidden[seg_parity ^ 1][1] = 0;
+    float* buf = merge + warp * kRows * C::kPad;
+    const bool whole = t_begin == 0 && t_end == wk.tiles;
+    const int slot = whole ? -1 : 2 * (int)blockIdx.x + !first;
+#pragma unroll
+    for (int g = 0; g < D / C::kMergeCols; ++g) {
+      if (g > 0) compute_sync();  // the columns before have been read
+#pragma unroll
+      for (int mt = 2 * g; mt < 2 * g + 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int col = kCodes ? 4 * n + 2 * (mt & 1) + (i >> 1) : 16 * (mt & 1) + n + 8 * (i >> 1);
+            buf[(8 * nt + 2 * c + (i & 1)) * C::kPad + col] = o[mt][nt][i];
+          }
+      compute_sync();
+      write_piece<D, kCodes, kRows, kWarps, C::kMergeCols>(
+          p, sq, wk.b, h, row0, slot, merge, C::kPad, C::kMergeCols * g, &sm_m[0][0], &sm_l[0][0],
+          (uint64_t)hidden[seg_parity][1] << 32 | hidden[seg_parity][0],
+          *vexpired || sm_bad[0] || sm_bad[1] || sm_bad[2] || sm_bad[3], threadIdx.x);
+    }
+    first = false;
+    seg_parity ^= 1;
+    } while (wk.next(p, w));
+  if (kCodes) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (__any_sync(0xffffffffu, *vexpired)) {  // let copies in flight land before the CTA leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace tree
+}  // namespace attn

@@ -653,400 +653,6 @@ tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
   __syncthreads();
 }
 
-// ------------------------------------------------------------ few rows --
-// Up to 8 kNT rows (one token, or a few drafts, of a key head's group): keys
-// take the 16-row side of the products and queries the 8-column side,
-//   S^T = K Q^T,   O^T += V^T P^T,
-// so a fragment holds 8 queries, not 16, and every warp takes whole tiles of
-// its own (tile t goes to warp t mod 4): no key or value is read or converted
-// twice, and the warps meet only at the end.  P^T is the score fragment
-// transposed in registers (movmatrix).  At d = 128 with 8 queries a lane holds
-// 32 output and 16 query registers, so three CTAs share an SM.
-constexpr int kFewTile = 32;  // keys per stage
-
-template <int D, bool kCodes>
-struct FewCfg : Row<D, kCodes> {
-  using Row<D, kCodes>::kRowBytes;
-  static constexpr int kMatBytes = kFewTile * kRowBytes;
-  static constexpr int kScaleBytes = kCodes ? kFewTile * 4 : 0;
-  static constexpr int kStage = 2 * kMatBytes;
-  static constexpr int kStages = 64 * 1024 / kStage < 12 ? 64 * 1024 / kStage : 12;
-  static constexpr int kRing = kStages * kStage;
-  static constexpr int kSmem = kRing + kStages * 2 * kScaleBytes + 1024;
-};
-
-__device__ __forceinline__ uint32_t transposed(uint32_t x) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
-template <int D, bool kCodes, int kNT>
-__global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2)
-tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                const __grid_constant__ Params p) {
-  using C = FewCfg<D, kCodes>;
-  constexpr int kQ = D / 16;  // k-steps of the score product
-  constexpr int kMT = D / 16;  // 16-column tiles of the output
-  constexpr int kHH = D / 64;  // 16-byte chunks of a lane's codes
-  constexpr int kRows = 8 * kNT;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages];
-  __shared__ uint32_t hidden[2];
-  __shared__ int flags[2];  // [0] a wait expired, [1] a page outside the cache
-  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  auto full = [&](int s) { return smem_u32(&bars[s]); };
-  auto empty = [&](int s) { return smem_u32(&bars[C::kStages + s]); };
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);  // the one warp that takes the tile
-    }
-    fence_mbar_init();
-    hidden[0] = hidden[1] = 0;
-    flags[0] = flags[1] = 0;
-  }
-  __syncthreads();
-  grid_dep_wait();
-  grid_dep_launch();
-
-  int item = blockIdx.x;
-  const int h = item % p.H;
-  item /= p.H;
-  const int split = item % p.S;
-  const int b = item / p.S;
-  const int k_lo = split * p.chunk;
-  // the producer's first page numbers, on their way beside the lengths
-  const int page = 1 << p.log_page;
-  const int box = min(page, kFewTile);  // rows of one copy
-  const int per = kFewTile / box;       // copies per tile (of each matrix)
-  const int batch = 32 / per;           // tiles whose page numbers one load fetches
-  const int* table = p.table + (int64_t)b * p.stride;
-  auto fetch = [&](int tile) {  // this lane's copy of the batch that starts at `tile`
-    const int64_t at = (k_lo + (int64_t)tile * kFewTile + lane * box) >> p.log_page;
-    return at < p.stride ? table[at] : 0;
-  };
-  int ids = warp == kWarps ? fetch(0) : 0;
-  Seq sq;
-  if (!load_seq(p, b, sq)) {
-    if (threadIdx.x == 0) atomicOr(p.err, rows::kBadSeqlens);
-    return;
-  }
-  const int M = sq.n * p.G;
-  if (M == 0 || k_lo >= sq.len) return;
-  const int k_hi = min(sq.len, k_lo + p.chunk);
-  const int ctx = sq.len - sq.n;
-  const int tiles = (k_hi - k_lo + kFewTile - 1) / kFewTile;
-  volatile int* vflags = flags;
-
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer --
-    for (int t0 = 0; t0 < tiles; t0 += batch) {
-      const int next = t0 + batch < tiles ? fetch(t0 + batch) : 0;
-      if ((unsigned)ids >= (unsigned)p.pages) {
-        if (k_lo + (int64_t)t0 * kFewTile + lane * box < k_hi) {  // a page that is read
-          flags[1] = 1;
-          atomicOr(p.err, rows::kBadIndex);
-        }
-        ids = 0;
-      }
-      for (int t = t0; t < min(t0 + batch, tiles); ++t) {
-        const int s = t % C::kStages;
-        if (t >= C::kStages && !vflags[0] &&
-            !mbar_wait(empty(s), ((t / C::kStages) & 1) ^ 1, kWaitNs)) {
-          vflags[0] = 1;
-          atomicOr(p.err, kTimedOut);
-        }
-        __syncwarp();
-        const int id = __shfl_sync(0xffffffffu, ids, (t - t0) * per + lane % per);
-        if (__any_sync(0xffffffffu, vflags[0])) continue;  // nothing more is copied
-        const int key0 = k_lo + t * kFewTile;
-        const int n = min(per, (k_hi - key0 + box - 1) / box);
-        if (lane == 0) mbar_arrive_expect_tx(full(s), n * box * 2 * (C::kRowBytes + (kCodes ? 4 : 0)));
-        __syncwarp();
-        if (lane < n) {
-          const int in = (key0 + lane * box) & (page - 1);
-          const int row = (id << p.log_page) + in;
-          const uint32_t dst = ring + s * C::kStage + lane * box * C::kBox;
-          constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
-#pragma unroll
-          for (int f = 0; f < C::kHalves; ++f) {
-            tma_load_3d(dst + f * kFewTile * C::kBox, &map_k, full(s), f * kElems, h, row);
-            tma_load_3d(dst + C::kMatBytes + f * kFewTile * C::kBox, &map_v, full(s), f * kElems, h, row);
-          }
-          if (kCodes) {
-            const int64_t at = (((int64_t)id * p.H + h) << p.log_page) + in;
-            const uint32_t sd = ring + C::kRing + s * 2 * C::kScaleBytes + lane * box * 4;
-            bulk_load(sd, p.kscale + at, box * 4, full(s));
-            bulk_load(sd + C::kScaleBytes, p.vscale + at, box * 4, full(s));
-          }
-        }
-      }
-      ids = next;
-    }
-    __syncwarp();
-    if (vflags[0]) {  // let copies in flight land before the CTA leaves
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000ull) {
-      }
-    }
-  } else {
-    // ------------------------------------------------------------- compute --
-    const int c = lane % 4, n = lane / 4;
-    uint64_t word[kNT][2];  // masks and score factors (log2 units) of queries 2c, 2c + 1
-    float rc[kNT][2];
-    uint32_t qb[kNT][kQ][2];  // query n's channels
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const int r = 8 * nt + n;
-      const bool live = r < M;
-      const int tok = live ? r / p.G : 0, g = live ? r % p.G : 0;
-      const __nv_bfloat16* q = p.q + (int64_t)(sq.q0 + tok) * p.q_ts + (int64_t)(h * p.G + g) * D;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int ri = 8 * nt + 2 * c + i;
-        word[nt][i] = ri < M ? mask_word(p.mask, sq.q0 + ri / p.G, ri / p.G) : 0;
-        rc[nt][i] = p.c;
-      }
-      if (!kCodes) {
-#pragma unroll
-        for (int s = 0; s < kQ; ++s)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qb[nt][s][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8 * i) : 0u;
-      } else {
-        // lane c's channels of k-step s: the four that its 16 bytes of a key's
-        // codes (chunk kHH c + s / 4) hold at 4 (s % 4)
-        float amax = 0.f;
-#pragma unroll
-        for (int s = 0; s < kQ; ++s) {
-          const int ch = 16 * (kHH * c + s / 4) + 4 * (s % 4);
-          const uint2 raw = live ? *reinterpret_cast<const uint2*>(q + ch) : make_uint2(0, 0);
-          qb[nt][s][0] = raw.x, qb[nt][s][1] = raw.y;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qb[nt][s][k] << 16)),
-                                     fabsf(__uint_as_float(qb[nt][s][k] & 0xffff0000u))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int e = (int)(__float_as_uint(amax) >> 23) - 127;
-        e = amax == 0.f ? 0 : min(max(e, -126), 126);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float up = p.c * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) rc[nt][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * c + i));
-#pragma unroll
-        for (int s = 0; s < kQ; ++s)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            qb[nt][s][k] = pack_half(__uint_as_float(qb[nt][s][k] << 16) * down,
-                                     __uint_as_float(qb[nt][s][k] & 0xffff0000u) * down);
-      }
-    }
-    float o[kMT][kNT][4], m[kNT][2], l[kNT][2];
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
-    }
-
-    for (int t = warp; t < tiles; t += kWarps) {
-      const int s = t % C::kStages;
-      if (!vflags[0] && !mbar_wait(full(s), (t / C::kStages) & 1, kWaitNs)) {
-        vflags[0] = 1;
-        atomicOr(p.err, kTimedOut);
-      }
-      __syncwarp();
-      const int key0 = k_lo + t * kFewTile;
-      const uint32_t kt = ring + s * C::kStage, vt = kt + C::kMatBytes;
-      const uint32_t ks = ring + C::kRing + s * 2 * C::kScaleBytes, vs = ks + C::kScaleBytes;
-      const bool edge = key0 + kFewTile > ctx;
-      if (edge) {
-        clean_values<D, kCodes, kFewTile, 32>(ring_ptr + s * C::kStage + C::kMatBytes, lane, key0, ctx, sq.len,
-                                              hidden);
-        __syncwarp();
-      }
-      float sc[2][kNT][4];  // [16-key half][query tile]: keys n, n + 8 x queries 2c, 2c + 1
-#pragma unroll
-      for (int ksub = 0; ksub < 2; ++ksub) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) sc[ksub][nt][0] = sc[ksub][nt][1] = sc[ksub][nt][2] = sc[ksub][nt][3] = 0.f;
-        if (!kCodes) {
-#pragma unroll
-          for (int q2 = 0; q2 < kQ; ++q2) {
-            uint32_t ka[4];
-            const int ch = 2 * q2 + lane / 16;  // 16-byte chunk of the key row
-            ldsm4(ka, kt + (ch / 8) * (kFewTile * 128) + swz<128>(16 * ksub + lane % 16, ch % 8));
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma<false>(sc[ksub][nt], ka, qb[nt][q2][0], qb[nt][q2][1]);
-          }
-        } else {
-#pragma unroll
-          for (int hh = 0; hh < kHH; ++hh) {
-            const uint4 w0 = lds128(kt + swz<C::kBox>(16 * ksub + n, kHH * c + hh));
-            const uint4 w1 = lds128(kt + swz<C::kBox>(16 * ksub + n + 8, kHH * c + hh));
-            const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t ka[4] = {codes_lo(x0[j]), codes_lo(x1[j]), codes_hi(x0[j]), codes_hi(x1[j])};
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
-                mma<true>(sc[ksub][nt], ka, qb[nt][4 * hh + j][0], qb[nt][4 * hh + j][1]);
-            }
-          }
-        }
-      }
-      // log2 scores, masked; their maxima (with the value scale for codes)
-      float vsc[2][2];
-      float top[kNT][2];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-#pragma unroll
-      for (int ksub = 0; ksub < 2; ++ksub)
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-          const int key = 16 * ksub + 8 * kh + n;
-          float ksc = 1.f, lg = 0.f;
-          if (kCodes) {
-            ksc = __uint_as_float(lds32(ks + key * 4));
-            vsc[ksub][kh] = __uint_as_float(lds32(vs + key * 4));
-            lg = lg2(fmaxf(vsc[ksub][kh], 0x1p-64f));
-          }
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x = sc[ksub][nt][2 * kh + i] * rc[nt][i];
-              if (kCodes) x *= ksc;
-              if (edge) {
-                const int d = key0 + key - ctx;
-                if (d >= sq.n || (d >= 0 && !sees(word[nt][i], d))) x = -INFINITY;
-              }
-              sc[ksub][nt][2 * kh + i] = x;
-              // a masked score stays -inf whatever the scale of its key holds
-              top[nt][i] = fmaxf(top[nt][i], kCodes && x != -INFINITY ? x + lg : x);
-            }
-        }
-      bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1)
-            top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], off));
-          grow |= top[nt][i] > m[nt][i] + kLazy;  // also the first finite one: m is -inf
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[nt][i], top[nt][i]);
-            const float a = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - mn);
-            m[nt][i] = mn;
-            l[nt][i] *= a;
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-              o[mt][nt][i] *= a;
-              o[mt][nt][2 + i] *= a;
-            }
-          }
-      }
-#pragma unroll
-      for (int ksub = 0; ksub < 2; ++ksub) {
-        uint32_t pb[kNT][2];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            float w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float x = sc[ksub][nt][2 * kh + i];
-              const float pr = ex2(x - (m[nt][i] == -INFINITY ? 0.f : m[nt][i]));
-              l[nt][i] += pr;
-              w[i] = kCodes ? (x == -INFINITY ? 0.f : pr * vsc[ksub][kh]) : pr;
-            }
-            pb[nt][kh] = transposed(kCodes ? pack_half(w[0], w[1]) : rows::pack2(w[0], w[1]));
-          }
-        if (!kCodes) {
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            uint32_t va[4];
-            const int ch = 2 * mt + ((lane / 8) & 1);
-            ldsm4t(va, vt + (ch / 8) * (kFewTile * 128) + swz<128>(16 * ksub + lane % 8 + 8 * (lane / 16), ch % 8));
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma<false>(o[mt][nt], va, pb[nt][0], pb[nt][1]);
-          }
-        } else {
-          // lane (n, c): columns 32 g + 4 n .. + 3 of keys 2c, 2c+1, 2c+8, 2c+9; the
-          // first two are rows n, n + 8 of output tile 2 g, the others of 2 g + 1
-#pragma unroll
-          for (int g = 0; g < D / 32; ++g) {
-            const int ch = 2 * g + n / 4, in = 4 * (n % 4), key = 16 * ksub + 2 * c;
-            const uint32_t w0 = lds32(vt + swz<C::kBox>(key, ch) + in);
-            const uint32_t w1 = lds32(vt + swz<C::kBox>(key + 1, ch) + in);
-            const uint32_t w2 = lds32(vt + swz<C::kBox>(key + 8, ch) + in);
-            const uint32_t w3 = lds32(vt + swz<C::kBox>(key + 9, ch) + in);
-            const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
-            const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
-            const uint32_t va[4] = {codes_lo(a01), codes_hi(a01), codes_lo(a23), codes_hi(a23)};
-            const uint32_t vb[4] = {codes_lo(b01), codes_hi(b01), codes_lo(b23), codes_hi(b23)};
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              mma<true>(o[2 * g][nt], va, pb[nt][0], pb[nt][1]);
-              mma<true>(o[2 * g + 1][nt], vb, pb[nt][0], pb[nt][1]);
-            }
-          }
-        }
-      }
-      if (edge) fence_async_smem();  // this thread wrote to the stage; a copy may follow
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-    }
-
-    // ---------------------------------------------------- merge the warps --
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
-        if (l[nt][i] != l[nt][i] && m[nt][i] == -INFINITY) m[nt][i] = 0.f;  // NaN scores alone: not an empty row
-        if (n == 0) {
-          sm_m[warp][8 * nt + 2 * c + i] = m[nt][i];
-          sm_l[warp][8 * nt + 2 * c + i] = l[nt][i];
-        }
-      }
-    compute_sync();  // every warp is through with the ring
-    constexpr int kPad = D + 4;
-    float* buf = reinterpret_cast<float*>(ring_ptr) + warp * kRows * kPad;
-#pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = kCodes ? 32 * (mt / 2) + 4 * n + 2 * (mt & 1) + (i >> 1) : 16 * mt + n + 8 * (i >> 1);
-          buf[(8 * nt + 2 * c + (i & 1)) * kPad + col] = o[mt][nt][i];
-        }
-    compute_sync();
-    write_rows<D, kCodes, kRows, kWarps>(p, sq, b, h, split, ctx, 0, M, reinterpret_cast<const float*>(ring_ptr), kPad,
-                                         &sm_m[0][0], &sm_l[0][0], (uint64_t)hidden[1] << 32 | hidden[0],
-                                         vflags[0] || vflags[1], threadIdx.x);
-  }
-  __syncthreads();
-}
-
 // Ranges of a row joined: weights e^(LSE_s - max), as for split keys elsewhere
 // in the library.  One warp per (new token, query head); lanes first take the
 // ranges' LSE, then d / 32 columns each.  Rows of a sequence with one range (or

@@ -156,10 +156,12 @@ def test_null_cache_and_empty_calls(lib):
 
 
 def test_tree_workspace_size():
-    # one range: none; 8 ranges: fp32 output and LSE of each
-    assert fa.attn_fwd_tree_workspace(2, 10, 8, 4, 128, 8, 4096, 1) == 0
-    assert fa.attn_fwd_tree_workspace(2, 10, 8, 4, 128, 8, 4096, 8) == 8 * 10 * 8 * 129 * 4
-    assert fa.attn_fwd_tree_workspace(2, 10, 7, 4, 128, 8, 4096, 8) == 0  # refused by the call itself
+    """Bounded by the launch, not by the lengths; nothing for a call that is refused or has no work."""
+    size = lambda *a: fa.attn_fwd_tree_workspace(*a)
+    assert 0 < size(2, 10, 8, 4, 128, 8, 4096, 8) <= 64 << 20
+    assert size(64, 64, 32, 8, 128, 1, 1 << 20, 0) == size(64, 64, 32, 8, 128, 1, 1 << 24, 0) <= 64 << 20
+    assert size(2, 10, 7, 4, 128, 8, 4096, 8) == 0  # refused by the call itself
+    assert size(0, 10, 8, 4, 128, 8, 4096, 0) == size(2, 10, 8, 4, 128, 0, 4096, 0) == 0
 
 
 def test_convenience_refusals():
