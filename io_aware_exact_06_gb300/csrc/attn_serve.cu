@@ -175,15 +175,17 @@ struct Plan {
   int rows;               // query rows of a CTA: 8 or 16 (few rows), 32 or 64
   int mtiles, chunk, S;   // 32 or 64: key ranges
   attn::tree::Work work;  // 8 or 16: the line of tiles
-  int64_t slots;          // parts in the workspace, `rows` rows each
+  int64_t ctas;
+  int64_t slots;  // parts in the workspace, `rows` rows each
+  bool many;      // eight warps join a row's pieces
 };
 
 bool few(const Plan& pl) { return pl.rows <= 16; }
 
 // Query rows of a CTA: the smallest tile that holds max_new * G of them.  Few
-// rows: as many persistent CTAs as fit the SMs (num_splits caps the pieces of a
+// rows: as many persistent warps as fit the SMs (num_splits caps the pieces of a
 // segment instead), at least four tiles (128 keys) each, below which starting a
-// CTA and merging its part cost more than its reading.  More rows: key ranges.
+// warp and joining its part cost more than its reading.  More rows: key ranges.
 Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
@@ -193,12 +195,18 @@ Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
   const int64_t segments = (int64_t)B * H * pl.mtiles;
   if (few(pl)) {
     const int64_t T = attn::tree::kFewTile, tiles = (len + T - 1) / T;
+    const int heads = H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // to a unit, one a warp
+    const int64_t groups = segments / heads;
     pl.work.rows = pl.rows;
+    pl.work.heads = heads;
     pl.work.log_tile = attn::tree::kLogFewTile;
     pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 4;
-    const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
-    pl.work.ctas = (int)std::min<int64_t>(most, kPlanSms * attn::tree::kFewCtas);
-    pl.slots = 2 * (int64_t)pl.work.ctas;
+    const int64_t per_cta = attn::tree::kWarps / heads;
+    const int64_t most = (int64_t)std::min((double)groups * (double)tiles / pl.work.min_share + 1, 1e9);
+    pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * attn::tree::kFewCtas);
+    pl.work.units = (int)(pl.ctas * per_cta);
+    pl.slots = 2 * (int64_t)pl.work.units * heads;
+    pl.many = pl.work.units > 32 * groups;  // pieces of a segment
     return pl;
   }
   const int64_t T = attn::tree::kTile;
@@ -253,8 +261,9 @@ int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
     auto kernel = pl.rows == 8 ? tree_few_kernel<D, kCodes, 1> : tree_few_kernel<D, kCodes, 2>;
     const int smem = pl.rows == 8 ? FewCfg<D, kCodes, 1>::kSmem : FewCfg<D, kCodes, 2>::kSmem;
     if ((st = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != ATTN_OK) return st;
-    if ((st = launch(kernel, pl.work.ctas, kFewThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK) return st;
-    return launch(tree_join_kernel<D>, join, 256, 0, s, p, pl.work);
+    if ((st = launch(kernel, pl.ctas, kFewThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK) return st;
+    return pl.many ? launch(tree_join_kernel<D, 8>, (int64_t)p.total * p.Hq, 256, 0, s, p, pl.work)
+                   : launch(tree_join_kernel<D, 1>, join, 256, 0, s, p, pl.work);
   }
   auto kernel = pl.rows == 32 ? tree_kernel<D, kCodes, 2> : tree_kernel<D, kCodes, 4>;
   constexpr int kSmem = Cfg<D, kCodes>::kSmem;
@@ -475,7 +484,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_SCRATCH;
   const double ctas = (double)B * std::max(pl.S, 1) * cache->H * pl.mtiles;
   const int64_t combine = ((int64_t)total * Hq + 7) / 8;
-  if (ctas > INT32_MAX || combine > INT32_MAX) return ATTN_ERR_SHAPE;
+  if (ctas > INT32_MAX || (int64_t)total * Hq > INT32_MAX) return ATTN_ERR_SHAPE;
   const int64_t grid = (int64_t)B * pl.S * cache->H * pl.mtiles;
   const bool codes = cache->k_scale != nullptr;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;

@@ -11,17 +11,21 @@ namespace tree {
 // Up to 8 kNT rows (one token, or a few drafts, of a key head's group): keys
 // take the 16-row side of the products and queries the 8-column side,
 //   S^T = K Q^T,   O^T += V^T P^T,
-// so a fragment holds 8 queries, not 16, and every warp takes whole tiles of
-// its own (tile i of the CTA's share goes to warp i mod 4): no key or value is
-// read or converted twice, and the warps meet only at the end of a piece.  P^T
-// is the score fragment transposed in registers (movmatrix).
+// so a fragment holds 8 queries, not 16, and a warp takes whole tiles of one
+// head: no key or value is read or converted twice.  P^T is the score fragment
+// transposed in registers (movmatrix).
 //
-// Persistent CTAs, three an SM.  Each warp owns its stages of the ring: when it
-// is done with a tile it issues the copies of a later one into the same stage
-// itself, across the ends of segments.  (A producer warp for the CTA spent about
-// 1000 cycles a 32-key tile on issue, against 365 that HBM needs for e4m3 tiles
-// of three CTAs; four warps share that work and need no barrier to hand a stage
-// back.)
+// Every warp works alone: it finds its place in the line, copies its tiles by
+// TMA into stages of its own (the copies of a later tile go out as soon as a
+// stage is free, across the ends of segments), keeps its softmax and writes its
+// pieces; the CTA, three an SM, is only where four warps live.  A segment is a
+// group of `heads` neighbouring heads, one to a warp, which so read neighbouring
+// lines of the cache's token rows at about the same time: with 128-byte head
+// rows (e4m3, d = 128) four warps on four heads read 512 contiguous bytes.
+// (One head to a CTA, its tiles dealt to the warps: 4.4 TB/s on 64 ragged
+// sequences of 8 heads against 5.4 TB/s on the same bytes with one head.  A
+// producer warp for the CTA instead spent about 1000 cycles on a 32-key tile's
+// issue, against 365 that HBM needs for the tiles of three CTAs.)
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
@@ -36,10 +40,10 @@ struct FewCfg : Row<D, kCodes> {
   static constexpr int kOwn = 16384 / kStage < 3 ? 16384 / kStage : 3;  // stages of a warp
   static constexpr int kStages = kOwn * kWarps;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kMergeCols = 32;  // the warps' sums meet 32 columns at a time
-  static constexpr int kPad = kMergeCols + 4;
-  static constexpr int kMerge = kWarps * 8 * kNT * kPad * 4;
-  static constexpr int kSmem = kRing + kStages * 2 * kScaleBytes + kMerge + 1024;
+  static constexpr int kTurn = 32;  // columns of the output turned to rows at a time
+  static constexpr int kPad = kTurn + 4;
+  static constexpr int kTurnBytes = kWarps * 8 * kNT * kPad * 4;
+  static constexpr int kSmem = kRing + kStages * 2 * kScaleBytes + kTurnBytes + 1024;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -67,30 +71,29 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   constexpr int kRows = 8 * kNT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[C::kStages];
-  __shared__ int64_t scratch[kWarps];
-  __shared__ Walk place;
-  __shared__ uint32_t hidden[2][2];    // by the segment's parity
-  __shared__ int expired;              // a wait ran out
-  __shared__ int sm_bad[kWarps];
+  __shared__ uint32_t hidden_all[kWarps][2];
   __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-  float* merge = reinterpret_cast<float*>(ring_ptr + C::kRing + C::kStages * 2 * C::kScaleBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float* turn = reinterpret_cast<float*>(ring_ptr + C::kRing + C::kStages * 2 * C::kScaleBytes) +
+                warp * kRows * C::kPad;
+  uint32_t* hidden = hidden_all[warp];
   auto full = [&](int s) { return smem_u32(&bars[s]); };
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), kCodes ? 17 : 1);  // the copies' bytes, and 16 lanes' scales
-    }
+  if (lane == 0) {
+    for (int s = 0; s < C::kOwn; ++s)
+      mbar_init(full(warp * C::kOwn + s), kCodes ? 17 : 1);  // the copies' bytes, and 16 lanes' scales
     fence_mbar_init();
-    hidden[0][0] = hidden[0][1] = hidden[1][0] = hidden[1][1] = 0;
-    expired = 0;
+    hidden[0] = hidden[1] = 0;
   }
+  __syncwarp();
   grid_dep_wait();
   grid_dep_launch();
+  const int units = kWarps / w.heads;  // of the CTA
+  const int unit = blockIdx.x * units + warp / w.heads, sub = warp % w.heads;
   Walk wk;
-  if (!find_place<kFewThreads>(p, w, scratch, &place, wk)) return;
-  volatile int* vexpired = &expired;
+  if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) return;
+  bool expired = false;  // a wait ran out: nothing more is copied, the rows come out as NaN
 
   // ------------------------------------------------------- the warp's copies --
   const int page = 1 << p.log_page;
@@ -98,30 +101,27 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   const int per = kFewTile / box;       // copies per tile (of each matrix)
   const int batch = 32 / per;           // tiles whose page numbers one load fetches
   Walk fw = wk;                         // runs ahead of wk
-  int f_tile, f_end, f_base = 0, f_at = 0, f_head, f_ids, f_next, f_stage = 0;
+  int f_tile, f_end, f_at = 0, f_head, f_ids, f_next, f_stage = 0;
   bool f_more = true;
-  uint32_t bad = 0;  // bit s: the tile in the warp's stage s reads a page outside the cache
-  auto fetch = [&](int tile) {  // this lane's copy of the warp's `batch` tiles from `tile` on
-    const int64_t pos = (tile + (int64_t)(lane / per) * kWarps) * kFewTile + lane % per * box;
+  uint32_t bad = 0;  // bit s: the tile in stage s reads a page outside the cache
+  auto fetch = [&](int tile) {  // this lane's copy of the `batch` tiles from `tile` on
+    const int64_t pos = (int64_t)tile * kFewTile + lane * box;
     return pos < fw.s.len ? p.table[(int64_t)fw.b * p.stride + (pos >> p.log_page)] : 0;
   };
-  auto enter = [&]() {  // the first tile of the warp in fw's segment
-    f_tile = fw.tile + ((warp - f_base) & (kWarps - 1));
+  auto enter = [&]() {
+    f_tile = fw.tile;
     f_end = fw.tile + fw.piece();
-    f_head = fw.seg / (fw.segs / p.H);
+    f_head = fw.seg / (fw.segs / (p.H / w.heads)) * w.heads + sub;
     f_at = 0;
-    if (f_tile < f_end) {
-      f_ids = fetch(f_tile);
-      f_next = fetch(f_tile + batch * kWarps);
-    }
+    f_ids = fetch(f_tile);
+    f_next = fetch(f_tile + batch);
   };
   auto feed = [&]() {  // copies of the warp's next tile into its stage f_stage
-    while (f_more && f_tile >= f_end) {
-      f_base += fw.piece();
+    if (f_more && f_tile >= f_end) {
       f_more = fw.next(p, w);
       if (f_more) enter();
     }
-    if (!f_more || __any_sync(0xffffffffu, *vexpired)) return;
+    if (!f_more || expired) return;
     const int s = warp * C::kOwn + f_stage, key0 = f_tile * kFewTile, len = fw.s.len;
     int id = __shfl_sync(0xffffffffu, f_ids, f_at * per + lane % per);
     const bool wrong = (unsigned)id >= (unsigned)p.pages;
@@ -157,11 +157,11 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       }
     }
     if (++f_stage == C::kOwn) f_stage = 0;
-    f_tile += kWarps;
+    ++f_tile;
     if (++f_at == batch) {
       f_at = 0;
       f_ids = f_next;
-      f_next = fetch(f_tile + batch * kWarps);
+      f_next = fetch(f_tile + batch);
     }
   };
   enter();
@@ -169,15 +169,16 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   for (int i = 0; i < C::kOwn; ++i) feed();
 
   // --------------------------------------------------------------- compute --
-    const int c = lane % 4, n = lane / 4;
-    int base = 0, stage = 0, parity = 0, seg_parity = 0;  // tiles before this piece; the warp's stage and its phase
-    bool first = true;
-    do {
+  const int c = lane % 4, n = lane / 4;
+  int stage = 0, parity = 0;
+  bool first = true;
+  do {
     const Seq sq = wk.s;
     const int M = sq.n * p.G, ctx = sq.len - sq.n;
-    const int mtiles = wk.segs / p.H, h = wk.seg / mtiles, row0 = (wk.seg - h * mtiles) * kRows;
+    const int mtiles = wk.segs / (p.H / w.heads), group = wk.seg / mtiles;
+    const int h = group * w.heads + sub, row0 = (wk.seg - group * mtiles) * kRows;
     const int t_begin = wk.tile, t_end = wk.tile + wk.piece();
-    int poison = 0;
+    bool poison = false;
     uint64_t word[kNT][2];  // masks and score factors (log2 units) of queries 2c, 2c + 1
     float rc[kNT][2];
     uint32_t qb[kNT][kQ][2];  // query n's channels
@@ -240,13 +241,12 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
     }
 
-    for (int t = t_begin + ((warp - base) & (kWarps - 1)); t < t_end; t += kWarps) {
+    for (int t = t_begin; t < t_end; ++t) {
       const int mine = warp * C::kOwn + stage;
-      if (!*vexpired && !mbar_wait(full(mine), parity, kWaitNs)) {
-        *vexpired = 1;
-        atomicOr(p.err, kTimedOut);
+      if (!expired) {
+        expired = __any_sync(0xffffffffu, !mbar_wait(full(mine), parity, kWaitNs));
+        if (expired && lane == 0) atomicOr(p.err, kTimedOut);
       }
-      __syncwarp();
       poison |= bad >> stage & 1;
       const int key0 = t * kFewTile;
       const uint32_t kt = ring + mine * C::kStage, vt = kt + C::kMatBytes;
@@ -254,7 +254,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       const bool edge = key0 + kFewTile > ctx;
       if (edge) {
         clean_values<D, kCodes, kFewTile, 32>(ring_ptr + mine * C::kStage + C::kMatBytes, lane, key0, ctx, sq.len,
-                                              hidden[seg_parity]);
+                                              hidden);
         __syncwarp();
       }
       float sc[2][kNT][4];  // [16-key half][query tile]: keys n, n + 8 x queries 2c, 2c + 1
@@ -397,30 +397,24 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       feed();
       if (++stage == C::kOwn) stage = 0, parity ^= 1;
     }
-    base += t_end - t_begin;
 
-    // ---------------------------------------------------- merge the warps --
-    compute_sync();  // the last piece's sums have been read
+    // ------------------------------------------------------ the piece's end --
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
-        if (l[nt][i] != l[nt][i] && m[nt][i] == -INFINITY) m[nt][i] = 0.f;  // NaN scores alone: not an empty row
+        close_row(m[nt][i], l[nt][i]);
         if (n == 0) {
           sm_m[warp][8 * nt + 2 * c + i] = m[nt][i];
           sm_l[warp][8 * nt + 2 * c + i] = l[nt][i];
         }
       }
-    if (lane == 0) sm_bad[warp] = poison;
-    if (threadIdx.x == 0) hidden[seg_parity ^ 1][0] = hidden[seg_parity ^ 1][1] = 0;
-    float* buf = merge + warp * kRows * C::kPad;
     const bool whole = t_begin == 0 && t_end == wk.tiles;
-    const int slot = whole ? -1 : 2 * (int)blockIdx.x + !first;
+    const int slot = whole ? -1 : (2 * unit + !first) * w.heads + sub;
 #pragma unroll
-    for (int g = 0; g < D / C::kMergeCols; ++g) {
-      if (g > 0) compute_sync();  // the columns before have been read
+    for (int g = 0; g < D / C::kTurn; ++g) {
 #pragma unroll
       for (int mt = 2 * g; mt < 2 * g + 2; ++mt)
 #pragma unroll
@@ -428,24 +422,24 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int col = kCodes ? 4 * n + 2 * (mt & 1) + (i >> 1) : 16 * (mt & 1) + n + 8 * (i >> 1);
-            buf[(8 * nt + 2 * c + (i & 1)) * C::kPad + col] = o[mt][nt][i];
+            turn[(8 * nt + 2 * c + (i & 1)) * C::kPad + col] = o[mt][nt][i];
           }
-      compute_sync();
-      write_piece<D, kCodes, kRows, kWarps, C::kMergeCols>(
-          p, sq, wk.b, h, row0, slot, merge, C::kPad, C::kMergeCols * g, &sm_m[0][0], &sm_l[0][0],
-          (uint64_t)hidden[seg_parity][1] << 32 | hidden[seg_parity][0],
-          *vexpired || sm_bad[0] || sm_bad[1] || sm_bad[2] || sm_bad[3], threadIdx.x);
+      __syncwarp();
+      write_piece<D, kCodes, kRows, C::kTurn>(p, sq, wk.b, h, row0, slot, turn, C::kPad, C::kTurn * g, sm_m[warp],
+                                              sm_l[warp], (uint64_t)hidden[1] << 32 | hidden[0], poison || expired,
+                                              lane);
+      __syncwarp();
     }
+    if (lane == 0) hidden[0] = hidden[1] = 0;
+    __syncwarp();
     first = false;
-    seg_parity ^= 1;
-    } while (wk.next(p, w));
+  } while (wk.next(p, w));
   if (kCodes) asm volatile("cp.async.wait_all;" ::: "memory");
-  if (__any_sync(0xffffffffu, *vexpired)) {  // let copies in flight land before the CTA leaves
+  if (expired) {  // let copies in flight land before the CTA leaves
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 1000000ull) {
     }
   }
-  __syncthreads();
 }
 
 }  // namespace tree

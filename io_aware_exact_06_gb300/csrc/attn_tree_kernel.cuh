@@ -184,6 +184,13 @@ __device__ __forceinline__ uint64_t mask_word(const int64_t* mask, int64_t tok, 
   return mask ? (uint64_t)mask[tok] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
 }
 
+// A row's maximum and sum at the end: NaN scores alone (no maximum) are not an
+// empty row, and an infinite score or value scale (no weight is left) makes it NaN.
+__device__ __forceinline__ void close_row(float& m, float& l) {
+  if (m == INFINITY) l = NAN;
+  if (l != l) m = 0.f;
+}
+
 // Values of the new tokens' keys in a stage made harmless: rows behind the
 // sequence become 0 (they hold whatever the page held), and so does every
 // infinity and NaN of a new token, whose row may be hidden from some query rows
@@ -627,7 +634,7 @@ tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (l[r] != l[r] && m[r] == -INFINITY) m[r] = 0.f;  // NaN scores alone: not an empty row
+      close_row(m[r], l[r]);
       if (c == 0) {
         sm_m[warp][n + 8 * r] = active ? m[r] : -INFINITY;
         sm_l[warp][n + 8 * r] = l[r];
