@@ -178,15 +178,15 @@ struct Plan {
   int64_t ctas;
   int64_t slots;  // parts in the workspace, `rows` rows each
   bool many;      // eight warps join a row's pieces
+  bool fits = true;  // the line's tiles are a 32-bit number
 };
 
 bool few(const Plan& pl) { return pl.rows <= 16; }
 
 // Query rows of a CTA: the smallest tile that holds max_new * G of them.  Few
 // rows: as many persistent warps as fit the SMs (num_splits caps the pieces of a
-// segment instead), at least four tiles (128 keys) each, below which starting a
-// warp and joining its part cost more than its reading.  More rows: key ranges.
-Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
+// segment instead).  More rows: key ranges.
+Plan tree_plan(int B, int total, int Hq, int H, int max_new, int max_len, int num_splits) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
   pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
@@ -200,13 +200,16 @@ Plan tree_plan(int B, int Hq, int H, int max_new, int max_len, int num_splits) {
     pl.work.rows = pl.rows;
     pl.work.heads = heads;
     pl.work.log_tile = attn::tree::kLogFewTile;
-    pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 4;
+    pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
     const int64_t per_cta = attn::tree::kWarps / heads;
     const int64_t most = (int64_t)std::min((double)groups * (double)tiles / pl.work.min_share + 1, 1e9);
     pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * attn::tree::kFewCtas);
     pl.work.units = (int)(pl.ctas * per_cta);
     pl.slots = 2 * (int64_t)pl.work.units * heads;
-    pl.many = pl.work.units > 32 * groups;  // pieces of a segment
+    // eight warps to a row where segments are cut into many pieces, and where the
+    // rows leave the SMs idle anyway
+    pl.many = pl.work.units > 32 * groups || (int64_t)total * Hq <= 8 * kPlanSms;
+    pl.fits = (double)groups * (double)tiles <= INT32_MAX;
     return pl;
   }
   const int64_t T = attn::tree::kTile;
@@ -459,7 +462,7 @@ extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d
                                           int max_len, int num_splits) {
   if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
   if (B == 0 || total == 0 || max_new == 0) return 0;
-  return tree_bytes(tree_plan(B, Hq, H, max_new, max_len, num_splits), total, Hq, d);
+  return tree_bytes(tree_plan(B, total, Hq, H, max_new, max_len, num_splits), total, Hq, d);
 }
 
 extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
@@ -479,7 +482,8 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(mask, 8) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGN;
-  const Plan pl = tree_plan(B, Hq, cache->H, max_new, max_len, num_splits);
+  const Plan pl = tree_plan(B, total, Hq, cache->H, max_new, max_len, num_splits);
+  if (!pl.fits) return ATTN_ERR_SHAPE;
   const size_t need = tree_bytes(pl, total, Hq, d);
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_SCRATCH;
   const double ctas = (double)B * std::max(pl.S, 1) * cache->H * pl.mtiles;

@@ -413,6 +413,10 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       }
     const bool whole = t_begin == 0 && t_end == wk.tiles;
     const int slot = whole ? -1 : (2 * unit + !first) * w.heads + sub;
+    __syncwarp();
+    PieceEnd<D, kCodes, kRows> end;
+    end.rows_of(p, sq, h, row0, slot, sm_m[warp], sm_l[warp], (uint64_t)hidden[1] << 32 | hidden[0],
+                poison || expired, lane);
 #pragma unroll
     for (int g = 0; g < D / C::kTurn; ++g) {
 #pragma unroll
@@ -425,9 +429,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             turn[(8 * nt + 2 * c + (i & 1)) * C::kPad + col] = o[mt][nt][i];
           }
       __syncwarp();
-      write_piece<D, kCodes, kRows, C::kTurn>(p, sq, wk.b, h, row0, slot, turn, C::kPad, C::kTurn * g, sm_m[warp],
-                                              sm_l[warp], (uint64_t)hidden[1] << 32 | hidden[0], poison || expired,
-                                              lane);
+      end.columns(p, sq, wk.b, h, turn, C::kPad, C::kTurn * g, lane);
       __syncwarp();
     }
     if (lane == 0) hidden[0] = hidden[1] = 0;

@@ -25,30 +25,28 @@ struct Work {
 };
 
 __device__ __forceinline__ int seq_tiles(const Seq& s, const Work& w) {
-  return (int)(((int64_t)s.len + (1 << w.log_tile) - 1) >> w.log_tile);
+  return (s.len + (1 << w.log_tile) - 1) >> w.log_tile;  // lengths end 256 below 2^31
 }
 __device__ __forceinline__ int seq_segments(const Params& p, const Seq& s, const Work& w) {
   return (s.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
 }
 // Tiles of sequence b in the line; 0 if it has no new token or impossible lengths.
-__device__ __forceinline__ int64_t line_tiles(const Params& p, const Work& w, int b, bool report) {
-  Seq s;
+__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq& s) {
   if (!load_seq(p, b, s)) {
     if (report) atomicOr(p.err, rows::kBadSeqlens);
     return 0;
   }
-  return (int64_t)seq_segments(p, s, w) * seq_tiles(s, w);
+  return seq_segments(p, s, w) * seq_tiles(s, w);  // the whole line is below 2^31 (checked on the host)
 }
-__device__ __forceinline__ int64_t share_of(int64_t total, const Work& w) {
-  const int64_t even = (total + w.units - 1) / w.units;
+__device__ __forceinline__ int share_of(int total, const Work& w) {
+  const int even = (total - 1) / w.units + 1;
   return even > w.min_share ? even : w.min_share;
 }
 
 // Where a unit is in the line: sequence b (lengths in s), segment seg of it, tile
 // of that, and how many tiles of its share are left.
 struct Walk {
-  int b, seg, segs, tile, tiles;
-  int64_t left;
+  int b, seg, segs, tile, tiles, left;
   Seq s;
   __device__ __forceinline__ void enter(const Params& p, const Work& w) {
     if (load_seq(p, b, s)) {
@@ -59,7 +57,7 @@ struct Walk {
     }
   }
   // tiles of the current segment that belong to the share
-  __device__ __forceinline__ int piece() const { return (int)(tiles - tile < left ? tiles - tile : left); }
+  __device__ __forceinline__ int piece() const { return min(tiles - tile, left); }
   // behind the piece; false at the end of the share
   __device__ __forceinline__ bool next(const Params& p, const Work& w) {
     left -= piece();
@@ -81,96 +79,114 @@ struct Walk {
 __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool report, Walk& walk) {
   const int t = threadIdx.x % 32, per = (p.B + 31) / 32;
   const int b0 = (int)min((int64_t)t * per, (int64_t)p.B), b1 = min(p.B - b0, per) + b0;
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report);
-  int64_t upto = mine;
+  Seq s{};
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report, s);
+  int upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+    const int v = __shfl_up_sync(0xffffffffu, upto, off);
     if (t >= off) upto += v;
   }
-  const int64_t total = __shfl_sync(0xffffffffu, upto, 31), before = upto - mine;
-  const int64_t share = share_of(total, w), first = share * unit;
-  if (first >= total) return false;
-  walk = Walk{};
-  int64_t at = 0;
+  const int total = __shfl_sync(0xffffffffu, upto, 31), before = upto - mine;
+  if (total == 0) return false;
+  const int share = share_of(total, w);
+  if ((int64_t)share * unit >= total) return false;
+  const int first = share * unit;
+  int at = first - before;
+  int b = b0;
   const bool here = first >= before && first < upto;
-  if (here) {
-    at = first - before;
-    for (walk.b = b0;; ++walk.b) {
-      const int64_t n = line_tiles(p, w, walk.b, false);
+  if (here && per > 1)  // else s is the one it has read
+    for (;; ++b) {
+      const int n = line_tiles(p, w, b, false, s);
       if (at < n) break;
       at -= n;
     }
-  }
   const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-  walk.b = __shfl_sync(0xffffffffu, walk.b, src);
+  walk.b = __shfl_sync(0xffffffffu, b, src);
+  walk.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+  walk.s.n = __shfl_sync(0xffffffffu, s.n, src);
+  walk.s.len = __shfl_sync(0xffffffffu, s.len, src);
   at = __shfl_sync(0xffffffffu, at, src);
-  walk.enter(p, w);
-  walk.seg = (int)(at / walk.tiles);
-  walk.tile = (int)(at - (int64_t)walk.seg * walk.tiles);
+  walk.segs = seq_segments(p, walk.s, w);
+  walk.tiles = seq_tiles(walk.s, w);
+  walk.seg = at / walk.tiles;
+  walk.tile = at - walk.seg * walk.tiles;
   walk.left = min(share, total - first);
   return true;
 }
 
-// The end of a piece: a warp writes kCols columns from col0 on of its kRows query
-// rows (sums at buf[r pad], maximum and sum at sm_m, sm_l[r]), as the result where
-// the piece is the whole segment (slot < 0), else into its slot of the workspace.
-template <int D, bool kCodes, int kRows, int kCols>
-__device__ __forceinline__ void write_piece(const Params& p, const Seq& sq, int b, int h, int row0, int slot,
-                                            const float* buf, int pad, int col0, const float* sm_m,
-                                            const float* sm_l, uint64_t hid, bool poison, int lane) {
-  const int ctx = sq.len - sq.n, M = sq.n * p.G;
-  constexpr int kVec = kCols / 4;  // lanes of a row, four columns each
-  for (int i = lane; i < kRows * kVec; i += 32) {
-    const int r = i / kVec, at_col = 4 * (i % kVec), col = col0 + at_col;
-    if (row0 + r >= M) continue;
-    const int tok = (row0 + r) / p.G, head = h * p.G + (row0 + r) - tok * p.G;
-    const float mm = sm_m[r], ls = mm == -INFINITY ? 0.f : sm_l[r];
-    const float4 x = *reinterpret_cast<const float4*>(buf + r * pad + at_col);
-    float f[4] = {x.x, x.y, x.z, x.w};
-    // a row of NaN sums keeps them; one that saw nothing is 0
-    const float inv = ls != 0.f ? 1.f / ls : 0.f;
+// The end of a piece: what a warp writes of its kRows query rows, as the result
+// where the piece is the whole segment (slot < 0), else into its slot of the
+// workspace.  Lane i takes columns 4 (i % 8) .. of rows i / 8, i / 8 + 4, ..
+template <int D, bool kCodes, int kRows>
+struct PieceEnd {
+  static constexpr int kN = kRows / 4;
+  int64_t at[kN];      // row of the output, or of the workspace
+  float inv[kN];
+  uint64_t hid[kN];    // new tokens with values that are not finite, seen by the row
+  bool live[kN], direct, poison;
+
+  __device__ __forceinline__ void rows_of(const Params& p, const Seq& sq, int h, int row0, int slot, const float* sm_m,
+                                          const float* sm_l, uint64_t hidden, bool bad, int lane) {
+    const int M = sq.n * p.G;
+    direct = slot < 0;
+    poison = bad;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = ls != 0.f ? f[k] * inv : 0.f;
-    float lse = ls != 0.f ? (mm + lg2(ls)) * 0.69314718055994531f : -INFINITY;
-    if (hid) {
-      uint64_t todo = hid & mask_word(p.mask, sq.q0 + tok, tok);
+    for (int j = 0; j < kN; ++j) {
+      const int r = lane / 8 + 4 * j;
+      live[j] = row0 + r < M;
+      if (!live[j]) continue;
+      const int tok = (row0 + r) / p.G, head = h * p.G + (row0 + r) - tok * p.G;
+      const float m = sm_m[r], l = m == -INFINITY ? 0.f : sm_l[r];
+      // a row of NaN sums keeps them; one that saw nothing is 0
+      inv[j] = l != 0.f ? 1.f / l : 0.f;
+      hid[j] = hidden ? hidden & mask_word(p.mask, sq.q0 + tok, tok) : 0;
+      at[j] = direct ? (int64_t)(sq.q0 + tok) * p.Hq + head : (int64_t)slot * kRows + r;
+      float lse = l != 0.f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+      if (poison) lse = direct ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
+      if (lane % 8 == 0) (direct ? p.lse : p.lse_part)[at[j]] = lse;
+    }
+  }
+
+  // 32 columns from col0 on; buf[r pad]: the rows' sums
+  __device__ __forceinline__ void columns(const Params& p, const Seq& sq, int b, int h, const float* buf, int pad,
+                                          int col0, int lane) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      if (!live[j]) continue;
+      const float4 x = *reinterpret_cast<const float4*>(buf + (lane / 8 + 4 * j) * pad + 4 * (lane % 8));
+      float f[4] = {x.x, x.y, x.z, x.w};
+      const int col = col0 + 4 * (lane % 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = inv[j] != 0.f ? f[k] * inv[j] : 0.f;
+      uint64_t todo = hid[j];
       while (todo) {
         const int t = __ffsll((long long)todo) - 1;
         todo &= todo - 1;
-        const int pos = ctx + t;
+        const int pos = sq.len - sq.n + t;
         const int id = p.table[(int64_t)b * p.stride + (pos >> p.log_page)];
         if ((unsigned)id >= (unsigned)p.pages) continue;
-        const int64_t at = ((((int64_t)id << p.log_page) + (pos & ((1 << p.log_page) - 1))) * p.H + h) * D + col;
+        const int64_t v = ((((int64_t)id << p.log_page) + (pos & ((1 << p.log_page) - 1))) * p.H + h) * D + col;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (kCodes) {
-            const uint8_t x = reinterpret_cast<const uint8_t*>(p.v)[at + k];
-            if ((x & 0x7f) == 0x7f) f[k] = NAN;
+            if ((reinterpret_cast<const uint8_t*>(p.v)[v + k] & 0x7f) == 0x7f) f[k] = NAN;
           } else {
-            const float x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at + k]);
-            if (!isfinite(x)) f[k] += x;
+            const float y = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[v + k]);
+            if (!isfinite(y)) f[k] += y;
           }
         }
       }
-    }
-    if (poison) {  // a NaN row; +inf makes the merge of the pieces one
-      f[0] = f[1] = f[2] = f[3] = NAN;
-      lse = slot < 0 ? NAN : INFINITY;
-    }
-    if (slot < 0) {
-      const int64_t out = (int64_t)(sq.q0 + tok) * p.Hq + head;
-      *reinterpret_cast<uint2*>(p.o + out * D + col) =
-          make_uint2(rows::pack2(f[0], f[1]), rows::pack2(f[2], f[3]));
-      if (col == 0) p.lse[out] = lse;
-    } else {
-      const int64_t at = (int64_t)slot * kRows + r;
-      *reinterpret_cast<float4*>(p.o_part + at * D + col) = make_float4(f[0], f[1], f[2], f[3]);
-      if (col == 0) p.lse_part[at] = lse;
+      if (poison) f[0] = f[1] = f[2] = f[3] = NAN;
+      if (direct)
+        *reinterpret_cast<uint2*>(p.o + at[j] * D + col) =
+            make_uint2(rows::pack2(f[0], f[1]), rows::pack2(f[2], f[3]));
+      else
+        *reinterpret_cast<float4*>(p.o_part + at[j] * D + col) = make_float4(f[0], f[1], f[2], f[3]);
     }
   }
-}
+};
 
 // Pieces of a row joined: weights e^(LSE - max), as for split keys elsewhere in
 // the library.  kPerRow warps for each (new token, query head): one, or eight
@@ -191,9 +207,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   if (b >= p.B) return;
   Seq sq;
   if (!load_seq(p, b, sq) || t < sq.q0 || t >= sq.q0 + sq.n) return;
-  int64_t total = 0, before = 0;
+  int total = 0, before = 0;
   for (int i = lane; i < p.B; i += 32) {
-    const int64_t n = line_tiles(p, w, i, false);
+    Seq other;
+    const int n = line_tiles(p, w, i, false, other);
     total += n;
     before += i < b ? n : 0;
   }
@@ -205,11 +222,11 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   const int h = head / p.G, row = (t - sq.q0) * p.G + head - h * p.G;
   const int group = h / w.heads, sub = h - group * w.heads;
   const int mtiles = (sq.n * p.G + w.rows - 1) / w.rows, mt = row / w.rows, r = row - mt * w.rows;
-  const int64_t share = share_of(total, w), tiles = seq_tiles(sq, w);
-  const int64_t first = before + ((int64_t)group * mtiles + mt) * tiles;
-  const int c0 = (int)(first / share), c1 = (int)((first + tiles - 1) / share);
+  const int share = share_of(total, w), tiles = seq_tiles(sq, w);
+  const int first = before + (group * mtiles + mt) * tiles;
+  const int c0 = first / share, c1 = (first + tiles - 1) / share;
   if (c0 == c1) return;
-  const bool inside = first % share != 0;  // the first piece begins inside its share
+  const bool inside = first != c0 * share;  // the first piece begins inside its share
   auto at = [&](int c) { return (((int64_t)2 * c + (c == c0 && inside)) * w.heads + sub) * w.rows + r; };
   float top = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
