@@ -1,7 +1,7 @@
 // Writing packed keys and values into a paged cache, and reading it back.
 //
-// The rows of a token (its H key heads, then its H value heads) are cut into
-// chunks; a warp takes one chunk of `run` tokens, `step` tokens apart, the next
+// The heads of a token's keys, and of its values, are cut into chunks of kSteps
+// row groups; a warp takes one chunk of tokens that are `step` apart, the next
 // token's rows on their way while it works on the current ones; all warps
 // together so sweep the packed rows in order, which DRAM serves faster than as
 // many streams as there are warps.  Writing: d / 8
@@ -94,17 +94,6 @@ __device__ __forceinline__ int64_t find_row(Cursor& c, const Pages& pg, const in
   return c.row0 < 0 ? -1 : c.row0 + (pos & ((1 << pg.log_page) - 1));
 }
 
-__device__ __forceinline__ int64_t scale_at(const Pages& c, int64_t r, int h) {
-  const int64_t page = r >> c.log_page, in = r & ((1 << c.log_page) - 1);
-  return ((page * c.H + h) << c.log_page) + in;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Two fp32 values as e4m3, nearest even, at most 448; lo in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -121,6 +110,14 @@ __device__ __forceinline__ void from_e4m3x2(uint16_t w, float& lo, float& hi) {
       : "r"(h));
 }
 
+// Largest magnitude of a pair of bf16, the pairs' maximum; a NaN wins.
+__device__ __forceinline__ uint32_t abs_pair(uint32_t x) { return x & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <int D, bool kCodes>
 __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_constant__ Write p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
@@ -129,57 +126,71 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_c
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
-  const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
+  const int H = p.c.H, chunks = (H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item / chunks >= p.step) return;
-  const int t0 = (int)(item / chunks);
-  const int h0 = (int)(item % chunks) * kChunk;
-  auto load = [&](int t, uint4 (&x)[kSteps]) {
+  const int64_t t0 = item / (2 * chunks);
+  if (t0 >= p.step) return;
+  const int ch = (int)(item - t0 * 2 * chunks);
+  const bool isv = ch >= chunks;
+  const int h0 = (isv ? ch - chunks : ch) * kChunk + row;  // this lane's first head
+  const int64_t ts = isv ? p.v_ts : p.k_ts;
+  const __nv_bfloat16* src = (isv ? p.v : p.k) + h0 * D + 8 * slice;
+  uint8_t* dst = static_cast<uint8_t*>(isv ? p.c.v : p.c.k) + (h0 * D + 8 * slice) * (kCodes ? 1 : 2);
+  float* sdst = (isv ? p.c.vs : p.c.ks) + ((int64_t)h0 << p.c.log_page);
+  auto load = [&](int64_t t, uint4 (&x)[kSteps]) {
+    const __nv_bfloat16* at = src + t * ts;
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const int h = h0 + u * kRows + row;
       x[u] = make_uint4(0, 0, 0, 0);
-      if (h < 2 * H)
-        x[u] = *reinterpret_cast<const uint4*>((h < H ? p.k + t * p.k_ts + (int64_t)h * D
-                                                      : p.v + t * p.v_ts + (int64_t)(h - H) * D) + 8 * slice);
+      if (h0 + u * kRows < H) x[u] = *reinterpret_cast<const uint4*>(at + u * kRows * D);
     }
   };
   uint4 x[kSteps];
   load(t0, x);  // on its way while the token's place is looked up
   Cursor cur;
-  for (int64_t tt = t0; tt < p.total; tt += p.step) {
-    const int t = (int)tt;
+  for (int64_t t = t0; t < p.total; t += p.step) {
     uint4 next[kSteps];
-    if (tt + p.step < p.total) load(t + p.step, next);
-    const int64_t r = find_row(cur, p.c, p.cu, p.lens, p.B, t, p.err);
+    if (t + p.step < p.total) load(t + p.step, next);
+    const int64_t r = find_row(cur, p.c, p.cu, p.lens, p.B, (int)t, p.err);
     if (r >= 0) {
+      uint8_t* at = dst + r * H * D * (kCodes ? 1 : 2);
+      if (!kCodes) {
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const int h = h0 + u * kRows + row;
-        const int hh = h < H ? h : h - H;
-        void* base = h < H ? p.c.k : p.c.v;
-        const int64_t at = (r * H + hh) * D + 8 * slice;
-        if (!kCodes) {
-          if (h < 2 * H) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at) = x[u];
-          continue;
-        }
-        float f[8], top = 0.f;
-        rows::unpack(x[u], f);
+        for (int u = 0; u < kSteps; ++u)
+          if (h0 + u * kRows < H) *reinterpret_cast<uint4*>(at + u * kRows * D * 2) = x[u];
+      } else {
+        // the rows' largest magnitudes, in bf16 (a maximum rounds nothing)
+        uint32_t top[kSteps];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
+        for (int u = 0; u < kSteps; ++u)
+          top[u] = max_pair(max_pair(abs_pair(x[u].x), abs_pair(x[u].y)), max_pair(abs_pair(x[u].z), abs_pair(x[u].w)));
 #pragma unroll
         for (int off = 1; off < kLanes; off <<= 1)
-          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+          for (int u = 0; u < kSteps; ++u) top[u] = max_pair(top[u], __shfl_xor_sync(0xffffffffu, top[u], off));
+        // lane u of a row does the division of row group u for all its lanes
+        uint32_t mine = top[0];
+#pragma unroll
+        for (int u = 1; u < kSteps; ++u) mine = slice % kSteps == u ? top[u] : mine;
+        mine = max_pair(mine, mine >> 16);
         // the floor keeps 1 / scale finite; a NaN passes it
-        float scale = __fdiv_rn(top, 448.f);
+        float scale = __fdiv_rn(__uint_as_float(mine << 16), 448.f);
         if (scale < 0x1p-64f) scale = 0x1p-64f;
         const float inv = __frcp_rn(scale);
-        if (h < 2 * H) {
+        const int64_t page = r >> p.c.log_page;
+        if (slice < kSteps && h0 + slice * kRows < H)
+          sdst[(page * H << p.c.log_page) + (r - (page << p.c.log_page)) + ((int64_t)slice * kRows << p.c.log_page)] = scale;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const float f = __shfl_sync(0xffffffffu, inv, row * kLanes + u);
+          float y[8];
+          rows::unpack(x[u], y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= f;
           uint2 codes;
-          codes.x = e4m3x2(f[0] * inv, f[1] * inv) | e4m3x2(f[2] * inv, f[3] * inv) << 16;
-          codes.y = e4m3x2(f[4] * inv, f[5] * inv) | e4m3x2(f[6] * inv, f[7] * inv) << 16;
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(base) + at) = codes;
-          if (slice == 0) (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)] = scale;
+          codes.x = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+          codes.y = e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16;
+          if (h0 + u * kRows < H) *reinterpret_cast<uint2*>(at + u * kRows * D) = codes;
         }
       }
     }
@@ -197,48 +208,50 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0 && warp == 0) rows::check_offsets(p.cu, p.B, p.total, p.err);
-  const int H = p.c.H, chunks = (2 * H + kChunk - 1) / kChunk;
+  const int H = p.c.H, chunks = (H + kChunk - 1) / kChunk;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item / chunks >= p.step) return;
-  const int t0 = (int)(item / chunks);
-  const int h0 = (int)(item % chunks) * kChunk;
-  Cursor cur;
+  const int64_t t0 = item / (2 * chunks);
+  if (t0 >= p.step) return;
+  const int ch = (int)(item - t0 * 2 * chunks);
+  const bool isv = ch >= chunks;
+  const int h0 = (isv ? ch - chunks : ch) * kChunk + row;  // this lane's first head
+  const uint8_t* src = static_cast<const uint8_t*>(isv ? p.c.v : p.c.k) + (h0 * D + kPer * slice) * (kCodes ? 1 : 2);
+  const float* ssrc = (isv ? p.c.vs : p.c.ks) + ((int64_t)h0 << p.c.log_page);
+  __nv_bfloat16* dst = (isv ? p.v : p.k) + h0 * D + kPer * slice;
   auto load = [&](int64_t r, uint4 (&x)[kSteps], float (&sc)[kSteps]) {
+    const uint8_t* at = src + r * H * D * (kCodes ? 1 : 2);
+    const int64_t page = r >> p.c.log_page;
+    const float* sat = ssrc + (page * H << p.c.log_page) + (r - (page << p.c.log_page));
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const int h = h0 + u * kRows + row;
-      const int hh = h < H ? h : h - H;
       x[u] = make_uint4(0, 0, 0, 0);
       sc[u] = 0.f;
-      if (r >= 0 && h < 2 * H) {
-        const char* base = reinterpret_cast<const char*>(h < H ? p.c.k : p.c.v);
-        x[u] = *reinterpret_cast<const uint4*>(base + ((r * H + hh) * D + kPer * slice) * (kCodes ? 1 : 2));
-        if (kCodes) sc[u] = (h < H ? p.c.ks : p.c.vs)[scale_at(p.c, r, hh)];
+      if (r >= 0 && h0 + u * kRows < H) {
+        x[u] = *reinterpret_cast<const uint4*>(at + u * kRows * D * (kCodes ? 1 : 2));
+        if (kCodes) sc[u] = sat[(int64_t)u * kRows << p.c.log_page];
       }
     }
   };
+  Cursor cur;
   uint4 x[kSteps];
   float sc[kSteps];
-  int64_t r = find_row(cur, p.c, p.cu, nullptr, p.B, t0, p.err);
+  int64_t r = find_row(cur, p.c, p.cu, nullptr, p.B, (int)t0, p.err);
   load(r, x, sc);
-  for (int64_t tt = t0; tt < p.total; tt += p.step) {
-    const int t = (int)tt;
+  for (int64_t t = t0; t < p.total; t += p.step) {
     uint4 next[kSteps];
     float nsc[kSteps];
     int64_t rn = -1;
-    if (tt + p.step < p.total) {
-      rn = find_row(cur, p.c, p.cu, nullptr, p.B, t + p.step, p.err);
+    if (t + p.step < p.total) {
+      rn = find_row(cur, p.c, p.cu, nullptr, p.B, (int)(t + p.step), p.err);
       load(rn, next, nsc);
     }
     if (r >= 0) {
+      __nv_bfloat16* at = dst + t * H * D;
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        const int h = h0 + u * kRows + row;
-        if (h >= 2 * H) continue;
-        __nv_bfloat16* dst =
-            (h < H ? p.k + ((int64_t)t * H + h) * D : p.v + ((int64_t)t * H + h - H) * D) + kPer * slice;
+        if (h0 + u * kRows >= H) continue;
         if (!kCodes) {
-          *reinterpret_cast<uint4*>(dst) = x[u];
+          *reinterpret_cast<uint4*>(at + u * kRows * D) = x[u];
           continue;
         }
         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
@@ -250,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
             from_e4m3x2((uint16_t)(w[2 * i + j / 2] >> (16 * (j & 1))), f[2 * j], f[2 * j + 1]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= sc[u];
-          *reinterpret_cast<uint4*>(dst + 8 * i) = rows::pack(f);
+          *reinterpret_cast<uint4*>(at + u * kRows * D + 8 * i) = rows::pack(f);
         }
       }
     }

@@ -1,12 +1,15 @@
 // Norm of every query and key head with the rotary rotation, and its gradient.
 //
-// A row (token, head) of d channels is held by d / 8 lanes, 16 bytes each, so
-// a warp holds 32 / (d / 8) rows (2 at d = 128, 4 at d = 64) at a time.  The
-// row's sum of squares is a shuffle reduction; the partner channel of a
-// half-split pair sits rot / 16 lanes away in the same register, that of an
-// interleaved pair in the same lane.  Nothing goes through shared memory in the
-// forward; each element is read and written once, so HBM bounds it (and launch
-// latency for a few tokens).
+// A row (token, head) of d channels is held by d / 8 lanes, so a warp holds
+// 32 / (d / 8) rows (2 at d = 128, 4 at d = 64) at a time.  A lane holds two
+// groups of four neighbouring channels, chosen so that both channels of a pair
+// are its own: groups s and s + rot / 8 of a half-split rotation, neighbouring
+// groups of an interleaved one and of the channels that do not rotate.  So the
+// rotation needs no exchange and a lane only its own four cosines and sines (a
+// 16-byte slice of the row instead took 8 shuffles a row and 16 registers of
+// angles); the row's sum of squares is a shuffle reduction.  Nothing goes through
+// shared memory in the forward; each element is read and written once, so HBM
+// bounds it (and launch latency for a few tokens).
 //
 // The heads of a token are cut into chunks of kSteps (forward) or kBwdSteps row
 // groups, and a warp takes a run of a token's chunks: it loads the next chunk
@@ -56,14 +59,34 @@ struct Bwd {
   int* err;
 };
 
-// cos and sin of this lane's pairs (8 half-split, 4 interleaved) for token t,
-// and whether the lane's channels rotate at all.  False if a position lies
-// outside the table.
+// The first channels of lane `slice`'s two groups.
 template <bool kInter>
-__device__ __forceinline__ bool load_angles(const Rotary& r, int T, int t, int slice, float (&c)[8],
-                                            float (&s)[8], bool* rotates) {
-  constexpr int kPairs = kInter ? 4 : 8;
-  *rotates = 8 * slice < 2 * r.half;
+__device__ __forceinline__ void lane_channels(int half, int slice, int& a, int& b) {
+  if (kInter || 8 * slice >= 2 * half) {
+    a = 8 * slice;
+    b = a + 4;
+  } else {
+    a = 4 * slice;
+    b = a + half;
+  }
+}
+
+// A lane's eight channels of a row: group a in the low half, b in the high.
+__device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int a, int b) {
+  const uint2 lo = *reinterpret_cast<const uint2*>(row + a), hi = *reinterpret_cast<const uint2*>(row + b);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int a, int b, const uint4& v) {
+  *reinterpret_cast<uint2*>(row + a) = make_uint2(v.x, v.y);
+  *reinterpret_cast<uint2*>(row + b) = make_uint2(v.z, v.w);
+}
+
+// cos and sin of this lane's four pairs for token t (1 and 0 where its channels
+// do not rotate).  False if a position lies outside the table.
+template <bool kInter>
+__device__ __forceinline__ bool load_angles(const Rotary& r, int T, int t, int slice, float (&c)[4], float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
   if (r.half == 0) return true;
   int p[3];
   bool ok = true;
@@ -73,22 +96,19 @@ __device__ __forceinline__ bool load_angles(const Rotary& r, int T, int t, int s
     ok &= (unsigned)p[a] < (unsigned)r.P;
   }
   if (!ok) return false;
-  if (*rotates) {
-    const int j0 = kInter ? 4 * slice : (8 * slice) % r.half;
+  const int j0 = 4 * slice;  // the lane's first pair, half-split or interleaved
+  if (j0 < r.half) {
     const int ax0 = (j0 >= r.edge0) + (j0 >= r.edge1);
-    const int ax1 = (j0 + kPairs - 1 >= r.edge0) + (j0 + kPairs - 1 >= r.edge1);
+    const int ax1 = (j0 + 3 >= r.edge0) + (j0 + 3 >= r.edge1);
     if (ax0 == ax1) {
       const int64_t at = (int64_t)(ax0 == 0 ? p[0] : ax0 == 1 ? p[1] : p[2]) * r.half + j0;
-#pragma unroll
-      for (int i = 0; i < kPairs; i += 4) {
-        const float4 cv = *reinterpret_cast<const float4*>(r.cos + at + i);
-        const float4 sv = *reinterpret_cast<const float4*>(r.sin + at + i);
-        c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
-        s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
-      }
+      const float4 cv = *reinterpret_cast<const float4*>(r.cos + at);
+      const float4 sv = *reinterpret_cast<const float4*>(r.sin + at);
+      c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+      s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
     } else {  // an axis ends inside the lane's pairs
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int j = j0 + i;
         const int64_t at = (int64_t)(j >= r.edge1 ? p[2] : j >= r.edge0 ? p[1] : p[0]) * r.half + j;
         c[i] = r.cos[at];
@@ -99,28 +119,15 @@ __device__ __forceinline__ bool load_angles(const Rotary& r, int T, int t, int s
   return true;
 }
 
-// y rotated by (c, s), or by its inverse with kBack.  Every lane of the warp calls it.
+// y rotated by (c, s), or by its inverse with kBack.
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void rotate(float (&y)[8], const float (&c)[8], const float (&s)[8],
-                                       bool rotates, int half, int slice) {
-  if (kInter) {
-    if (!rotates) return;
+__device__ __forceinline__ void rotate(float (&y)[8], const float (&c)[4], const float (&s)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1], si = kBack ? -s[i] : s[i];
-      y[2 * i] = a * c[i] - b * si;
-      y[2 * i + 1] = b * c[i] + a * si;
-    }
-  } else {
-    const bool low = 8 * slice < half;
-    const int lane = threadIdx.x % 32;
-    const int src = rotates ? lane + (low ? half / 8 : -(half / 8)) : lane;
-    const float sign = low != kBack ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, y[i], src);
-      if (rotates) y[i] = y[i] * c[i] + sign * (other * s[i]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 4;
+    const float a = y[ia], b = y[ib], si = kBack ? -s[i] : s[i];
+    y[ia] = a * c[i] - b * si;
+    y[ib] = b * c[i] + a * si;
   }
 }
 
@@ -138,28 +145,28 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
   if (item >= (int64_t)p.T * runs) return;
   const int t = (int)(item / runs);
   const int c0 = (int)(item - (int64_t)t * runs) * p.run, c1 = min(chunks, c0 + p.run);
-  const __nv_bfloat16* qs = p.q + t * p.q_ts + row * D + 8 * slice;
-  const __nv_bfloat16* ks = p.k + t * p.k_ts + row * D + 8 * slice;
-  __nv_bfloat16* qd = p.qo + t * p.qo_ts + row * D + 8 * slice;
-  __nv_bfloat16* kd = p.ko + t * p.ko_ts + row * D + 8 * slice;
+  int ca, cb;
+  lane_channels<kInter>(p.rot.half, slice, ca, cb);
+  const __nv_bfloat16* qs = p.q + t * p.q_ts + row * D;
+  const __nv_bfloat16* ks = p.k + t * p.k_ts + row * D;
+  __nv_bfloat16* qd = p.qo + t * p.qo_ts + row * D;
+  __nv_bfloat16* kd = p.ko + t * p.ko_ts + row * D;
   auto load = [&](int chunk, uint4 (&x)[kSteps]) {
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const int h = chunk * kChunk + u * kRows;  // of the group's first row
       x[u] = make_uint4(0, 0, 0, 0);
       if (h + row < H)
-        x[u] = *reinterpret_cast<const uint4*>(h + row < p.Hq ? qs + (int64_t)h * D
-                                                              : ks + (int64_t)(h - p.Hq) * D);
+        x[u] = load_row(h + row < p.Hq ? qs + h * D : ks + (h - p.Hq) * D, ca, cb);
     }
   };
   uint4 x[kSteps];
   load(c0, x);
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (p.Hq) wq = *reinterpret_cast<const uint4*>(p.wq + 8 * slice);
-  if (p.Hk) wk = *reinterpret_cast<const uint4*>(p.wk + 8 * slice);
-  float c[8], s[8];
-  bool rotates;
-  if (!load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates)) {  // the same for the whole warp: one token
+  if (p.Hq) wq = load_row(p.wq, ca, cb);
+  if (p.Hk) wk = load_row(p.wk, ca, cb);
+  float c[4], s[4];
+  if (!load_angles<kInter>(p.rot, p.T, t, slice, c, s)) {  // the same for the whole warp: one token
     if (lane == 0) atomicOr(p.err, rows::kBadIndex);
     return;
   }
@@ -179,9 +186,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
       const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-      rotate<kInter, false>(y, c, s, rotates, p.rot.half, slice);
+      rotate<kInter, false>(y, c, s);
       if (h + row < H)
-        *reinterpret_cast<uint4*>(isq ? qd + (int64_t)h * D : kd + (int64_t)(h - p.Hq) * D) = rows::pack(y);
+        store_row(isq ? qd + h * D : kd + (h - p.Hq) * D, ca, cb, rows::pack(y));
     }
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) x[u] = next[u];
@@ -209,12 +216,14 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
   const int H = p.H[kind], run = p.run[kind];
   const int chunks = (H + kChunk - 1) / kChunk, runs = (chunks + run - 1) / run;
   const int64_t items = (int64_t)p.T * runs, stride = (int64_t)ctas * kWarps;
-  const __nv_bfloat16* xb = p.x[kind] + row * D + 8 * slice;
-  const __nv_bfloat16* gb = p.g[kind] + row * D + 8 * slice;
-  __nv_bfloat16* db = p.dx[kind] + row * D + 8 * slice;
+  int ca, cb;
+  lane_channels<kInter>(p.rot.half, slice, ca, cb);
+  const __nv_bfloat16* xb = p.x[kind] + row * D;
+  const __nv_bfloat16* gb = p.g[kind] + row * D;
+  __nv_bfloat16* db = p.dx[kind] + row * D;
   const int64_t x_ts = p.x_ts[kind], g_ts = p.g_ts[kind], dx_ts = p.dx_ts[kind];
   float acc[8], w[8];
-  rows::unpack(*reinterpret_cast<const uint4*>(p.w[kind] + 8 * slice), w);
+  rows::unpack(load_row(p.w[kind], ca, cb), w);
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   auto load = [&](int t, int chunk, uint4 (&xv)[kBwdSteps], uint4 (&gv)[kBwdSteps]) {
@@ -223,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
       const int h = chunk * kChunk + u * kRows;
       xv[u] = gv[u] = make_uint4(0, 0, 0, 0);
       if (h + row < H) {
-        xv[u] = *reinterpret_cast<const uint4*>(xb + t * x_ts + (int64_t)h * D);
-        gv[u] = *reinterpret_cast<const uint4*>(gb + t * g_ts + (int64_t)h * D);
+        xv[u] = load_row(xb + t * x_ts + h * D, ca, cb);
+        gv[u] = load_row(gb + t * g_ts + h * D, ca, cb);
       }
     }
   };
@@ -241,9 +250,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
     load(t, ch, xv, gv);
   }
   while (item < items) {
-    float c[8], s[8];
-    bool rotates;
-    const bool ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s, &rotates);
+    float c[4], s[4];
+    const bool ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
     if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
     while (true) {  // the run's chunks; the next one, of this run or the next, is on its way
       const int ct = t, cc = ch;
@@ -261,24 +269,26 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
           float x[8], g[8];
           rows::unpack(xv[u], x);
           rows::unpack(gv[u], g);
-          rotate<kInter, true>(g, c, s, rotates, p.rot.half, slice);
+          rotate<kInter, true>(g, c, s);
           float sq = 0.f, dot = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            const float xg = x[i] * g[i];
             sq = fmaf(x[i], x[i], sq);
-            dot = fmaf(g[i] * w[i], x[i], dot);
+            dot = fmaf(xg, w[i], dot);
           }
           sq = rows::row_sum<kLanes>(sq);
           dot = rows::row_sum<kLanes>(dot);
-          const float r = rsqrtf(sq * (1.0f / D) + p.eps);
+          // rows that do not exist hold zeros, and with eps = 0 would give 0 * inf
+          const float r = h + row < H ? rsqrtf(sq * (1.0f / D) + p.eps) : 0.f;
           const float coef = dot * (1.0f / D) * r * r;
           float dx[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             dx[i] = r * (g[i] * w[i] - x[i] * coef);
-            if (h + row < H) acc[i] += g[i] * (x[i] * r);
+            acc[i] = fmaf(g[i] * x[i], r, acc[i]);
           }
-          if (h + row < H) *reinterpret_cast<uint4*>(db + ct * dx_ts + (int64_t)h * D) = rows::pack(dx);
+          if (h + row < H) store_row(db + ct * dx_ts + h * D, ca, cb, rows::pack(dx));
         }
       }
 #pragma unroll
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
   for (int i = 0; i < 8; ++i) {
 #pragma unroll
     for (int off = kLanes; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-    if (row == 0) sm[warp][8 * slice + i] = acc[i];
+    if (row == 0) sm[warp][(i < 4 ? ca : cb) + i % 4] = acc[i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += kThreads) {

@@ -399,7 +399,7 @@ extern "C" int attn_cache_write(const attn_paged_cache* cache, const void* k, in
   if (!seqlens || !cu_seqlens) return ATTN_ERR_NULL;
   if (!aligned(seqlens, 4) || !aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
   attn::cache::Write p{};
-  const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps);
+  const int64_t chunks = 2 * chunks_of(cache->H, cache->d, attn::cache::kSteps);
   const int run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
   p.step = (total - 1) / run + 1;
   const int64_t items = p.step * chunks;
@@ -437,7 +437,7 @@ extern "C" int attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
   if (!aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
   const bool codes = cache->k_scale != nullptr;
   attn::cache::Read p{};
-  const int64_t chunks = chunks_of(2 * cache->H, cache->d, attn::cache::kSteps * (codes ? 2 : 1));
+  const int64_t chunks = 2 * chunks_of(cache->H, cache->d, attn::cache::kSteps * (codes ? 2 : 1));
   const int run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
   p.step = (total - 1) / run + 1;
   const int64_t items = p.step * chunks;
