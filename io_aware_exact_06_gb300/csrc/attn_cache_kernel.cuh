@@ -4,11 +4,10 @@
 // row groups; a warp takes one chunk of tokens that are `step` apart, the next
 // token's rows on their way while it works on the current ones; all warps
 // together so sweep the packed rows in order, which DRAM serves faster than as
-// many streams as there are warps.  Writing: d / 8
-// lanes hold a row's bf16 channels, 16 bytes each; the row maximum is a shuffle
-// reduction and the codes leave 8 bytes a lane.  Reading: d / 16 lanes hold a
-// row's codes, 16 bytes each (bf16 caches: d / 8 lanes), and write 32 bytes a
-// lane.  Every byte moves once, so HBM bounds both (launch latency for a few
+// many streams as there are warps.  d / 8 lanes
+// hold a row, eight channels each: 16 bytes of bf16, 8 bytes of codes.  Writing,
+// the row maximum is a shuffle reduction in bf16.  (Reading 16 codes a lane makes
+// each 16-byte store fill half a sector: 122 us for 612 MB against  Every byte moves once, so HBM bounds both (launch latency for a few
 // tokens: runs of one).
 #pragma once
 
@@ -199,10 +198,23 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const __grid_c
   }
 }
 
+// A lane's eight channels: 16 bytes of bf16, or 8 of codes (in the low half).
+template <bool kCodes>
+__device__ __forceinline__ void load8(const uint8_t* at, uint32_t (&x)[kCodes ? 2 : 4]) {
+  if (kCodes) {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    x[0] = v.x, x[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    x[0] = v.x, x[1] = v.y, x[kCodes ? 0 : 2] = v.z, x[kCodes ? 1 : 3] = v.w;
+  }
+}
+
 template <int D, bool kCodes>
 __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_constant__ Read p) {
-  constexpr int kPer = kCodes ? 16 : 8;  // channels a lane holds
-  constexpr int kLanes = D / kPer, kRows = 32 / kLanes, kChunk = kRows * kSteps;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
+  constexpr int kSize = kCodes ? 1 : 2;  // bytes of a channel
+  constexpr int kWords = kCodes ? 2 : 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
   grid_dep_wait();
@@ -215,30 +227,27 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
   const int ch = (int)(item - t0 * 2 * chunks);
   const bool isv = ch >= chunks;
   const int h0 = (isv ? ch - chunks : ch) * kChunk + row;  // this lane's first head
-  const uint8_t* src = static_cast<const uint8_t*>(isv ? p.c.v : p.c.k) + (h0 * D + kPer * slice) * (kCodes ? 1 : 2);
+  const uint8_t* src = static_cast<const uint8_t*>(isv ? p.c.v : p.c.k) + (h0 * D + 8 * slice) * kSize;
   const float* ssrc = (isv ? p.c.vs : p.c.ks) + ((int64_t)h0 << p.c.log_page);
-  __nv_bfloat16* dst = (isv ? p.v : p.k) + h0 * D + kPer * slice;
-  auto load = [&](int64_t r, uint4 (&x)[kSteps], float (&sc)[kSteps]) {
-    const uint8_t* at = src + r * H * D * (kCodes ? 1 : 2);
+  __nv_bfloat16* dst = (isv ? p.v : p.k) + h0 * D + 8 * slice;
+  auto load = [&](int64_t r, uint32_t (&x)[kSteps][kWords], float (&sc)[kSteps]) {
+    const uint8_t* at = src + r * H * D * kSize;
     const int64_t page = r >> p.c.log_page;
     const float* sat = ssrc + (page * H << p.c.log_page) + (r - (page << p.c.log_page));
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      sc[u] = 0.f;
+    for (int u = 0; u < kSteps; ++u)
       if (r >= 0 && h0 + u * kRows < H) {
-        x[u] = *reinterpret_cast<const uint4*>(at + u * kRows * D * (kCodes ? 1 : 2));
+        load8<kCodes>(at + u * kRows * D * kSize, x[u]);
         if (kCodes) sc[u] = sat[(int64_t)u * kRows << p.c.log_page];
       }
-    }
   };
   Cursor cur;
-  uint4 x[kSteps];
+  uint32_t x[kSteps][kWords];
   float sc[kSteps];
   int64_t r = find_row(cur, p.c, p.cu, nullptr, p.B, (int)t0, p.err);
   load(r, x, sc);
   for (int64_t t = t0; t < p.total; t += p.step) {
-    uint4 next[kSteps];
+    uint32_t next[kSteps][kWords];
     float nsc[kSteps];
     int64_t rn = -1;
     if (t + p.step < p.total) {
@@ -250,26 +259,28 @@ __global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
         if (h0 + u * kRows >= H) continue;
-        if (!kCodes) {
-          *reinterpret_cast<uint4*>(at + u * kRows * D) = x[u];
-          continue;
-        }
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        uint4 out;
+        if (kCodes) {
           float f[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            from_e4m3x2((uint16_t)(w[2 * i + j / 2] >> (16 * (j & 1))), f[2 * j], f[2 * j + 1]);
+            from_e4m3x2((uint16_t)(x[u][j / 2] >> (16 * (j & 1))), f[2 * j], f[2 * j + 1]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= sc[u];
-          *reinterpret_cast<uint4*>(at + u * kRows * D + 8 * i) = rows::pack(f);
+          out = rows::pack(f);
+        } else {
+          out = make_uint4(x[u][0], x[u][1], x[u][kCodes ? 0 : 2], x[u][kCodes ? 1 : 3]);
         }
+        *reinterpret_cast<uint4*>(at + u * kRows * D) = out;
       }
     }
     r = rn;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) x[u] = next[u], sc[u] = nsc[u];
+    for (int u = 0; u < kSteps; ++u) {
+      sc[u] = nsc[u];
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) x[u][j] = next[u][j];
+    }
   }
 }
 

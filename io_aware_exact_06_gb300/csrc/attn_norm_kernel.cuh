@@ -12,10 +12,13 @@
 // bounds it (and launch latency for a few tokens).
 //
 // The heads of a token are cut into chunks of kSteps (forward) or kBwdSteps row
-// groups, and a warp takes a run of a token's chunks: it loads the next chunk
-// before it works on the current one, and the token's position and angles, two
-// dependent loads, once per run.  The run is the whole token when there are
-// tokens enough to fill the GPU four times over, one chunk when there are few.
+// groups, and a warp takes runs of a token's chunks, one run after the other:
+// the whole token when there are tokens enough to fill the GPU four times over,
+// one chunk when there are few.  Loads run kStages - 1 chunks ahead: each lane
+// copies its own channels to its own place in shared memory (cp.async) and reads
+// them back there, so no thread waits for another and the depth costs no
+// registers (one chunk ahead in registers left 2 KB a warp in flight in the
+// gradient, 4.1 TB/s).
 #pragma once
 
 #include "attn_rows.cuh"
@@ -27,6 +30,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 4;     // row groups of a chunk, forward
 constexpr int kBwdSteps = 2;  // gradient: two tensors are loaded
+constexpr int kStages = 4;    // chunks in shared memory, forward and gradient: 64 bytes a lane each
+constexpr int kSmem = kStages * kThreads * 64;
 
 struct Rotary {
   const float *cos, *sin;  // [P, half]
@@ -131,67 +136,124 @@ __device__ __forceinline__ void rotate(float (&y)[8], const float (&c)[4], const
   }
 }
 
+// 8 bytes from global to shared memory; zeros where `there` is false.
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until this thread's copies of all but its last kStages - 2 chunks have landed.
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+}
+__device__ __forceinline__ uint4 lane_load(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
+
+// A warp's chunks in order: run after run (item, item + stride, ..), chunk after
+// chunk of a run.
+struct Runs {
+  int64_t item, items, stride;
+  int runs, run, chunks;  // runs of a token, chunks of a run and of a token
+  int t, ch, end;
+  __device__ __forceinline__ void place() {
+    t = (int)(item / runs);
+    ch = (int)(item - (int64_t)t * runs) * run;
+    end = min(chunks, ch + run);
+  }
+  __device__ __forceinline__ bool more() const { return item < items; }
+  // true when the next chunk begins a run
+  __device__ __forceinline__ bool next() {
+    if (++ch < end) return false;
+    item += stride;
+    if (more()) place();
+    return true;
+  }
+};
+
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ Fwd p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kSteps;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
+  const uint32_t mine = smem_u32(smem) + (warp * kStages * kSteps * 32 + lane) * 16;
   grid_dep_wait();
   grid_dep_launch();
   const int H = p.Hq + p.Hk;
-  const int chunks = (H + kChunk - 1) / kChunk;
-  const int runs = (chunks + p.run - 1) / p.run;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item >= (int64_t)p.T * runs) return;
-  const int t = (int)(item / runs);
-  const int c0 = (int)(item - (int64_t)t * runs) * p.run, c1 = min(chunks, c0 + p.run);
   int ca, cb;
   lane_channels<kInter>(p.rot.half, slice, ca, cb);
-  const __nv_bfloat16* qs = p.q + t * p.q_ts + row * D;
-  const __nv_bfloat16* ks = p.k + t * p.k_ts + row * D;
-  __nv_bfloat16* qd = p.qo + t * p.qo_ts + row * D;
-  __nv_bfloat16* kd = p.ko + t * p.ko_ts + row * D;
-  auto load = [&](int chunk, uint4 (&x)[kSteps]) {
+  Runs use;
+  use.chunks = (H + kChunk - 1) / kChunk;
+  use.run = p.run;
+  use.runs = (use.chunks + p.run - 1) / p.run;
+  use.items = (int64_t)p.T * use.runs;
+  use.stride = (int64_t)gridDim.x * kWarps;
+  use.item = (int64_t)blockIdx.x * kWarps + warp;
+  if (!use.more()) return;
+  use.place();
+  Runs ahead = use;
+  int slot = 0;
+  auto feed = [&]() {
+    if (ahead.more()) {
+      const __nv_bfloat16* qs = p.q + ahead.t * p.q_ts;
+      const __nv_bfloat16* ks = p.k + ahead.t * p.k_ts;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int h = chunk * kChunk + u * kRows;  // of the group's first row
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (h + row < H)
-        x[u] = load_row(h + row < p.Hq ? qs + h * D : ks + (h - p.Hq) * D, ca, cb);
+      for (int u = 0; u < kSteps; ++u) {
+        const int h = ahead.ch * kChunk + u * kRows + row;
+        const __nv_bfloat16* src = h < p.Hq ? qs + h * D : ks + (h - p.Hq) * D;
+        if (h >= H) src = p.Hq ? p.q : p.k;  // not read
+        const uint32_t dst = mine + (slot * kSteps + u) * 512;
+        copy8(dst, src + ca, h < H);
+        copy8(dst + 8, src + cb, h < H);
+      }
+      ahead.next();
     }
+    copies_done();
+    slot = slot == kStages - 1 ? 0 : slot + 1;
   };
-  uint4 x[kSteps];
-  load(c0, x);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) feed();
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
   if (p.Hq) wq = load_row(p.wq, ca, cb);
   if (p.Hk) wk = load_row(p.wk, ca, cb);
   float c[4], s[4];
-  if (!load_angles<kInter>(p.rot, p.T, t, slice, c, s)) {  // the same for the whole warp: one token
-    if (lane == 0) atomicOr(p.err, rows::kBadIndex);
-    return;
-  }
-  for (int ch = c0; ch < c1; ++ch) {
-    uint4 next[kSteps];
-    if (ch + 1 < c1) load(ch + 1, next);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int h = ch * kChunk + u * kRows;
-      const bool isq = h + row < p.Hq;
-      float y[8], w[8];
-      rows::unpack(x[u], y);
-      rows::unpack(isq ? wq : wk, w);
-      float sq = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-      const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-      rotate<kInter, false>(y, c, s);
-      if (h + row < H)
-        store_row(isq ? qd + h * D : kd + (h - p.Hq) * D, ca, cb, rows::pack(y));
+  bool ok = false, fresh = true;
+  int from = 0;
+  while (use.more()) {
+    const int t = use.t, ch = use.ch;
+    if (fresh) {  // the same for the whole warp: one token
+      ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
+      if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
     }
+    copies_wait();
+    feed();
+    if (ok) {
+      __nv_bfloat16* qd = p.qo + t * p.qo_ts;
+      __nv_bfloat16* kd = p.ko + t * p.ko_ts;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) x[u] = next[u];
+      for (int u = 0; u < kSteps; ++u) {
+        const int h = ch * kChunk + u * kRows + row;
+        const bool isq = h < p.Hq;
+        float y[8], w[8];
+        rows::unpack(lane_load(mine + (from * kSteps + u) * 512), y);
+        rows::unpack(isq ? wq : wk, w);
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
+        const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+        rotate<kInter, false>(y, c, s);
+        if (h < H) store_row(isq ? qd + h * D : kd + (h - p.Hq) * D, ca, cb, rows::pack(y));
+      }
+    }
+    from = from == kStages - 1 ? 0 : from + 1;
+    fresh = use.next();
   }
 }
 
@@ -206,95 +268,99 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ Bwd p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kChunk = kRows * kBwdSteps;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float sm[kWarps][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slice = lane % kLanes, row = lane / kLanes;
-  __shared__ float sm[kWarps][D];
+  const uint32_t mine = smem_u32(smem) + (warp * kStages * 2 * kBwdSteps * 32 + lane) * 16;
   grid_dep_wait();
   grid_dep_launch();
   const int kind = (int)blockIdx.x >= p.ctas_q;
   const int cta = blockIdx.x - (kind ? p.ctas_q : 0), ctas = kind ? gridDim.x - p.ctas_q : p.ctas_q;
-  const int H = p.H[kind], run = p.run[kind];
-  const int chunks = (H + kChunk - 1) / kChunk, runs = (chunks + run - 1) / run;
-  const int64_t items = (int64_t)p.T * runs, stride = (int64_t)ctas * kWarps;
+  const int H = p.H[kind];
+  Runs use;
+  use.chunks = (H + kChunk - 1) / kChunk;
+  use.run = p.run[kind];
+  use.runs = (use.chunks + use.run - 1) / use.run;
+  use.items = (int64_t)p.T * use.runs;
+  use.stride = (int64_t)ctas * kWarps;
+  use.item = (int64_t)cta * kWarps + warp;
+  if (use.more()) use.place();
+  Runs ahead = use;
   int ca, cb;
   lane_channels<kInter>(p.rot.half, slice, ca, cb);
-  const __nv_bfloat16* xb = p.x[kind] + row * D;
-  const __nv_bfloat16* gb = p.g[kind] + row * D;
-  __nv_bfloat16* db = p.dx[kind] + row * D;
+  const __nv_bfloat16 *xb = p.x[kind], *gb = p.g[kind];
+  __nv_bfloat16* db = p.dx[kind];
   const int64_t x_ts = p.x_ts[kind], g_ts = p.g_ts[kind], dx_ts = p.dx_ts[kind];
+  int slot = 0;
+  auto feed = [&]() {
+    if (ahead.more()) {
+      const __nv_bfloat16 *xs = xb + ahead.t * x_ts, *gs = gb + ahead.t * g_ts;
+#pragma unroll
+      for (int u = 0; u < kBwdSteps; ++u) {
+        const int h = ahead.ch * kChunk + u * kRows + row;
+        const bool there = h < H;
+        const int at = there ? h * D : 0;
+        const uint32_t dst = mine + (slot * kBwdSteps + u) * 1024;
+        copy8(dst, xs + at + ca, there);
+        copy8(dst + 8, xs + at + cb, there);
+        copy8(dst + 512, gs + at + ca, there);
+        copy8(dst + 520, gs + at + cb, there);
+      }
+      ahead.next();
+    }
+    copies_done();
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) feed();
   float acc[8], w[8];
   rows::unpack(load_row(p.w[kind], ca, cb), w);
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  auto load = [&](int t, int chunk, uint4 (&xv)[kBwdSteps], uint4 (&gv)[kBwdSteps]) {
-#pragma unroll
-    for (int u = 0; u < kBwdSteps; ++u) {
-      const int h = chunk * kChunk + u * kRows;
-      xv[u] = gv[u] = make_uint4(0, 0, 0, 0);
-      if (h + row < H) {
-        xv[u] = load_row(xb + t * x_ts + h * D, ca, cb);
-        gv[u] = load_row(gb + t * g_ts + h * D, ca, cb);
-      }
+  float c[4], s[4];
+  bool ok = false, fresh = true;
+  int from = 0;
+  while (use.more()) {
+    const int t = use.t, ch = use.ch;
+    if (fresh) {
+      ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
+      if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
     }
-  };
-  int64_t item = (int64_t)cta * kWarps + warp;
-  uint4 xv[kBwdSteps], gv[kBwdSteps];
-  int t = 0, ch = 0, c1 = 0;
-  auto place = [&](int64_t it) {
-    t = (int)(it / runs);
-    ch = (int)(it - (int64_t)t * runs) * run;
-    c1 = min(chunks, ch + run);
-  };
-  if (item < items) {
-    place(item);
-    load(t, ch, xv, gv);
-  }
-  while (item < items) {
-    float c[4], s[4];
-    const bool ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
-    if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
-    while (true) {  // the run's chunks; the next one, of this run or the next, is on its way
-      const int ct = t, cc = ch;
-      const bool last = ++ch == c1;
-      if (last) {
-        item += stride;
-        if (item < items) place(item);
-      }
-      uint4 nx[kBwdSteps], ng[kBwdSteps];
-      if (item < items) load(t, ch, nx, ng);
-      if (ok) {
+    copies_wait();
+    feed();
+    if (ok) {
 #pragma unroll
-        for (int u = 0; u < kBwdSteps; ++u) {
-          const int h = cc * kChunk + u * kRows;
-          float x[8], g[8];
-          rows::unpack(xv[u], x);
-          rows::unpack(gv[u], g);
-          rotate<kInter, true>(g, c, s);
-          float sq = 0.f, dot = 0.f;
+      for (int u = 0; u < kBwdSteps; ++u) {
+        const int h = ch * kChunk + u * kRows + row;
+        const uint32_t at = mine + (from * kBwdSteps + u) * 1024;
+        float x[8], g[8];
+        rows::unpack(lane_load(at), x);
+        rows::unpack(lane_load(at + 512), g);
+        rotate<kInter, true>(g, c, s);
+        float sq = 0.f, dot = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float xg = x[i] * g[i];
-            sq = fmaf(x[i], x[i], sq);
-            dot = fmaf(xg, w[i], dot);
-          }
-          sq = rows::row_sum<kLanes>(sq);
-          dot = rows::row_sum<kLanes>(dot);
-          // rows that do not exist hold zeros, and with eps = 0 would give 0 * inf
-          const float r = h + row < H ? rsqrtf(sq * (1.0f / D) + p.eps) : 0.f;
-          const float coef = dot * (1.0f / D) * r * r;
-          float dx[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dx[i] = r * (g[i] * w[i] - x[i] * coef);
-            acc[i] = fmaf(g[i] * x[i], r, acc[i]);
-          }
-          if (h + row < H) store_row(db + ct * dx_ts + h * D, ca, cb, rows::pack(dx));
+        for (int i = 0; i < 8; ++i) {
+          const float xg = x[i] * g[i];
+          sq = fmaf(x[i], x[i], sq);
+          dot = fmaf(xg, w[i], dot);
         }
-      }
+        sq = rows::row_sum<kLanes>(sq);
+        dot = rows::row_sum<kLanes>(dot);
+        // rows that do not exist hold zeros, and with eps = 0 would give 0 * inf
+        const float r = h < H ? rsqrtf(sq * (1.0f / D) + p.eps) : 0.f;
+        const float coef = dot * (1.0f / D) * r * r;
+        float dx[8];
 #pragma unroll
-      for (int u = 0; u < kBwdSteps; ++u) xv[u] = nx[u], gv[u] = ng[u];
-      if (last) break;
+        for (int i = 0; i < 8; ++i) {
+          dx[i] = r * (g[i] * w[i] - x[i] * coef);
+          acc[i] = fmaf(g[i] * x[i], r, acc[i]);
+        }
+        if (h < H) store_row(db + t * dx_ts + h * D, ca, cb, rows::pack(dx));
+      }
     }
+    from = from == kStages - 1 ? 0 : from + 1;
+    fresh = use.next();
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

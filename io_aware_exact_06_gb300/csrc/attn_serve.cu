@@ -52,6 +52,25 @@ int launch(void (*kernel)(KArgs...), int64_t grid, int threads, int smem, cudaSt
   return e == cudaSuccess ? ATTN_OK : attn_host::lib_cuda_fail(e);
 }
 
+// Raises the dynamic shared-memory limit of a kernel, once per device.  Call
+// with the library lock held.
+int allow_smem(const void* kernel, int bytes) {
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  if (done.count({dev, kernel})) return ATTN_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  done.insert({dev, kernel});
+  return ATTN_OK;
+}
+
+int allow_smem_locked(const void* kernel, int bytes) {
+  std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
+  return allow_smem(kernel, bytes);
+}
+
 // ------------------------------------------------------------ norm, rotation --
 int check_rows(const void* x, int64_t stride, int H, int d) {
   if (H == 0) return ATTN_OK;
@@ -241,20 +260,6 @@ int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len,
   return ATTN_OK;
 }
 
-// Raises the dynamic shared-memory limit of a kernel, once per device.  Call
-// with the library lock held.
-int allow_smem(const void* kernel, int bytes) {
-  static std::set<std::pair<int, const void*>> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  if (done.count({dev, kernel})) return ATTN_OK;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  done.insert({dev, kernel});
-  return ATTN_OK;
-}
-
 template <int D, bool kCodes>
 int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                 int64_t grid, int64_t join, cudaStream_t s) {
@@ -295,8 +300,7 @@ extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
   const int64_t chunks = chunks_of(Hq + Hk, d, attn::norm::kSteps);
   p.run = run_of(T * chunks, chunks, 3 * attn::norm::kWarps);
   const int64_t items = T * ((chunks + p.run - 1) / p.run);
-  const int64_t grid = (items + attn::norm::kWarps - 1) / attn::norm::kWarps;
-  if (grid > INT32_MAX) return ATTN_ERR_SHAPE;
+  const int64_t grid = std::min<int64_t>((items + attn::norm::kWarps - 1) / attn::norm::kWarps, 3 * kPlanSms);
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -317,7 +321,8 @@ extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
                                               : attn::norm::norm_rope_kernel<64, false>
                 : rotary->interleaved ? attn::norm::norm_rope_kernel<128, true>
                                       : attn::norm::norm_rope_kernel<128, false>;
-  return launch(kernel, grid, attn::norm::kThreads, 0, s, p);
+  if ((st = allow_smem_locked(reinterpret_cast<const void*>(kernel), attn::norm::kSmem)) != ATTN_OK) return st;
+  return launch(kernel, grid, attn::norm::kThreads, attn::norm::kSmem, s, p);
 }
 
 extern "C" size_t attn_qk_norm_rope_bwd_workspace(int T, int Hq, int Hk, int d) {
@@ -380,7 +385,8 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
                                                 : attn::norm::norm_rope_bwd_kernel<64, false>
                   : rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<128, true>
                                         : attn::norm::norm_rope_bwd_kernel<128, false>;
-    if ((st = launch(kernel, grid, attn::norm::kThreads, 0, s, p)) != ATTN_OK) return st;
+    if ((st = allow_smem_locked(reinterpret_cast<const void*>(kernel), attn::norm::kSmem)) != ATTN_OK) return st;
+    if ((st = launch(kernel, grid, attn::norm::kThreads, attn::norm::kSmem, s, p)) != ATTN_OK) return st;
   }
   const attn::norm::WeightSum w{static_cast<const float*>(workspace), Hq ? dwq : nullptr,
                                 Hk ? dwk : nullptr, (int)pl.ctas[0], (int)pl.ctas[1], d};
@@ -437,7 +443,7 @@ extern "C" int attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
   if (!aligned(cu_seqlens, 4)) return ATTN_ERR_ALIGN;
   const bool codes = cache->k_scale != nullptr;
   attn::cache::Read p{};
-  const int64_t chunks = 2 * chunks_of(cache->H, cache->d, attn::cache::kSteps * (codes ? 2 : 1));
+  const int64_t chunks = 2 * chunks_of(cache->H, cache->d, attn::cache::kSteps);
   const int run = run_of(total * chunks, kMaxRun, 4 * attn::cache::kWarps);
   p.step = (total - 1) / run + 1;
   const int64_t items = p.step * chunks;
