@@ -6,8 +6,9 @@
 // together so sweep the packed rows in order, which DRAM serves faster than as
 // many streams as there are warps.  d / 8 lanes
 // hold a row, eight channels each: 16 bytes of bf16, 8 bytes of codes.  Writing,
-// the row maximum is a shuffle reduction in bf16.  (Reading 16 codes a lane makes
-// each 16-byte store fill half a sector: 122 us for 612 MB against  Every byte moves once, so HBM bounds both (launch latency for a few
+// the row maximum is a shuffle reduction in bf16.  (With 16 codes a lane each 16-byte
+// store fills half a sector: 113 us for the 612 MB of reading back a batch of
+// eight, 99.7 with eight.)  Every byte moves once, so HBM bounds both (launch latency for a few
 // tokens: runs of one).
 #pragma once
 

@@ -64,6 +64,52 @@ struct Bwd {
   int* err;
 };
 
+// Two fp32 values in a 64-bit register and the packed instructions on them: half
+// the issue slots of a row's arithmetic, which bounds the gradient.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void parts(Two x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two swapped(Two x) {
+  float lo, hi;
+  parts(x, lo, hi);
+  return two(hi, lo);
+}
+// Two bf16 (a word) as fp32, and back with one rounding.
+__device__ __forceinline__ Two wide(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t narrow(Two x) {
+  float lo, hi;
+  parts(x, lo, hi);
+  return rows::pack2(lo, hi);
+}
+// A lane's eight channels as four pairs.
+__device__ __forceinline__ void wide(const uint4& v, Two (&y)[4]) {
+  y[0] = wide(v.x), y[1] = wide(v.y), y[2] = wide(v.z), y[3] = wide(v.w);
+}
+__device__ __forceinline__ uint4 narrow(const Two (&y)[4]) {
+  return make_uint4(narrow(y[0]), narrow(y[1]), narrow(y[2]), narrow(y[3]));
+}
+
 // The first channels of lane `slice`'s two groups.
 template <bool kInter>
 __device__ __forceinline__ void lane_channels(int half, int slice, int& a, int& b) {
@@ -124,17 +170,40 @@ __device__ __forceinline__ bool load_angles(const Rotary& r, int T, int t, int s
   return true;
 }
 
-// y rotated by (c, s), or by its inverse with kBack.
+// A lane's rotation: the factors of y and of the other channel of its pair.
+// Half-split, pair i of channels (i, i + 4): own[i / 2], other[i / 2] hold two
+// pairs; interleaved, (2 i, 2 i + 1): own[i], other[i] hold (c, c) and (-s, s).
+// kBack turns the other way.
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void rotate(float (&y)[8], const float (&c)[4], const float (&s)[4]) {
+struct Turn {
+  Two own[kInter ? 4 : 2], other[kInter ? 4 : 2];
+  __device__ __forceinline__ void set(const float (&c)[4], const float (&s0)[4]) {
+    float s[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 4;
-    const float a = y[ia], b = y[ib], si = kBack ? -s[i] : s[i];
-    y[ia] = a * c[i] - b * si;
-    y[ib] = b * c[i] + a * si;
+    for (int i = 0; i < 4; ++i) s[i] = kBack ? -s0[i] : s0[i];
+    if (kInter) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = two(c[i], c[i]), other[i] = two(-s[i], s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) own[i] = two(c[2 * i], c[2 * i + 1]), other[i] = two(s[2 * i], s[2 * i + 1]);
+    }
   }
-}
+  __device__ __forceinline__ void turn(Two (&y)[4]) const {
+    if (kInter) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = fma2(swapped(y[i]), other[i], mul2(y[i], own[i]));
+    } else {
+      const Two minus = two(-1.f, -1.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Two a = y[i], b = y[i + 2], bs = mul2(b, other[i]);
+        y[i] = fma2(a, own[i], mul2(bs, minus));
+        y[i + 2] = fma2(b, own[i], mul2(a, other[i]));
+      }
+    }
+  }
+};
 
 // 8 bytes from global to shared memory; zeros where `there` is false.
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool there) {
@@ -221,13 +290,15 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
   if (p.Hq) wq = load_row(p.wq, ca, cb);
   if (p.Hk) wk = load_row(p.wk, ca, cb);
-  float c[4], s[4];
+  Turn<kInter, false> turn;
   bool ok = false, fresh = true;
   int from = 0;
   while (use.more()) {
     const int t = use.t, ch = use.ch;
     if (fresh) {  // the same for the whole warp: one token
+      float c[4], s[4];
       ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
+      turn.set(c, s);
       if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
     }
     copies_wait();
@@ -239,17 +310,19 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
       for (int u = 0; u < kSteps; ++u) {
         const int h = ch * kChunk + u * kRows + row;
         const bool isq = h < p.Hq;
-        float y[8], w[8];
-        rows::unpack(lane_load(mine + (from * kSteps + u) * 512), y);
-        rows::unpack(isq ? wq : wk, w);
-        float sq = 0.f;
+        Two y[4], w[4];
+        wide(lane_load(mine + (from * kSteps + u) * 512), y);
+        wide(isq ? wq : wk, w);
+        Two sq2 = mul2(y[0], y[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-        const float r = rsqrtf(rows::row_sum<kLanes>(sq) * (1.0f / D) + p.eps);
+        for (int i = 1; i < 4; ++i) sq2 = fma2(y[i], y[i], sq2);
+        float sq, hi;
+        parts(sq2, sq, hi);
+        const float r = rsqrtf(rows::row_sum<kLanes>(sq + hi) * (1.0f / D) + p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-        rotate<kInter, false>(y, c, s);
-        if (h < H) store_row(isq ? qd + h * D : kd + (h - p.Hq) * D, ca, cb, rows::pack(y));
+        for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], two(r, r)), w[i]);
+        turn.turn(y);
+        if (h < H) store_row(isq ? qd + h * D : kd + (h - p.Hq) * D, ca, cb, narrow(y));
       }
     }
     from = from == kStages - 1 ? 0 : from + 1;
@@ -314,17 +387,19 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
   };
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) feed();
-  float acc[8], w[8];
-  rows::unpack(load_row(p.w[kind], ca, cb), w);
+  Two acc[4], w[4];
+  wide(load_row(p.w[kind], ca, cb), w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  float c[4], s[4];
+  for (int i = 0; i < 4; ++i) acc[i] = two(0.f, 0.f);
+  Turn<kInter, true> turn;
   bool ok = false, fresh = true;
   int from = 0;
   while (use.more()) {
     const int t = use.t, ch = use.ch;
     if (fresh) {
+      float c[4], s[4];
       ok = load_angles<kInter>(p.rot, p.T, t, slice, c, s);
+      turn.set(c, s);
       if (!ok && lane == 0) atomicOr(p.err, rows::kBadIndex);
     }
     copies_wait();
@@ -334,39 +409,54 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
       for (int u = 0; u < kBwdSteps; ++u) {
         const int h = ch * kChunk + u * kRows + row;
         const uint32_t at = mine + (from * kBwdSteps + u) * 1024;
-        float x[8], g[8];
-        rows::unpack(lane_load(at), x);
-        rows::unpack(lane_load(at + 512), g);
-        rotate<kInter, true>(g, c, s);
-        float sq = 0.f, dot = 0.f;
+        Two x[4], g[4];
+        wide(lane_load(at), x);
+        wide(lane_load(at + 512), g);
+        turn.turn(g);
+        Two sq2 = mul2(x[0], x[0]), xg[4], dot2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xg = x[i] * g[i];
-          sq = fmaf(x[i], x[i], sq);
-          dot = fmaf(xg, w[i], dot);
+        for (int i = 0; i < 4; ++i) {
+          xg[i] = mul2(x[i], g[i]);
+          if (i) sq2 = fma2(x[i], x[i], sq2);
+          dot2 = i ? fma2(xg[i], w[i], dot2) : mul2(xg[i], w[i]);
         }
-        sq = rows::row_sum<kLanes>(sq);
-        dot = rows::row_sum<kLanes>(dot);
+        float sa, sb, da, db2;
+        parts(sq2, sa, sb);
+        parts(dot2, da, db2);
+        Two sums = two(sa + sb, da + db2);
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) {
+          float a, b;
+          parts(sums, a, b);
+          sums = add2(sums, two(__shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, b, off)));
+        }
+        float sq, dot;
+        parts(sums, sq, dot);
         // rows that do not exist hold zeros, and with eps = 0 would give 0 * inf
         const float r = h < H ? rsqrtf(sq * (1.0f / D) + p.eps) : 0.f;
-        const float coef = dot * (1.0f / D) * r * r;
-        float dx[8];
+        const float coef = -dot * (1.0f / D) * r * r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dx[i] = r * (g[i] * w[i] - x[i] * coef);
-          acc[i] = fmaf(g[i] * x[i], r, acc[i]);
+        for (int i = 0; i < 4; ++i) {
+          acc[i] = fma2(xg[i], two(r, r), acc[i]);
+          x[i] = mul2(fma2(x[i], two(coef, coef), mul2(g[i], w[i])), two(r, r));
         }
-        if (h < H) store_row(db + t * dx_ts + h * D, ca, cb, rows::pack(dx));
+        if (h < H) store_row(db + t * dx_ts + h * D, ca, cb, narrow(x));
       }
     }
     from = from == kStages - 1 ? 0 : from + 1;
     fresh = use.next();
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    parts(acc[i], a, b);
 #pragma unroll
-    for (int off = kLanes; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-    if (row == 0) sm[warp][(i < 4 ? ca : cb) + i % 4] = acc[i];
+    for (int off = kLanes; off < 32; off <<= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, off);
+      b += __shfl_xor_sync(0xffffffffu, b, off);
+    }
+    const int ch = (i < 2 ? ca : cb) + 2 * (i & 1);
+    if (row == 0) sm[warp][ch] = a, sm[warp][ch + 1] = b;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += kThreads) {
