@@ -20,7 +20,7 @@
 #include "attn_host.h"
 #include "attn_norm_kernel.cuh"
 #include "attn_tree_few_kernel.cuh"
-#include "attn_tree_kernel.cuh"
+#include "attn_tree_tile_kernel.cuh"
 
 namespace {
 
@@ -191,65 +191,45 @@ attn::cache::Pages pages_of(const attn_paged_cache* c) {
 
 // ---------------------------------------------------------------------- tree --
 struct Plan {
-  int rows;               // query rows of a CTA: 8 or 16 (few rows), 32 or 64
-  int mtiles, chunk, S;   // 32 or 64: key ranges
-  attn::tree::Work work;  // 8 or 16: the line of tiles
+  int rows;  // query rows of a segment: 8 or 16 (few rows), 128
+  attn::tree::Work work;
   int64_t ctas;
   int64_t slots;  // parts in the workspace, `rows` rows each
   bool many;      // eight warps join a row's pieces
-  bool fits = true;  // the line's tiles are a 32-bit number
+  bool fits;      // the line's tiles are a 32-bit number
 };
 
 bool few(const Plan& pl) { return pl.rows <= 16; }
 
-// Query rows of a CTA: the smallest tile that holds max_new * G of them.  Few
-// rows: as many persistent warps as fit the SMs (num_splits caps the pieces of a
-// segment instead).  More rows: key ranges.
+// Query rows of a segment: the smallest tile that holds max_new * G of them.
+// Few rows: as many persistent warps as fit the SMs; more: a persistent CTA an SM
+// with tcgen05 products.  num_splits caps the pieces of a segment instead.
 Plan tree_plan(int B, int total, int Hq, int H, int max_new, int max_len, int num_splits) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
-  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  pl.mtiles = (int)((M + pl.rows - 1) / pl.rows);
-  const int64_t len = std::max(max_len, 1);
-  const int64_t segments = (int64_t)B * H * pl.mtiles;
-  if (few(pl)) {
-    const int64_t T = attn::tree::kFewTile, tiles = (len + T - 1) / T;
-    const int heads = H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // to a unit, one a warp
-    const int64_t groups = segments / heads;
-    pl.work.rows = pl.rows;
-    pl.work.heads = heads;
-    pl.work.log_tile = attn::tree::kLogFewTile;
-    pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
-    const int64_t per_cta = attn::tree::kWarps / heads;
-    const int64_t most = (int64_t)std::min((double)groups * (double)tiles / pl.work.min_share + 1, 1e9);
-    pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * attn::tree::kFewCtas);
-    pl.work.units = (int)(pl.ctas * per_cta);
-    pl.slots = 2 * (int64_t)pl.work.units * heads;
-    // eight warps to a row where segments are cut into many pieces, and where the
-    // rows leave the SMs idle anyway
-    pl.many = pl.work.units > 32 * groups || (int64_t)total * Hq <= 8 * kPlanSms;
-    pl.fits = (double)groups * (double)tiles <= INT32_MAX;
-    return pl;
-  }
-  const int64_t T = attn::tree::kTile;
-  int64_t chunk;
-  if (num_splits > 0)
-    chunk = (len + num_splits - 1) / num_splits;
-  else
-    chunk = std::max<int64_t>(
-        {128, (int64_t)std::min(1e9, (double)len * (double)segments / (kPlanSms * 6)), (len + 255) / 256});
-  chunk = std::min((chunk + T - 1) / T * T, (len + T - 1) / T * T);
-  pl.chunk = (int)chunk;
-  pl.S = (int)((len + chunk - 1) / chunk);
+  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : attn::tree::kBigRows;
+  const int64_t T = few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile;
+  const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
+  const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
+  const int64_t segments = (int64_t)B * (H / heads) * ((M + pl.rows - 1) / pl.rows);
+  const int per_cta = few(pl) ? attn::tree::kWarps / heads : 1;
+  pl.work.rows = pl.rows;
+  pl.work.heads = heads;
+  pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
+  pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
+  const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
+  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? attn::tree::kFewCtas : 1));
+  pl.work.units = (int)(pl.ctas * per_cta);
+  pl.slots = 2 * (int64_t)pl.work.units * heads;
+  // eight warps to a row where segments are cut into many pieces, and where the
+  // rows leave the SMs idle anyway
+  pl.many = pl.work.units > 32 * segments || (int64_t)total * Hq <= 8 * kPlanSms;
+  pl.fits = (double)segments * (double)tiles <= INT32_MAX;
   return pl;
 }
 
-size_t tree_rows(const Plan& pl, int total, int Hq) {
-  return few(pl) ? (size_t)pl.slots * pl.rows : pl.S == 1 ? 0 : (size_t)pl.S * total * Hq;
-}
-size_t tree_bytes(const Plan& pl, int total, int Hq, int d) {
-  return tree_rows(pl, total, Hq) * (d + 1) * sizeof(float);
-}
+size_t tree_rows(const Plan& pl) { return (size_t)pl.slots * pl.rows; }
+size_t tree_bytes(const Plan& pl, int d) { return tree_rows(pl) * (d + 1) * sizeof(float); }
 
 int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
   if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
@@ -262,22 +242,21 @@ int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len,
 
 template <int D, bool kCodes>
 int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
-                int64_t grid, int64_t join, cudaStream_t s) {
+                cudaStream_t s) {
   using namespace attn::tree;
-  int st;
-  if (few(pl)) {
-    auto kernel = pl.rows == 8 ? tree_few_kernel<D, kCodes, 1> : tree_few_kernel<D, kCodes, 2>;
-    const int smem = pl.rows == 8 ? FewCfg<D, kCodes, 1>::kSmem : FewCfg<D, kCodes, 2>::kSmem;
-    if ((st = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != ATTN_OK) return st;
-    if ((st = launch(kernel, pl.ctas, kFewThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK) return st;
-    return pl.many ? launch(tree_join_kernel<D, 8>, (int64_t)p.total * p.Hq, 256, 0, s, p, pl.work)
-                   : launch(tree_join_kernel<D, 1>, join, 256, 0, s, p, pl.work);
-  }
-  auto kernel = pl.rows == 32 ? tree_kernel<D, kCodes, 2> : tree_kernel<D, kCodes, 4>;
-  constexpr int kSmem = Cfg<D, kCodes>::kSmem;
-  if ((st = allow_smem(reinterpret_cast<const void*>(kernel), kSmem)) != ATTN_OK) return st;
-  if ((st = launch(kernel, grid, kThreads, kSmem, s, mk, mv, p)) != ATTN_OK || pl.S == 1) return st;
-  return launch(tree_combine_kernel<D>, join, 256, 0, s, p);
+  auto kernel = pl.rows == 8    ? tree_few_kernel<D, kCodes, 1>
+                : pl.rows == 16 ? tree_few_kernel<D, kCodes, 2>
+                                : tree_tile_kernel<D, kCodes>;
+  const int smem = pl.rows == 8    ? FewCfg<D, kCodes, 1>::kSmem
+                   : pl.rows == 16 ? FewCfg<D, kCodes, 2>::kSmem
+                                   : BigCfg<D, kCodes>::kSmem;
+  int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (st != ATTN_OK) return st;
+  if ((st = launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK)
+    return st;
+  const int64_t rows = (int64_t)p.total * p.Hq;
+  return pl.many ? launch(tree_join_kernel<D, 8>, rows, 256, 0, s, p, pl.work)
+                 : launch(tree_join_kernel<D, 1>, (rows + 7) / 8, 256, 0, s, p, pl.work);
 }
 
 }  // namespace
@@ -468,7 +447,7 @@ extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d
                                           int max_len, int num_splits) {
   if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
   if (B == 0 || total == 0 || max_new == 0) return 0;
-  return tree_bytes(tree_plan(B, total, Hq, H, max_new, max_len, num_splits), total, Hq, d);
+  return tree_bytes(tree_plan(B, total, Hq, H, max_new, max_len, num_splits), d);
 }
 
 extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
@@ -490,15 +469,12 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
     return ATTN_ERR_ALIGN;
   const Plan pl = tree_plan(B, total, Hq, cache->H, max_new, max_len, num_splits);
   if (!pl.fits) return ATTN_ERR_SHAPE;
-  const size_t need = tree_bytes(pl, total, Hq, d);
-  if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_SCRATCH;
-  const double ctas = (double)B * std::max(pl.S, 1) * cache->H * pl.mtiles;
-  const int64_t combine = ((int64_t)total * Hq + 7) / 8;
-  if (ctas > INT32_MAX || (int64_t)total * Hq > INT32_MAX) return ATTN_ERR_SHAPE;
-  const int64_t grid = (int64_t)B * pl.S * cache->H * pl.mtiles;
+  const size_t need = tree_bytes(pl, d);
+  if (!workspace || workspace_bytes < need) return ATTN_ERR_SCRATCH;
+  if ((int64_t)total * Hq > INT32_MAX) return ATTN_ERR_SHAPE;
   const bool codes = cache->k_scale != nullptr;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
-  const int box = std::min(cache->page_size, few(pl) ? attn::tree::kFewTile : attn::tree::kTile);
+  const int box = std::min(cache->page_size, few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile);
 
   const attn::cache::Pages pg = pages_of(cache);
   attn::tree::Params p{};
@@ -514,7 +490,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = need ? p.o_part + tree_rows(pl, total, Hq) * d : nullptr;
+  p.lse_part = p.o_part + tree_rows(pl) * d;
   p.B = B;
   p.total = total;
   p.Hq = Hq;
@@ -525,9 +501,6 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   p.log_page = pg.log_page;
   p.max_new = max_new;
   p.max_len = max_len;
-  p.chunk = pl.chunk;
-  p.S = pl.S;
-  p.mtiles = pl.mtiles;
   // scale 0 weighs every key alike; the smallest normal factor does, without 0 * inf
   p.c = (float)std::max((double)scale * 1.4426950408889634, (double)FLT_MIN);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -537,8 +510,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   CUtensorMap mk, mv;
   if ((st = attn_host::lib_make_cache_map(&mk, cache->k, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
   if ((st = attn_host::lib_make_cache_map(&mv, cache->v, rows, cache->H, d, codes, box)) != ATTN_OK) return st;
-  return d == 64 ? codes ? launch_tree<64, true>(pl, mk, mv, p, grid, combine, s)
-                         : launch_tree<64, false>(pl, mk, mv, p, grid, combine, s)
-         : codes ? launch_tree<128, true>(pl, mk, mv, p, grid, combine, s)
-                 : launch_tree<128, false>(pl, mk, mv, p, grid, combine, s);
+  return d == 64 ? codes ? launch_tree<64, true>(pl, mk, mv, p, s) : launch_tree<64, false>(pl, mk, mv, p, s)
+         : codes ? launch_tree<128, true>(pl, mk, mv, p, s)
+                 : launch_tree<128, false>(pl, mk, mv, p, s);
 }

@@ -1,6 +1,7 @@
 // Attention of the newest tokens over the paged cache for few query rows of a key
-// head, on the warp-level tensor instructions (see attn_tree_kernel.cuh for what
-// is computed and how codes and scales enter).
+// head, on the warp-level tensor instructions.  Codes become fp16 in registers; a
+// query row is divided by a power of two that brings its largest channel into
+// [1, 2), which keeps its bf16 values exact in fp16 down to 2^-14 of that.
 #pragma once
 
 #include "attn_tree_work.cuh"
@@ -26,6 +27,7 @@ namespace tree {
 // sequences of 8 heads against 5.4 TB/s on the same bytes with one head.  A
 // producer warp for the CTA instead spent about 1000 cycles on a 32-key tile's
 // issue, against 365 that HBM needs for the tiles of three CTAs.)
+constexpr int kWarps = 4;     // of a CTA
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
@@ -45,14 +47,6 @@ struct FewCfg : Row<D, kCodes> {
   static constexpr int kTurnBytes = kWarps * 8 * kNT * kPad * 4;
   static constexpr int kSmem = kRing + kStages * 2 * kScaleBytes + kTurnBytes + 1024;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// One arrive on the barrier once this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;

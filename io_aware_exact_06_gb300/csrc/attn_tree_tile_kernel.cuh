@@ -1,0 +1,769 @@
+// Attention of the newest tokens over the paged cache for many query rows of a
+// key head (a tree of drafts times the heads of a group), on the tensor cores'
+// tcgen05 products.
+//
+// A segment is (sequence, key head, tile of 128 query rows); persistent CTAs, one
+// an SM, take equal shares of the line of 128-key tiles.  A key tile costs the
+// tensor core 1024 cycles (S = Q K^T and O += P V, 128 x 128 x d each) whatever
+// part of the 128 rows is real, below the 1410 cycles that its e4m3 bytes (2820:
+// bf16) take from HBM; with several row tiles of one head the key tiles come from
+// L2 and the products and the softmax bound it.
+//
+// Warps: 0-3 and 4-7 softmax groups A and B (a thread owns a row; A takes the
+// even key tiles of a segment, B the odd ones, each with its own S and O in TMEM,
+// so that one group's softmax runs beside the other's products; they meet at the
+// segment's end); 8-11 operands: they write the segment's Q tile, turn a tile's
+// codes of V into fp16 and its scales into the factors the softmax needs, and
+// clean values that rows may not see; 12 TMA producer; 13 MMA issuer.
+//
+// With e4m3 codes S = (Q_hi + Q_lo) K^T takes the codes of K as they lie in the
+// cache: a query row, scaled by a power of two to at most 256, is the sum of two
+// e4m3 values (4 + 4 significant bits hold bf16's 8 exactly, down to 2^-11 of the
+// row's largest channel, where the quantum 2^-9 of the small part ends it: an
+// error below 2^-18 of the largest), and the two e4m3 products cost what one fp16
+// product does.  P V takes fp16 (V's codes are exact in it, P is rounded to
+// 2^-11), with the value scale in P and the running maximum over log2(p * value
+// scale), as for few rows.
+#pragma once
+
+#include "attn_tree_work.cuh"
+
+namespace attn {
+namespace tree {
+
+constexpr int kBigTile = 128;  // keys
+constexpr int kLogBigTile = 7;
+constexpr int kBigRows = 128;
+constexpr int kBigThreads = 512;
+// registers after setmaxnreg; 128 threads each: two softmax groups, operands, the
+// rest.  Their sum is the launch's 512 x 128.
+constexpr int kSoftmaxRegs = 192, kOperandRegs = 80, kRestRegs = 48;
+constexpr int kRing = 8;  // segments whose flags are kept
+
+template <int D, bool kCodes>
+struct BigCfg : Row<D, kCodes> {
+  using Row<D, kCodes>::kRowBytes;
+  static constexpr int kMat = kBigTile * kRowBytes;             // K or V of a tile, as in the cache
+  static constexpr int kChunk = kBigTile * 128;                 // 128 rows of 128 bytes
+  static constexpr int kConv = kCodes ? kBigTile * D * 2 : 0;   // V in fp16
+  static constexpr int kQ = kBigRows * D * 2;                   // bf16, or the two e4m3 parts
+  static constexpr int kK = kCodes || D == 64 ? 4 : 3;          // stages
+  static constexpr int kV = kCodes ? (D == 128 ? 3 : 4) : D == 64 ? 4 : 2;
+  static constexpr int kReady = kCodes ? 2 : kV;                // V operand buffers
+  static constexpr int kMeta = kCodes ? 4 : 1;                  // tiles whose factors are kept
+  static constexpr int kOffK = kQ;
+  static constexpr int kOffV = kOffK + kK * kMat;
+  static constexpr int kOffC = kOffV + kV * kMat;
+  static constexpr int kOffScale = kOffC + kReady * kConv;            // [kK][2][128] raw scales
+  static constexpr int kOffMeta = kOffScale + (kCodes ? kK * 1024 : 0);  // [kMeta][3][128]
+  static constexpr int kSmem = kOffMeta + (kCodes ? kMeta * 1536 : 0) + 1024;
+  static_assert(kSmem + 6 * 1024 <= 227 * 1024, "shared memory");
+  // barriers
+  static constexpr int bKF = 0, bKE = bKF + kK, bVF = bKE + kK, bVE = bVF + kV, bRF = bVE + kV, bRE = bRF + kReady,
+                       bMF = bRE + kReady, bME = bMF + kMeta, bSF = bME + kMeta, bPF = bSF + 2, bOF = bPF + 2,
+                       bQF = bOF + 2, bQE = bQF + 1, bOFree = bQE + 1, bDrain = bOFree + 1, kBars = bDrain + 1;
+};
+
+// kind::f16 with fp16 A and B (formats 0), fp32 D; B MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_mn(uint32_t M, uint32_t N) {
+  return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// kind::f8f6f4 with e4m3 A and B (formats 0), fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Packed fp32 pairs.
+__device__ __forceinline__ void pmul(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y, r;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 r, x, y;\n mov.b64 {%0, %1}, r;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void padd(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y, r;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 r, x, y;\n mov.b64 {%0, %1}, r;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+// (d0, d1) = (a0, a1) * b + (c0, c1)
+__device__ __forceinline__ void pfma(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+  asm("{\n .reg .b64 x, y, z, r;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %6};\n"
+      " fma.rn.f32x2 r, x, y, z;\n mov.b64 {%0, %1}, r;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct BigShared {
+  uint64_t bars[48];
+  uint32_t tmem;
+  int abort;                    // a wait ran out
+  int bad[kRing];               // the segment reads a page outside the cache
+  uint32_t hidden[kRing][2];    // its new tokens with values that are not finite
+  float2 ml[2][2][kBigRows];    // [segment's parity][group]: maxima and sums
+  float rc[2][kBigRows];        // [segment's parity]: log2 units of a row's raw score
+};
+
+template <int D, bool kCodes>
+struct Big {
+  using C = BigCfg<D, kCodes>;
+  const Params& p;
+  const Work& w;
+  BigShared& ss;
+  uint32_t smem;  // 1024-byte aligned
+  uint32_t tmem;
+
+  __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&ss.bars[i]); }
+  // Bounded; once one wait has run out nothing waits any more, every role goes
+  // through its loops to the end, and the rows come out as NaN.
+  __device__ __forceinline__ void wait(int i, uint32_t parity) const {
+    volatile int* abort = &ss.abort;
+    if (*abort) return;
+    if (!mbar_wait(bar(i), parity, kWaitNs)) {
+      *abort = 1;
+      atomicOr(p.err, kTimedOut);
+    }
+  }
+  __device__ __forceinline__ bool aborted() const { return *(volatile int*)&ss.abort != 0; }
+  __device__ __forceinline__ int head(const Walk& k) const { return k.seg / (k.segs / p.H); }
+  __device__ __forceinline__ int row0(const Walk& k) const { return k.seg % (k.segs / p.H) * kBigRows; }
+
+  // ------------------------------------------------------------- producer --
+  __device__ __forceinline__ void produce(Walk k, const CUtensorMap* mk, const CUtensorMap* mv) {
+    const int lane = threadIdx.x % 32;
+    const int page = 1 << p.log_page;
+    const int box = min(page, kBigTile), per = kBigTile / box;  // rows of a copy, copies of a tile
+    const int batch = 32 / per;  // tiles whose page numbers one load fetches
+    int ks = 0, kr = 0, vs = 0, vr = 0, seg = 0;
+    do {
+      const int h = head(k), len = k.s.len, end = k.tile + k.piece();
+      const int* table = p.table + (int64_t)k.b * p.stride;
+      auto fetch = [&](int tile) {
+        const int64_t pos = (int64_t)tile * kBigTile + lane * box;
+        return pos < len ? table[pos >> p.log_page] : 0;
+      };
+      int ids = fetch(k.tile);
+      for (int t0 = k.tile; t0 < end; t0 += batch) {
+        const int next = t0 + batch < end ? fetch(t0 + batch) : 0;
+        const bool wrong = (unsigned)ids >= (unsigned)p.pages;
+        if (wrong) ids = 0;
+        const uint32_t wrongs = __ballot_sync(0xffffffffu, wrong);
+        for (int t = t0; t < min(t0 + batch, end); ++t) {
+          const int key0 = t * kBigTile, n = min(per, (len - key0 + box - 1) / box);
+          const int id = __shfl_sync(0xffffffffu, ids, (t - t0) * per + lane % per);
+          const int row = (id << p.log_page) + ((key0 + lane * box) & (page - 1));
+          const uint32_t mine = per == 32 ? 0xffffffffu : ((1u << per) - 1) << ((t - t0) * per);
+          constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
+          if (kr > 0) wait(C::bKE + ks, (kr & 1) ^ 1);
+          __syncwarp();
+          const bool stop = __any_sync(0xffffffffu, aborted());
+          if (!stop) {
+            if (lane == 0) {
+              if (wrongs & mine) {
+                ss.bad[seg % kRing] = 1;
+                atomicOr(p.err, rows::kBadIndex);
+              }
+              mbar_arrive_expect_tx(bar(C::bKF + ks), n * box * C::kRowBytes);
+            }
+            __syncwarp();
+            const uint32_t dst = smem + C::kOffK + ks * C::kMat + lane * box * C::kBox;
+            if (lane < n)
+#pragma unroll
+              for (int f = 0; f < C::kHalves; ++f)
+                tma_load_3d(dst + f * kBigTile * C::kBox, mk, bar(C::bKF + ks), f * kElems, h, row);
+            if (kCodes) {  // each lane: four key scales and four value scales
+              const int key = key0 + 4 * lane;
+              const int sid = __shfl_sync(0xffffffffu, id, 4 * lane / box);
+              if (key < len) {
+                const int64_t at = (((int64_t)sid * p.H + h) << p.log_page) + (key & (page - 1));
+                const uint32_t sd = smem + C::kOffScale + ks * 1024 + 16 * lane;
+                cp_async16(sd, p.kscale + at);
+                cp_async16(sd + 512, p.vscale + at);
+              }
+              cp_async_arrive(bar(C::bKF + ks));
+            }
+          }
+          if (++ks == C::kK) ks = 0, ++kr;
+          if (vr > 0) wait(C::bVE + vs, (vr & 1) ^ 1);
+          __syncwarp();
+          if (!__any_sync(0xffffffffu, aborted())) {
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::bVF + vs), n * box * C::kRowBytes);
+            __syncwarp();
+            const uint32_t dst = smem + C::kOffV + vs * C::kMat + lane * box * C::kBox;
+            if (lane < n)
+#pragma unroll
+              for (int f = 0; f < C::kHalves; ++f)
+                tma_load_3d(dst + f * kBigTile * C::kBox, mv, bar(C::bVF + vs), f * kElems, h, row);
+          }
+          if (++vs == C::kV) vs = 0, ++vr;
+        }
+        ids = next;
+      }
+      ++seg;
+    } while (k.next(p, w));
+    if (kCodes) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+
+  // -------------------------------------------------------------- products --
+  __device__ __forceinline__ void scores(int g, int ks) {
+    const uint32_t k = smem + C::kOffK + ks * C::kMat, d = tmem + 128 * g;
+    if (kCodes) {
+      constexpr uint32_t kSwz = C::kBox == 128 ? 2 : 4;  // 128- or 64-byte swizzle
+      const uint64_t hi = make_sdesc(smem, 16, 8 * C::kBox, kSwz);
+      const uint64_t lo = make_sdesc(smem + kBigRows * C::kBox, 16, 8 * C::kBox, kSwz);
+      const uint64_t b = make_sdesc(k, 16, 8 * C::kBox, kSwz);
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, hi + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, lo + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), 1);
+    } else {
+      const uint64_t a = make_sdesc(smem, 16, 1024, kSwizzle128B), b = make_sdesc(k, 16, 1024, kSwizzle128B);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk / 4) * C::kChunk + (kk % 4) * 32) >> 4);
+        mma_ss(d, a + off, b + off, make_idesc_bf16(128, 128, false), kk > 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void values(int g, int r, bool accumulate) {
+    const uint32_t v = kCodes ? smem + C::kOffC + r * C::kConv : smem + C::kOffV + r * C::kMat;
+    const uint64_t b = make_sdesc(v, C::kChunk, 1024, kSwizzle128B);
+    constexpr uint32_t kI = kCodes ? idesc_f16_mn(128, D) : make_idesc_bf16(128, D, true);
+#pragma unroll
+    for (int kk = 0; kk < kBigTile / 16; ++kk)
+      mma_ts(tmem + 256 + D * g, tmem + 128 * g + 8 * kk, b + (uint64_t)((kk * 2048) >> 4), kI, kk > 0 || accumulate);
+  }
+  // One thread issues every product, in the order of the tiles:
+  // S(0), S(1), then for each tile j its P V and S(j + 2).
+  __device__ __forceinline__ void multiply(Walk k) {
+    int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
+    uint32_t pcount[2] = {0, 0};
+    auto next_scores = [&](int g, bool last) {
+      wait(C::bKF + ks, kr & 1);
+      tc_fence_after();
+      if (!aborted()) {
+        scores(g, ks);
+        mma_commit(bar(C::bSF + g));
+        mma_commit(bar(C::bKE + ks));
+        if (last) mma_commit(bar(C::bQE));
+      }
+      if (++ks == C::kK) ks = 0, ++kr;
+    };
+    do {
+      const int n = k.piece();
+      wait(C::bQF, seg & 1);
+      tc_fence_after();
+      next_scores(0, n == 1);
+      if (n > 1) next_scores(1, n == 2);
+      for (int j = 0; j < n; ++j) {
+        const int g = j & 1;
+        if (j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
+        wait(C::bRF + rs, rr & 1);
+        wait(C::bPF + g, pcount[g]++ & 1);
+        tc_fence_after();
+        if (!aborted()) {
+          values(g, rs, j > 1);
+          mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
+        }
+        if (++rs == C::kReady) rs = 0, ++rr;
+        if (j + 2 < n)
+          next_scores(g, j + 3 == n);
+        else if (!aborted())
+          mma_commit(bar(C::bOF + g));
+      }
+      ++seg;
+    } while (k.next(p, w));
+    mma_commit(bar(C::bDrain));
+    mbar_wait(bar(C::bDrain), 0, 100000000ull);
+  }
+
+  // -------------------------------------------------------------- operands --
+  // This thread's query row of the segment into the Q tile.
+  __device__ __forceinline__ void write_query(const Walk& k, int seg) {
+    const int r = threadIdx.x % 128;
+    const int h = head(k), row = row0(k) + r, M = k.s.n * p.G;
+    const bool live = row < M;
+    const int tok = live ? row / p.G : 0;
+    const __nv_bfloat16* q = p.q + (int64_t)(k.s.q0 + tok) * p.q_ts + (int64_t)(h * p.G + (live ? row - tok * p.G : 0)) * D;
+    if (!kCodes) {
+#pragma unroll 8
+      for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 8 * ch) : make_uint4(0, 0, 0, 0);
+        sts128(smem + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), x.x, x.y, x.z, x.w);
+      }
+    } else {
+      uint32_t top = 0;  // largest magnitude: bf16 bits order like the values
+#pragma unroll 8
+      for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 8 * ch) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+      }
+      int e = (int)(top >> 7) - 127;
+      e = top == 0 ? 0 : min(max(e, -119), 126);
+      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      ss.rc[seg & 1][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+#pragma unroll 2
+      for (int ch = 0; ch < D / 16; ++ch) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 16 * ch + 8 * half) : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hp[4], lp[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(u[i] << 16) * up, b = __uint_as_float(u[i] & 0xffff0000u) * up;
+            hp[i] = e4m3_pair(a, b);
+            const uint32_t back = codes_lo(hp[i]);
+            float ha, hb;
+            asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n cvt.f32.f16 %0, x;\n cvt.f32.f16 %1, y;\n}\n"
+                : "=f"(ha), "=f"(hb)
+                : "r"(back));
+            lp[i] = e4m3_pair(a - ha, b - hb);
+          }
+          hi[2 * half] = hp[0] | hp[1] << 16, hi[2 * half + 1] = hp[2] | hp[3] << 16;
+          lo[2 * half] = lp[0] | lp[1] << 16, lo[2 * half + 1] = lp[2] | lp[3] << 16;
+        }
+        const uint32_t at = smem + swz<C::kBox>(r, ch);
+        sts128(at, hi[0], hi[1], hi[2], hi[3]);
+        sts128(at + kBigRows * C::kBox, lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(bar(C::bQF));
+  }
+
+  __device__ __forceinline__ void prepare(Walk k) {
+    const int r = threadIdx.x % 128, lane = threadIdx.x % 32;  // thread r: key r of a tile
+    int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0;
+    do {
+      if (seg > 0) wait(C::bQE, (seg - 1) & 1);
+      write_query(k, seg);
+      const int len = k.s.len, ctx = len - k.s.n, end = k.tile + k.piece();
+      uint32_t* hidden = ss.hidden[seg % kRing];
+      for (int t = k.tile; t < end; ++t) {
+        const int pos = t * kBigTile + r;
+        bool cut = false;  // the value scale is not finite, for a key that rows may not see
+        if (kCodes) {
+          wait(C::bKF + ks, kr & 1);
+          if (mr > 0) wait(C::bME + ms, (mr & 1) ^ 1);
+          const uint32_t sc = smem + C::kOffScale + ks * 1024 + 4 * r, me = smem + C::kOffMeta + ms * 1536 + 4 * r;
+          const float kscale = __uint_as_float(lds32(sc));
+          float vscale = __uint_as_float(lds32(sc + 512));
+          if (pos >= ctx && !(fabsf(vscale) < INFINITY)) {
+            cut = pos < len;
+            vscale = 0.f;
+          }
+          if (pos >= len) vscale = 0.f;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me), "f"(kscale * p.c) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me + 512), "f"(lg2(fmaxf(vscale, 0x1p-64f))) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me + 1024), "f"(vscale) : "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::bMF + ms));
+            mbar_arrive(bar(C::bKE + ks));
+          }
+          if (++ks == C::kK) ks = 0, ++kr;
+          if (++ms == C::kMeta) ms = 0, ++mr;
+        }
+        wait(C::bVF + vs, vr & 1);
+        const uint32_t v = smem + C::kOffV + vs * C::kMat;
+        bool odd = cut;  // something of this key's row is hidden from the products
+        if (kCodes) {
+          if (rr > 0) wait(C::bRE + rs, (rr & 1) ^ 1);
+          const uint32_t dst = smem + C::kOffC + rs * C::kConv;
+#pragma unroll 4
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const uint4 x = lds128(v + swz<C::kBox>(r, ch));
+            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            if (pos >= ctx) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (pos >= len) u[i] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                  if (((u[i] >> (8 * b)) & 0x7fu) == 0x7fu) u[i] &= ~(0xffu << (8 * b)), odd = true;
+              }
+            }
+            const int o = 2 * ch;  // 16-byte chunk of the fp16 row
+            const uint32_t base = dst + (o / 8) * C::kChunk;
+            sts128(base + swz<128>(r, o % 8), codes_lo(u[0]), codes_hi(u[0]), codes_lo(u[1]), codes_hi(u[1]));
+            sts128(base + swz<128>(r, o % 8 + 1), codes_lo(u[2]), codes_hi(u[2]), codes_lo(u[3]), codes_hi(u[3]));
+          }
+        } else if (pos >= ctx) {
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint32_t at = v + (ch / 8) * C::kChunk + swz<128>(r, ch % 8);
+            const uint4 x = lds128(at);
+            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (pos >= len) u[i] = 0;
+              if ((u[i] & 0x7f80u) == 0x7f80u) u[i] &= 0xffff0000u, odd = true;
+              if ((u[i] & 0x7f800000u) == 0x7f800000u) u[i] &= 0xffffu, odd = true;
+            }
+            sts128(at, u[0], u[1], u[2], u[3]);
+          }
+        }
+        if (odd) atomicOr(hidden + ((pos - ctx) >> 5), 1u << ((pos - ctx) & 31));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::bRF + rs));
+          if (kCodes) mbar_arrive(bar(C::bVE + vs));
+        }
+        if (++vs == C::kV) vs = 0, ++vr;
+        if (++rs == C::kReady) rs = 0, ++rr;
+      }
+      ++seg;
+    } while (k.next(p, w));
+  }
+
+  // --------------------------------------------------------------- softmax --
+  __device__ __forceinline__ void softmax(Walk k, int g) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int r = 32 * (warp % 4) + lane;
+    const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);  // this warp's lanes of TMEM
+    const uint32_t colS = mine + 128 * g;
+    uint32_t scount = 0, ocount[2] = {0, 0};
+    int ms = 0, mr = 0, seg = 0;
+    bool firstp = true;
+    do {
+      const Seq sq = k.s;
+      const int M = sq.n * p.G, ctx = sq.len - sq.n, r0 = row0(k), h = head(k);
+      const int row = r0 + r, n = k.piece();
+      const bool live = row < M, busy = r0 + 32 * (warp % 4) < M;  // the thread; its warp
+      const int tok = live ? row / p.G : 0;
+      const uint64_t word = (live ? mask_word(p.mask, sq.q0 + tok, tok) : 0) &
+                            (sq.n >= 64 ? ~0ull : (1ull << sq.n) - 1);
+      float rc = p.c, m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if ((j & 1) == g) {
+          wait(C::bSF + g, scount++ & 1);
+          tc_fence_after();
+          if (kCodes) wait(C::bMF + ms, mr & 1);
+          if (__any_sync(0xffffffffu, busy)) {
+            if (kCodes && j == g) rc = ss.rc[seg & 1][r];
+            tile(k.tile + j, g, j > 1, ctx, sq.n, word, rc, smem + C::kOffMeta + ms * 1536, mine, colS, m, l);
+          }
+          tc_fence_before();
+          mbar_arrive(bar(C::bPF + g));
+          if (kCodes) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bME + ms));
+          }
+        }
+        if (++ms == C::kMeta) ms = 0, ++mr;
+      }
+      // ------------------------------------------------- the segment's end --
+      wait(C::bOF + 0, ocount[0]++ & 1);
+      if (n > 1) wait(C::bOF + 1, ocount[1]++ & 1);
+      tc_fence_after();
+      close_row(m, l);
+      float2(*ml)[kBigRows] = ss.ml[seg & 1];
+      ml[g][r] = make_float2(m, l);
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      const bool poison = aborted() || *(volatile int*)&ss.bad[seg % kRing];
+      const uint64_t hid = (uint64_t) * (volatile uint32_t*)&ss.hidden[seg % kRing][1] << 32 |
+                           *(volatile uint32_t*)&ss.hidden[seg % kRing][0];
+      if (threadIdx.x == 0) {  // the entry of the segment before, which every thread has read
+        const int old = (seg + kRing - 1) % kRing;
+        ss.bad[old] = 0;
+        ss.hidden[old][0] = ss.hidden[old][1] = 0;
+      }
+      if (__any_sync(0xffffffffu, busy)) {
+        const float2 a = ml[0][r], b = ml[1][r];
+        const float mm = fmaxf(a.x, b.x);
+        const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), wb = b.x == -INFINITY ? 0.f : ex2(b.x - mm);
+        const float ls = (wa != 0.f ? wa * a.y : 0.f) + (wb != 0.f ? wb * b.y : 0.f);
+        const float inv = ls != 0.f ? 1.f / ls : 0.f;
+        const bool whole = k.tile == 0 && n == k.tiles;
+        const int slot = whole ? -1 : 2 * (int)blockIdx.x + !firstp;
+        const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * kBigRows + r;
+        if (live && g == 0) {
+          float lse = ls != 0.f ? (mm + lg2(ls)) * 0.69314718055994531f : -INFINITY;
+          if (poison) lse = whole ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
+          (whole ? p.lse : p.lse_part)[at] = lse;
+        }
+#pragma unroll 1
+        for (int col = g * (D / 2); col < (g + 1) * (D / 2); col += 32) {
+          uint32_t xa[32], xb[32];
+          tmem_ld_x32(mine + 256 + col, xa);
+          tmem_ld_x32(mine + 256 + D + col, xb);
+          tmem_ld_wait_x32(xa);
+          tmem_ld_wait_x32(xb);
+          float f[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            f[i] = (wa != 0.f ? wa * __uint_as_float(xa[i]) : 0.f) + (wb != 0.f ? wb * __uint_as_float(xb[i]) : 0.f);
+            f[i] = inv != 0.f ? f[i] * inv : 0.f;
+            if (poison) f[i] = NAN;
+          }
+          if (live && hid) add_hidden(f, hid & word, k.b, h, ctx, col);
+          if (live && whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(p.o + at * D + col + 8 * i) =
+                  make_uint4(rows::pack2(f[8 * i], f[8 * i + 1]), rows::pack2(f[8 * i + 2], f[8 * i + 3]),
+                             rows::pack2(f[8 * i + 4], f[8 * i + 5]), rows::pack2(f[8 * i + 6], f[8 * i + 7]));
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(p.o_part + at * D + col + 4 * i) =
+                  make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(C::bOFree));
+      firstp = false;
+      ++seg;
+    } while (k.next(p, w));
+  }
+
+  // What cleaning took out of the products, for a row that sees it.
+  __device__ __forceinline__ void add_hidden(float (&f)[32], uint64_t todo, int b, int h, int ctx, int col) {
+    while (todo) {
+      const int t = __ffsll((long long)todo) - 1;
+      todo &= todo - 1;
+      const int pos = ctx + t;
+      const int id = p.table[(int64_t)b * p.stride + (pos >> p.log_page)];
+      if ((unsigned)id >= (unsigned)p.pages) continue;
+      const int in = pos & ((1 << p.log_page) - 1);
+      const int64_t v = ((((int64_t)id << p.log_page) + in) * p.H + h) * D + col;
+      const bool wild = kCodes && !(fabsf(p.vscale[(((int64_t)id * p.H + h) << p.log_page) + in]) < INFINITY);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (kCodes) {
+          if (wild || (reinterpret_cast<const uint8_t*>(p.v)[v + i] & 0x7f) == 0x7f) f[i] = NAN;
+        } else {
+          const float y = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[v + i]);
+          if (!isfinite(y)) f[i] += y;
+        }
+      }
+    }
+  }
+
+  // Softmax of this thread's row of key tile t: S from TMEM, P back to it, over S.
+  __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, int n, uint64_t word, float rc,
+                                       uint32_t meta, uint32_t mine, uint32_t colS, float& m, float& l) {
+    float y[128];
+    {
+      uint32_t x0[32], x1[32], x2[32], x3[32];
+      tmem_ld_x32(colS, x0);
+      tmem_ld_x32(colS + 32, x1);
+      tmem_ld_x32(colS + 64, x2);
+      tmem_ld_x32(colS + 96, x3);
+      tmem_ld_wait_x32(x0);
+      tmem_ld_wait_x32(x1);
+      tmem_ld_wait_x32(x2);
+      tmem_ld_wait_x32(x3);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        y[i] = __uint_as_float(x0[i]);
+        y[32 + i] = __uint_as_float(x1[i]);
+        y[64 + i] = __uint_as_float(x2[i]);
+        y[96 + i] = __uint_as_float(x3[i]);
+      }
+    }
+    if (kCodes) {  // times the key scale and scale * log2 e
+#pragma unroll
+      for (int i = 0; i < 128; i += 4) {
+        const float4 f = lds_f4(meta + 4 * i);
+        pmul(y[i], y[i + 1], f.x, f.y);
+        pmul(y[i + 2], y[i + 3], f.z, f.w);
+      }
+    }
+    const int key0 = t * kBigTile;
+    if (key0 + kBigTile > ctx) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int d0 = key0 + 32 * b - ctx;  // new token of the first of 32 keys
+        uint32_t vis;
+        if (d0 <= -32)
+          vis = 0xffffffffu;
+        else if (d0 < 0)
+          vis = (uint32_t)(word << -d0) | ((1u << -d0) - 1);
+        else
+          vis = d0 < 64 ? (uint32_t)(word >> d0) : 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[32 * b + i] = (vis >> i) & 1 ? y[32 * b + i] : -INFINITY;
+      }
+    }
+    float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 128; i += 8) {
+      float a[8];
+      if (kCodes) {  // of probability times value scale
+        const float4 f = lds_f4(meta + 512 + 4 * i), e = lds_f4(meta + 512 + 4 * i + 16);
+        pfma(a[0], a[1], y[i], y[i + 1], rc, f.x, f.y);
+        pfma(a[2], a[3], y[i + 2], y[i + 3], rc, f.z, f.w);
+        pfma(a[4], a[5], y[i + 4], y[i + 5], rc, e.x, e.y);
+        pfma(a[6], a[7], y[i + 6], y[i + 7], rc, e.z, e.w);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = y[i + q];
+      }
+      top0 = max3f(top0, a[0], a[1]);
+      top1 = max3f(top1, a[2], a[3]);
+      top2 = max3f(top2, a[4], a[5]);
+      top3 = max3f(top3, a[6], a[7]);
+    }
+    float top = fmaxf(max3f(top0, top1, top2), top3);
+    if (!kCodes) top *= rc;  // rc > 0: -inf stays
+    bool grow = top > m + kLazy;  // also the first finite one
+    float alpha = 1.f;
+    if (grow) {
+      alpha = m == -INFINITY ? 0.f : ex2(m - top);
+      m = top;
+    }
+    if (__any_sync(0xffffffffu, grow) && accumulate) {
+#pragma unroll 1
+      for (int col = 0; col < D; col += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(mine + 256 + D * g + col, o);
+        tmem_ld_wait_x32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st_x32(mine + 256 + D * g + col, o);
+      }
+    }
+    const float neg = m == -INFINITY ? 0.f : -m;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t pw[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        float e[4];
+        const int at = 64 * half + i;
+        pfma(e[0], e[1], y[at], y[at + 1], rc, neg, neg);
+        pfma(e[2], e[3], y[at + 2], y[at + 3], rc, neg, neg);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
+        padd(s0, s1, e[0], e[1]);
+        padd(s2, s3, e[2], e[3]);
+        if (kCodes) {
+          const float4 f = lds_f4(meta + 1024 + 4 * at);
+          pmul(e[0], e[1], f.x, f.y);
+          pmul(e[2], e[3], f.z, f.w);
+        }
+        pw[i / 2] = kCodes ? pack_half(e[0], e[1]) : rows::pack2(e[0], e[1]);
+        pw[i / 2 + 1] = kCodes ? pack_half(e[2], e[3]) : rows::pack2(e[2], e[3]);
+      }
+      tmem_st_x32(colS + 32 * half, pw);
+    }
+    tmem_st_wait();
+    l = l * alpha + ((s0 + s1) + (s2 + s3));
+  }
+};
+
+template <int D, bool kCodes>
+__global__ void __launch_bounds__(kBigThreads, 1)
+tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ Params p, const __grid_constant__ Work w) {
+  using C = BigCfg<D, kCodes>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ BigShared ss;
+  static_assert(C::kBars <= 48, "barriers");
+  const int warp = threadIdx.x / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  Walk k;
+  if (!find_place(p, w, blockIdx.x, blockIdx.x == 0 && warp == 0, k)) return;  // the whole CTA
+  auto init = [&](int first, int n, int count) {
+    for (int i = 0; i < n; ++i) mbar_init(smem_u32(&ss.bars[first + i]), count);
+  };
+  if (threadIdx.x == 0) {
+    init(C::bKF, C::kK, kCodes ? 33 : 1);  // the copies' bytes, and 32 lanes' scales
+    init(C::bKE, C::kK, kCodes ? 5 : 1);   // the products, and the operand warps
+    init(C::bVF, C::kV, 1);
+    init(C::bVE, C::kV, kCodes ? 4 : 1);   // the operand warps, or the products
+    init(C::bRF, C::kReady, 4);
+    init(C::bRE, C::kReady, 1);
+    init(C::bMF, C::kMeta, 4);
+    init(C::bME, C::kMeta, 4);
+    init(C::bSF, 2, 1);
+    init(C::bPF, 2, 128);
+    init(C::bOF, 2, 1);
+    init(C::bQF, 1, 128);
+    init(C::bQE, 1, 1);
+    init(C::bOFree, 1, 256);
+    init(C::bDrain, 1, 1);
+    fence_mbar_init();
+    ss.abort = 0;
+    for (int i = 0; i < kRing; ++i) ss.bad[i] = ss.hidden[i][0] = ss.hidden[i][1] = 0;
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(&ss.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  Big<D, kCodes> big{p, w, ss, (smem_u32(smem_raw) + 1023u) & ~1023u, ss.tmem};
+  if (warp < 8) {
+    regs_inc<kSoftmaxRegs>();
+    big.softmax(k, warp / 4);
+  } else if (warp < 12) {
+    regs_dec<kOperandRegs>();
+    big.prepare(k);
+  } else {
+    regs_dec<kRestRegs>();
+    if (warp == 12) {
+      big.produce(k, &map_k, &map_v);
+    } else if (warp == 13) {
+      if (threadIdx.x % 32 == 0) big.multiply(k);
+    }
+    __syncwarp();
+  }
+  if (big.aborted()) {  // let copies in flight land before the CTA leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(ss.tmem, 512);
+  }
+}
+
+}  // namespace tree
+}  // namespace attn

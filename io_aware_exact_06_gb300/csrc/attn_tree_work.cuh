@@ -1,11 +1,19 @@
 // The line of key tiles that attention over the paged cache works through, and
-// the end of its pieces (see attn_tree_kernel.cuh).
+// the end of its pieces.
 #pragma once
 
-#include "attn_tree_kernel.cuh"
+#include "attn_tree_common.cuh"
 
 namespace attn {
 namespace tree {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrive on the barrier once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // The work of a launch as one line of key tiles, cut into equal shares: for
 // sequence after sequence, for each group of its key heads and row tile (a
