@@ -14,7 +14,8 @@
 // so that one group's softmax runs beside the other's products; they meet at the
 // segment's end); 8-11 operands: they write the segment's Q tile, turn a tile's
 // codes of V into fp16 and its scales into the factors the softmax needs, and
-// clean values that rows may not see; 12 TMA producer; 13 MMA issuer.
+// clean values that rows may not see; 12 and 14 TMA producers of keys and values;
+// 13 MMA issuer.
 //
 // With e4m3 codes S = (Q_hi + Q_lo) K^T takes the codes of K as they lie in the
 // cache: a query row, scaled by a power of two to at most 256, is the sum of two
@@ -106,11 +107,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 r;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a) : "memory");
-  return r;
-}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -144,8 +140,8 @@ struct Big {
   const Params& p;
   const Work& w;
   BigShared& ss;
-  uint32_t smem;  // 1024-byte aligned
-  uint32_t tmem;
+  uint8_t* smem_ptr;  // 1024-byte aligned
+  uint32_t smem, tmem;
 
   __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&ss.bars[i]); }
   // Bounded; once one wait has run out nothing waits any more, every role goes
@@ -162,13 +158,18 @@ struct Big {
   __device__ __forceinline__ int head(const Walk& k) const { return k.seg / (k.segs / p.H); }
   __device__ __forceinline__ int row0(const Walk& k) const { return k.seg % (k.segs / p.H) * kBigRows; }
 
-  // ------------------------------------------------------------- producer --
-  __device__ __forceinline__ void produce(Walk k, const CUtensorMap* mk, const CUtensorMap* mv) {
+  // ------------------------------------------------------------- producers --
+  // One warp copies the keys (and the scales), another the values, each as far
+  // ahead as its stages reach.
+  template <bool kKeys>
+  __device__ __forceinline__ void produce(Walk k, const CUtensorMap* map) {
+    constexpr int kN = kKeys ? C::kK : C::kV, kFull = kKeys ? C::bKF : C::bVF, kEmpty = kKeys ? C::bKE : C::bVE;
+    constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
     const int lane = threadIdx.x % 32;
     const int page = 1 << p.log_page;
     const int box = min(page, kBigTile), per = kBigTile / box;  // rows of a copy, copies of a tile
     const int batch = 32 / per;  // tiles whose page numbers one load fetches
-    int ks = 0, kr = 0, vs = 0, vr = 0, seg = 0;
+    int s = 0, round = 0, seg = 0;
     do {
       const int h = head(k), len = k.s.len, end = k.tile + k.piece();
       const int* table = p.table + (int64_t)k.b * p.stride;
@@ -185,57 +186,44 @@ struct Big {
         for (int t = t0; t < min(t0 + batch, end); ++t) {
           const int key0 = t * kBigTile, n = min(per, (len - key0 + box - 1) / box);
           const int id = __shfl_sync(0xffffffffu, ids, (t - t0) * per + lane % per);
-          const int row = (id << p.log_page) + ((key0 + lane * box) & (page - 1));
-          const uint32_t mine = per == 32 ? 0xffffffffu : ((1u << per) - 1) << ((t - t0) * per);
-          constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
-          if (kr > 0) wait(C::bKE + ks, (kr & 1) ^ 1);
+          if (round > 0) wait(kEmpty + s, (round & 1) ^ 1);
           __syncwarp();
-          const bool stop = __any_sync(0xffffffffu, aborted());
-          if (!stop) {
+          if (!__any_sync(0xffffffffu, aborted())) {
+            const uint32_t full = bar(kFull + s);
             if (lane == 0) {
-              if (wrongs & mine) {
+              if (kKeys && (wrongs >> ((t - t0) * per) & ((1u << per) - 1))) {
                 ss.bad[seg % kRing] = 1;
                 atomicOr(p.err, rows::kBadIndex);
               }
-              mbar_arrive_expect_tx(bar(C::bKF + ks), n * box * C::kRowBytes);
+              mbar_arrive_expect_tx(full, n * box * C::kRowBytes);
             }
             __syncwarp();
-            const uint32_t dst = smem + C::kOffK + ks * C::kMat + lane * box * C::kBox;
-            if (lane < n)
+            if (lane < n) {
+              const int row = (id << p.log_page) + ((key0 + lane * box) & (page - 1));
+              const uint32_t dst = smem + (kKeys ? C::kOffK : C::kOffV) + s * C::kMat + lane * box * C::kBox;
 #pragma unroll
               for (int f = 0; f < C::kHalves; ++f)
-                tma_load_3d(dst + f * kBigTile * C::kBox, mk, bar(C::bKF + ks), f * kElems, h, row);
-            if (kCodes) {  // each lane: four key scales and four value scales
+                tma_load_3d(dst + f * kBigTile * C::kBox, map, full, f * kElems, h, row);
+            }
+            if (kKeys && kCodes) {  // each lane: four key scales and four value scales
               const int key = key0 + 4 * lane;
               const int sid = __shfl_sync(0xffffffffu, id, 4 * lane / box);
               if (key < len) {
                 const int64_t at = (((int64_t)sid * p.H + h) << p.log_page) + (key & (page - 1));
-                const uint32_t sd = smem + C::kOffScale + ks * 1024 + 16 * lane;
+                const uint32_t sd = smem + C::kOffScale + s * 1024 + 16 * lane;
                 cp_async16(sd, p.kscale + at);
                 cp_async16(sd + 512, p.vscale + at);
               }
-              cp_async_arrive(bar(C::bKF + ks));
+              cp_async_arrive(full);
             }
           }
-          if (++ks == C::kK) ks = 0, ++kr;
-          if (vr > 0) wait(C::bVE + vs, (vr & 1) ^ 1);
-          __syncwarp();
-          if (!__any_sync(0xffffffffu, aborted())) {
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::bVF + vs), n * box * C::kRowBytes);
-            __syncwarp();
-            const uint32_t dst = smem + C::kOffV + vs * C::kMat + lane * box * C::kBox;
-            if (lane < n)
-#pragma unroll
-              for (int f = 0; f < C::kHalves; ++f)
-                tma_load_3d(dst + f * kBigTile * C::kBox, mv, bar(C::bVF + vs), f * kElems, h, row);
-          }
-          if (++vs == C::kV) vs = 0, ++vr;
+          if (++s == kN) s = 0, ++round;
         }
         ids = next;
       }
       ++seg;
     } while (k.next(p, w));
-    if (kCodes) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (kKeys && kCodes) asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   // -------------------------------------------------------------- products --
@@ -408,11 +396,26 @@ struct Big {
         if (kCodes) {
           if (rr > 0) wait(C::bRE + rs, (rr & 1) ^ 1);
           const uint32_t dst = smem + C::kOffC + rs * C::kConv;
-#pragma unroll 4
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const uint4 x = lds128(v + swz<C::kBox>(r, ch));
-            uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            if (pos >= ctx) {
+          auto put = [&](int ch, const uint32_t (&u)[4]) {
+            const int o = 2 * ch;  // 16-byte chunk of the fp16 row
+            const uint32_t base = dst + (o / 8) * C::kChunk;
+            sts128(base + swz<128>(r, o % 8), codes_lo(u[0]), codes_hi(u[0]), codes_lo(u[1]), codes_hi(u[1]));
+            sts128(base + swz<128>(r, o % 8 + 1), codes_lo(u[2]), codes_hi(u[2]), codes_lo(u[3]), codes_hi(u[3]));
+          };
+          if (pos < ctx) {
+            uint4 x[D / 16];
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) x[ch] = lds128(v + swz<C::kBox>(r, ch));
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint32_t u[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
+              put(ch, u);
+            }
+          } else {
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint4 x = lds128(v + swz<C::kBox>(r, ch));
+              uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (pos >= len) u[i] = 0;
@@ -420,13 +423,11 @@ struct Big {
                 for (int b = 0; b < 4; ++b)
                   if (((u[i] >> (8 * b)) & 0x7fu) == 0x7fu) u[i] &= ~(0xffu << (8 * b)), odd = true;
               }
+              put(ch, u);
             }
-            const int o = 2 * ch;  // 16-byte chunk of the fp16 row
-            const uint32_t base = dst + (o / 8) * C::kChunk;
-            sts128(base + swz<128>(r, o % 8), codes_lo(u[0]), codes_hi(u[0]), codes_lo(u[1]), codes_hi(u[1]));
-            sts128(base + swz<128>(r, o % 8 + 1), codes_lo(u[2]), codes_hi(u[2]), codes_lo(u[3]), codes_hi(u[3]));
           }
         } else if (pos >= ctx) {
+#pragma unroll 1
           for (int ch = 0; ch < D / 8; ++ch) {
             const uint32_t at = v + (ch / 8) * C::kChunk + swz<128>(r, ch % 8);
             const uint4 x = lds128(at);
@@ -479,7 +480,8 @@ struct Big {
           if (kCodes) wait(C::bMF + ms, mr & 1);
           if (__any_sync(0xffffffffu, busy)) {
             if (kCodes && j == g) rc = ss.rc[seg & 1][r];
-            tile(k.tile + j, g, j > 1, ctx, sq.n, word, rc, smem + C::kOffMeta + ms * 1536, mine, colS, m, l);
+            tile(k.tile + j, g, j > 1, ctx, sq.n, word, rc,
+                 reinterpret_cast<const float4*>(smem_ptr + C::kOffMeta + ms * 1536), mine, colS, m, l);
           }
           tc_fence_before();
           mbar_arrive(bar(C::bPF + g));
@@ -581,7 +583,7 @@ struct Big {
 
   // Softmax of this thread's row of key tile t: S from TMEM, P back to it, over S.
   __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, int n, uint64_t word, float rc,
-                                       uint32_t meta, uint32_t mine, uint32_t colS, float& m, float& l) {
+                                       const float4* meta, uint32_t mine, uint32_t colS, float& m, float& l) {
     float y[128];
     {
       uint32_t x0[32], x1[32], x2[32], x3[32];
@@ -604,7 +606,7 @@ struct Big {
     if (kCodes) {  // times the key scale and scale * log2 e
 #pragma unroll
       for (int i = 0; i < 128; i += 4) {
-        const float4 f = lds_f4(meta + 4 * i);
+        const float4 f = meta[i / 4];
         pmul(y[i], y[i + 1], f.x, f.y);
         pmul(y[i + 2], y[i + 3], f.z, f.w);
       }
@@ -630,7 +632,7 @@ struct Big {
     for (int i = 0; i < 128; i += 8) {
       float a[8];
       if (kCodes) {  // of probability times value scale
-        const float4 f = lds_f4(meta + 512 + 4 * i), e = lds_f4(meta + 512 + 4 * i + 16);
+        const float4 f = meta[32 + i / 4], e = meta[33 + i / 4];
         pfma(a[0], a[1], y[i], y[i + 1], rc, f.x, f.y);
         pfma(a[2], a[3], y[i + 2], y[i + 3], rc, f.z, f.w);
         pfma(a[4], a[5], y[i + 4], y[i + 5], rc, e.x, e.y);
@@ -679,7 +681,7 @@ struct Big {
         padd(s0, s1, e[0], e[1]);
         padd(s2, s3, e[2], e[3]);
         if (kCodes) {
-          const float4 f = lds_f4(meta + 1024 + 4 * at);
+          const float4 f = meta[64 + at / 4];
           pmul(e[0], e[1], f.x, f.y);
           pmul(e[2], e[3], f.z, f.w);
         }
@@ -736,7 +738,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Big<D, kCodes> big{p, w, ss, (smem_u32(smem_raw) + 1023u) & ~1023u, ss.tmem};
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  Big<D, kCodes> big{p, w, ss, smem_raw + (base - smem_u32(smem_raw)), base, ss.tmem};
   if (warp < 8) {
     regs_inc<kSoftmaxRegs>();
     big.softmax(k, warp / 4);
@@ -746,7 +749,9 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   } else {
     regs_dec<kRestRegs>();
     if (warp == 12) {
-      big.produce(k, &map_k, &map_v);
+      big.template produce<true>(k, &map_k);
+    } else if (warp == 14) {
+      big.template produce<false>(k, &map_v);
     } else if (warp == 13) {
       if (threadIdx.x % 32 == 0) big.multiply(k);
     }
