@@ -249,7 +249,7 @@ int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
                                 : tree_tile_kernel<D, kCodes>;
   const int smem = pl.rows == 8    ? FewCfg<D, kCodes, 1>::kSmem
                    : pl.rows == 16 ? FewCfg<D, kCodes, 2>::kSmem
-                                   : BigCfg<D, kCodes>::kSmem;
+                                   : big_smem<D, kCodes>();
   int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != ATTN_OK) return st;
   if ((st = launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK)

@@ -13,8 +13,7 @@
 // even key tiles of a segment, B the odd ones, each with its own S and O in TMEM,
 // so that one group's softmax runs beside the other's products; they meet at the
 // segment's end); 8-11 operands: they write the segment's Q tile, turn a tile's
-// codes of V into fp16 and its scales into the factors the softmax needs, and
-// clean values that rows may not see; 12 and 14 TMA producers of keys and values;
+// codes of V into fp16 values, and clean values that rows may not see; 12 and 14 TMA producers of keys and values;
 // 13 MMA issuer.
 //
 // With e4m3 codes S = (Q_hi + Q_lo) K^T takes the codes of K as they lie in the
@@ -22,9 +21,13 @@
 // e4m3 values (4 + 4 significant bits hold bf16's 8 exactly, down to 2^-11 of the
 // row's largest channel, where the quantum 2^-9 of the small part ends it: an
 // error below 2^-18 of the largest), and the two e4m3 products cost what one fp16
-// product does.  P V takes fp16 (V's codes are exact in it, P is rounded to
-// 2^-11), with the value scale in P and the running maximum over log2(p * value
-// scale), as for few rows.
+// product does; the softmax multiplies a score by its key's scale.  V is converted
+// with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-12, F a running
+// exponent of the segment's value scales (all of a CTA's tiles; O is rescaled when
+// it grows), which leaves values 2^-30 of the largest their full precision.  P is
+// fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.  (With the value scale
+// in P, as for few rows, a score took three factors from shared memory and 1200
+// instructions a row and tile, 4500 cycles; 420 us for trees of 64 drafts.)
 #pragma once
 
 #include "attn_tree_work.cuh"
@@ -40,6 +43,7 @@ constexpr int kBigThreads = 512;
 // rest.  Their sum is the launch's 512 x 128.
 constexpr int kSoftmaxRegs = 192, kOperandRegs = 80, kRestRegs = 48;
 constexpr int kRing = 8;  // segments whose flags are kept
+constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
 
 template <int D, bool kCodes>
 struct BigCfg : Row<D, kCodes> {
@@ -49,16 +53,15 @@ struct BigCfg : Row<D, kCodes> {
   static constexpr int kConv = kCodes ? kBigTile * D * 2 : 0;   // V in fp16
   static constexpr int kQ = kBigRows * D * 2;                   // bf16, or the two e4m3 parts
   static constexpr int kK = kCodes || D == 64 ? 4 : 3;          // stages
-  static constexpr int kV = kCodes ? (D == 128 ? 3 : 4) : D == 64 ? 4 : 2;
+  static constexpr int kV = D == 128 ? 3 : 4;
   static constexpr int kReady = kCodes ? 2 : kV;                // V operand buffers
   static constexpr int kMeta = kCodes ? 4 : 1;                  // tiles whose factors are kept
   static constexpr int kOffK = kQ;
   static constexpr int kOffV = kOffK + kK * kMat;
   static constexpr int kOffC = kOffV + kV * kMat;
   static constexpr int kOffScale = kOffC + kReady * kConv;            // [kK][2][128] raw scales
-  static constexpr int kOffMeta = kOffScale + (kCodes ? kK * 1024 : 0);  // [kMeta][3][128]
-  static constexpr int kSmem = kOffMeta + (kCodes ? kMeta * 1536 : 0) + 1024;
-  static_assert(kSmem + 6 * 1024 <= 227 * 1024, "shared memory");
+  static constexpr int kOffMeta = kOffScale + (kCodes ? kK * 1024 : 0);  // [kMeta][128] key factors
+  static constexpr int kOffShared = kOffMeta + (kCodes ? kMeta * 512 : 0);
   // barriers
   static constexpr int bKF = 0, bKE = bKF + kK, bVF = bKE + kK, bVE = bVF + kV, bRF = bVE + kV, bRE = bRF + kReady,
                        bMF = bRE + kReady, bME = bMF + kMeta, bSF = bME + kMeta, bPF = bSF + 2, bOF = bPF + 2,
@@ -124,15 +127,37 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Behind the tiles in dynamic shared memory (there is no static one, so the
+// dynamic one begins at an address that is a multiple of 1024; the kernel checks).
 struct BigShared {
   uint64_t bars[48];
   uint32_t tmem;
-  int abort;                    // a wait ran out
-  int bad[kRing];               // the segment reads a page outside the cache
-  uint32_t hidden[kRing][2];    // its new tokens with values that are not finite
-  float2 ml[2][2][kBigRows];    // [segment's parity][group]: maxima and sums
-  float rc[2][kBigRows];        // [segment's parity]: log2 units of a row's raw score
+  int abort;                  // a wait ran out
+  int bad[kRing];             // the segment reads a page outside the cache
+  uint32_t hidden[kRing][2];  // its new tokens with values that are not finite
+  int vexp[2][4];             // [tile's parity][operand warp]: largest exponent of a value scale
+  int vref[4];                // by tile: the exponent F of its values
+  float2 ml[2][kBigRows];     // [group]: maxima and sums
+  int fend[2];                // [group]: F of its O
+  float rc[2][kBigRows];      // [segment's parity]: log2 units of a row's raw score
 };
+template <int D, bool kCodes>
+__host__ __device__ constexpr int big_smem() {
+  return BigCfg<D, kCodes>::kOffShared + (int)sizeof(BigShared) - (kCodes ? 0 : (int)sizeof(float) * 2 * kBigRows);
+}
+
+__device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// 2^e for e in -126 .. 127, 0 below.
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(e, 127)) << 23); }
 
 template <int D, bool kCodes>
 struct Big {
@@ -359,7 +384,7 @@ struct Big {
 
   __device__ __forceinline__ void prepare(Walk k) {
     const int r = threadIdx.x % 128, lane = threadIdx.x % 32;  // thread r: key r of a tile
-    int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0;
+    int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0, vref = 0, tile_parity = 0;
     do {
       if (seg > 0) wait(C::bQE, (seg - 1) & 1);
       write_query(k, seg);
@@ -368,20 +393,30 @@ struct Big {
       for (int t = k.tile; t < end; ++t) {
         const int pos = t * kBigTile + r;
         bool cut = false;  // the value scale is not finite, for a key that rows may not see
+        float vscale = 0.f;
         if (kCodes) {
           wait(C::bKF + ks, kr & 1);
           if (mr > 0) wait(C::bME + ms, (mr & 1) ^ 1);
-          const uint32_t sc = smem + C::kOffScale + ks * 1024 + 4 * r, me = smem + C::kOffMeta + ms * 1536 + 4 * r;
+          const uint32_t sc = smem + C::kOffScale + ks * 1024 + 4 * r;
           const float kscale = __uint_as_float(lds32(sc));
-          float vscale = __uint_as_float(lds32(sc + 512));
+          vscale = __uint_as_float(lds32(sc + 512));
           if (pos >= ctx && !(fabsf(vscale) < INFINITY)) {
             cut = pos < len;
             vscale = 0.f;
           }
           if (pos >= len) vscale = 0.f;
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me), "f"(kscale * p.c) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me + 512), "f"(lg2(fmaxf(vscale, 0x1p-64f))) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(me + 1024), "f"(vscale) : "memory");
+          // F: the largest exponent so far, with room to grow by two before O is rescaled
+          const uint32_t bits = __float_as_uint(vscale) & 0x7fffffffu;
+          const int e = bits < 0x7f800000u ? (int)(bits >> 23) - 127 : -127;
+          const int most = __reduce_max_sync(0xffffffffu, e);
+          const int turn = tile_parity;
+          tile_parity ^= 1;
+          if (lane == 0) ss.vexp[turn][threadIdx.x / 32 % 4] = most;
+          asm volatile("bar.sync 3, 128;" ::: "memory");
+          const int all = max(max(ss.vexp[turn][0], ss.vexp[turn][1]), max(ss.vexp[turn][2], ss.vexp[turn][3]));
+          if (t == k.tile || all > vref) vref = max(all, -100) + 2;
+          *reinterpret_cast<float*>(smem_ptr + C::kOffMeta + ms * 512 + 4 * r) = kscale * p.c;
+          if (r == 0) ss.vref[ms] = vref;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar(C::bMF + ms));
@@ -396,11 +431,20 @@ struct Big {
         if (kCodes) {
           if (rr > 0) wait(C::bRE + rs, (rr & 1) ^ 1);
           const uint32_t dst = smem + C::kOffC + rs * C::kConv;
+          // the scale as a sum of two fp16: code * hi + code * lo, rounded once more
+          const float f = vscale * pow2(6 - vref);
+          const uint32_t hi = pack_half(f, f);
+          float fh;
+          asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.f32.f16 %0, x;\n}\n" : "=f"(fh) : "r"(hi));
+          const uint32_t lo = pack_half(f - fh, f - fh);
+          auto times = [&](uint32_t v) { return half_fma2(v, hi, half_mul2(v, lo)); };
           auto put = [&](int ch, const uint32_t (&u)[4]) {
             const int o = 2 * ch;  // 16-byte chunk of the fp16 row
             const uint32_t base = dst + (o / 8) * C::kChunk;
-            sts128(base + swz<128>(r, o % 8), codes_lo(u[0]), codes_hi(u[0]), codes_lo(u[1]), codes_hi(u[1]));
-            sts128(base + swz<128>(r, o % 8 + 1), codes_lo(u[2]), codes_hi(u[2]), codes_lo(u[3]), codes_hi(u[3]));
+            sts128(base + swz<128>(r, o % 8), times(codes_lo(u[0])), times(codes_hi(u[0])), times(codes_lo(u[1])),
+                   times(codes_hi(u[1])));
+            sts128(base + swz<128>(r, o % 8 + 1), times(codes_lo(u[2])), times(codes_hi(u[2])), times(codes_lo(u[3])),
+                   times(codes_hi(u[3])));
           };
           if (pos < ctx) {
             uint4 x[D / 16];
@@ -473,6 +517,7 @@ struct Big {
       const uint64_t word = (live ? mask_word(p.mask, sq.q0 + tok, tok) : 0) &
                             (sq.n >= 64 ? ~0ull : (1ull << sq.n) - 1);
       float rc = p.c, m = -INFINITY, l = 0.f;
+      int vref = 0;
       for (int j = 0; j < n; ++j) {
         if ((j & 1) == g) {
           wait(C::bSF + g, scount++ & 1);
@@ -480,8 +525,11 @@ struct Big {
           if (kCodes) wait(C::bMF + ms, mr & 1);
           if (__any_sync(0xffffffffu, busy)) {
             if (kCodes && j == g) rc = ss.rc[seg & 1][r];
-            tile(k.tile + j, g, j > 1, ctx, sq.n, word, rc,
-                 reinterpret_cast<const float4*>(smem_ptr + C::kOffMeta + ms * 1536), mine, colS, m, l);
+            const int f = kCodes ? ss.vref[ms] : 0;
+            const float shrink = j > 1 && f != vref ? pow2(vref - f) : 1.f;
+            vref = f;
+            tile(k.tile + j, g, j > 1, ctx, word, rc, shrink,
+                 reinterpret_cast<const float4*>(smem_ptr + C::kOffMeta + ms * 512), mine, colS, m, l);
           }
           tc_fence_before();
           mbar_arrive(bar(C::bPF + g));
@@ -497,8 +545,9 @@ struct Big {
       if (n > 1) wait(C::bOF + 1, ocount[1]++ & 1);
       tc_fence_after();
       close_row(m, l);
-      float2(*ml)[kBigRows] = ss.ml[seg & 1];
-      ml[g][r] = make_float2(m, l);
+      // (the other group has read the last segment's: O is free only when it has)
+      ss.ml[g][r] = make_float2(m, l);
+      if (kCodes && busy) ss.fend[g] = vref;
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const bool poison = aborted() || *(volatile int*)&ss.bad[seg % kRing];
       const uint64_t hid = (uint64_t) * (volatile uint32_t*)&ss.hidden[seg % kRing][1] << 32 |
@@ -509,16 +558,18 @@ struct Big {
         ss.hidden[old][0] = ss.hidden[old][1] = 0;
       }
       if (__any_sync(0xffffffffu, busy)) {
-        const float2 a = ml[0][r], b = ml[1][r];
+        const float2 a = ss.ml[0][r], b = ss.ml[1][r];
         const float mm = fmaxf(a.x, b.x);
         const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), wb = b.x == -INFINITY ? 0.f : ex2(b.x - mm);
         const float ls = (wa != 0.f ? wa * a.y : 0.f) + (wb != 0.f ? wb * b.y : 0.f);
         const float inv = ls != 0.f ? 1.f / ls : 0.f;
+        // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
+        const float ua = kCodes ? wa * pow2(ss.fend[0] - 6) : wa, ub = kCodes ? wb * pow2(ss.fend[1] - 6) : wb;
         const bool whole = k.tile == 0 && n == k.tiles;
         const int slot = whole ? -1 : 2 * (int)blockIdx.x + !firstp;
         const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * kBigRows + r;
         if (live && g == 0) {
-          float lse = ls != 0.f ? (mm + lg2(ls)) * 0.69314718055994531f : -INFINITY;
+          float lse = ls != 0.f ? (mm + lg2(ls) - (kCodes ? kPLog2 : 0.f)) * 0.69314718055994531f : -INFINITY;
           if (poison) lse = whole ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
           (whole ? p.lse : p.lse_part)[at] = lse;
         }
@@ -532,7 +583,7 @@ struct Big {
           float f[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            f[i] = (wa != 0.f ? wa * __uint_as_float(xa[i]) : 0.f) + (wb != 0.f ? wb * __uint_as_float(xb[i]) : 0.f);
+            f[i] = (wa != 0.f ? ua * __uint_as_float(xa[i]) : 0.f) + (wb != 0.f ? ub * __uint_as_float(xb[i]) : 0.f);
             f[i] = inv != 0.f ? f[i] * inv : 0.f;
             if (poison) f[i] = NAN;
           }
@@ -582,15 +633,25 @@ struct Big {
   }
 
   // Softmax of this thread's row of key tile t: S from TMEM, P back to it, over S.
-  __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, int n, uint64_t word, float rc,
+  // O (accumulate: it holds something) takes `shrink` and the growth of the maximum.
+  __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, uint64_t word, float rc, float shrink,
                                        const float4* meta, uint32_t mine, uint32_t colS, float& m, float& l) {
     float y[128];
+    // The key scales (times scale * log2 e), 16 keys at a time and a batch ahead:
+    // shared memory is busy with the products' operands, and a load that is used at
+    // once waits for it alone (4600 cycles a tile).
+    float4 fa[4], fb[4];
+    auto factors = [&](float4 (&f)[4], int b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = meta[4 * b + i];
+    };
     {
       uint32_t x0[32], x1[32], x2[32], x3[32];
       tmem_ld_x32(colS, x0);
       tmem_ld_x32(colS + 32, x1);
       tmem_ld_x32(colS + 64, x2);
       tmem_ld_x32(colS + 96, x3);
+      if (kCodes) factors(fa, 0);
       tmem_ld_wait_x32(x0);
       tmem_ld_wait_x32(x1);
       tmem_ld_wait_x32(x2);
@@ -603,26 +664,29 @@ struct Big {
         y[96 + i] = __uint_as_float(x3[i]);
       }
     }
-    if (kCodes) {  // times the key scale and scale * log2 e
+    if (kCodes) {
 #pragma unroll
-      for (int i = 0; i < 128; i += 4) {
-        const float4 f = meta[i / 4];
-        pmul(y[i], y[i + 1], f.x, f.y);
-        pmul(y[i + 2], y[i + 3], f.z, f.w);
+      for (int b = 0; b < 8; ++b) {
+        if (b < 7) factors(b & 1 ? fa : fb, b + 1);
+        asm volatile("" ::: "memory");  // the loads stay ahead of the products below
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = b & 1 ? fb[i] : fa[i];
+          const int at = 16 * b + 4 * i;
+          pmul(y[at], y[at + 1], f.x, f.y);
+          pmul(y[at + 2], y[at + 3], f.z, f.w);
+        }
       }
     }
-    const int key0 = t * kBigTile;
-    if (key0 + kBigTile > ctx) {
+    const int d = t * kBigTile - ctx;  // new token of the tile's first key
+    if (d + kBigTile > 0) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int d0 = key0 + 32 * b - ctx;  // new token of the first of 32 keys
-        uint32_t vis;
-        if (d0 <= -32)
-          vis = 0xffffffffu;
-        else if (d0 < 0)
-          vis = (uint32_t)(word << -d0) | ((1u << -d0) - 1);
-        else
-          vis = d0 < 64 ? (uint32_t)(word >> d0) : 0u;
+        const int d0 = d + 32 * b;
+        const uint32_t vis = d0 <= -32 ? 0xffffffffu
+                             : d0 < 0  ? (uint32_t)(word << -d0) | ((1u << -d0) - 1)
+                             : d0 < 64 ? (uint32_t)(word >> d0)
+                                       : 0u;
 #pragma unroll
         for (int i = 0; i < 32; ++i) y[32 * b + i] = (vis >> i) & 1 ? y[32 * b + i] : -INFINITY;
       }
@@ -630,42 +694,31 @@ struct Big {
     float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 128; i += 8) {
-      float a[8];
-      if (kCodes) {  // of probability times value scale
-        const float4 f = meta[32 + i / 4], e = meta[33 + i / 4];
-        pfma(a[0], a[1], y[i], y[i + 1], rc, f.x, f.y);
-        pfma(a[2], a[3], y[i + 2], y[i + 3], rc, f.z, f.w);
-        pfma(a[4], a[5], y[i + 4], y[i + 5], rc, e.x, e.y);
-        pfma(a[6], a[7], y[i + 6], y[i + 7], rc, e.z, e.w);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) a[q] = y[i + q];
-      }
-      top0 = max3f(top0, a[0], a[1]);
-      top1 = max3f(top1, a[2], a[3]);
-      top2 = max3f(top2, a[4], a[5]);
-      top3 = max3f(top3, a[6], a[7]);
+      top0 = max3f(top0, y[i], y[i + 1]);
+      top1 = max3f(top1, y[i + 2], y[i + 3]);
+      top2 = max3f(top2, y[i + 4], y[i + 5]);
+      top3 = max3f(top3, y[i + 6], y[i + 7]);
     }
-    float top = fmaxf(max3f(top0, top1, top2), top3);
-    if (!kCodes) top *= rc;  // rc > 0: -inf stays
-    bool grow = top > m + kLazy;  // also the first finite one
+    const float top = fmaxf(max3f(top0, top1, top2), top3) * rc;  // rc > 0: -inf stays
+    const bool grow = top > m + kLazy;  // also the first finite one
     float alpha = 1.f;
     if (grow) {
       alpha = m == -INFINITY ? 0.f : ex2(m - top);
       m = top;
     }
-    if (__any_sync(0xffffffffu, grow) && accumulate) {
+    if (accumulate && __any_sync(0xffffffffu, grow || shrink != 1.f)) {
+      const float f = alpha * shrink;
 #pragma unroll 1
       for (int col = 0; col < D; col += 32) {
         uint32_t o[32];
         tmem_ld_x32(mine + 256 + D * g + col, o);
         tmem_ld_wait_x32(o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
         tmem_st_x32(mine + 256 + D * g + col, o);
       }
     }
-    const float neg = m == -INFINITY ? 0.f : -m;
+    const float neg = (m == -INFINITY ? 0.f : -m) + (kCodes ? kPLog2 : 0.f);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -680,11 +733,6 @@ struct Big {
         for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
         padd(s0, s1, e[0], e[1]);
         padd(s2, s3, e[2], e[3]);
-        if (kCodes) {
-          const float4 f = meta[64 + at / 4];
-          pmul(e[0], e[1], f.x, f.y);
-          pmul(e[2], e[3], f.z, f.w);
-        }
         pw[i / 2] = kCodes ? pack_half(e[0], e[1]) : rows::pack2(e[0], e[1]);
         pw[i / 2 + 1] = kCodes ? pack_half(e[2], e[3]) : rows::pack2(e[2], e[3]);
       }
@@ -700,12 +748,17 @@ __global__ void __launch_bounds__(kBigThreads, 1)
 tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ Params p, const __grid_constant__ Work w) {
   using C = BigCfg<D, kCodes>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ BigShared ss;
+  extern __shared__ __align__(1024) uint8_t smem_big[];
   static_assert(C::kBars <= 48, "barriers");
+  static_assert(big_smem<D, kCodes>() <= 227 * 1024, "shared memory");
+  BigShared& ss = *reinterpret_cast<BigShared*>(smem_big + C::kOffShared);
   const int warp = threadIdx.x / 32;
   grid_dep_wait();
   grid_dep_launch();
+  if (smem_u32(smem_big) & 1023u) {  // the swizzled tiles would be read askew
+    if (threadIdx.x == 0) atomicOr(p.err, kTimedOut);
+    return;
+  }
   Walk k;
   if (!find_place(p, w, blockIdx.x, blockIdx.x == 0 && warp == 0, k)) return;  // the whole CTA
   auto init = [&](int first, int n, int count) {
@@ -738,8 +791,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  Big<D, kCodes> big{p, w, ss, smem_raw + (base - smem_u32(smem_raw)), base, ss.tmem};
+  Big<D, kCodes> big{p, w, ss, smem_big, smem_u32(smem_big), ss.tmem};
   if (warp < 8) {
     regs_inc<kSoftmaxRegs>();
     big.softmax(k, warp / 4);
