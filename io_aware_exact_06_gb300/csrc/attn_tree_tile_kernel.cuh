@@ -259,10 +259,12 @@ struct Big {
       const uint64_t hi = make_sdesc(smem, 16, 8 * C::kBox, kSwz);
       const uint64_t lo = make_sdesc(smem + kBigRows * C::kBox, 16, 8 * C::kBox, kSwz);
       const uint64_t b = make_sdesc(k, 16, 8 * C::kBox, kSwz);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const uint64_t a = part ? lo : hi;
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, hi + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), kk > 0);
-#pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, lo + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), 1);
+        for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, a + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), part | kk);
+      }
     } else {
       const uint64_t a = make_sdesc(smem, 16, 1024, kSwizzle128B), b = make_sdesc(k, 16, 1024, kSwizzle128B);
 #pragma unroll
@@ -276,7 +278,7 @@ struct Big {
     const uint32_t v = kCodes ? smem + C::kOffC + r * C::kConv : smem + C::kOffV + r * C::kMat;
     const uint64_t b = make_sdesc(v, C::kChunk, 1024, kSwizzle128B);
     constexpr uint32_t kI = kCodes ? idesc_f16_mn(128, D) : make_idesc_bf16(128, D, true);
-#pragma unroll
+#pragma unroll 2
     for (int kk = 0; kk < kBigTile / 16; ++kk)
       mma_ts(tmem + 256 + D * g, tmem + 128 * g + 8 * kk, b + (uint64_t)((kk * 2048) >> 4), kI, kk > 0 || accumulate);
   }
@@ -285,38 +287,35 @@ struct Big {
   __device__ __forceinline__ void multiply(Walk k) {
     int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
     uint32_t pcount[2] = {0, 0};
-    auto next_scores = [&](int g, bool last) {
-      wait(C::bKF + ks, kr & 1);
-      tc_fence_after();
-      if (!aborted()) {
-        scores(g, ks);
-        mma_commit(bar(C::bSF + g));
-        mma_commit(bar(C::bKE + ks));
-        if (last) mma_commit(bar(C::bQE));
-      }
-      if (++ks == C::kK) ks = 0, ++kr;
-    };
     do {
       const int n = k.piece();
       wait(C::bQF, seg & 1);
-      tc_fence_after();
-      next_scores(0, n == 1);
-      if (n > 1) next_scores(1, n == 2);
-      for (int j = 0; j < n; ++j) {
-        const int g = j & 1;
-        if (j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
-        wait(C::bRF + rs, rr & 1);
-        wait(C::bPF + g, pcount[g]++ & 1);
-        tc_fence_after();
-        if (!aborted()) {
-          values(g, rs, j > 1);
-          mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
+#pragma unroll 1
+      for (int i = 0; i < n + 2; ++i) {
+        const int g = i & 1, j = i - 2;
+        if (j >= 0) {
+          if (j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
+          wait(C::bRF + rs, rr & 1);
+          wait(C::bPF + g, pcount[g]++ & 1);
+          tc_fence_after();
+          if (!aborted()) {
+            values(g, rs, j > 1);
+            mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
+            if (i >= n) mma_commit(bar(C::bOF + g));
+          }
+          if (++rs == C::kReady) rs = 0, ++rr;
         }
-        if (++rs == C::kReady) rs = 0, ++rr;
-        if (j + 2 < n)
-          next_scores(g, j + 3 == n);
-        else if (!aborted())
-          mma_commit(bar(C::bOF + g));
+        if (i < n) {
+          wait(C::bKF + ks, kr & 1);
+          tc_fence_after();
+          if (!aborted()) {
+            scores(g, ks);
+            mma_commit(bar(C::bSF + g));
+            mma_commit(bar(C::bKE + ks));
+            if (i == n - 1) mma_commit(bar(C::bQE));
+          }
+          if (++ks == C::kK) ks = 0, ++kr;
+        }
       }
       ++seg;
     } while (k.next(p, w));
@@ -446,20 +445,12 @@ struct Big {
             sts128(base + swz<128>(r, o % 8 + 1), times(codes_lo(u[2])), times(codes_hi(u[2])), times(codes_lo(u[3])),
                    times(codes_hi(u[3])));
           };
-          if (pos < ctx) {
-            uint4 x[D / 16];
-#pragma unroll
-            for (int ch = 0; ch < D / 16; ++ch) x[ch] = lds128(v + swz<C::kBox>(r, ch));
-#pragma unroll
-            for (int ch = 0; ch < D / 16; ++ch) {
-              const uint32_t u[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
-              put(ch, u);
-            }
-          } else {
+          uint4 ahead = lds128(v + swz<C::kBox>(r, 0));
 #pragma unroll 1
-            for (int ch = 0; ch < D / 16; ++ch) {
-              const uint4 x = lds128(v + swz<C::kBox>(r, ch));
-              uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t u[4] = {ahead.x, ahead.y, ahead.z, ahead.w};
+            ahead = lds128(v + swz<C::kBox>(r, min(ch + 1, D / 16 - 1)));
+            if (pos >= ctx) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (pos >= len) u[i] = 0;
@@ -467,8 +458,8 @@ struct Big {
                 for (int b = 0; b < 4; ++b)
                   if (((u[i] >> (8 * b)) & 0x7fu) == 0x7fu) u[i] &= ~(0xffu << (8 * b)), odd = true;
               }
-              put(ch, u);
             }
+            put(ch, u);
           }
         } else if (pos >= ctx) {
 #pragma unroll 1
