@@ -627,69 +627,52 @@ struct Big {
   // O (accumulate: it holds something) takes `shrink` and the growth of the maximum.
   __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, uint64_t word, float rc, float shrink,
                                        const float4* meta, uint32_t mine, uint32_t colS, float& m, float& l) {
-    float y[128];
-    // The key scales (times scale * log2 e), 16 keys at a time and a batch ahead:
-    // shared memory is busy with the products' operands, and a load that is used at
-    // once waits for it alone (4600 cycles a tile).
-    float4 fa[4], fb[4];
-    auto factors = [&](float4 (&f)[4], int b) {
+    const int d = t * kBigTile - ctx;  // new token of the tile's first key
+    const bool edge = d + kBigTile > 0;
+    float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[32];
+      float4 f[8];
+      tmem_ld_x32(colS + 32 * c, x);
+      if (kCodes) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = meta[4 * b + i];
-    };
-    {
-      uint32_t x0[32], x1[32], x2[32], x3[32];
-      tmem_ld_x32(colS, x0);
-      tmem_ld_x32(colS + 32, x1);
-      tmem_ld_x32(colS + 64, x2);
-      tmem_ld_x32(colS + 96, x3);
-      if (kCodes) factors(fa, 0);
-      tmem_ld_wait_x32(x0);
-      tmem_ld_wait_x32(x1);
-      tmem_ld_wait_x32(x2);
-      tmem_ld_wait_x32(x3);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        y[i] = __uint_as_float(x0[i]);
-        y[32 + i] = __uint_as_float(x1[i]);
-        y[64 + i] = __uint_as_float(x2[i]);
-        y[96 + i] = __uint_as_float(x3[i]);
+        for (int i = 0; i < 8; ++i) f[i] = meta[8 * c + i];
       }
-    }
-    if (kCodes) {
+      tmem_ld_wait_x32(x);
+      float y[32];
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (b < 7) factors(b & 1 ? fa : fb, b + 1);
-        asm volatile("" ::: "memory");  // the loads stay ahead of the products below
+      for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(x[i]);
+      if (kCodes) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 f = b & 1 ? fb[i] : fa[i];
-          const int at = 16 * b + 4 * i;
-          pmul(y[at], y[at + 1], f.x, f.y);
-          pmul(y[at + 2], y[at + 3], f.z, f.w);
+        for (int i = 0; i < 8; ++i) {
+          pmul(y[4 * i], y[4 * i + 1], f[i].x, f[i].y);
+          pmul(y[4 * i + 2], y[4 * i + 3], f[i].z, f[i].w);
         }
       }
-    }
-    const int d = t * kBigTile - ctx;  // new token of the tile's first key
-    if (d + kBigTile > 0) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int d0 = d + 32 * b;
+      if (edge) {
+        const int d0 = d + 32 * c;
         const uint32_t vis = d0 <= -32 ? 0xffffffffu
                              : d0 < 0  ? (uint32_t)(word << -d0) | ((1u << -d0) - 1)
                              : d0 < 64 ? (uint32_t)(word >> d0)
                                        : 0u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[32 * b + i] = (vis >> i) & 1 ? y[32 * b + i] : -INFINITY;
+        for (int i = 0; i < 32; ++i) y[i] = (vis >> i) & 1 ? y[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        top0 = max3f(top0, y[i], y[i + 1]);
+        top1 = max3f(top1, y[i + 2], y[i + 3]);
+        top2 = max3f(top2, y[i + 4], y[i + 5]);
+        top3 = max3f(top3, y[i + 6], y[i + 7]);
+      }
+      if (kCodes || edge) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(y[i]);
+        tmem_st_x32(colS + 32 * c, x);
       }
     }
-    float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 128; i += 8) {
-      top0 = max3f(top0, y[i], y[i + 1]);
-      top1 = max3f(top1, y[i + 2], y[i + 3]);
-      top2 = max3f(top2, y[i + 4], y[i + 5]);
-      top3 = max3f(top3, y[i + 6], y[i + 7]);
-    }
+    if (kCodes || edge) tmem_st_wait();
     const float top = fmaxf(max3f(top0, top1, top2), top3) * rc;  // rc > 0: -inf stays
     const bool grow = top > m + kLazy;  // also the first finite one
     float alpha = 1.f;
@@ -711,15 +694,19 @@ struct Big {
     }
     const float neg = (m == -INFINITY ? 0.f : -m) + (kCodes ? kPLog2 : 0.f);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      uint32_t pw[32];
+      uint32_t x0[32], x1[32], pw[32];
+      tmem_ld_x32(colS + 64 * half, x0);
+      tmem_ld_x32(colS + 64 * half + 32, x1);
+      tmem_ld_wait_x32(x0);
+      tmem_ld_wait_x32(x1);
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
         float e[4];
-        const int at = 64 * half + i;
-        pfma(e[0], e[1], y[at], y[at + 1], rc, neg, neg);
-        pfma(e[2], e[3], y[at + 2], y[at + 3], rc, neg, neg);
+        const uint32_t* x = i < 32 ? x0 + i : x1 + (i - 32);
+        pfma(e[0], e[1], __uint_as_float(x[0]), __uint_as_float(x[1]), rc, neg, neg);
+        pfma(e[2], e[3], __uint_as_float(x[2]), __uint_as_float(x[3]), rc, neg, neg);
 #pragma unroll
         for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
         padd(s0, s1, e[0], e[1]);
