@@ -169,13 +169,18 @@ struct Big {
   uint32_t smem, tmem;
 
   __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&ss.bars[i]); }
-  // Bounded; once one wait has run out nothing waits any more, every role goes
-  // through its loops to the end, and the rows come out as NaN.
+  // Bounded; once one wait of a CTA has run out no thread waits twice more, every
+  // role goes through its loops to the end, and the rows come out as NaN.  (The
+  // flag is looked at only when a barrier is not there yet: the thread that issues
+  // the products passes three barriers a tile.)
+  mutable bool dead = false;
   __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-    volatile int* abort = &ss.abort;
-    if (*abort) return;
-    if (!mbar_wait(bar(i), parity, kWaitNs)) {
-      *abort = 1;
+    if (dead || mbar_try_wait(bar(i), parity)) return;
+    if (aborted()) {
+      dead = true;
+    } else if (!mbar_wait(bar(i), parity, kWaitNs)) {
+      dead = true;
+      *(volatile int*)&ss.abort = 1;
       atomicOr(p.err, kTimedOut);
     }
   }
@@ -213,7 +218,7 @@ struct Big {
           const int id = __shfl_sync(0xffffffffu, ids, (t - t0) * per + lane % per);
           if (round > 0) wait(kEmpty + s, (round & 1) ^ 1);
           __syncwarp();
-          if (!__any_sync(0xffffffffu, aborted())) {
+          if (!__any_sync(0xffffffffu, dead)) {
             const uint32_t full = bar(kFull + s);
             if (lane == 0) {
               if (kKeys && (wrongs >> ((t - t0) * per) & ((1u << per) - 1))) {
@@ -259,7 +264,7 @@ struct Big {
       const uint64_t hi = make_sdesc(smem, 16, 8 * C::kBox, kSwz);
       const uint64_t lo = make_sdesc(smem + kBigRows * C::kBox, 16, 8 * C::kBox, kSwz);
       const uint64_t b = make_sdesc(k, 16, 8 * C::kBox, kSwz);
-#pragma unroll 1
+#pragma unroll
       for (int part = 0; part < 2; ++part) {
         const uint64_t a = part ? lo : hi;
 #pragma unroll
@@ -278,49 +283,53 @@ struct Big {
     const uint32_t v = kCodes ? smem + C::kOffC + r * C::kConv : smem + C::kOffV + r * C::kMat;
     const uint64_t b = make_sdesc(v, C::kChunk, 1024, kSwizzle128B);
     constexpr uint32_t kI = kCodes ? idesc_f16_mn(128, D) : make_idesc_bf16(128, D, true);
-#pragma unroll 2
+#pragma unroll
     for (int kk = 0; kk < kBigTile / 16; ++kk)
       mma_ts(tmem + 256 + D * g, tmem + 128 * g + 8 * kk, b + (uint64_t)((kk * 2048) >> 4), kI, kk > 0 || accumulate);
   }
-  // One thread issues every product, in the order of the tiles:
-  // S(0), S(1), then for each tile j its P V and S(j + 2).
+  // One thread issues every product, in the order of the tiles: S(0), S(1), then
+  // for each tile j its P V and S(j + 2).  The warp's lanes wait for what a step
+  // takes side by side: a look at a barrier is some 200 cycles.
   __device__ __forceinline__ void multiply(Walk k) {
+    const int lane = threadIdx.x % 32;
     int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
-    uint32_t pcount[2] = {0, 0};
+    uint32_t pcount = 0;  // bit g: parity of group g's next probabilities
     do {
       const int n = k.piece();
-      wait(C::bQF, seg & 1);
 #pragma unroll 1
       for (int i = 0; i < n + 2; ++i) {
         const int g = i & 1, j = i - 2;
-        if (j >= 0) {
-          if (j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
-          wait(C::bRF + rs, rr & 1);
-          wait(C::bPF + g, pcount[g]++ & 1);
-          tc_fence_after();
-          if (!aborted()) {
+        if (lane == 0 && i < n) wait(C::bKF + ks, kr & 1);
+        if (lane == 1 && j >= 0) wait(C::bRF + rs, rr & 1);
+        if (lane == 2 && j >= 0) wait(C::bPF + g, pcount >> g & 1);
+        if (lane == 3 && i == 0) wait(C::bQF, seg & 1);
+        if (lane == 4 && j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
+        dead = __any_sync(0xffffffffu, dead);
+        tc_fence_after();
+        if (lane == 0 && !dead) {
+          if (j >= 0) {
             values(g, rs, j > 1);
             mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
             if (i >= n) mma_commit(bar(C::bOF + g));
           }
-          if (++rs == C::kReady) rs = 0, ++rr;
-        }
-        if (i < n) {
-          wait(C::bKF + ks, kr & 1);
-          tc_fence_after();
-          if (!aborted()) {
+          if (i < n) {
             scores(g, ks);
             mma_commit(bar(C::bSF + g));
-            mma_commit(bar(C::bKE + ks));
-            if (i == n - 1) mma_commit(bar(C::bQE));
           }
-          if (++ks == C::kK) ks = 0, ++kr;
         }
+        __syncwarp();
+        if (j >= 0) {
+          pcount ^= 1u << g;
+          if (++rs == C::kReady) rs = 0, ++rr;
+        }
+        if (i < n && ++ks == C::kK) ks = 0, ++kr;
       }
       ++seg;
     } while (k.next(p, w));
-    mma_commit(bar(C::bDrain));
-    mbar_wait(bar(C::bDrain), 0, 100000000ull);
+    if (lane == 0) {
+      mma_commit(bar(C::bDrain));
+      mbar_wait(bar(C::bDrain), 0, 100000000ull);
+    }
   }
 
   // -------------------------------------------------------------- operands --
@@ -497,7 +506,7 @@ struct Big {
     const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);  // this warp's lanes of TMEM
     const uint32_t colS = mine + 128 * g;
     uint32_t scount = 0, ocount[2] = {0, 0};
-    int ms = 0, mr = 0, seg = 0;
+    int ms = 0, mr = 0, ks = 0, seg = 0;
     bool firstp = true;
     do {
       const Seq sq = k.s;
@@ -513,6 +522,10 @@ struct Big {
         if ((j & 1) == g) {
           wait(C::bSF + g, scount++ & 1);
           tc_fence_after();
+          if (threadIdx.x % 128 == 0) {  // the product that read them is done
+            mbar_arrive(bar(C::bKE + ks));
+            if (j == n - 1) mbar_arrive(bar(C::bQE));
+          }
           if (kCodes) wait(C::bMF + ms, mr & 1);
           if (__any_sync(0xffffffffu, busy)) {
             if (kCodes && j == g) rc = ss.rc[seg & 1][r];
@@ -530,6 +543,7 @@ struct Big {
           }
         }
         if (++ms == C::kMeta) ms = 0, ++mr;
+        if (++ks == C::kK) ks = 0;
       }
       // ------------------------------------------------- the segment's end --
       wait(C::bOF + 0, ocount[0]++ & 1);
@@ -744,7 +758,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   };
   if (threadIdx.x == 0) {
     init(C::bKF, C::kK, kCodes ? 33 : 1);  // the copies' bytes, and 32 lanes' scales
-    init(C::bKE, C::kK, kCodes ? 5 : 1);   // the products, and the operand warps
+    init(C::bKE, C::kK, kCodes ? 5 : 1);   // the softmax group that has the scores, and the operand warps
     init(C::bVF, C::kV, 1);
     init(C::bVE, C::kV, kCodes ? 4 : 1);   // the operand warps, or the products
     init(C::bRF, C::kReady, 4);
@@ -783,7 +797,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     } else if (warp == 14) {
       big.template produce<false>(k, &map_v);
     } else if (warp == 13) {
-      if (threadIdx.x % 32 == 0) big.multiply(k);
+      big.multiply(k);
     }
     __syncwarp();
   }
