@@ -41,7 +41,7 @@ constexpr int kBigRows = 128;
 constexpr int kBigThreads = 512;
 // registers after setmaxnreg; 128 threads each: two softmax groups, operands, the
 // rest.  Their sum is the launch's 512 x 128.
-constexpr int kSoftmaxRegs = 192, kOperandRegs = 80, kRestRegs = 48;
+constexpr int kSoftmaxRegs = 176, kOperandRegs = 80, kRestRegs = 80;
 constexpr int kRing = 8;  // segments whose flags are kept
 constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
 
