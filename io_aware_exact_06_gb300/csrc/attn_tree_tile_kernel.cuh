@@ -709,18 +709,15 @@ struct Big {
     const float neg = (m == -INFINITY ? 0.f : -m) + (kCodes ? kPLog2 : 0.f);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      uint32_t x0[32], x1[32], pw[32];
-      tmem_ld_x32(colS + 64 * half, x0);
-      tmem_ld_x32(colS + 64 * half + 32, x1);
-      tmem_ld_wait_x32(x0);
-      tmem_ld_wait_x32(x1);
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[32], pw[16];
+      tmem_ld_x32(colS + 32 * c, x);
+      tmem_ld_wait_x32(x);
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
+      for (int i = 0; i < 32; i += 4) {
         float e[4];
-        const uint32_t* x = i < 32 ? x0 + i : x1 + (i - 32);
-        pfma(e[0], e[1], __uint_as_float(x[0]), __uint_as_float(x[1]), rc, neg, neg);
-        pfma(e[2], e[3], __uint_as_float(x[2]), __uint_as_float(x[3]), rc, neg, neg);
+        pfma(e[0], e[1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]), rc, neg, neg);
+        pfma(e[2], e[3], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]), rc, neg, neg);
 #pragma unroll
         for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
         padd(s0, s1, e[0], e[1]);
@@ -728,7 +725,7 @@ struct Big {
         pw[i / 2] = kCodes ? pack_half(e[0], e[1]) : rows::pack2(e[0], e[1]);
         pw[i / 2 + 1] = kCodes ? pack_half(e[2], e[3]) : rows::pack2(e[2], e[3]);
       }
-      tmem_st_x32(colS + 32 * half, pw);
+      tmem_st_x16(colS + 16 * c, pw);
     }
     tmem_st_wait();
     l = l * alpha + ((s0 + s1) + (s2 + s3));
