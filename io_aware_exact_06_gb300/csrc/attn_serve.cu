@@ -207,7 +207,7 @@ bool few(const Plan& pl) { return pl.rows <= 16; }
 Plan tree_plan(int B, int total, int Hq, int H, int max_new, int max_len, int num_splits) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
-  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : attn::tree::kBigRows;
+  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= attn::tree::kBigRows ? attn::tree::kBigRows : 2 * attn::tree::kBigRows;
   const int64_t T = few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile;
   const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
   const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
@@ -244,12 +244,14 @@ template <int D, bool kCodes>
 int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                 cudaStream_t s) {
   using namespace attn::tree;
-  auto kernel = pl.rows == 8    ? tree_few_kernel<D, kCodes, 1>
-                : pl.rows == 16 ? tree_few_kernel<D, kCodes, 2>
-                                : tree_tile_kernel<D, kCodes>;
-  const int smem = pl.rows == 8    ? FewCfg<D, kCodes, 1>::kSmem
-                   : pl.rows == 16 ? FewCfg<D, kCodes, 2>::kSmem
-                                   : big_smem<D, kCodes>();
+  auto kernel = pl.rows == 8          ? tree_few_kernel<D, kCodes, 1>
+                : pl.rows == 16       ? tree_few_kernel<D, kCodes, 2>
+                : pl.rows == kBigRows ? tree_tile_kernel<D, kCodes, false>
+                                      : tree_tile_kernel<D, kCodes, true>;
+  const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1>::kSmem
+                   : pl.rows == 16       ? FewCfg<D, kCodes, 2>::kSmem
+                   : pl.rows == kBigRows ? big_smem<D, kCodes, false>()
+                                         : big_smem<D, kCodes, true>();
   int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != ATTN_OK) return st;
   if ((st = launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK)

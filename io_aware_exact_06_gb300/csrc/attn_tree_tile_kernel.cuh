@@ -45,15 +45,18 @@ constexpr int kSoftmaxRegs = 176, kOperandRegs = 80, kRestRegs = 80;
 constexpr int kRing = 8;  // segments whose flags are kept
 constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
 
-template <int D, bool kCodes>
+template <int D, bool kCodes, bool kPair>
 struct BigCfg : Row<D, kCodes> {
   using Row<D, kCodes>::kRowBytes;
   static constexpr int kMat = kBigTile * kRowBytes;             // K or V of a tile, as in the cache
   static constexpr int kChunk = kBigTile * 128;                 // 128 rows of 128 bytes
   static constexpr int kConv = kCodes ? kBigTile * D * 2 : 0;   // V in fp16
-  static constexpr int kQ = kBigRows * D * 2;                   // bf16, or the two e4m3 parts
-  static constexpr int kK = kCodes || D == 64 ? 4 : 3;          // stages
-  static constexpr int kV = D == 128 ? 3 : 4;
+  static constexpr int kQ1 = kBigRows * D * 2;                  // bf16, or the two e4m3 parts
+  static constexpr int kQ = (kPair ? 2 : 1) * kQ1;
+  static constexpr int kRows = (kPair ? 2 : 1) * kBigRows;      // of a segment
+  // stages
+  static constexpr int kK = D == 64 ? 4 : kCodes ? (kPair ? 3 : 4) : (kPair ? 2 : 3);
+  static constexpr int kV = D == 64 ? 4 : kCodes && kPair ? 2 : 3;
   static constexpr int kReady = kCodes ? 2 : kV;                // V operand buffers
   static constexpr int kMeta = kCodes ? 4 : 1;                  // tiles whose factors are kept
   static constexpr int kOffK = kQ;
@@ -139,11 +142,11 @@ struct BigShared {
   int vref[4];                // by tile: the exponent F of its values
   float2 ml[2][kBigRows];     // [group]: maxima and sums
   int fend[2];                // [group]: F of its O
-  float rc[2][kBigRows];      // [segment's parity]: log2 units of a row's raw score
+  float rc[2][2 * kBigRows];  // [segment's parity]: log2 units of a row's raw score
 };
-template <int D, bool kCodes>
+template <int D, bool kCodes, bool kPair>
 __host__ __device__ constexpr int big_smem() {
-  return BigCfg<D, kCodes>::kOffShared + (int)sizeof(BigShared) - (kCodes ? 0 : (int)sizeof(float) * 2 * kBigRows);
+  return BigCfg<D, kCodes, kPair>::kOffShared + (int)sizeof(BigShared) - (kCodes ? 0 : (int)sizeof(BigShared::rc));
 }
 
 __device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
@@ -159,9 +162,9 @@ __device__ __forceinline__ uint32_t half_fma2(uint32_t a, uint32_t b, uint32_t c
 // 2^e for e in -126 .. 127, 0 below.
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(e, 127)) << 23); }
 
-template <int D, bool kCodes>
+template <int D, bool kCodes, bool kPair>
 struct Big {
-  using C = BigCfg<D, kCodes>;
+  using C = BigCfg<D, kCodes, kPair>;
   const Params& p;
   const Work& w;
   BigShared& ss;
@@ -186,7 +189,7 @@ struct Big {
   }
   __device__ __forceinline__ bool aborted() const { return *(volatile int*)&ss.abort != 0; }
   __device__ __forceinline__ int head(const Walk& k) const { return k.seg / (k.segs / p.H); }
-  __device__ __forceinline__ int row0(const Walk& k) const { return k.seg % (k.segs / p.H) * kBigRows; }
+  __device__ __forceinline__ int row0(const Walk& k) const { return k.seg % (k.segs / p.H) * C::kRows; }
 
   // ------------------------------------------------------------- producers --
   // One warp copies the keys (and the scales), another the values, each as far
@@ -258,11 +261,11 @@ struct Big {
 
   // -------------------------------------------------------------- products --
   __device__ __forceinline__ void scores(int g, int ks) {
-    const uint32_t k = smem + C::kOffK + ks * C::kMat, d = tmem + 128 * g;
+    const uint32_t k = smem + C::kOffK + ks * C::kMat, d = tmem + 128 * g, q = smem + (kPair ? g * C::kQ1 : 0);
     if (kCodes) {
       constexpr uint32_t kSwz = C::kBox == 128 ? 2 : 4;  // 128- or 64-byte swizzle
-      const uint64_t hi = make_sdesc(smem, 16, 8 * C::kBox, kSwz);
-      const uint64_t lo = make_sdesc(smem + kBigRows * C::kBox, 16, 8 * C::kBox, kSwz);
+      const uint64_t hi = make_sdesc(q, 16, 8 * C::kBox, kSwz);
+      const uint64_t lo = make_sdesc(q + kBigRows * C::kBox, 16, 8 * C::kBox, kSwz);
       const uint64_t b = make_sdesc(k, 16, 8 * C::kBox, kSwz);
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
@@ -271,7 +274,7 @@ struct Big {
         for (int kk = 0; kk < D / 32; ++kk) mma_e4m3(d, a + 2 * kk, b + 2 * kk, idesc_e4m3(128, 128), part | kk);
       }
     } else {
-      const uint64_t a = make_sdesc(smem, 16, 1024, kSwizzle128B), b = make_sdesc(k, 16, 1024, kSwizzle128B);
+      const uint64_t a = make_sdesc(q, 16, 1024, kSwizzle128B), b = make_sdesc(k, 16, 1024, kSwizzle128B);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk / 4) * C::kChunk + (kk % 4) * 32) >> 4);
@@ -295,12 +298,13 @@ struct Big {
     int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
     uint32_t pcount = 0;  // bit g: parity of group g's next probabilities
     do {
-      const int n = k.piece();
+      const int n = kPair ? 2 * k.piece() : k.piece();
 #pragma unroll 1
       for (int i = 0; i < n + 2; ++i) {
         const int g = i & 1, j = i - 2;
-        if (lane == 0 && i < n) wait(C::bKF + ks, kr & 1);
-        if (lane == 1 && j >= 0) wait(C::bRF + rs, rr & 1);
+        const bool first = !kPair || g == 0, last = !kPair || g == 1;  // of a key tile
+        if (lane == 0 && i < n && first) wait(C::bKF + ks, kr & 1);
+        if (lane == 1 && j >= 0 && first) wait(C::bRF + rs, rr & 1);
         if (lane == 2 && j >= 0) wait(C::bPF + g, pcount >> g & 1);
         if (lane == 3 && i == 0) wait(C::bQF, seg & 1);
         if (lane == 4 && j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
@@ -309,7 +313,7 @@ struct Big {
         if (lane == 0 && !dead) {
           if (j >= 0) {
             values(g, rs, j > 1);
-            mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
+            if (last) mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
             if (i >= n) mma_commit(bar(C::bOF + g));
           }
           if (i < n) {
@@ -320,9 +324,9 @@ struct Big {
         __syncwarp();
         if (j >= 0) {
           pcount ^= 1u << g;
-          if (++rs == C::kReady) rs = 0, ++rr;
+          if (last && ++rs == C::kReady) rs = 0, ++rr;
         }
-        if (i < n && ++ks == C::kK) ks = 0, ++kr;
+        if (i < n && last && ++ks == C::kK) ks = 0, ++kr;
       }
       ++seg;
     } while (k.next(p, w));
@@ -333,10 +337,17 @@ struct Big {
   }
 
   // -------------------------------------------------------------- operands --
-  // This thread's query row of the segment into the Q tile.
+  // This thread's query row of the segment (of each of its tiles) into the Q tile.
   __device__ __forceinline__ void write_query(const Walk& k, int seg) {
+#pragma unroll 1
+    for (int i = 0; i < C::kRows / kBigRows; ++i) write_row(k, seg, i);
+    fence_async_smem();
+    mbar_arrive(bar(C::bQF));
+  }
+  __device__ __forceinline__ void write_row(const Walk& k, int seg, int part) {
     const int r = threadIdx.x % 128;
-    const int h = head(k), row = row0(k) + r, M = k.s.n * p.G;
+    const int h = head(k), row = row0(k) + part * kBigRows + r, M = k.s.n * p.G;
+    const uint32_t to = smem + part * C::kQ1;
     const bool live = row < M;
     const int tok = live ? row / p.G : 0;
     const __nv_bfloat16* q = p.q + (int64_t)(k.s.q0 + tok) * p.q_ts + (int64_t)(h * p.G + (live ? row - tok * p.G : 0)) * D;
@@ -344,7 +355,7 @@ struct Big {
 #pragma unroll 8
       for (int ch = 0; ch < D / 8; ++ch) {
         const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 8 * ch) : make_uint4(0, 0, 0, 0);
-        sts128(smem + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), x.x, x.y, x.z, x.w);
+        sts128(to + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), x.x, x.y, x.z, x.w);
       }
     } else {
       uint32_t top = 0;  // largest magnitude: bf16 bits order like the values
@@ -358,7 +369,7 @@ struct Big {
       int e = (int)(top >> 7) - 127;
       e = top == 0 ? 0 : min(max(e, -119), 126);
       const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      ss.rc[seg & 1][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+      ss.rc[seg & 1][part * kBigRows + r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
 #pragma unroll 2
       for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t hi[4], lo[4];
@@ -381,13 +392,11 @@ struct Big {
           hi[2 * half] = hp[0] | hp[1] << 16, hi[2 * half + 1] = hp[2] | hp[3] << 16;
           lo[2 * half] = lp[0] | lp[1] << 16, lo[2 * half + 1] = lp[2] | lp[3] << 16;
         }
-        const uint32_t at = smem + swz<C::kBox>(r, ch);
+        const uint32_t at = to + swz<C::kBox>(r, ch);
         sts128(at, hi[0], hi[1], hi[2], hi[3]);
         sts128(at + kBigRows * C::kBox, lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    fence_async_smem();
-    mbar_arrive(bar(C::bQF));
   }
 
   __device__ __forceinline__ void prepare(Walk k) {
@@ -510,7 +519,7 @@ struct Big {
     bool firstp = true;
     do {
       const Seq sq = k.s;
-      const int M = sq.n * p.G, ctx = sq.len - sq.n, r0 = row0(k), h = head(k);
+      const int M = sq.n * p.G, ctx = sq.len - sq.n, r0 = row0(k) + (kPair ? g * kBigRows : 0), h = head(k);
       const int row = r0 + r, n = k.piece();
       const bool live = row < M, busy = r0 + 32 * (warp % 4) < M;  // the thread; its warp
       const int tok = live ? row / p.G : 0;
@@ -519,7 +528,7 @@ struct Big {
       float rc = p.c, m = -INFINITY, l = 0.f;
       int vref = 0;
       for (int j = 0; j < n; ++j) {
-        if ((j & 1) == g) {
+        if (kPair || (j & 1) == g) {
           wait(C::bSF + g, scount++ & 1);
           tc_fence_after();
           if (threadIdx.x % 128 == 0) {  // the product that read them is done
@@ -528,11 +537,12 @@ struct Big {
           }
           if (kCodes) wait(C::bMF + ms, mr & 1);
           if (__any_sync(0xffffffffu, busy)) {
-            if (kCodes && j == g) rc = ss.rc[seg & 1][r];
+            if (kCodes && j == (kPair ? 0 : g)) rc = ss.rc[seg & 1][(kPair ? g * kBigRows : 0) + r];
             const int f = kCodes ? ss.vref[ms] : 0;
-            const float shrink = j > 1 && f != vref ? pow2(vref - f) : 1.f;
+            const bool more = j > (kPair ? 0 : 1);  // O holds something
+            const float shrink = more && f != vref ? pow2(vref - f) : 1.f;
             vref = f;
-            tile(k.tile + j, g, j > 1, ctx, word, rc, shrink,
+            tile(k.tile + j, g, more, ctx, word, rc, shrink,
                  reinterpret_cast<const float4*>(smem_ptr + C::kOffMeta + ms * 512), mine, colS, m, l);
           }
           tc_fence_before();
@@ -546,8 +556,8 @@ struct Big {
         if (++ks == C::kK) ks = 0;
       }
       // ------------------------------------------------- the segment's end --
-      wait(C::bOF + 0, ocount[0]++ & 1);
-      if (n > 1) wait(C::bOF + 1, ocount[1]++ & 1);
+      if (!kPair || g == 0) wait(C::bOF + 0, ocount[0]++ & 1);
+      if (kPair ? g == 1 : n > 1) wait(C::bOF + 1, ocount[1]++ & 1);
       tc_fence_after();
       close_row(m, l);
       // (the other group has read the last segment's: O is free only when it has)
@@ -563,32 +573,34 @@ struct Big {
         ss.hidden[old][0] = ss.hidden[old][1] = 0;
       }
       if (__any_sync(0xffffffffu, busy)) {
-        const float2 a = ss.ml[0][r], b = ss.ml[1][r];
+        const float2 a = kPair ? make_float2(m, l) : ss.ml[0][r];
+        const float2 b = kPair ? make_float2(-INFINITY, 0.f) : ss.ml[1][r];
         const float mm = fmaxf(a.x, b.x);
         const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), wb = b.x == -INFINITY ? 0.f : ex2(b.x - mm);
         const float ls = (wa != 0.f ? wa * a.y : 0.f) + (wb != 0.f ? wb * b.y : 0.f);
         const float inv = ls != 0.f ? 1.f / ls : 0.f;
         // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
-        const float ua = kCodes ? wa * pow2(ss.fend[0] - 6) : wa, ub = kCodes ? wb * pow2(ss.fend[1] - 6) : wb;
+        const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0]) - 6) : wa, ub = kCodes ? wb * pow2(ss.fend[1] - 6) : wb;
         const bool whole = k.tile == 0 && n == k.tiles;
         const int slot = whole ? -1 : 2 * (int)blockIdx.x + !firstp;
-        const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * kBigRows + r;
-        if (live && g == 0) {
+        const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * C::kRows + (row - row0(k));
+        if (live && (kPair || g == 0)) {
           float lse = ls != 0.f ? (mm + lg2(ls) - (kCodes ? kPLog2 : 0.f)) * 0.69314718055994531f : -INFINITY;
           if (poison) lse = whole ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
           (whole ? p.lse : p.lse_part)[at] = lse;
         }
 #pragma unroll 1
-        for (int col = g * (D / 2); col < (g + 1) * (D / 2); col += 32) {
+        for (int col = kPair ? 0 : g * (D / 2); col < (kPair ? D : (g + 1) * (D / 2)); col += 32) {
           uint32_t xa[32], xb[32];
-          tmem_ld_x32(mine + 256 + col, xa);
-          tmem_ld_x32(mine + 256 + D + col, xb);
+          tmem_ld_x32(mine + 256 + (kPair ? g * D : 0) + col, xa);
+          if (!kPair) tmem_ld_x32(mine + 256 + D + col, xb);
           tmem_ld_wait_x32(xa);
-          tmem_ld_wait_x32(xb);
+          if (!kPair) tmem_ld_wait_x32(xb);
           float f[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            f[i] = (wa != 0.f ? ua * __uint_as_float(xa[i]) : 0.f) + (wb != 0.f ? ub * __uint_as_float(xb[i]) : 0.f);
+            f[i] = wa != 0.f ? ua * __uint_as_float(xa[i]) : 0.f;
+            if (!kPair) f[i] += wb != 0.f ? ub * __uint_as_float(xb[i]) : 0.f;
             f[i] = inv != 0.f ? f[i] * inv : 0.f;
             if (poison) f[i] = NAN;
           }
@@ -732,14 +744,14 @@ struct Big {
   }
 };
 
-template <int D, bool kCodes>
+template <int D, bool kCodes, bool kPair>
 __global__ void __launch_bounds__(kBigThreads, 1)
 tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ Params p, const __grid_constant__ Work w) {
-  using C = BigCfg<D, kCodes>;
+  using C = BigCfg<D, kCodes, kPair>;
   extern __shared__ __align__(1024) uint8_t smem_big[];
   static_assert(C::kBars <= 48, "barriers");
-  static_assert(big_smem<D, kCodes>() <= 227 * 1024, "shared memory");
+  static_assert(big_smem<D, kCodes, kPair>() <= 227 * 1024, "shared memory");
   BigShared& ss = *reinterpret_cast<BigShared*>(smem_big + C::kOffShared);
   const int warp = threadIdx.x / 32;
   grid_dep_wait();
@@ -755,18 +767,19 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   };
   if (threadIdx.x == 0) {
     init(C::bKF, C::kK, kCodes ? 33 : 1);  // the copies' bytes, and 32 lanes' scales
-    init(C::bKE, C::kK, kCodes ? 5 : 1);   // the softmax group that has the scores, and the operand warps
+    constexpr int kBoth = kPair ? 2 : 1;                   // softmax groups that take a key tile
+    init(C::bKE, C::kK, kBoth + (kCodes ? 4 : 0));         // they, and the operand warps
     init(C::bVF, C::kV, 1);
     init(C::bVE, C::kV, kCodes ? 4 : 1);   // the operand warps, or the products
     init(C::bRF, C::kReady, 4);
     init(C::bRE, C::kReady, 1);
     init(C::bMF, C::kMeta, 4);
-    init(C::bME, C::kMeta, 4);
+    init(C::bME, C::kMeta, 4 * kBoth);
     init(C::bSF, 2, 1);
     init(C::bPF, 2, 128);
     init(C::bOF, 2, 1);
     init(C::bQF, 1, 128);
-    init(C::bQE, 1, 1);
+    init(C::bQE, 1, kBoth);
     init(C::bOFree, 1, 256);
     init(C::bDrain, 1, 1);
     fence_mbar_init();
@@ -780,7 +793,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Big<D, kCodes> big{p, w, ss, smem_big, smem_u32(smem_big), ss.tmem};
+  Big<D, kCodes, kPair> big{p, w, ss, smem_big, smem_u32(smem_big), ss.tmem};
   if (warp < 8) {
     regs_inc<kSoftmaxRegs>();
     big.softmax(k, warp / 4);
