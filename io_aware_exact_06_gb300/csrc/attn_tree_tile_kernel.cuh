@@ -303,11 +303,13 @@ struct Big {
       for (int i = 0; i < n + 2; ++i) {
         const int g = i & 1, j = i - 2;
         const bool first = !kPair || g == 0, last = !kPair || g == 1;  // of a key tile
-        if (lane == 0 && i < n && first) wait(C::bKF + ks, kr & 1);
-        if (lane == 1 && j >= 0 && first) wait(C::bRF + rs, rr & 1);
-        if (lane == 2 && j >= 0) wait(C::bPF + g, pcount >> g & 1);
-        if (lane == 3 && i == 0) wait(C::bQF, seg & 1);
-        if (lane == 4 && j == 0 && seg > 0) wait(C::bOFree, (seg - 1) & 1);
+        int on = -1, parity = 0;  // what this lane waits for
+        if (lane == 0 && i < n && first) on = C::bKF + ks, parity = kr;
+        if (lane == 1 && j >= 0 && first) on = C::bRF + rs, parity = rr;
+        if (lane == 2 && j >= 0) on = C::bPF + g, parity = pcount >> g;
+        if (lane == 3 && i == 0) on = C::bQF, parity = seg;
+        if (lane == 4 && j == 0 && seg > 0) on = C::bOFree, parity = seg - 1;
+        if (on >= 0) wait(on, parity & 1);
         dead = __any_sync(0xffffffffu, dead);
         tc_fence_after();
         if (lane == 0 && !dead) {
