@@ -203,11 +203,15 @@ bool few(const Plan& pl) { return pl.rows <= 16; }
 
 // Query rows of a segment: the smallest tile that holds max_new * G of them.
 // Few rows: as many persistent warps as fit the SMs; more: a persistent CTA an SM
-// with tcgen05 products.  num_splits caps the pieces of a segment instead.
-Plan tree_plan(int B, int total, int Hq, int H, int max_new, int max_len, int num_splits) {
+// with tcgen05 products.  9 to 16 rows take the former at d = 64 only: their sums
+// and query rows are 128 registers a lane at d = 128 (12 rows, 16 sequences of 4096
+// keys, bf16 / e4m3, few : many: d = 64 56 / 56 : 63 / 75 us, d = 128 106 / 113 :
+// 83 / 86 us).  num_splits caps the pieces of a segment instead.
+Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
-  pl.rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= attn::tree::kBigRows ? attn::tree::kBigRows : 2 * attn::tree::kBigRows;
+  constexpr int kBig = attn::tree::kBigRows;
+  pl.rows = M <= 8 ? 8 : M <= 16 && d == 64 ? 16 : M <= kBig ? kBig : 2 * kBig;
   const int64_t T = few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile;
   const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
   const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
@@ -245,11 +249,11 @@ int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
                 cudaStream_t s) {
   using namespace attn::tree;
   auto kernel = pl.rows == 8          ? tree_few_kernel<D, kCodes, 1>
-                : pl.rows == 16       ? tree_few_kernel<D, kCodes, 2>
+                : pl.rows == 16       ? tree_few_kernel<64, kCodes, 2>  // d = 64 only
                 : pl.rows == kBigRows ? tree_tile_kernel<D, kCodes, false>
                                       : tree_tile_kernel<D, kCodes, true>;
   const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1>::kSmem
-                   : pl.rows == 16       ? FewCfg<D, kCodes, 2>::kSmem
+                   : pl.rows == 16       ? FewCfg<64, kCodes, 2>::kSmem
                    : pl.rows == kBigRows ? big_smem<D, kCodes, false>()
                                          : big_smem<D, kCodes, true>();
   int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
@@ -449,7 +453,7 @@ extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d
                                           int max_len, int num_splits) {
   if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
   if (B == 0 || total == 0 || max_new == 0) return 0;
-  return tree_bytes(tree_plan(B, total, Hq, H, max_new, max_len, num_splits), d);
+  return tree_bytes(tree_plan(B, total, Hq, H, d, max_new, max_len, num_splits), d);
 }
 
 extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
@@ -469,7 +473,7 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(mask, 8) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGN;
-  const Plan pl = tree_plan(B, total, Hq, cache->H, max_new, max_len, num_splits);
+  const Plan pl = tree_plan(B, total, Hq, cache->H, d, max_new, max_len, num_splits);
   if (!pl.fits) return ATTN_ERR_SHAPE;
   const size_t need = tree_bytes(pl, d);
   if (!workspace || workspace_bytes < need) return ATTN_ERR_SCRATCH;
