@@ -6,15 +6,15 @@
 // are its G = Hq / H query heads for every new token, row = token * G + head, so
 // that keys and values are read once for all of them: per key the products take
 // 4 M d flops for M rows against 4 d bytes (bf16) or 2 d bytes (e4m3) of cache.
-// Up to 16 rows run on the warp-level products (attn_tree_few_kernel.cuh), more on
-// tcgen05 (attn_tree_tile_kernel.cuh); attn_tree_work.cuh cuts the work.
+// Up to 8 rows (16 at d = 64) run on the warp-level products
+// (attn_tree_few_kernel.cuh), more on tcgen05 (attn_tree_tile_kernel.cuh);
+// attn_tree_work.cuh cuts the work.
 //
-// With e4m3 codes a score is code . q times the key's scale, and a probability
-// takes the value's scale before it meets the codes of V, as fp16: codes are exact
-// in it and its rounding (2^-11) is below the output's (2^-8).  The running maximum
-// is taken over log2(probability * value scale), so that this operand stays in
-// range whatever the scales.  With a bf16 cache probabilities are rounded to bf16,
-// the type of V (tensor products take one type).  Sums, maxima and scores are fp32.
+// With e4m3 codes a score is code . q times the key's scale, and the products with V
+// take fp16 operands, whose rounding (2^-11) is below the output's (2^-8); each
+// kernel says which of them takes the value's scale.  With a bf16 cache
+// probabilities are rounded to bf16, the type of V (tensor products take one type).
+// Sums, maxima and scores are fp32.
 #pragma once
 
 #include "attn_rows.cuh"

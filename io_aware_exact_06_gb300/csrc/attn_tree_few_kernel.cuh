@@ -1,7 +1,10 @@
 // Attention of the newest tokens over the paged cache for few query rows of a key
 // head, on the warp-level tensor instructions.  Codes become fp16 in registers; a
 // query row is divided by a power of two that brings its largest channel into
-// [1, 2), which keeps its bf16 values exact in fp16 down to 2^-14 of that.
+// [1, 2), which keeps its bf16 values exact in fp16 down to 2^-14 of that.  A
+// probability takes its value's scale before it meets the codes of V; the running
+// maximum is taken over log2(probability * value scale), so that this fp16 operand
+// stays in range whatever the scales.
 #pragma once
 
 #include "attn_tree_work.cuh"

@@ -2,19 +2,28 @@
 // key head (a tree of drafts times the heads of a group), on the tensor cores'
 // tcgen05 products.
 //
-// A segment is (sequence, key head, tile of 128 query rows); persistent CTAs, one
-// an SM, take equal shares of the line of 128-key tiles.  A key tile costs the
-// tensor core 1024 cycles (S = Q K^T and O += P V, 128 x 128 x d each) whatever
-// part of the 128 rows is real, below the 1410 cycles that its e4m3 bytes (2820:
-// bf16) take from HBM; with several row tiles of one head the key tiles come from
-// L2 and the products and the softmax bound it.
+// A segment is (sequence, key head, 128 or 256 query rows); persistent CTAs, one an
+// SM, take equal shares of the line of 128-key tiles.  A key tile costs the tensor
+// core 1024 cycles for 128 rows (S = Q K^T and O += P V, 128 x 128 x d each; d = 128)
+// whatever part of the rows is real; its e4m3 bytes take 1410 cycles from HBM (bf16:
+// 2820).  Trees of 64 drafts (8 sequences of up to 16384 keys, 64 query and 8 key
+// heads, d = 128) take 290 us with e4m3 codes and 248 us with a bf16 cache, 800 and
+// 940 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
+// 600 cycles, softmax 2100 or 1650, P V 600, and some 200 for each look at a
+// barrier), of which two are under way at a time.
 //
-// Warps: 0-3 and 4-7 softmax groups A and B (a thread owns a row; A takes the
-// even key tiles of a segment, B the odd ones, each with its own S and O in TMEM,
-// so that one group's softmax runs beside the other's products; they meet at the
-// segment's end); 8-11 operands: they write the segment's Q tile, turn a tile's
-// codes of V into fp16 values, and clean values that rows may not see; 12 and 14 TMA producers of keys and values;
-// 13 MMA issuer.
+// Warps: 0-3 and 4-7 softmax groups A and B (a thread owns a row), each with its own
+// S and O in TMEM, so that one group's softmax runs beside the other's products;
+// 8-11 operands: they write the segment's Q tile, turn a tile's codes of V into fp16
+// values, and clean values that rows may not see; 12 and 14 TMA producers of keys and
+// values; 13 issues the products.  kPair, for more than 128 rows of a head: A and B
+// take the two row tiles over the same key tiles, which are copied and converted once
+// for both (trees of 64 drafts 311 -> 299 us, bf16 320 -> 268).  Else: A takes the
+// even key tiles of a segment, B the odd ones, and they meet at the segment's end.
+//
+// The roles' code lies in loops kept short (32 keys of a softmax row, 16 channels
+// of a conversion at a time): fourteen warps run six different loops at once, and
+// unrolled through a tile they wait for instructions (424 us against 311).
 //
 // With e4m3 codes S = (Q_hi + Q_lo) K^T takes the codes of K as they lie in the
 // cache: a query row, scaled by a power of two to at most 256, is the sum of two
@@ -25,9 +34,7 @@
 // with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-12, F a running
 // exponent of the segment's value scales (all of a CTA's tiles; O is rescaled when
 // it grows), which leaves values 2^-30 of the largest their full precision.  P is
-// fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.  (With the value scale
-// in P, as for few rows, a score took three factors from shared memory and 1200
-// instructions a row and tile, 4500 cycles; 420 us for trees of 64 drafts.)
+// fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.
 #pragma once
 
 #include "attn_tree_work.cuh"
@@ -39,8 +46,9 @@ constexpr int kBigTile = 128;  // keys
 constexpr int kLogBigTile = 7;
 constexpr int kBigRows = 128;
 constexpr int kBigThreads = 512;
-// registers after setmaxnreg; 128 threads each: two softmax groups, operands, the
-// rest.  Their sum is the launch's 512 x 128.
+// Registers after setmaxnreg; 128 threads each: two softmax groups, operands, the
+// rest.  Their sum is the launch's 512 x 128, and with them nothing spills (192, 80
+// and 48 spilled 260 bytes: 340 us against 313).
 constexpr int kSoftmaxRegs = 176, kOperandRegs = 80, kRestRegs = 80;
 constexpr int kRing = 8;  // segments whose flags are kept
 constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
@@ -290,9 +298,10 @@ struct Big {
     for (int kk = 0; kk < kBigTile / 16; ++kk)
       mma_ts(tmem + 256 + D * g, tmem + 128 * g + 8 * kk, b + (uint64_t)((kk * 2048) >> 4), kI, kk > 0 || accumulate);
   }
-  // One thread issues every product, in the order of the tiles: S(0), S(1), then
-  // for each tile j its P V and S(j + 2).  The warp's lanes wait for what a step
-  // takes side by side: a look at a barrier is some 200 cycles.
+  // One thread issues every product, in the order of the steps (a step is a key tile,
+  // or with kPair a key tile of one row tile): S(0), S(1), then for each step j its
+  // P V and S(j + 2).  The warp's lanes look at the barriers of a step together: one
+  // look is some 200 cycles (370 -> 340 us, and 299 -> 290 in one call).
   __device__ __forceinline__ void multiply(Walk k) {
     const int lane = threadIdx.x % 32;
     int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
