@@ -81,12 +81,18 @@ int attn_cache_read(const attn_paged_cache *cache, void *k, void *v, const int32
  * o: [total, Hq, d] bf16, lse: [total, Hq] fp32, contiguous.  mask: int64
  * [total] on the device.
  * max_new >= every n_b, at most 64; max_len >= every seqlens[b] (they size the
- * launch; larger values on the device are an error).  num_splits: key ranges of
- * the longest sequence, 1..256, or 0 to choose.
- * workspace: attn_fwd_tree_workspace(...) bytes of the caller's device memory
- * (0 when the keys are not cut), 16-byte aligned, not initialised, in use until
- * the call's work on stream has finished; calls that may run at the same time
- * need one each.  Missing or too small: ATTN_ERR_SCRATCH.
+ * launch; larger values on the device are an error).  All sequences' keys, taken
+ * together, are cut into equal shares for the GPU; num_splits, 1..256, bounds the
+ * pieces that the keys of a sequence of max_len fall into (num_splits + 1 at most;
+ * shorter sequences fall into fewer), 0 leaves them to the launch.  Results depend
+ * on it, on the lengths and on the sizes by rounding alone, and repeat bit for bit.
+ * workspace: attn_fwd_tree_workspace(...) bytes of the caller's device memory, for
+ * the pieces (it does not grow with the lengths beyond a launch's pieces), 16-byte
+ * aligned, not initialised, in use until the call's work on stream has finished;
+ * calls that may run at the same time need one each.  Missing or too small:
+ * ATTN_ERR_SCRATCH.
+ * ATTN_ERR_SHAPE also where B * H * max_len keys are more than 2^31 tiles of 32 (of
+ * 128, for more than 16 query rows a key head: times the tiles of rows).
  * Errors in the error word: ATTN_ERR_SEQLENS (lengths as above; the rows of
  * that sequence are not written), ATTN_ERR_INDEX (a page outside the cache; the
  * rows that read it come out as NaN), ATTN_ERR_DEVICE_TIMEOUT (NaN as well).

@@ -33,7 +33,7 @@
 // product does; the softmax multiplies a score by its key's scale.  V is converted
 // with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-12, F a running
 // exponent of the segment's value scales (all of a CTA's tiles; O is rescaled when
-// it grows), which leaves values 2^-30 of the largest their full precision.  P is
+// it grows), which leaves values 2^-26 of the largest their full precision.  P is
 // fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.
 #pragma once
 
