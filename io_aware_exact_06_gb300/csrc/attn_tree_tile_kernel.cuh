@@ -31,7 +31,7 @@
 // row's largest channel, where the quantum 2^-9 of the small part ends it: an
 // error below 2^-18 of the largest), and the two e4m3 products cost what one fp16
 // product does; the softmax multiplies a score by its key's scale.  V is converted
-// with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-12, F a running
+// with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-11, F a running
 // exponent of the segment's value scales (all of a CTA's tiles; O is rescaled when
 // it grows), which leaves values 2^-26 of the largest their full precision.  P is
 // fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.

@@ -6,7 +6,8 @@ the largest scale * sum |q k| of a row:
   - O is rounded to bf16 once: 2^-8 |O|;
   - probabilities are rounded to bf16 (2^-8 of each, so 2^-8 A), or with codes,
     times the value scale, to fp16 (2^-11 A, and 2^-25 of the largest weight for
-    each key below fp16's normal range: 2^-25 L max|v|);
+    each key below fp16's normal range: 2^-25 L max|v|); where many rows share a
+    key, probabilities and scaled values are, each (2^-11 A twice, so 2^-10 A);
   - scores are fp32 sums of d products (below 2^-19 S), a probability errs by
     its score's error and that of exp2 and the sums (2^-18): (2^-19 S + 2^-17) A;
   - LSE: 2^-19 S + 2^-20 |LSE| + 2^-18.
@@ -93,7 +94,7 @@ def check(c, q, lens, ns, mask, got, scale=None, rows=None):
     assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
     fine = ~empty
     vmax = v[torch.isfinite(v)].abs().max()
-    step = 2.0 ** -11 if codes else 2.0 ** -8
+    step = 2.0 ** -10 if codes else 2.0 ** -8
     tol = 2.0 ** -8 * wo.abs() + A * (step + 2.0 ** -19 * S[..., None] + 2.0 ** -17)
     if codes:
         tol = tol + 2.0 ** -25 * max(lens) * vmax
