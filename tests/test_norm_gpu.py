@@ -214,3 +214,20 @@ def test_positions_outside_the_table(dev, bad, axis):
     for i, n in enumerate("qk"):
         _, dw, _, mag = ref.norm_rope_backward(sub[n].cpu(), x["w" + n], sub["g" + n].cpu(), c, s, 128, False, EPS)
         assert ((got[2 + i].cpu().double() - dw).abs() <= 2 ** -16 * mag).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradient_without_eps(dev, d):
+    """eps = 0 and head counts that leave rows of a warp without a head: those are not rows of zeros."""
+    T, Hq, Hk = 19, 5, 3
+    x = inputs(77, T, Hq, Hk, d, d, 1, None)
+    y = to(dev, x)
+    got = fa.qk_norm_rope_backward(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"], y["gq"],
+                                   y["gk"], eps=0.0, sections=y["sections"], interleaved=False)
+    assert fa.attn_last_device_error() == 0
+    c, s = ref.angles(x["cos"], x["sin"], x["positions"], x["sections"])
+    for i, n in enumerate("qk"):
+        dx, dw, dx_mag, dw_mag = ref.norm_rope_backward(x[n], x["w" + n], x["g" + n], c, s, d, False, 0.0)
+        assert ((got[i].cpu().double() - dx).abs() <= 2 ** -8 * dx.abs() + 2 ** -19 * dx_mag).all(), n
+        rows = T * x[n].shape[1]
+        assert ((got[2 + i].cpu().double() - dw).abs() <= (2 ** -20 + 2 ** -24 * (rows + 80)) * dw_mag).all(), n
