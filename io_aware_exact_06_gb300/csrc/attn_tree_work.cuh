@@ -211,17 +211,26 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   const int64_t rowi = ((int64_t)blockIdx.x * 8 + warp) / kPerRow;
   if (rowi >= (int64_t)p.total * p.Hq) return;  // with eight warps to a row, the whole CTA
   const int t = (int)(rowi / p.Hq), head = (int)(rowi - (int64_t)t * p.Hq);
-  const int b = rows::find_sequence(p.cu, p.B, t);
-  if (b >= p.B) return;
-  Seq sq;
-  if (!load_seq(p, b, sq) || t < sq.q0 || t >= sq.q0 + sq.n) return;
-  int total = 0, before = 0;
+  // The row's sequence and its place in the line: a lane reads sequences lane,
+  // lane + 32, ..  The first that holds t has it.
+  Seq sq{}, other;
+  int total = 0, before = 0, tiles0 = 0, b = p.B;
   for (int i = lane; i < p.B; i += 32) {
-    Seq other;
-    const int n = line_tiles(p, w, i, false, other);
-    total += n;
-    before += i < b ? n : 0;
+    tiles0 = line_tiles(p, w, i, false, other);
+    total += tiles0;
+    if (tiles0 && b == p.B && t >= other.q0 && t < other.q0 + other.n) b = i, sq = other;
   }
+  const int mine = b;
+  b = __reduce_min_sync(0xffffffffu, b);
+  if (b == p.B) return;
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine == b)) - 1;
+  sq.q0 = __shfl_sync(0xffffffffu, sq.q0, src);
+  sq.n = __shfl_sync(0xffffffffu, sq.n, src);
+  sq.len = __shfl_sync(0xffffffffu, sq.len, src);
+  if (p.B <= 32)
+    before = lane < b ? tiles0 : 0;
+  else
+    for (int i = lane; i < b; i += 32) before += line_tiles(p, w, i, false, other);
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
     total += __shfl_xor_sync(0xffffffffu, total, off);
@@ -236,6 +245,21 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   if (c0 == c1) return;
   const bool inside = first != c0 * share;  // the first piece begins inside its share
   auto at = [&](int c) { return (((int64_t)2 * c + (c == c0 && inside)) * w.heads + sub) * w.rows + r; };
+  // kBatch pieces on their way at a time, the first of them beside the maxima
+  constexpr int kBatch = 8;
+  float x[kBatch][kPer], ls[kBatch];
+  auto load = [&](int from) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int c = from + j * kPerRow;
+      ls[j] = -INFINITY;
+      if (c > c1) continue;
+      ls[j] = p.lse_part[at(c)];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[j][i] = p.o_part[at(c) * D + lane * kPer + i];
+    }
+  };
+  load(c0 + k);
   float top = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
 #pragma unroll
@@ -243,17 +267,18 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   float acc[kPer], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0 + k; c <= c1; c += kPerRow) {
-    const float ls = p.lse_part[at(c)];
-    float x[kPer];
+  for (int c = c0 + k;;) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = p.o_part[at(c) * D + lane * kPer + i];
-    if (ls == -INFINITY) continue;
-    const float wt = __expf(ls - top);  // a NaN stays one: fmaxf has passed it over
-    sum += wt;
+    for (int j = 0; j < kBatch; ++j) {
+      if (ls[j] == -INFINITY) continue;
+      const float wt = __expf(ls[j] - top);  // a NaN stays one: fmaxf has passed it over
+      sum += wt;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wt, x[i], acc[i]);
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wt, x[j][i], acc[i]);
+    }
+    c += kBatch * kPerRow;
+    if (c > c1) break;
+    load(c);
   }
   if (kPerRow > 1) {  // the row's warps are the CTA's
     if (lane == 0) sm_sum[k] = sum;
