@@ -255,8 +255,14 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
       ls[j] = -INFINITY;
       if (c > c1) continue;
       ls[j] = p.lse_part[at(c)];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) x[j][i] = p.o_part[at(c) * D + lane * kPer + i];
+      const float* from_part = p.o_part + at(c) * D + lane * kPer;
+      if (kPer == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(from_part);
+        x[j][0] = y.x, x[j][1] = y.y, x[j][kPer - 2] = y.z, x[j][kPer - 1] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(from_part);
+        x[j][0] = y.x, x[j][1] = y.y;
+      }
     }
   };
   load(c0 + k);
