@@ -261,8 +261,9 @@ int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
   if ((st = launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK)
     return st;
   const int64_t rows = (int64_t)p.total * p.Hq;
-  return pl.many ? launch(tree_join_kernel<D, 8>, rows, 256, 0, s, p, pl.work)
-                 : launch(tree_join_kernel<D, 1>, (rows + 7) / 8, 256, 0, s, p, pl.work);
+  if (pl.many) return launch(tree_join_kernel<D, 8>, rows, 256, 0, s, p, pl.work, 1);
+  const int run = (int)std::clamp<int64_t>(rows / (32 * kPlanSms), 1, 8);  // 32 warps an SM at least
+  return launch(tree_join_kernel<D, 1>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, p, pl.work, run);
 }
 
 }  // namespace

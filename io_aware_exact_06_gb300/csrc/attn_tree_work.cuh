@@ -197,114 +197,136 @@ struct PieceEnd {
 };
 
 // Pieces of a row joined: weights e^(LSE - max), as for split keys elsewhere in
-// the library.  kPerRow warps for each (new token, query head): one, or eight
-// where segments are cut into many pieces; warp k takes pieces k, k + kPerRow, ..
+// the library.  A row, (new token, query head), has one warp, or eight where segments
+// are cut into many pieces (warp k takes pieces k, k + kPerRow, ..); a warp takes
+// `run` rows one after the other, and looks a segment's place in the line up once
+// (trees of 64 drafts, 30000 rows: 292 us in all with a row to a warp, 284 so).
 // Rows whose segment lies in one share (or whose sequence the attention refused)
 // are left as they are.
 template <int D, int kPerRow>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ Params p, const __grid_constant__ Work w) {
+__global__ void __launch_bounds__(256, kPerRow == 1 ? 4 : 3)
+tree_join_kernel(const __grid_constant__ Params p, const __grid_constant__ Work w, int run) {
   constexpr int kPer = D / 32;
   __shared__ float sm_sum[8], sm_acc[8][D];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp % kPerRow;
-  const int64_t rowi = ((int64_t)blockIdx.x * 8 + warp) / kPerRow;
-  if (rowi >= (int64_t)p.total * p.Hq) return;  // with eight warps to a row, the whole CTA
-  const int t = (int)(rowi / p.Hq), head = (int)(rowi - (int64_t)t * p.Hq);
-  // The row's sequence and its place in the line: a lane reads sequences lane,
+  const int64_t all = (int64_t)p.total * p.Hq, row0 = ((int64_t)blockIdx.x * 8 + warp) / kPerRow * run;
+  Seq sq{};
+  int total = 0, before = 0;
+  // The sequence of token t and its place in the line: a lane reads sequences lane,
   // lane + 32, ..  The first that holds t has it.
-  Seq sq{}, other;
-  int total = 0, before = 0, tiles0 = 0, b = p.B;
-  for (int i = lane; i < p.B; i += 32) {
-    tiles0 = line_tiles(p, w, i, false, other);
-    total += tiles0;
-    if (tiles0 && b == p.B && t >= other.q0 && t < other.q0 + other.n) b = i, sq = other;
-  }
-  const int mine = b;
-  b = __reduce_min_sync(0xffffffffu, b);
-  if (b == p.B) return;
-  const int src = __ffs(__ballot_sync(0xffffffffu, mine == b)) - 1;
-  sq.q0 = __shfl_sync(0xffffffffu, sq.q0, src);
-  sq.n = __shfl_sync(0xffffffffu, sq.n, src);
-  sq.len = __shfl_sync(0xffffffffu, sq.len, src);
-  if (p.B <= 32)
-    before = lane < b ? tiles0 : 0;
-  else
-    for (int i = lane; i < b; i += 32) before += line_tiles(p, w, i, false, other);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
-  const int h = head / p.G, row = (t - sq.q0) * p.G + head - h * p.G;
-  const int group = h / w.heads, sub = h - group * w.heads;
-  const int mtiles = (sq.n * p.G + w.rows - 1) / w.rows, mt = row / w.rows, r = row - mt * w.rows;
-  const int share = share_of(total, w), tiles = seq_tiles(sq, w);
-  const int first = before + (group * mtiles + mt) * tiles;
-  const int c0 = first / share, c1 = (first + tiles - 1) / share;
-  if (c0 == c1) return;
-  const bool inside = first != c0 * share;  // the first piece begins inside its share
-  auto at = [&](int c) { return (((int64_t)2 * c + (c == c0 && inside)) * w.heads + sub) * w.rows + r; };
-  // kBatch pieces on their way at a time, the first of them beside the maxima
-  constexpr int kBatch = 8;
-  float x[kBatch][kPer], ls[kBatch];
-  auto load = [&](int from) {
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int c = from + j * kPerRow;
-      ls[j] = -INFINITY;
-      if (c > c1) continue;
-      ls[j] = p.lse_part[at(c)];
-      const float* from_part = p.o_part + at(c) * D + lane * kPer;
-      if (kPer == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(from_part);
-        x[j][0] = y.x, x[j][1] = y.y, x[j][kPer - 2] = y.z, x[j][kPer - 1] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(from_part);
-        x[j][0] = y.x, x[j][1] = y.y;
+  auto find = [&](int t) {
+    Seq other;
+    int n = 0, b = p.B;
+    total = before = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      n = line_tiles(p, w, i, false, other);
+      total += n;
+      if (n && b == p.B && t >= other.q0 && t < other.q0 + other.n) b = i, sq = other;
+    }
+    const int mine = b;
+    b = __reduce_min_sync(0xffffffffu, b);
+    const int src = __ffs(__ballot_sync(0xffffffffu, mine == b)) - 1;
+    sq.q0 = __shfl_sync(0xffffffffu, sq.q0, src);
+    sq.n = __shfl_sync(0xffffffffu, sq.n, src);
+    sq.len = __shfl_sync(0xffffffffu, sq.len, src);
+    if (b == p.B) sq.n = 0;
+    if (p.B <= 32)
+      before = lane < b ? n : 0;
+    else
+      for (int i = lane; i < b; i += 32) before += line_tiles(p, w, i, false, other);
+    total = __reduce_add_sync(0xffffffffu, total);
+    before = __reduce_add_sync(0xffffffffu, before);
+    return b < p.B;
+  };
+  int left = 0, r = 0, c0 = 0, c1 = 0, sub = 0;  // rows that follow in the same segment; row of it, its pieces
+  bool inside = false, cut = false;
+  const int64_t end = min(row0 + run, all);
+#pragma unroll 1
+  for (int64_t rowi = row0; rowi < end; ++rowi, ++r, --left) {
+    if (left <= 0) {
+      const int t = (int)(rowi / p.Hq), head = (int)(rowi - (int64_t)t * p.Hq);
+      const int h = head / p.G, g = head - h * p.G;
+      left = p.G - g;
+      cut = t >= sq.q0 && t < sq.q0 + sq.n;
+      if (!cut) cut = find(t);
+      if (cut) {
+        const int row = (t - sq.q0) * p.G + g, group = h / w.heads;
+        sub = h - group * w.heads;
+        const int mtiles = (sq.n * p.G + w.rows - 1) / w.rows, mt = row / w.rows;
+        r = row - mt * w.rows;
+        left = min(left, w.rows - r);
+        const int share = share_of(total, w), tiles = seq_tiles(sq, w);
+        const int first = before + (group * mtiles + mt) * tiles;
+        c0 = first / share, c1 = (first + tiles - 1) / share;
+        inside = first != c0 * share;  // the first piece begins inside its share
+        cut = c0 != c1;
       }
     }
-  };
-  load(c0 + k);
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
+    if (!cut) continue;
+    auto at = [&](int c) { return (((int64_t)2 * c + (c == c0 && inside)) * w.heads + sub) * w.rows + r; };
+    // kBatch pieces on their way at a time, the first of them beside the maxima
+    constexpr int kBatch = kPerRow == 1 ? 4 : 8;
+    float x[kBatch][kPer], ls[kBatch];
+    auto load = [&](int from) {
 #pragma unroll
-  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float acc[kPer], sum = 0.f;
+      for (int j = 0; j < kBatch; ++j) {
+        const int c = from + j * kPerRow;
+        ls[j] = -INFINITY;
+        if (c > c1) continue;
+        ls[j] = p.lse_part[at(c)];
+        const float* from_part = p.o_part + at(c) * D + lane * kPer;
+        if (kPer == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(from_part);
+          x[j][0] = y.x, x[j][1] = y.y, x[j][kPer - 2] = y.z, x[j][kPer - 1] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(from_part);
+          x[j][0] = y.x, x[j][1] = y.y;
+        }
+      }
+    };
+    load(c0 + k);
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  for (int c = c0 + k;;) {
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float acc[kPer], sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (ls[j] == -INFINITY) continue;
-      const float wt = __expf(ls[j] - top);  // a NaN stays one: fmaxf has passed it over
-      sum += wt;
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    for (int c = c0 + k;;) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wt, x[j][i], acc[i]);
+      for (int j = 0; j < kBatch; ++j) {
+        if (ls[j] == -INFINITY) continue;
+        const float wt = __expf(ls[j] - top);  // a NaN stays one: fmaxf has passed it over
+        sum += wt;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wt, x[j][i], acc[i]);
+      }
+      c += kBatch * kPerRow;
+      if (c > c1) break;
+      load(c);
     }
-    c += kBatch * kPerRow;
-    if (c > c1) break;
-    load(c);
-  }
-  if (kPerRow > 1) {  // the row's warps are the CTA's
-    if (lane == 0) sm_sum[k] = sum;
+    if (kPerRow > 1) {  // the row's warps are the CTA's
+      if (lane == 0) sm_sum[k] = sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sm_acc[k][lane * kPer + i] = acc[i];
-    __syncthreads();
-    if (k != 0) return;
-    for (int j = 1; j < kPerRow; ++j) {
-      sum += sm_sum[j];
+      for (int i = 0; i < kPer; ++i) sm_acc[k][lane * kPer + i] = acc[i];
+      __syncthreads();
+      if (k != 0) return;  // (run is 1)
+      for (int j = 1; j < kPerRow; ++j) {
+        sum += sm_sum[j];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += sm_acc[j][lane * kPer + i];
+        for (int i = 0; i < kPer; ++i) acc[i] += sm_acc[j][lane * kPer + i];
+      }
     }
-  }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  __nv_bfloat16* dst = p.o + rowi * D + lane * kPer;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    __nv_bfloat16* dst = p.o + rowi * D + lane * kPer;
 #pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) =
-        sum != 0.f ? rows::pack2(acc[i] * inv, acc[i + 1] * inv) : 0u;
-  if (lane == 0) p.lse[rowi] = sum != 0.f ? top + __logf(sum) : -INFINITY;
+    for (int i = 0; i < kPer; i += 2)
+      *reinterpret_cast<uint32_t*>(dst + i) =
+          sum != 0.f ? rows::pack2(acc[i] * inv, acc[i + 1] * inv) : 0u;
+    if (lane == 0) p.lse[rowi] = sum != 0.f ? top + __logf(sum) : -INFINITY;
+  }
 }
 
 }  // namespace tree
