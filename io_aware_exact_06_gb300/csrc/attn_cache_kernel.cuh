@@ -8,7 +8,7 @@
 // hold a row, eight channels each: 16 bytes of bf16, 8 bytes of codes.  Writing,
 // the row maximum is a shuffle reduction in bf16.  (With 16 codes a lane each 16-byte
 // store fills half a sector: 113 us for the 612 MB of reading back a batch of
-// eight, 99.7 with eight.)  Every byte moves once, so HBM bounds both (launch latency for a few
+// eight, 99.7 with eight, and 96.5 since runs are shorter.)  Every byte moves once, so HBM bounds both (launch latency for a few
 // tokens: runs of one).
 #pragma once
 

@@ -14,11 +14,13 @@
 // The heads of a token are cut into chunks of kSteps (forward) or kBwdSteps row
 // groups, and a warp takes runs of a token's chunks, one run after the other:
 // the whole token when there are tokens enough to fill the GPU four times over,
-// one chunk when there are few.  Loads run kStages - 1 chunks ahead: each lane
-// copies its own channels to its own place in shared memory (cp.async) and reads
-// them back there, so no thread waits for another and the depth costs no
-// registers (one chunk ahead in registers left 2 KB a warp in flight in the
-// gradient, 4.1 TB/s).
+// one chunk when there are few.  Loads run a chunk ahead: each lane copies its own
+// channels to its own place in shared memory (cp.async) and reads them back there,
+// so no thread waits for another and no register is held.  More in flight is
+// slower: 16381 tokens of 32 + 8 heads, d = 128, take 61.7 us (5.5 TB/s) forward
+// with two stages, 62.5 with three, 63.6 with four, 67.3 with two and a fourth CTA
+// an SM; the gradient of 16384 tokens 92.7 us (5.5 TB/s), 96.8 and 100.1 with
+// three and four stages.
 #pragma once
 
 #include "attn_rows.cuh"
@@ -30,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 4;     // row groups of a chunk, forward
 constexpr int kBwdSteps = 2;  // gradient: two tensors are loaded
-constexpr int kStages = 4;    // chunks in shared memory, forward and gradient: 64 bytes a lane each
+constexpr int kStages = 2;    // chunks in shared memory, forward and gradient: 64 bytes a lane each
 constexpr int kSmem = kStages * kThreads * 64;
 
 struct Rotary {
