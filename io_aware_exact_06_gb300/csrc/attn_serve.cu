@@ -208,7 +208,7 @@ bool few(const Plan& pl) { return pl.rows <= 16; }
 // and query rows are 128 registers a lane at d = 128 (12 rows, 16 sequences of 4096
 // keys, bf16 / e4m3, few : many: d = 64 56 / 56 : 63 / 75 us, d = 128 106 / 113 :
 // 83 / 86 us).  num_splits caps the pieces of a segment instead.
-Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
+Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, int few_ctas) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
   constexpr int kBig = attn::tree::kBigRows;
@@ -223,7 +223,7 @@ Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len,
   pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
   pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
   const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
-  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? attn::tree::kFewCtas : 1));
+  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? few_ctas : 1));
   pl.work.units = (int)(pl.ctas * per_cta);
   pl.slots = 2 * (int64_t)pl.work.units * heads;
   // eight warps to a row where segments are cut into many pieces, and where the
@@ -453,7 +453,7 @@ extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d
                                           int max_len, int num_splits) {
   if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
   if (B == 0 || total == 0 || max_new == 0) return 0;
-  return tree_bytes(tree_plan(B, total, Hq, H, d, max_new, max_len, num_splits), d);
+  return tree_bytes(tree_plan(B, total, Hq, H, d, max_new, max_len, num_splits, attn::tree::kMostFewCtas), d);
 }
 
 extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
@@ -473,7 +473,8 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(mask, 8) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGN;
-  const Plan pl = tree_plan(B, total, Hq, cache->H, d, max_new, max_len, num_splits);
+  const Plan pl = tree_plan(B, total, Hq, cache->H, d, max_new, max_len, num_splits,
+                            attn::tree::few_ctas(d, cache->k_scale != nullptr));
   if (!pl.fits) return ATTN_ERR_SHAPE;
   const size_t need = tree_bytes(pl, d);
   if (!workspace || workspace_bytes < need) return ATTN_ERR_SCRATCH;

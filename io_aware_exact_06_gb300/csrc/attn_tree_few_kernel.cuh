@@ -22,19 +22,28 @@ namespace tree {
 // Every warp works alone: it finds its place in the line, copies its tiles by
 // TMA into stages of its own (the copies of a later tile go out as soon as a
 // stage is free, across the ends of segments), keeps its softmax and writes its
-// pieces; the CTA, three an SM, is only where four warps live.  A segment is a
+// pieces; the CTA is only where four warps live.  A segment is a
 // group of `heads` neighbouring heads, one to a warp, which so read neighbouring
 // lines of the cache's token rows at about the same time: with 128-byte head
 // rows (e4m3, d = 128) four warps on four heads read 512 contiguous bytes.
 // (One head to a CTA, its tiles dealt to the warps: 4.4 TB/s on 64 ragged
 // sequences of 8 heads against 5.4 TB/s on the same bytes with one head.  A
 // producer warp for the CTA instead spent about 1000 cycles on a 32-key tile's
-// issue, against 365 that HBM needs for the tiles of three CTAs.)
+// issue, against 365 that HBM needs for the tiles of twelve warps.)
 constexpr int kWarps = 4;     // of a CTA
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
-constexpr int kFewCtas = 3;  // per SM
+// CTAs per SM.  Two leave a lane 255 registers and DRAM fewer streams; d = 64 codes
+// are bound by their arithmetic and want three (64 ragged sequences of up to 8192
+// keys, one token, 32 + 8 heads, two : three CTAs: d = 128 e4m3 143 : 145 us, bf16
+// 241 : 247, d = 64 bf16 131 : 136, e4m3 142 : 103).
+__host__ __device__ constexpr int few_ctas(int d, bool codes) { return d == 64 && codes ? 3 : 2; }
+constexpr int kMostFewCtas = 3;
+// For the registers: d = 128 bf16 does better held to three CTAs' (241 against 243 us,
+// one token for four short sequences 11.8 against 12.5), e4m3 does not (184 : 143).
+__host__ __device__ constexpr int few_bound(int d, bool codes) { return (d == 128) != codes ? 3 : 2; }
+constexpr int kFewRing = 16384;  // bytes of a warp's stages (24576: d = 64 bf16 137 us)
 
 template <int D, bool kCodes, int kNT>
 struct FewCfg : Row<D, kCodes> {
@@ -42,7 +51,7 @@ struct FewCfg : Row<D, kCodes> {
   static constexpr int kMatBytes = kFewTile * kRowBytes;
   static constexpr int kScaleBytes = kCodes ? kFewTile * 4 : 0;
   static constexpr int kStage = 2 * kMatBytes;
-  static constexpr int kOwn = 16384 / kStage < 3 ? 16384 / kStage : 3;  // stages of a warp
+  static constexpr int kOwn = kFewRing / kStage < 3 ? kFewRing / kStage : 3;  // stages of a warp
   static constexpr int kStages = kOwn * kWarps;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kTurn = 32;  // columns of the output turned to rows at a time
@@ -58,7 +67,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 template <int D, bool kCodes, int kNT>
-__global__ void __launch_bounds__(kFewThreads, kFewCtas)
+__global__ void __launch_bounds__(kFewThreads, few_bound(D, kCodes))
 tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ Params p, const __grid_constant__ Work w) {
   using C = FewCfg<D, kCodes, kNT>;
