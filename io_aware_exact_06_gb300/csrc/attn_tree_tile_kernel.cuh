@@ -7,8 +7,8 @@
 // core 1024 cycles for 128 rows (S = Q K^T and O += P V, 128 x 128 x d each; d = 128)
 // whatever part of the rows is real; its e4m3 bytes take 1410 cycles from HBM (bf16:
 // 2820).  Trees of 64 drafts (8 sequences of up to 16384 keys, 64 query and 8 key
-// heads, d = 128) take 290 us with e4m3 codes and 248 us with a bf16 cache, 800 and
-// 940 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
+// heads, d = 128) take 284 us with e4m3 codes and 241 us with a bf16 cache, 820 and
+// 970 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
 // 600 cycles, softmax 2100 or 1650, P V 600, and some 200 for each look at a
 // barrier), of which two are under way at a time.
 //
