@@ -10,7 +10,12 @@
 // heads, d = 128) take 284 us with e4m3 codes and 241 us with a bf16 cache, 820 and
 // 970 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
 // 600 cycles, softmax 2100 or 1650, P V 600, and some 200 for each look at a
-// barrier), of which two are under way at a time.
+// barrier), of which two are under way at a time.  Shared memory is busy for 3200 of
+// the 5300 cycles that two row tiles take over codes: 1536 for the products'
+// operands, 1024 for the key scales (every thread takes all 128 of a tile, 512 bytes
+// into its registers), 640 for copies and conversions.  So a score is multiplied by
+// its key's scale once, and goes back to tensor memory (reading the scales again in
+// the second pass: 330 us; loading them a batch ahead: 292).
 //
 // Warps: 0-3 and 4-7 softmax groups A and B (a thread owns a row), each with its own
 // S and O in TMEM, so that one group's softmax runs beside the other's products;
