@@ -91,8 +91,8 @@ int attn_cache_read(const attn_paged_cache *cache, void *k, void *v, const int32
  * aligned, not initialised, in use until the call's work on stream has finished;
  * calls that may run at the same time need one each.  Missing or too small:
  * ATTN_ERR_SCRATCH.
- * ATTN_ERR_SHAPE also where B * H * max_len keys are more than 2^31 tiles of 32 (of
- * 128, for more than 16 query rows a key head: times the tiles of rows).
+ * ATTN_ERR_SHAPE also where the key tiles of a batch (at most B * H * max_len / 32,
+ * times max_new * Hq / H / 256 rounded up) could be more than 2^31 - 1.
  * Errors in the error word: ATTN_ERR_SEQLENS (lengths as above; the rows of
  * that sequence are not written), ATTN_ERR_INDEX (a page outside the cache; the
  * rows that read it come out as NaN), ATTN_ERR_DEVICE_TIMEOUT (NaN as well).

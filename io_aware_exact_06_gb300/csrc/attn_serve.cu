@@ -192,7 +192,7 @@ attn::cache::Pages pages_of(const attn_paged_cache* c) {
 
 // ---------------------------------------------------------------------- tree --
 struct Plan {
-  int rows;  // query rows of a segment: 8 or 16 (few rows), 128
+  int rows;  // query rows of a segment: 8 or 16 (few rows), 128 or 256
   attn::tree::Work work;
   int64_t ctas;
   int64_t slots;  // parts in the workspace, `rows` rows each
@@ -204,15 +204,16 @@ bool few(const Plan& pl) { return pl.rows <= 16; }
 
 // Query rows of a segment: the smallest tile that holds max_new * G of them.
 // Few rows: as many persistent warps as fit the SMs; more: a persistent CTA an SM
-// with tcgen05 products.  9 to 16 rows take the former at d = 64 only: their sums
-// and query rows are 128 registers a lane at d = 128 (12 rows, 16 sequences of 4096
-// keys, bf16 / e4m3, few : many: d = 64 56 / 56 : 63 / 75 us, d = 128 106 / 113 :
-// 83 / 86 us).  num_splits caps the pieces of a segment instead.
-Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, int few_ctas) {
+// with tcgen05 products.  9 to 16 rows take the former but for a bf16 cache with
+// d = 128, where HBM outruns its arithmetic (us, few : many; 12 rows, 16 sequences of
+// 4096 keys: d = 128 bf16 104 : 82, e4m3 69 : 84, d = 64 50 : 63 and 54 : 75; 16 rows,
+// 64 sequences of 8192 keys: d = 128 bf16 284 : 254, e4m3 192 : 247).  num_splits caps
+// the pieces of a segment instead.
+Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, bool codes) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
   constexpr int kBig = attn::tree::kBigRows;
-  pl.rows = M <= 8 ? 8 : M <= 16 && d == 64 ? 16 : M <= kBig ? kBig : 2 * kBig;
+  pl.rows = M <= 8 ? 8 : M <= 16 && (d == 64 || codes) ? 16 : M <= kBig ? kBig : 2 * kBig;
   const int64_t T = few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile;
   const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
   const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
@@ -223,7 +224,7 @@ Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len,
   pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
   pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
   const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
-  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? few_ctas : 1));
+  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? attn::tree::few_ctas(d, codes) : 1));
   pl.work.units = (int)(pl.ctas * per_cta);
   pl.slots = 2 * (int64_t)pl.work.units * heads;
   // eight warps to a row where segments are cut into many pieces, and where the
@@ -249,12 +250,13 @@ template <int D, bool kCodes>
 int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                 cudaStream_t s) {
   using namespace attn::tree;
+  constexpr int kTwo = D == 64 || kCodes ? 2 : 1;  // no plan has 16 rows of the other kind
   auto kernel = pl.rows == 8          ? tree_few_kernel<D, kCodes, 1>
-                : pl.rows == 16       ? tree_few_kernel<64, kCodes, 2>  // d = 64 only
+                : pl.rows == 16       ? tree_few_kernel<D, kCodes, kTwo>
                 : pl.rows == kBigRows ? tree_tile_kernel<D, kCodes, false>
                                       : tree_tile_kernel<D, kCodes, true>;
   const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1>::kSmem
-                   : pl.rows == 16       ? FewCfg<64, kCodes, 2>::kSmem
+                   : pl.rows == 16       ? FewCfg<D, kCodes, kTwo>::kSmem
                    : pl.rows == kBigRows ? big_smem<D, kCodes, false>()
                                          : big_smem<D, kCodes, true>();
   int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
@@ -453,7 +455,11 @@ extern "C" size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d
                                           int max_len, int num_splits) {
   if (check_tree(B, total, Hq, H, d, max_new, max_len, num_splits) != ATTN_OK) return 0;
   if (B == 0 || total == 0 || max_new == 0) return 0;
-  return tree_bytes(tree_plan(B, total, Hq, H, d, max_new, max_len, num_splits, attn::tree::kMostFewCtas), d);
+  // the cache's type is not known here
+  size_t most = 0;
+  for (bool codes : {false, true})
+    most = std::max(most, tree_bytes(tree_plan(B, total, Hq, H, d, max_new, max_len, num_splits, codes), d));
+  return most;
 }
 
 extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_cache* cache,
@@ -473,13 +479,12 @@ extern "C" int attn_fwd_tree(const void* q, int64_t q_stride, const attn_paged_c
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(mask, 8) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGN;
-  const Plan pl = tree_plan(B, total, Hq, cache->H, d, max_new, max_len, num_splits,
-                            attn::tree::few_ctas(d, cache->k_scale != nullptr));
+  const bool codes = cache->k_scale != nullptr;
+  const Plan pl = tree_plan(B, total, Hq, cache->H, d, max_new, max_len, num_splits, codes);
   if (!pl.fits) return ATTN_ERR_SHAPE;
   const size_t need = tree_bytes(pl, d);
   if (!workspace || workspace_bytes < need) return ATTN_ERR_SCRATCH;
   if ((int64_t)total * Hq > INT32_MAX) return ATTN_ERR_SHAPE;
-  const bool codes = cache->k_scale != nullptr;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
   const int box = std::min(cache->page_size, few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile);
 

@@ -6,7 +6,7 @@
 // are its G = Hq / H query heads for every new token, row = token * G + head, so
 // that keys and values are read once for all of them: per key the products take
 // 4 M d flops for M rows against 4 d bytes (bf16) or 2 d bytes (e4m3) of cache.
-// Up to 8 rows (16 at d = 64) run on the warp-level products
+// Up to 8 rows (16, but for bf16 with d = 128) run on the warp-level products
 // (attn_tree_few_kernel.cuh), more on tcgen05 (attn_tree_tile_kernel.cuh);
 // attn_tree_work.cuh cuts the work.
 //

@@ -39,7 +39,6 @@ constexpr int kFewThreads = 32 * kWarps;
 // keys, one token, 32 + 8 heads, two : three CTAs: d = 128 e4m3 143 : 145 us, bf16
 // 241 : 247, d = 64 bf16 131 : 136, e4m3 142 : 103).
 __host__ __device__ constexpr int few_ctas(int d, bool codes) { return d == 64 && codes ? 3 : 2; }
-constexpr int kMostFewCtas = 3;
 // For the registers: d = 128 bf16 does better held to three CTAs' (241 against 243 us,
 // one token for four short sequences 11.8 against 12.5), e4m3 does not (184 : 143).
 __host__ __device__ constexpr int few_bound(int d, bool codes) { return (d == 128) != codes ? 3 : 2; }
