@@ -7,9 +7,9 @@
 // groups of an interleaved one and of the channels that do not rotate.  So the
 // rotation needs no exchange and a lane only its own four cosines and sines (a
 // 16-byte slice of the row instead took 8 shuffles a row and 16 registers of
-// angles); the row's sum of squares is a shuffle reduction.  Nothing goes through
-// shared memory in the forward; each element is read and written once, so HBM
-// bounds it (and launch latency for a few tokens).
+// angles); the row's sum of squares is a shuffle reduction.  Each element
+// is read and written once: HBM and instruction issue bound it (launch latency for
+// a few tokens).
 //
 // The heads of a token are cut into chunks of kSteps (forward) or kBwdSteps row
 // groups, and a warp takes runs of a token's chunks, one run after the other:
@@ -19,8 +19,7 @@
 // so no thread waits for another and no register is held.  More in flight is
 // slower: 16381 tokens of 32 + 8 heads, d = 128, take 61.7 us (5.5 TB/s) forward
 // with two stages, 62.5 with three, 63.6 with four, 67.3 with two and a fourth CTA
-// an SM; the gradient of 16384 tokens 92.7 us (5.5 TB/s), 96.8 and 100.1 with
-// three and four stages.
+// an SM; the gradient of 16384 tokens 92.7 us (5.5 TB/s), 94.7 with three stages.
 #pragma once
 
 #include "attn_rows.cuh"
