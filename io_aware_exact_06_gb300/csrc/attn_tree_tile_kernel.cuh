@@ -7,8 +7,8 @@
 // core 1024 cycles for 128 rows (S = Q K^T and O += P V, 128 x 128 x d each; d = 128)
 // whatever part of the rows is real; its e4m3 bytes take 1410 cycles from HBM (bf16:
 // 2820).  Trees of 64 drafts (8 sequences of up to 16384 keys, 64 query and 8 key
-// heads, d = 128) take 284 us with e4m3 codes and 241 us with a bf16 cache, 820 and
-// 970 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
+// heads, d = 128) take 284 us with e4m3 codes and 225 us with a bf16 cache, 820 and
+// 1040 TFLOP/s: what bounds them is the way of one row tile around the roles (scores
 // 600 cycles, softmax 2100 or 1650, P V 600, and some 200 for each look at a
 // barrier), of which two are under way at a time.  Shared memory is busy for 3200 of
 // the 5300 cycles that two row tiles take over codes: 1536 for the products'
@@ -273,7 +273,7 @@ struct Big {
   }
 
   // -------------------------------------------------------------- products --
-  __device__ __forceinline__ void scores(int g, int ks) {
+  __device__ __forceinline__ void scores(uint32_t tmem, int g, int ks) {
     const uint32_t k = smem + C::kOffK + ks * C::kMat, d = tmem + 128 * g, q = smem + (kPair ? g * C::kQ1 : 0);
     if (kCodes) {
       constexpr uint32_t kSwz = C::kBox == 128 ? 2 : 4;  // 128- or 64-byte swizzle
@@ -295,7 +295,7 @@ struct Big {
       }
     }
   }
-  __device__ __forceinline__ void values(int g, int r, bool accumulate) {
+  __device__ __forceinline__ void values(uint32_t tmem, int g, int r, bool accumulate) {
     const uint32_t v = kCodes ? smem + C::kOffC + r * C::kConv : smem + C::kOffV + r * C::kMat;
     const uint64_t b = make_sdesc(v, C::kChunk, 1024, kSwizzle128B);
     constexpr uint32_t kI = kCodes ? idesc_f16_mn(128, D) : make_idesc_bf16(128, D, true);
@@ -309,6 +309,12 @@ struct Big {
   // look is some 200 cycles (370 -> 340 us, and 299 -> 290 in one call).
   __device__ __forceinline__ void multiply(Walk k) {
     const int lane = threadIdx.x % 32;
+    // Values that are the same in every lane, for the compiler to see: descriptors are
+    // then made in uniform registers, and products follow each other faster (trees of
+    // 64 drafts, bf16 cache 241 -> 225 us).  Over codes that takes shared memory from
+    // the softmax and the conversions (285 -> 295).
+    auto uniform = [](int x) { return kCodes ? x : __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uniform(tmem);
     int ks = 0, kr = 0, rs = 0, rr = 0, seg = 0;
     uint32_t pcount = 0;  // bit g: parity of group g's next probabilities
     do {
@@ -326,14 +332,15 @@ struct Big {
         if (on >= 0) wait(on, parity & 1);
         dead = __any_sync(0xffffffffu, dead);
         tc_fence_after();
+        const int gu = uniform(g), ku = uniform(ks), ru = uniform(rs);
         if (lane == 0 && !dead) {
           if (j >= 0) {
-            values(g, rs, j > 1);
+            values(tm, gu, ru, j > 1);
             if (last) mma_commit(bar(kCodes ? C::bRE + rs : C::bVE + rs));
             if (i >= n) mma_commit(bar(C::bOF + g));
           }
           if (i < n) {
-            scores(g, ks);
+            scores(tm, gu, ku);
             mma_commit(bar(C::bSF + g));
           }
         }
