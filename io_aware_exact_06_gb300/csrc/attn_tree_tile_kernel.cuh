@@ -599,8 +599,10 @@ struct Big {
         const float2 a = kPair ? make_float2(m, l) : ss.ml[0][r];
         const float2 b = kPair ? make_float2(-INFINITY, 0.f) : ss.ml[1][r];
         const float mm = fmaxf(a.x, b.x);
-        const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), wb = b.x == -INFINITY ? 0.f : ex2(b.x - mm);
-        const float ls = (wa != 0.f ? wa * a.y : 0.f) + (wb != 0.f ? wb * b.y : 0.f);
+        // a side counts unless it saw nothing: a NaN sum, or an infinite value, survives a weight of 0
+        const bool sa = a.x != -INFINITY, sb = b.x != -INFINITY;
+        const float wa = sa ? ex2(a.x - mm) : 0.f, wb = sb ? ex2(b.x - mm) : 0.f;
+        const float ls = (sa ? wa * a.y : 0.f) + (sb ? wb * b.y : 0.f);
         const float inv = ls != 0.f ? 1.f / ls : 0.f;
         // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
         const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0]) - 6) : wa, ub = kCodes ? wb * pow2(ss.fend[1] - 6) : wb;
@@ -622,8 +624,8 @@ struct Big {
           float f[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            f[i] = wa != 0.f ? ua * __uint_as_float(xa[i]) : 0.f;
-            if (!kPair) f[i] += wb != 0.f ? ub * __uint_as_float(xb[i]) : 0.f;
+            f[i] = sa ? ua * __uint_as_float(xa[i]) : 0.f;
+            if (!kPair) f[i] += sb ? ub * __uint_as_float(xb[i]) : 0.f;
             f[i] = inv != 0.f ? f[i] * inv : 0.f;
             if (poison) f[i] = NAN;
           }
