@@ -75,7 +75,8 @@ int attn_cache_read(const attn_paged_cache *cache, void *k, void *v, const int32
  * its ancestors).  mask == NULL: every new token sees itself and the ones
  * before it (n_b = 1: decoding).  A row that sees no key gets O = 0 and
  * LSE = -inf; what keys and values hold where a row does not see them,
- * infinities and NaN included, does not reach it.
+ * infinities and NaN included, does not reach it.  A query with an infinity or a
+ * NaN gives a row of NaN (LSE too) wherever it sees a key.
  * q: [total, Hq, d] bf16, token stride in elements (multiple of 8, at least
  * Hq * d); Hq a multiple of cache->H, head h reads key head h / (Hq / H).
  * o: [total, Hq, d] bf16, lse: [total, Hq] fp32, contiguous.  mask: int64

@@ -128,6 +128,18 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   return h;
 }
 
+// Two bf16 channels of a query, an infinity as a NaN: every score of the row is NaN
+// then, and so is the row wherever it sees a key.  (An infinity itself could make all
+// its scores -inf, an empty row's, and saturates where a query is split into codes.)
+__device__ __forceinline__ uint32_t no_infinity(uint32_t x) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(r) : "r"(x), "r"(0u));  // x 0 + x
+  return r;
+}
+__device__ __forceinline__ uint4 no_infinity(uint4 x) {
+  return make_uint4(no_infinity(x.x), no_infinity(x.y), no_infinity(x.z), no_infinity(x.w));
+}
+
 // The rows and keys of a sequence; false if they are not what the caller's
 // bounds allow.
 struct Seq {

@@ -204,7 +204,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         for (int s = 0; s < kQ; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            qb[nt][s][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8 * i) : 0u;
+            qb[nt][s][i] = live ? no_infinity(*reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8 * i)) : 0u;
       } else {
         // lane c's channels of k-step s: the four that its 16 bytes of a key's
         // codes (chunk kHH c + s / 4) hold at 4 (s % 4)
@@ -213,7 +213,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         for (int s = 0; s < kQ; ++s) {
           const int ch = 16 * (kHH * c + s / 4) + 4 * (s % 4);
           const uint2 raw = live ? *reinterpret_cast<const uint2*>(q + ch) : make_uint2(0, 0);
-          qb[nt][s][0] = raw.x, qb[nt][s][1] = raw.y;
+          qb[nt][s][0] = no_infinity(raw.x), qb[nt][s][1] = no_infinity(raw.y);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qb[nt][s][k] << 16)),

@@ -377,7 +377,7 @@ struct Big {
     if (!kCodes) {
 #pragma unroll 8
       for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 8 * ch) : make_uint4(0, 0, 0, 0);
+        const uint4 x = live ? no_infinity(*reinterpret_cast<const uint4*>(q + 8 * ch)) : make_uint4(0, 0, 0, 0);
         sts128(to + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), x.x, x.y, x.z, x.w);
       }
     } else {
@@ -398,7 +398,8 @@ struct Big {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 16 * ch + 8 * half) : make_uint4(0, 0, 0, 0);
+          const uint4 x =
+              live ? no_infinity(*reinterpret_cast<const uint4*>(q + 16 * ch + 8 * half)) : make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {x.x, x.y, x.z, x.w};
           uint32_t hp[4], lp[4];
 #pragma unroll

@@ -1,8 +1,11 @@
-"""What the norm, the paged cache and attention over it do at their edges, for
-instance with values that are not finite where a kernel could lose or spread them.
+"""What the norm, the paged cache and attention over it do at their edges: values
+that are not finite where a kernel could lose or spread them, value scales far
+apart, plans whose offsets are no batch, kinds without heads.
 
 Tolerances as in test_tree_gpu.py, where nothing else is said.
 """
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -10,7 +13,7 @@ torch = pytest.importorskip("torch")
 import io_aware_exact_06_gb300 as fa
 from tests import serve_ref as ref
 from tests.test_cache_gpu import make, normal, put
-from tests.test_tree_gpu import call
+from tests.test_tree_gpu import call, fill, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +28,43 @@ def dev():
         pytest.skip("no CUDA device")
     __graft_entry__.build()
     return torch.device("cuda:0")
+
+
+def want_of(c, q, lens, ns, mask):
+    cu = [sum(ns[:i]) for i in range(len(ns) + 1)]
+    return ref.tree(q.cpu(), *rows_of(c), c["page_table"].cpu(), c["page"], lens, cu, mask, q.shape[-1] ** -0.5)
+
+
+def near(got, want, codes, which, heaviest=None):
+    """O and LSE of the rows `which` [total, Hq] to the tolerances of test_tree_gpu.py.  heaviest: a row's
+    largest p_j max|v_j|, of which a key may lose 2^-20 where its weight (over codes an fp16) is below
+    fp16's normal range; given per row, times the keys."""
+    o, lse = (t.cpu().double() for t in got)
+    wo, wl, A, S = want
+    step = 2.0 ** -10 if codes else 2.0 ** -8
+    tol = 2.0 ** -8 * wo.abs() + A * (step + 2.0 ** -19 * S[..., None] + 2.0 ** -17)
+    if codes and heaviest is not None:
+        tol = tol + 2.0 ** -20 * heaviest[..., None]
+    off = (o - wo).abs()
+    assert (off[which] <= tol[which]).all(), (off[which] / tol[which]).max()
+    off, tol = (lse - wl).abs(), 2.0 ** -19 * S + 2.0 ** -20 * wl.abs() + 2.0 ** -18
+    assert (off[which] <= tol[which]).all(), (off[which] / tol[which]).max()
+
+
+def heaviest_of(c, q, lens, ns, mask):
+    """[total, Hq]: the keys of a row's sequence times its largest p_j max_c |v_jc|, in fp64."""
+    k, v = rows_of(c)
+    G, out, at = q.shape[1] // k.shape[1], [], 0
+    for b, (L, n) in enumerate(zip(lens, ns)):
+        r = ref.row_index(c["page_table"].cpu(), c["page"], b, torch.arange(L))
+        x = torch.einsum("thd,lhd->thl", q[at:at + n].cpu().double(), k[r].repeat_interleave(G, 1)) * q.shape[-1] ** -0.5
+        j = torch.arange(n)
+        word = (mask[at:at + n, None] >> j) & 1 if mask is not None else (j <= j[:, None]).long()
+        x[:, :, L - n:] = x[:, :, L - n:].masked_fill(word[:, None] == 0, -math.inf)
+        p = torch.softmax(x, -1).nan_to_num(0.0)
+        out.append(L * (p * v[r].abs().amax(-1).t().repeat_interleave(G, 0)).amax(-1))
+        at += n
+    return torch.cat(out)
 
 
 @pytest.mark.parametrize("G", ROWS)
@@ -71,3 +111,32 @@ def test_infinite_values_beside_large_scores(dev, codes, G, spot, large):
     assert fa.attn_last_device_error() == 0
     assert not o[..., 3].isfinite().any() and lse.isfinite().all()
     assert o[..., :3].isfinite().all() and o[..., 4:].isfinite().all()
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_queries_that_are_not_finite(dev, codes, d, G, splits):
+    """A query row with an infinity or a NaN is NaN wherever it sees a key, and no
+    other row is touched: whatever the kernel, also where its one key's score is -inf
+    (the third sequence).  Rows that see nothing stay 0 and -inf."""
+    lens, ns, H = [300, 6, 1, 1], [6, 6, 1, 1], 2
+    Hq = H * G
+    c = fill(dev, 610, lens, H, d, 16, codes)
+    q = normal(dev, 611, sum(ns), Hq, d)
+    mask = torch.tensor([(1 << i + 1) - 1 for i in range(6)] + [0, 1, 0, 8, 0, 63, 1, 1], dtype=torch.int64)
+    want, most = want_of(c, q, lens, ns, mask), heaviest_of(c, q, lens, ns, mask)
+    bad = torch.zeros(sum(ns), Hq, dtype=torch.bool)
+    q = q.clone()
+    for t, h, ch, x in ((0, 0, 3, INF), (2, Hq - 1, d - 1, -INF), (3, Hq // 2, 17, NAN), (8, 0, 0, INF), (9, Hq - 1, 8, NAN),
+                        (11, 0, 31, -INF), (12, 0, 5, INF), (13, 0, 5, -INF)):
+        q[t, h, ch] = x
+        bad[t, h] = True
+    got = call(dev, c, q, lens, ns, mask, num_splits=splits)
+    assert fa.attn_last_device_error() == 0
+    empty = (mask == 0)[:, None].expand(-1, Hq)
+    assert (got[0][empty.to(dev)] == 0).all() and (got[1][empty.to(dev)] == -math.inf).all()
+    hit = (bad & ~empty).to(dev)
+    assert got[0][hit].isnan().all() and got[1][hit].isnan().all()
+    near(got, want, codes, ~bad & ~empty, most)
