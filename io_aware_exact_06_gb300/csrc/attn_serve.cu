@@ -306,10 +306,15 @@ extern "C" int attn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
   p.Hk = Hk;
   p.eps = eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto kernel = d == 64 ? rotary->interleaved ? attn::norm::norm_rope_kernel<64, true>
-                                              : attn::norm::norm_rope_kernel<64, false>
-                : rotary->interleaved ? attn::norm::norm_rope_kernel<128, true>
-                                      : attn::norm::norm_rope_kernel<128, false>;
+  const bool part = rotary->rot < d;
+  auto kernel = d == 64 ? rotary->interleaved ? part ? attn::norm::norm_rope_kernel<64, true, true>
+                                                     : attn::norm::norm_rope_kernel<64, true, false>
+                          : part ? attn::norm::norm_rope_kernel<64, false, true>
+                                 : attn::norm::norm_rope_kernel<64, false, false>
+                : rotary->interleaved ? part ? attn::norm::norm_rope_kernel<128, true, true>
+                                             : attn::norm::norm_rope_kernel<128, true, false>
+                : part ? attn::norm::norm_rope_kernel<128, false, true>
+                       : attn::norm::norm_rope_kernel<128, false, false>;
   return launch(kernel, grid, attn::norm::kThreads, attn::norm::kSmem, s, p);
 }
 
@@ -369,10 +374,15 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
     p.ctas_q = (int)pl.ctas[0];
     p.eps = eps;
     p.part = static_cast<float*>(workspace);
-    auto kernel = d == 64 ? rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<64, true>
-                                                : attn::norm::norm_rope_bwd_kernel<64, false>
-                  : rotary->interleaved ? attn::norm::norm_rope_bwd_kernel<128, true>
-                                        : attn::norm::norm_rope_bwd_kernel<128, false>;
+    const bool part = rotary->rot < d;
+    auto kernel = d == 64 ? rotary->interleaved ? part ? attn::norm::norm_rope_bwd_kernel<64, true, true>
+                                                       : attn::norm::norm_rope_bwd_kernel<64, true, false>
+                            : part ? attn::norm::norm_rope_bwd_kernel<64, false, true>
+                                   : attn::norm::norm_rope_bwd_kernel<64, false, false>
+                  : rotary->interleaved ? part ? attn::norm::norm_rope_bwd_kernel<128, true, true>
+                                               : attn::norm::norm_rope_bwd_kernel<128, true, false>
+                  : part ? attn::norm::norm_rope_bwd_kernel<128, false, true>
+                         : attn::norm::norm_rope_bwd_kernel<128, false, false>;
     if ((st = launch(kernel, grid, attn::norm::kThreads, attn::norm::kSmem, s, p)) != ATTN_OK) return st;
   }
   const attn::norm::WeightSum w{static_cast<const float*>(workspace), Hq ? dwq : nullptr,

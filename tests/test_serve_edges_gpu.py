@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 import io_aware_exact_06_gb300 as fa
 from tests import serve_ref as ref
 from tests.test_cache_gpu import make, normal, put
+from tests.test_norm_gpu import inputs, to
 from tests.test_tree_gpu import call, fill, rows_of
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +141,41 @@ def test_queries_that_are_not_finite(dev, codes, d, G, splits):
     hit = (bad & ~empty).to(dev)
     assert got[0][hit].isnan().all() and got[1][hit].isnan().all()
     near(got, want, codes, ~bad & ~empty, most)
+
+
+def same_finiteness(got, want, what):
+    got = got.cpu().double()
+    assert torch.equal(got.isfinite(), want.isfinite()), what
+    fine = want.isfinite()
+    assert ((got - want)[fine].abs() <= 2 ** -7 * want[fine].abs() + 2 ** -16).all(), what
+
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 0, False), (128, 0, True), (64, 32, False), (128, 48, True), (128, 16, False)])
+def test_channels_that_do_not_rotate_stand_alone(dev, d, rot, inter):
+    """An infinity or NaN in a channel from rot on reaches what the formula says: its own
+    output and the row's norm, the gradient's row and its own weight, not a neighbour."""
+    x = inputs(620, 9, 3, 2, d, rot, 1, None)
+    x["wq"][d - 3] = INF                    # one weight: its channel of every query row
+    x["k"] = x["k"].clone()
+    x["k"][2, 1, d - 6] = NAN               # one input: its row, by the norm
+    x["k"][4, 0, d - 1] = INF
+    y = to(dev, {**x, "q": x["q"].clone()})
+    got = fa.qk_norm_rope(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"], interleaved=inter)
+    assert fa.attn_last_device_error() == 0
+    c, s = ref.angles(x["cos"], x["sin"], x["positions"], (rot // 2,)) if rot else (None, None)
+    for n, o in zip("qk", got):
+        same_finiteness(o, ref.norm_rope(x[n], x["w" + n], c, s, rot, inter, 1e-6)[0], n)
+    # the gradient: one output gradient that is not finite
+    x = inputs(621, 9, 3, 2, d, rot, 1, None)
+    c, s = ref.angles(x["cos"], x["sin"], x["positions"], (rot // 2,)) if rot else (None, None)
+    x["gq"][5, 2, d - 4] = INF
+    x["gk"][1, 0, d - 7] = NAN
+    y = to(dev, x)
+    got = fa.qk_norm_rope_backward(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"], y["gq"], y["gk"],
+                                   interleaved=inter)
+    assert fa.attn_last_device_error() == 0
+    for i, n in enumerate("qk"):
+        dx, dw, _, _ = ref.norm_rope_backward(x[n], x["w" + n], x["g" + n], c, s, rot, inter, 1e-6)
+        same_finiteness(got[i], dx, n)
+        same_finiteness(got[2 + i], dw, n)
+        assert (~dw.isfinite()).sum() == 1
