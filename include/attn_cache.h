@@ -46,10 +46,11 @@ typedef struct {
  * attn_cache_write: k, v [total, H, d] bf16 (token strides in elements,
  * multiples of 8, at least H * d) into the cache.  Two sequences whose tables
  * share a page must not both write to it.
- * Errors in the error word: ATTN_ERR_SEQLENS (cu_seqlens not increasing from
- * 0 or past total; a sequence shorter than its new tokens or longer than its
- * table) and ATTN_ERR_INDEX (a page outside the cache); the tokens concerned
- * are not written.
+ * Errors in the error word: ATTN_ERR_SEQLENS and ATTN_ERR_INDEX (a page outside
+ * the cache; its tokens are not written).  ATTN_ERR_SEQLENS: cu_seqlens decreases
+ * somewhere, which places no token: nothing is written; or a sequence that begins
+ * below 0 (the first: anywhere but at 0), ends past total, is shorter than its new
+ * tokens or longer than its table: its tokens are not written.
  */
 int attn_cache_write(const attn_paged_cache *cache, const void *k, int64_t k_stride, const void *v,
                      int64_t v_stride, const int32_t *seqlens, const int32_t *cu_seqlens, int B,

@@ -71,5 +71,13 @@ __device__ __forceinline__ void check_offsets(const int* __restrict__ cu, int B,
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(err, kBadSeqlens);
 }
 
+// Whether the packed offsets decrease anywhere, as far as this one of `n` threads
+// looks: then they place no token (a search in them finds any sequence).
+__device__ __forceinline__ bool offsets_fall(const int* __restrict__ cu, int B, int thread, int n) {
+  bool falls = false;
+  for (int i = thread; i < B; i += n) falls |= cu[i + 1] < cu[i];
+  return falls;
+}
+
 }  // namespace rows
 }  // namespace attn

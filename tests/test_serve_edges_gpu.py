@@ -179,3 +179,78 @@ def test_channels_that_do_not_rotate_stand_alone(dev, d, rot, inter):
         same_finiteness(got[i], dx, n)
         same_finiteness(got[2 + i], dw, n)
         assert (~dw.isfinite()).sum() == 1
+
+
+PLANS = {  # offsets of three sequences with 3, 2 and 4 new tokens (9 packed rows): the sequences that stay sound
+    "start": ([1, 3, 5, 9], [1, 2]),
+    "negative start": ([-2, 3, 5, 9], [1, 2]),
+    "past total": ([0, 3, 5, 10], [0, 1]),
+    "far past total": ([0, 3, 5, 2**31 - 1], [0, 1]),
+    "two past total": ([0, 3, 10, 12], [0]),
+    "decreasing": ([0, 3, 2, 9], []),
+    "decreasing over a sequence": ([0, 7, 2, 9], []),
+    "falling back to the start": ([0, 3, 5, 0], []),
+    "past total and back": ([0, 3, 40, 9], []),
+}
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("what", PLANS)
+def test_offsets_that_are_no_batch(dev, what, codes):
+    """Offsets that decrease place no token: nothing is written.  A first sequence that does not
+    begin at 0 or one that ends past the packed rows is refused by itself."""
+    lens, ns, H, d, page = [40, 50, 60], [3, 2, 4], 2, 64, 16
+    offsets, sound = PLANS[what]
+    start = [0, 3, 5]
+    c = make(dev, 630, lens, H, d, page, codes)
+    kv = normal(dev, 631, 9, 2 * H, d)
+    table, cu = c["page_table"], torch.tensor(offsets, dtype=torch.int32, device=dev)
+    fa.cache_write(kv[:, :H], kv[:, H:], c["k_cache"], c["v_cache"], table, torch.tensor(lens, dtype=torch.int32, device=dev),
+                   cu, k_scale=c["k_scale"], v_scale=c["v_scale"])
+    assert fa.attn_last_device_error() == -8
+    k, v = rows_of(c)
+    mine = torch.zeros(k.shape[0], dtype=torch.bool)
+    for b in sound:
+        at = ref.row_index(table.cpu(), page, b, torch.arange(lens[b] - ns[b], lens[b]))
+        mine[at] = True
+        for x, got in ((kv[:, :H], k), (kv[:, H:], v)):
+            x = x[start[b]:start[b] + ns[b]].cpu()
+            if codes:
+                values, scale = ref.quantise(x)
+                x = values * scale.double()[..., None]
+            assert torch.equal(got[at], x.double()), b
+    assert k[~mine].isnan().all() and v[~mine].isnan().all()
+    # reading back: the same sequences, each from its first position on
+    full = fill(dev, 632, lens, H, d, page, codes)
+    out = [torch.full((9, H, d), 3.0, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    ptr = lambda t: None if t is None else t.data_ptr()
+    cache = fa.AttnPagedCache(*(ptr(full[n]) for n in ("k_cache", "v_cache", "k_scale", "v_scale", "page_table")),
+                              full["page_table"].shape[1], full["k_cache"].shape[0], page, H, d)
+    fa.attn_cache_read(cache, *out, cu, 3, 9)
+    assert fa.attn_last_device_error() == -8
+    for got, rows in zip(out, rows_of(full)):
+        left = torch.ones(9, dtype=torch.bool)
+        for b in sound:
+            at = ref.row_index(full["page_table"].cpu(), page, b, torch.arange(ns[b]))
+            assert torch.equal(got[start[b]:start[b] + ns[b]].cpu(), rows[at].to(torch.bfloat16))
+            left[start[b]:start[b] + ns[b]] = False
+        assert (got.cpu()[left] == 3).all()
+
+
+@pytest.mark.parametrize("fall", [1, 700, 1299])
+def test_offsets_that_fall_in_a_large_batch(dev, fall):
+    """One decrease among 1300 sequences (more than a CTA looks at in one go), at either end or inside."""
+    B, H, d, page = 1300, 1, 64, 16
+    c = make(dev, 635, [3] * B, H, d, page, True)
+    kv = normal(dev, 636, B, 2 * H, d)
+    cu = torch.arange(B + 1, dtype=torch.int32, device=dev)
+    lens = torch.full((B,), 3, dtype=torch.int32, device=dev)
+    write = lambda: fa.cache_write(kv[:, :H], kv[:, H:], c["k_cache"], c["v_cache"], c["page_table"], lens, cu,
+                                   k_scale=c["k_scale"], v_scale=c["v_scale"])
+    cu[fall] += 2
+    write()
+    assert fa.attn_last_device_error() == -8
+    assert rows_of(c)[0].isnan().all()
+    cu[fall] -= 2
+    write()
+    assert fa.attn_last_device_error() == 0
