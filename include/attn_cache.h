@@ -95,9 +95,11 @@ int attn_cache_read(const attn_paged_cache *cache, void *k, void *v, const int32
  * ATTN_ERR_SCRATCH.
  * ATTN_ERR_SHAPE also where the key tiles of a batch (at most B * H * max_len / 32,
  * times max_new * Hq / H / 256 rounded up) could be more than 2^31 - 1.
- * Errors in the error word: ATTN_ERR_SEQLENS (lengths as above; the rows of
- * that sequence are not written), ATTN_ERR_INDEX (a page outside the cache; the
- * rows that read it come out as NaN), ATTN_ERR_DEVICE_TIMEOUT (NaN as well).
+ * Errors in the error word: ATTN_ERR_SEQLENS (offsets and lengths as for
+ * attn_cache_write, and the bounds max_new and max_len; the rows of that sequence,
+ * with offsets that decrease all rows, are not written), ATTN_ERR_INDEX (a page
+ * outside the cache; the rows that read it come out as NaN),
+ * ATTN_ERR_DEVICE_TIMEOUT (NaN as well).
  */
 int attn_fwd_tree(const void *q, int64_t q_stride, const attn_paged_cache *cache,
                   const int32_t *seqlens, const int32_t *cu_seqlens, const int64_t *mask, void *o,

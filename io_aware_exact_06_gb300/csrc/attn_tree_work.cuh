@@ -38,9 +38,13 @@ __device__ __forceinline__ int seq_tiles(const Seq& s, const Work& w) {
 __device__ __forceinline__ int seq_segments(const Params& p, const Seq& s, const Work& w) {
   return (s.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
 }
-// Tiles of sequence b in the line; 0 if it has no new token or impossible lengths.
-__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq& s) {
-  if (!load_seq(p, b, s)) {
+// Tiles of sequence b in the line; 0 if it has no new token, impossible lengths, or is
+// the first and does not begin at 0.  falls is set where the offsets decrease: then they
+// place no row at all (a row could belong to two sequences).
+__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq& s, bool& falls) {
+  const bool fits = load_seq(p, b, s);
+  falls |= (int)((uint32_t)s.q0 + (uint32_t)s.n) < s.q0;
+  if (!fits || (b == 0 && s.q0 != 0)) {
     if (report) atomicOr(p.err, rows::kBadSeqlens);
     return 0;
   }
@@ -89,7 +93,9 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   const int b0 = (int)min((int64_t)t * per, (int64_t)p.B), b1 = min(p.B - b0, per) + b0;
   Seq s{};
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report, s);
+  bool falls = false;
+  for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report, s, falls);
+  if (__any_sync(0xffffffffu, falls)) return false;
   int upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -106,7 +112,7 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   const bool here = first >= before && first < upto;
   if (here && per > 1)  // else s is the one it has read
     for (;; ++b) {
-      const int n = line_tiles(p, w, b, false, s);
+      const int n = line_tiles(p, w, b, false, s, falls);
       if (at < n) break;
       at -= n;
     }
@@ -219,26 +225,29 @@ tree_join_kernel(const __grid_constant__ Params p, const __grid_constant__ Work 
   auto find = [&](int t) {
     Seq other;
     int n = 0, b = p.B;
+    bool falls = false;
     total = before = 0;
     for (int i = lane; i < p.B; i += 32) {
-      n = line_tiles(p, w, i, false, other);
+      n = line_tiles(p, w, i, false, other, falls);
       total += n;
       if (n && b == p.B && t >= other.q0 && t < other.q0 + other.n) b = i, sq = other;
     }
+    if (falls) b = -1;  // no row has a sequence
     const int mine = b;
     b = __reduce_min_sync(0xffffffffu, b);
     const int src = __ffs(__ballot_sync(0xffffffffu, mine == b)) - 1;
     sq.q0 = __shfl_sync(0xffffffffu, sq.q0, src);
     sq.n = __shfl_sync(0xffffffffu, sq.n, src);
     sq.len = __shfl_sync(0xffffffffu, sq.len, src);
-    if (b == p.B) sq.n = 0;
+    const bool found = (unsigned)b < (unsigned)p.B;
+    if (!found) sq.n = 0;
     if (p.B <= 32)
       before = lane < b ? n : 0;
     else
-      for (int i = lane; i < b; i += 32) before += line_tiles(p, w, i, false, other);
+      for (int i = lane; i < b; i += 32) before += line_tiles(p, w, i, false, other, falls);
     total = __reduce_add_sync(0xffffffffu, total);
     before = __reduce_add_sync(0xffffffffu, before);
-    return b < p.B;
+    return found;
   };
   int left = 0, r = 0, c0 = 0, c1 = 0, sub = 0;  // rows that follow in the same segment; row of it, its pieces
   bool inside = false, cut = false;

@@ -254,3 +254,44 @@ def test_offsets_that_fall_in_a_large_batch(dev, fall):
     cu[fall] -= 2
     write()
     assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("what", PLANS)
+def test_attention_of_offsets_that_are_no_batch(dev, what, codes, G):
+    """As for the cache: reported, no row written of a sequence that does not begin at 0 or ends past
+    the packed rows, none at all where the offsets decrease."""
+    lens, ns, H, d = [200, 300, 50], [3, 2, 4], 2, 64
+    offsets, sound = PLANS[what]
+    start = [0, 3, 5]
+    c = fill(dev, 640, lens, H, d, 16, codes)
+    q = normal(dev, 641, 9, H * G, d)
+    want, most = want_of(c, q, lens, ns, None), heaviest_of(c, q, lens, ns, None)
+    lens_d, cu = torch.tensor(lens, dtype=torch.int32, device=dev), torch.tensor(offsets, dtype=torch.int32, device=dev)
+    which = torch.zeros(9, H * G, dtype=torch.bool)
+    for b in sound:
+        which[start[b]:start[b] + ns[b]] = True
+    for splits in (0, 1):
+        out = torch.full((9, H * G, d), 7.0, dtype=torch.bfloat16, device=dev)
+        lse = torch.full((9, H * G), 7.0, device=dev)
+        fa.tree_decode(q, c["k_cache"], c["v_cache"], c["page_table"], lens_d, cu, 8, 300, k_scale=c["k_scale"],
+                       v_scale=c["v_scale"], num_splits=splits, out=out, lse=lse)
+        assert fa.attn_last_device_error() == -8
+        near((out, lse), want, codes, which, most)
+        assert (out.cpu()[~which] == 7).all() and (lse.cpu()[~which] == 7).all()
+
+
+def test_attention_of_offsets_that_fall_in_a_large_batch(dev):
+    B, H, d, page = 1300, 1, 64, 16
+    c = fill(dev, 645, [3] * B, H, d, page, True)
+    q = normal(dev, 646, B, 2, d)
+    lens = torch.full((B,), 3, dtype=torch.int32, device=dev)
+    for fall in (1, 700, 1299):
+        cu = torch.arange(B + 1, dtype=torch.int32, device=dev)
+        cu[fall] += 2
+        out = torch.full((B, 2, d), 7.0, dtype=torch.bfloat16, device=dev)
+        fa.tree_decode(q, c["k_cache"], c["v_cache"], c["page_table"], lens, cu, 3, 3, k_scale=c["k_scale"],
+                       v_scale=c["v_scale"], out=out)
+        assert fa.attn_last_device_error() == -8
+        assert (out == 7).all()
