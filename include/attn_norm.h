@@ -68,7 +68,8 @@ int attn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_
  * depends on the shape alone, so that results repeat bit for bit).  dq may be
  * dq_out itself and dk dk_out itself (same stride); no other overlap.  A token
  * with a position outside its table adds nothing to dwq and dwk and its dq and
- * dk are not written (ATTN_ERR_INDEX).  T == 0 writes dwq = dwk = 0.
+ * dk are not written (ATTN_ERR_INDEX).  T == 0 writes dwq = dwk = 0; Hq = 0
+ * writes dwq = 0 and Hk = 0 dwk = 0, unless they are NULL.
  * workspace: attn_qk_norm_rope_bwd_workspace(T, Hq, Hk, d) bytes of the
  * caller's device memory, 16-byte aligned, not initialised, in use until the
  * call's work on stream has finished (calls that may run at the same time

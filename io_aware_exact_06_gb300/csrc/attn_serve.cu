@@ -335,12 +335,12 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
   if (st != ATTN_OK) return st;
   attn::norm::Bwd p{};
   if ((st = check_rotary(rotary, T, d, &p.rot)) != ATTN_OK) return st;
-  if (Hq + Hk == 0) return ATTN_OK;
+  if (Hq + Hk == 0 && !dwq && !dwk) return ATTN_OK;
   if ((Hq && !dwq) || (Hk && !dwk)) return ATTN_ERR_NULL;
   if (!aligned(dwq, 4) || !aligned(dwk, 4)) return ATTN_ERR_ALIGN;
   const BwdPlan pl = bwd_plan(T, Hq, Hk, d);
   const int64_t grid = pl.ctas[0] + pl.ctas[1];
-  if (T > 0) {
+  if (grid > 0) {
     if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
     if ((st = check_rows(k, k_stride, Hk, d)) != ATTN_OK) return st;
     if ((st = check_rows(dq_out, dq_out_stride, Hq, d)) != ATTN_OK) return st;
@@ -354,7 +354,7 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
   }
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T > 0) {
+  if (grid > 0) {
     const void *x[2] = {q, k}, *w[2] = {wq, wk}, *g[2] = {dq_out, dk_out};
     void* dx[2] = {dq, dk};
     const int64_t x_ts[2] = {q_stride, k_stride}, g_ts[2] = {dq_out_stride, dk_out_stride},
@@ -385,8 +385,8 @@ extern "C" int attn_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void
                          : attn::norm::norm_rope_bwd_kernel<128, false, false>;
     if ((st = launch(kernel, grid, attn::norm::kThreads, attn::norm::kSmem, s, p)) != ATTN_OK) return st;
   }
-  const attn::norm::WeightSum w{static_cast<const float*>(workspace), Hq ? dwq : nullptr,
-                                Hk ? dwk : nullptr, (int)pl.ctas[0], (int)pl.ctas[1], d};
+  // a kind without heads, as well as a batch without tokens, has no partial rows: 0
+  const attn::norm::WeightSum w{static_cast<const float*>(workspace), dwq, dwk, (int)pl.ctas[0], (int)pl.ctas[1], d};
   return launch(attn::norm::norm_weight_kernel, 2 * d / 32, 1024, 0, s, w);
 }
 

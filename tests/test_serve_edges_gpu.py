@@ -295,3 +295,25 @@ def test_attention_of_offsets_that_fall_in_a_large_batch(dev):
                        v_scale=c["v_scale"], out=out)
         assert fa.attn_last_device_error() == -8
         assert (out == 7).all()
+
+
+@pytest.mark.parametrize("T", [0, 5])
+@pytest.mark.parametrize("Hq,Hk", [(0, 3), (3, 0), (0, 0)])
+def test_gradient_of_a_kind_without_heads(dev, T, Hq, Hk):
+    """No rows, so the sum over them is 0: its weight gradient is written, not left as it was."""
+    d = 64
+    x = inputs(650, T, Hq, Hk, d, d, 1, None)
+    y = to(dev, {**x, "q": x["q"].clone(), "k": x["k"].clone()})
+    dq, dk, dwq, dwk = fa.qk_norm_rope_backward(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"],
+                                                y["gq"], y["gk"])
+    assert dq.shape == (T, Hq, d) and dk.shape == (T, Hk, d)
+    dws = [torch.full((d,), 7.0, device=dev) for _ in "qk"]
+    rot = fa.AttnRotary(y["cos"].data_ptr(), y["sin"].data_ptr(), y["positions"].data_ptr(), y["cos"].shape[0], d, 1)
+    ws = torch.empty(max(1, fa.attn_qk_norm_rope_bwd_workspace(T, Hq, Hk, d)), dtype=torch.uint8, device=dev)
+    p = lambda t: t.data_ptr() or None
+    fa.attn_qk_norm_rope_bwd(p(y["q"]), Hq * d, p(y["k"]), Hk * d, y["wq"], y["wk"], p(y["gq"]), Hq * d, p(y["gk"]), Hk * d,
+                             p(dq), Hq * d, p(dk), Hk * d, *dws, T, Hq, Hk, d, 1e-6, rot, ws, ws.numel())
+    assert fa.attn_last_device_error() == 0
+    for H, w, got in ((Hq, dws[0], dwq), (Hk, dws[1], dwk)):
+        assert torch.equal(w, got)
+        assert (w == 0).all() if H * T == 0 else (w != 7).all()
