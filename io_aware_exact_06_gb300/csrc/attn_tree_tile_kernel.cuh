@@ -37,10 +37,18 @@
 // error below 2^-18 of the largest), and the two e4m3 products cost what one fp16
 // product does; the softmax multiplies a score by its key's scale.  V is converted
 // with its scale: fp16(code * scale * 2^(6 - F)), off by 2^-11, F a running
-// exponent of the segment's value scales (all of a CTA's tiles; O is rescaled when
-// it grows), which leaves values 2^-26 of the largest their full precision.  P is
+// exponent of a piece's value scales (O is rescaled when it grows).  P is
 // fp16(2^7 p): 2^-11, and 2^-32 absolute for the smallest.
+//
+// One F for all rows serves while the scales of the piece lie within 2^kSpread of each
+// other.  From the tile on where they do not (a hidden draft with huge values, a token
+// with tiny ones that takes nearly all the weight) V is the codes alone and P takes the
+// scales: fp16(2^(13 - F) p scale), F each row's own, from the largest p scale that it
+// sees.  Such a tile takes a third pass over the scores.
 #pragma once
+
+#include <climits>
+#include <cstddef>
 
 #include "attn_tree_work.cuh"
 
@@ -57,6 +65,9 @@ constexpr int kBigThreads = 512;
 constexpr int kSoftmaxRegs = 176, kOperandRegs = 80, kRestRegs = 80;
 constexpr int kRing = 8;  // segments whose flags are kept
 constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
+constexpr int kSpread = 12;       // log2
+constexpr int kFar = INT_MAX;     // in place of a tile's F: the scales lie further apart
+constexpr int kScaleFloor = -64;  // exponent of cache_write's smallest scale, a row of zeros: not counted
 
 template <int D, bool kCodes, bool kPair>
 struct BigCfg : Row<D, kCodes> {
@@ -77,7 +88,8 @@ struct BigCfg : Row<D, kCodes> {
   static constexpr int kOffC = kOffV + kV * kMat;
   static constexpr int kOffScale = kOffC + kReady * kConv;            // [kK][2][128] raw scales
   static constexpr int kOffMeta = kOffScale + (kCodes ? kK * 1024 : 0);  // [kMeta][128] key factors
-  static constexpr int kOffShared = kOffMeta + (kCodes ? kMeta * 512 : 0);
+  static constexpr int kOffFar = kOffMeta + (kCodes ? kMeta * 512 : 0);  // [kMeta][128] log2 of value scales, where far apart
+  static constexpr int kOffShared = kOffFar + (kCodes ? kMeta * 512 : 0);
   // barriers
   static constexpr int bKF = 0, bKE = bKF + kK, bVF = bKE + kK, bVE = bVF + kV, bRF = bVE + kV, bRE = bRF + kReady,
                        bMF = bRE + kReady, bME = bMF + kMeta, bSF = bME + kMeta, bPF = bSF + 2, bOF = bPF + 2,
@@ -151,15 +163,17 @@ struct BigShared {
   int abort;                  // a wait ran out
   int bad[kRing];             // the segment reads a page outside the cache
   uint32_t hidden[kRing][2];  // its new tokens with values that are not finite
-  int vexp[2][4];             // [tile's parity][operand warp]: largest exponent of a value scale
-  int vref[4];                // by tile: the exponent F of its values
   float2 ml[2][kBigRows];     // [group]: maxima and sums
-  int fend[2];                // [group]: F of its O
+  // for codes
+  int4 vexp[2];               // [tile's parity], of the four operand warps: exponents of value scales,
+                              // the largest (low half) and minus the smallest
+  int vref[4];                // by tile: the exponent F of its values, or kFar
+  int fend[2][kBigRows];      // [group]: F of a row's O
   float rc[2][2 * kBigRows];  // [segment's parity]: log2 units of a row's raw score
 };
 template <int D, bool kCodes, bool kPair>
 __host__ __device__ constexpr int big_smem() {
-  return BigCfg<D, kCodes, kPair>::kOffShared + (int)sizeof(BigShared) - (kCodes ? 0 : (int)sizeof(BigShared::rc));
+  return BigCfg<D, kCodes, kPair>::kOffShared + (kCodes ? (int)sizeof(BigShared) : (int)offsetof(BigShared, vexp));
 }
 
 __device__ __forceinline__ uint32_t half_mul2(uint32_t a, uint32_t b) {
@@ -425,7 +439,7 @@ struct Big {
 
   __device__ __forceinline__ void prepare(Walk k) {
     const int r = threadIdx.x % 128, lane = threadIdx.x % 32;  // thread r: key r of a tile
-    int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0, vref = 0, tile_parity = 0;
+    int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0, vref = 0, low = 0, tile_parity = 0;
     do {
       if (seg > 0) wait(C::bQE, (seg - 1) & 1);
       write_query(k, seg);
@@ -434,6 +448,7 @@ struct Big {
       for (int t = k.tile; t < end; ++t) {
         const int pos = t * kBigTile + r;
         bool cut = false;  // the value scale is not finite, for a key that rows may not see
+        bool far = false;  // the piece's value scales so far lie too far apart for one F
         float vscale = 0.f;
         if (kCodes) {
           wait(C::bKF + ks, kr & 1);
@@ -450,14 +465,21 @@ struct Big {
           const uint32_t bits = __float_as_uint(vscale) & 0x7fffffffu;
           const int e = bits < 0x7f800000u ? (int)(bits >> 23) - 127 : -127;
           const int most = __reduce_max_sync(0xffffffffu, e);
+          const int minus = __reduce_max_sync(0xffffffffu, e > kScaleFloor ? -e : -127);
           const int turn = tile_parity;
           tile_parity ^= 1;
-          if (lane == 0) ss.vexp[turn][threadIdx.x / 32 % 4] = most;
+          if (lane == 0)
+            reinterpret_cast<uint32_t*>(&ss.vexp[turn])[threadIdx.x / 32 % 4] = (uint32_t)(most & 0xffff) | (uint32_t)minus << 16;
           asm volatile("bar.sync 3, 128;" ::: "memory");
-          const int all = max(max(ss.vexp[turn][0], ss.vexp[turn][1]), max(ss.vexp[turn][2], ss.vexp[turn][3]));
+          const int4 by = ss.vexp[turn];
+          const uint32_t both = __vmaxs2(__vmaxs2(by.x, by.y), __vmaxs2(by.z, by.w));
+          const int all = (int16_t)(both & 0xffff), least = -((int)both >> 16);
           if (t == k.tile || all > vref) vref = max(all, -100) + 2;
+          low = t == k.tile ? least : min(low, least);
+          far = vref - low > kSpread + 2;
           *reinterpret_cast<float*>(smem_ptr + C::kOffMeta + ms * 512 + 4 * r) = kscale * p.c;
-          if (r == 0) ss.vref[ms] = vref;
+          if (far) *reinterpret_cast<float*>(smem_ptr + C::kOffFar + ms * 512 + 4 * r) = lg2(vscale);
+          if (r == 0) ss.vref[ms] = far ? kFar : vref;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar(C::bMF + ms));
@@ -473,7 +495,7 @@ struct Big {
           if (rr > 0) wait(C::bRE + rs, (rr & 1) ^ 1);
           const uint32_t dst = smem + C::kOffC + rs * C::kConv;
           // the scale as a sum of two fp16: code * hi + code * lo, rounded once more
-          const float f = vscale * pow2(6 - vref);
+          const float f = far ? 1.f : vscale * pow2(6 - vref);
           const uint32_t hi = pack_half(f, f);
           float fh;
           asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.f32.f16 %0, x;\n}\n" : "=f"(fh) : "r"(hi));
@@ -564,10 +586,15 @@ struct Big {
             if (kCodes && j == (kPair ? 0 : g)) rc = ss.rc[seg & 1][(kPair ? g * kBigRows : 0) + r];
             const int f = kCodes ? ss.vref[ms] : 0;
             const bool more = j > (kPair ? 0 : 1);  // O holds something
-            const float shrink = more && f != vref ? pow2(vref - f) : 1.f;
-            vref = f;
-            tile(k.tile + j, g, more, ctx, word, rc, shrink,
-                 reinterpret_cast<const float4*>(smem_ptr + C::kOffMeta + ms * 512), mine, colS, m, l);
+            uint8_t* const meta = smem_ptr + C::kOffMeta + ms * 512;
+            if (!kCodes || f != kFar) {
+              const float shrink = more && f != vref ? pow2(vref - f) : 1.f;
+              vref = f;
+              tile(k.tile + j, g, more, ctx, word, rc, shrink, reinterpret_cast<const float4*>(meta), mine, colS, m, l);
+            } else {
+              tile_far(k.tile + j, g, more, ctx, word, rc, reinterpret_cast<const float*>(meta),
+                       reinterpret_cast<const float*>(meta + C::kOffFar - C::kOffMeta), mine, colS, m, l, vref);
+            }
           }
           tc_fence_before();
           mbar_arrive(bar(C::bPF + g));
@@ -586,7 +613,7 @@ struct Big {
       close_row(m, l);
       // (the other group has read the last segment's: O is free only when it has)
       ss.ml[g][r] = make_float2(m, l);
-      if (kCodes && busy) ss.fend[g] = vref;
+      if (kCodes) ss.fend[g][r] = vref;
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const bool poison = aborted() || *(volatile int*)&ss.bad[seg % kRing];
       const uint64_t hid = (uint64_t) * (volatile uint32_t*)&ss.hidden[seg % kRing][1] << 32 |
@@ -606,7 +633,8 @@ struct Big {
         const float ls = (sa ? wa * a.y : 0.f) + (sb ? wb * b.y : 0.f);
         const float inv = ls != 0.f ? 1.f / ls : 0.f;
         // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
-        const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0]) - 6) : wa, ub = kCodes ? wb * pow2(ss.fend[1] - 6) : wb;
+        const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0][r]) - 6) : wa;
+        const float ub = kCodes ? wb * pow2((kPair ? vref : ss.fend[1][r]) - 6) : wb;
         const bool whole = k.tile == 0 && n == k.tiles;
         const int slot = whole ? -1 : 2 * (int)blockIdx.x + !firstp;
         const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * C::kRows + (row - row0(k));
@@ -767,6 +795,85 @@ struct Big {
     }
     tmem_st_wait();
     l = l * alpha + ((s0 + s1) + (s2 + s3));
+  }
+
+  // tile() where the piece's value scales lie far apart: P takes them (their log2 in
+  // `scales`), the row's F is `frame`.  Rare, and its code is kept small.
+  __device__ __forceinline__ void tile_far(int t, int g, bool accumulate, int ctx, uint64_t word, float rc,
+                                           const float* meta, const float* scales, uint32_t mine, uint32_t colS, float& m,
+                                           float& l, int& frame) {
+    const int d = t * kBigTile - ctx;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {  // scores in log2, masked
+      uint32_t x[16];
+      tmem_ld_x16(colS + 16 * c, x);
+      tmem_ld_wait_x16(x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = d + 16 * c + i;  // new token of the key
+        const float y = __uint_as_float(x[i]) * meta[16 * c + i] * rc;
+        x[i] = __float_as_uint(j < 0 || (j < 64 && sees(word, j)) ? y : -INFINITY);
+        top = fmaxf(top, __uint_as_float(x[i]));
+      }
+      tmem_st_x16(colS + 16 * c, x);
+    }
+    tmem_st_wait();
+    const float was = m;
+    float alpha = 1.f;
+    if (top > m + kLazy) {
+      alpha = m == -INFINITY ? 0.f : ex2(m - top);
+      m = top;
+    }
+    const float zero = m == -INFINITY ? 0.f : m;
+    float heavy = -INFINITY, sum = 0.f;  // log2 of the largest p scale
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      uint32_t x[16];
+      tmem_ld_x16(colS + 16 * c, x);
+      tmem_ld_wait_x16(x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float y = __uint_as_float(x[i]) - zero;
+        sum += ex2(y + kPLog2);
+        heavy = fmaxf(heavy, y + scales[16 * c + i]);
+      }
+    }
+    l = l * alpha + sum;
+    int to = (int)ceilf(fminf(fmaxf(heavy, -100.f), 127.f));
+    if (accumulate) {  // what O holds has shrunk with the growth of the maximum
+      const float now = was == -INFINITY ? -INFINITY : (float)frame + (was - m);
+      to = max(to, (int)ceilf(fmaxf(now, -100.f)));
+      const float f = ex2(now - (float)to);
+#pragma unroll 1
+      for (int col = 0; col < D; col += 16) {
+        uint32_t o[16];
+        tmem_ld_x16(mine + 256 + D * g + col, o);
+        tmem_ld_wait_x16(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st_x16(mine + 256 + D * g + col, o);
+      }
+    }
+    frame = to;
+    const float neg = 6.f + kPLog2 - (float)to - zero;  // to fp16(2^(13 - F) p scale)
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t pw[16];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[16];
+        tmem_ld_x16(colS + 32 * c + 16 * half, x);
+        tmem_ld_wait_x16(x);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float* s = scales + 32 * c + 16 * half + i;
+          pw[8 * half + i / 2] = pack_half(ex2(__uint_as_float(x[i]) + s[0] + neg), ex2(__uint_as_float(x[i + 1]) + s[1] + neg));
+        }
+      }
+      tmem_st_x16(colS + 16 * c, pw);
+    }
+    tmem_st_wait();
   }
 };
 

@@ -317,3 +317,71 @@ def test_gradient_of_a_kind_without_heads(dev, T, Hq, Hk):
     for H, w, got in ((Hq, dws[0], dwq), (Hk, dws[1], dwk)):
         assert torch.equal(w, got)
         assert (w == 0).all() if H * T == 0 else (w != 7).all()
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("up", [40, 90])
+def test_large_values_of_hidden_tokens(dev, codes, d, G, up):
+    """A drafted token whose values are 2^40 or 2^90 times the others' does not cost the rows that do
+    not see it a bit, nor do they cost the row that does."""
+    lens, ns, H = [200, 131, 64], [6, 6, 6], 2
+    c = make(dev, 660, lens, H, d, 16, codes)
+    kv = normal(dev, 661, sum(lens), 2 * H, d)
+    ends = [sum(lens[:i + 1]) for i in range(3)]
+    for end, j in zip(ends, (1, 3, 5)):
+        kv[end - 6 + j, H:] *= 2.0 ** up
+    put(dev, c, kv[:, :H], kv[:, H:], lens, lens)
+    q = normal(dev, 662, 18, H * G, d)
+    mask = torch.tensor([1 | 1 << i for _ in ns for i in range(6)], dtype=torch.int64)
+    want, most = want_of(c, q, lens, ns, mask), heaviest_of(c, q, lens, ns, mask)
+    for splits in (0, 1, 2):
+        got = call(dev, c, q, lens, ns, mask, num_splits=splits)
+        assert fa.attn_last_device_error() == 0
+        near(got, want, codes, torch.ones(18, H * G, dtype=torch.bool), most)
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("sink", [0, 130, 290, 399])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_small_values_that_take_the_weight(dev, codes, G, sink, splits):
+    """One token takes the weight (the others e^-80 and less) and its values are 2^-45 of the others':
+    O is those values, to their own size."""
+    L, ns, H, d = 400, [6], 1, 128
+    c = make(dev, 670, [L], H, d, 16, codes)
+    kv = normal(dev, 671, L, 2, d)
+    kv[:, 0] *= 0.25
+    kv[sink, 0] = 100.0 / d ** 0.5
+    kv[sink, 1] *= 2.0 ** -45
+    put(dev, c, kv[:, :1], kv[:, 1:], [L], [L])
+    q = torch.ones(6, H * G, d, dtype=torch.bfloat16, device=dev)
+    mask = torch.full((6,), 63, dtype=torch.int64)
+    got = call(dev, c, q, [L], ns, mask, num_splits=splits)
+    assert fa.attn_last_device_error() == 0
+    near(got, want_of(c, q, [L], ns, mask), codes, torch.ones(6, H * G, dtype=torch.bool),
+         heaviest_of(c, q, [L], ns, mask))
+
+
+@pytest.mark.parametrize("G", [3, 24, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_value_scales_without_order(dev, d, G):
+    """Value scales drawn from 2^-50 .. 2^50, scores that move the maximum often, tiles of one size
+    between them: a row's frame moves both ways."""
+    lens, ns, H = [1500, 700], [6, 6], 2
+    c = make(dev, 680, lens, H, d, 32, True)
+    g = torch.Generator().manual_seed(681)
+    kv = normal(dev, 682, sum(lens), 2 * H, d)
+    e = torch.randint(-50, 51, (sum(lens), 1, 1), generator=g).double()
+    at = torch.arange(sum(lens)) // 128
+    e[(at % 3 == 0)[:, None, None]] = 0.0  # every third stretch is of one size
+    kv[:, H:] = (kv[:, H:].double() * torch.exp2(e).to(dev)).to(torch.bfloat16)
+    put(dev, c, kv[:, :H], kv[:, H:], lens, lens)
+    q = normal(dev, 683, 12, H * G, d, std=4.0)
+    mask = torch.tensor([1 | 1 << i for _ in ns for i in range(6)], dtype=torch.int64)
+    want, most = want_of(c, q, lens, ns, mask), heaviest_of(c, q, lens, ns, mask)
+    for splits in (0, 1, 3):
+        got = call(dev, c, q, lens, ns, mask, num_splits=splits)
+        assert fa.attn_last_device_error() == 0
+        near(got, want, True, torch.ones(12, H * G, dtype=torch.bool), most)
