@@ -545,7 +545,7 @@ def _native():
 
         import torch  # noqa: F401  (the module links against it)
         L = lib()
-        path = _build.BINDING
+        path = _build.binding_path()
         if not os.path.exists(path):
             raise RuntimeError(f"CPython module not built: {path} is missing "
                                "(run `python -m io_aware_exact_06_gb300.build`)")

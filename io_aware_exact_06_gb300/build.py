@@ -1,5 +1,6 @@
 """Builds the sm_103a attention library in-tree: _build/libattn_fwd.so, and the
-CPython module of its norm and cache conveniences: _build/_serve.so.
+CPython module of its norm and cache conveniences: _build/_serve.<versions>.so,
+for this interpreter and this torch.  The library needs neither.
 
 nvcc compiles the CUDA sources for sm_103a only and links the CUDA runtime
 statically, so the library loads on a machine without a GPU (every CUDA call
@@ -20,7 +21,6 @@ LIB = os.path.join(OUT_DIR, "libattn_fwd.so")
 SOURCES = [os.path.join(CSRC, "attn_fwd.cu"), os.path.join(CSRC, "attn_bwd.cu"),
            os.path.join(CSRC, "attn_serve.cu")]
 # the torch conveniences of the norm and cache calls, as a CPython module
-BINDING = os.path.join(OUT_DIR, "_serve.so")
 BINDING_SOURCE = os.path.join(CSRC, "serve_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -39,6 +39,14 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def binding_path() -> str:
+    """The module's file; its name holds what it is compiled against, so that another
+    Python or torch gets one of its own."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(OUT_DIR, f"_serve.{sys.implementation.cache_tag}.torch-{torch.__version__}.abi{abi}.so")
+
+
 def _binding_command(out: str) -> list[str]:
     """g++ on the binding, with the headers and libraries of this interpreter and torch."""
     import sysconfig
@@ -55,27 +63,32 @@ def _binding_command(out: str) -> list[str]:
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
-def _binding_fresh() -> bool:
+def _binding_fresh(path: str) -> bool:
     deps = [BINDING_SOURCE, __file__] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in deps)
+    return os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(p) for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Builds what is missing or older than its sources; returns the library's path."""
+    """Builds what is missing or older than its sources; returns the library's path.
+    Without torch the module of torch conveniences is left out."""
     os.makedirs(OUT_DIR, exist_ok=True)
     binding = None
-    if force or not _binding_fresh():
-        tmp = BINDING + f".tmp{os.getpid()}"
-        cmd = _binding_command(tmp)
-        binding = (cmd, tmp, subprocess.Popen(cmd))  # beside the kernels
+    try:
+        path = binding_path()
+        if force or not _binding_fresh(path):
+            tmp = path + f".tmp{os.getpid()}"
+            cmd = _binding_command(tmp)
+            binding = (cmd, tmp, path, subprocess.Popen(cmd))  # beside the kernels
+    except ImportError as e:
+        print(f"no torch ({e}): the library alone is built", file=sys.stderr)
     try:
         return _build_library(force, verbose)
     finally:
         if binding:
-            cmd, tmp, pr = binding
+            cmd, tmp, path, pr = binding
             if pr.wait() != 0:
                 raise subprocess.CalledProcessError(pr.returncode, cmd)
-            os.replace(tmp, BINDING)
+            os.replace(tmp, path)
 
 
 def _build_library(force: bool, verbose: bool) -> str:
