@@ -569,6 +569,8 @@ def _call(name: str, stream, device, *args):
         import torch
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream.device != device:  # made current, it would leave the tensors' device on its own stream
+            raise ValueError(f"stream must be on {device}, not {stream.device}")
         with torch.cuda.stream(stream):
             got = f(*args)
     if type(got) is int and got != ATTN_OK:

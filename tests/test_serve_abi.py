@@ -186,3 +186,20 @@ def test_convenience_refusals():
             call(k_scale=torch.zeros(2, 2, 16))
         with pytest.raises(TypeError):  # scales with a bf16 cache
             call(k_scale=torch.zeros(2, 2, 16), v_scale=torch.zeros(2, 2, 16))
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would run on the tensors' device, on whatever stream is current there."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    stream = SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    k, kc = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)
+    lens, cu, table = torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    w, c, pos = torch.zeros(64, dtype=torch.bfloat16), torch.zeros(8, 32), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: fa.qk_norm_rope(k, k, w, w, c, c, pos, stream=stream),
+                 lambda: fa.qk_norm_rope_backward(k, k, w, w, c, c, pos, k, k, stream=stream),
+                 lambda: fa.cache_write(k, k, kc, kc, table, lens, cu, stream=stream),
+                 lambda: fa.cache_read(kc, kc, table, cu, 3, stream=stream),
+                 lambda: fa.tree_decode(k, kc, kc, table, lens, cu, 3, 16, stream=stream)):
+        with pytest.raises(ValueError, match="stream must be on"):
+            call()

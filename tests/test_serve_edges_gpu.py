@@ -385,3 +385,18 @@ def test_value_scales_without_order(dev, d, G):
         got = call(dev, c, q, lens, ns, mask, num_splits=splits)
         assert fa.attn_last_device_error() == 0
         near(got, want, True, torch.ones(12, H * G, dtype=torch.bool), most)
+
+
+def test_streams_by_address(dev):
+    """`stream` may be a torch stream or its address, the default stream's 0 among them."""
+    x = inputs(690, 33, 4, 2, 64, 64, 1, None)
+    y = to(dev, x)
+    call_ = lambda **kw: fa.qk_norm_rope(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"], **kw)
+    want = call_()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for stream in (0, torch.cuda.current_stream(), torch.cuda.current_stream().cuda_stream, other, other.cuda_stream):
+        got = call_(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa.attn_last_device_error() == 0
