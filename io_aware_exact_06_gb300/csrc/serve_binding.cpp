@@ -119,7 +119,9 @@ attn_rotary rotary_of(PyObject* cos_o, PyObject* sin_o, PyObject* pos_o, PyObjec
   TORCH_CHECK_VALUE(c.size(1) <= 1 << 20, "cos has too many columns");
   r.rot = 2 * static_cast<int>(c.size(1));
   r.axes = static_cast<int>(axes);
-  r.interleaved = PyObject_IsTrue(interleaved) == 1;
+  const int inter = PyObject_IsTrue(interleaved);
+  if (inter < 0) throw python_error();
+  r.interleaved = inter;
   if (sections == Py_None) {
     TORCH_CHECK_VALUE(axes == 1, "positions with several axes need sections");
     return r;

@@ -400,3 +400,13 @@ def test_streams_by_address(dev):
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert fa.attn_last_device_error() == 0
+
+
+def test_interleaved_without_a_truth_value(dev):
+    """Its own error, not a result with an error behind it."""
+    x = inputs(695, 3, 2, 1, 64, 64, 1, None)
+    y = to(dev, x)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        fa.qk_norm_rope(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"],
+                        interleaved=torch.tensor([True, False]))
+    assert fa.attn_last_device_error() == 0
