@@ -164,6 +164,7 @@ struct BigShared {
   int bad[kRing];             // the segment reads a page outside the cache
   uint32_t hidden[kRing][2];  // its new tokens with values that are not finite
   float2 ml[2][kBigRows];     // [group]: maxima and sums
+  __nv_bfloat16 fix[2][kBigRows];  // [group]: bf16: what rounding the largest probabilities adds to the sum
   // for codes
   int4 vexp[2];               // [tile's parity], of the four operand warps: exponents of value scales,
                               // the largest (low half) and minus the smallest
@@ -571,7 +572,7 @@ struct Big {
       const int tok = live ? row / p.G : 0;
       const uint64_t word = (live ? mask_word(p.mask, sq.q0 + tok, tok) : 0) &
                             (sq.n >= 64 ? ~0ull : (1ull << sq.n) - 1);
-      float rc = p.c, m = -INFINITY, l = 0.f;
+      float rc = p.c, m = -INFINITY, l = 0.f, fix = 0.f;
       int vref = 0;
       for (int j = 0; j < n; ++j) {
         if (kPair || (j & 1) == g) {
@@ -590,7 +591,8 @@ struct Big {
             if (!kCodes || f != kFar) {
               const float shrink = more && f != vref ? pow2(vref - f) : 1.f;
               vref = f;
-              tile(k.tile + j, g, more, ctx, word, rc, shrink, reinterpret_cast<const float4*>(meta), mine, colS, m, l);
+              tile(k.tile + j, g, more, ctx, word, rc, shrink, reinterpret_cast<const float4*>(meta), mine, colS, m, l,
+                   fix);
             } else {
               tile_far(k.tile + j, g, more, ctx, word, rc, reinterpret_cast<const float*>(meta),
                        reinterpret_cast<const float*>(meta + C::kOffFar - C::kOffMeta), mine, colS, m, l, vref);
@@ -614,6 +616,7 @@ struct Big {
       // (the other group has read the last segment's: O is free only when it has)
       ss.ml[g][r] = make_float2(m, l);
       if (kCodes) ss.fend[g][r] = vref;
+      else if (!kPair) ss.fix[g][r] = __float2bfloat16(fix);
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const bool poison = aborted() || *(volatile int*)&ss.bad[seg % kRing];
       const uint64_t hid = (uint64_t) * (volatile uint32_t*)&ss.hidden[seg % kRing][1] << 32 |
@@ -631,7 +634,11 @@ struct Big {
         const bool sa = a.x != -INFINITY, sb = b.x != -INFINITY;
         const float wa = sa ? ex2(a.x - mm) : 0.f, wb = sb ? ex2(b.x - mm) : 0.f;
         const float ls = (sa ? wa * a.y : 0.f) + (sb ? wb * b.y : 0.f);
-        const float inv = ls != 0.f ? 1.f / ls : 0.f;
+        // O's sum is of the probabilities as the products took them
+        float lo = ls;
+        if (!kCodes && kPair) lo += fix;
+        if (!kCodes && !kPair) lo += wa * __bfloat162float(ss.fix[0][r]) + wb * __bfloat162float(ss.fix[1][r]);
+        const float inv = ls != 0.f ? 1.f / lo : 0.f;
         // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
         const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0][r]) - 6) : wa;
         const float ub = kCodes ? wb * pow2((kPair ? vref : ss.fend[1][r]) - 6) : wb;
@@ -706,7 +713,8 @@ struct Big {
   // Softmax of this thread's row of key tile t: S from TMEM, P back to it, over S.
   // O (accumulate: it holds something) takes `shrink` and the growth of the maximum.
   __device__ __forceinline__ void tile(int t, int g, bool accumulate, int ctx, uint64_t word, float rc, float shrink,
-                                       const float4* meta, uint32_t mine, uint32_t colS, float& m, float& l) {
+                                       const float4* meta, uint32_t mine, uint32_t colS, float& m, float& l,
+                                       float& fix) {
     const int d = t * kBigTile - ctx;  // new token of the tile's first key
     const bool edge = d + kBigTile > 0;
     float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
@@ -753,7 +761,7 @@ struct Big {
       }
     }
     if (kCodes || edge) tmem_st_wait();
-    const float top = fmaxf(max3f(top0, top1, top2), top3) * rc;  // rc > 0: -inf stays
+    const float raw = fmaxf(max3f(top0, top1, top2), top3), top = raw * rc;  // rc > 0: -inf stays
     const bool grow = top > m + kLazy;  // also the first finite one
     float alpha = 1.f;
     if (grow) {
@@ -773,6 +781,10 @@ struct Big {
       }
     }
     const float neg = (m == -INFINITY ? 0.f : -m) + (kCodes ? kPLog2 : 0.f);
+    if (!kCodes) {  // the largest probability alone is worth it (2^-9 of it, near all of a peaked row's sum)
+      const float pm = ex2(fmaf(raw, rc, neg));
+      fix = fix * alpha + (__bfloat162float(__float2bfloat16(pm)) - pm);
+    }
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {

@@ -410,3 +410,27 @@ def test_interleaved_without_a_truth_value(dev):
         fa.qk_norm_rope(y["q"], y["k"], y["wq"], y["wk"], y["cos"], y["sin"], y["positions"],
                         interleaved=torch.tensor([True, False]))
     assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_weights_that_are_rounded_add_up_to_one(dev, d, G, splits):
+    """Keys that all hold the same values give back those values: the bf16 probabilities of a bf16 cache
+    are divided by their own sum.  One key takes 0.98 of a row, against a running maximum that an earlier
+    one has set (its weight is no power of two); the rounding of the others, 2^-8 of 0.02, stays under half
+    a step of the result (2^-9 of it at least), so it is exact."""
+    lens, ns, H = [700, 333], [6, 6], 2
+    c = make(dev, 700, lens, H, d, 16, False)
+    kv = normal(dev, 701, sum(lens), 2 * H, d, std=0.05)
+    for first in (0, lens[0]):
+        kv[first + 3, :H], kv[first + 300, :H] = 40.0 / d ** 0.5, 45.0 / d ** 0.5  # scores f 40 and f 45
+    value = (1.99 * torch.exp2(torch.arange(d, device=dev) % 9 - 4.0)).to(torch.bfloat16)
+    kv[:, H:] = value
+    put(dev, c, kv[:, :H], kv[:, H:], lens, lens)
+    g = torch.Generator().manual_seed(702)
+    f = 0.82 + 0.18 * torch.rand(12, H * G, 1, generator=g)  # e^(-5 f) < 0.02, e^(-38 f) next to nothing
+    q = f.expand(-1, -1, d).to(torch.bfloat16).to(dev).contiguous()
+    o, lse = call(dev, c, q, lens, ns, None, num_splits=splits)
+    assert fa.attn_last_device_error() == 0
+    assert (o == value).all()
