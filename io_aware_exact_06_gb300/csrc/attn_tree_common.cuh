@@ -13,9 +13,9 @@
 // With e4m3 codes a score is code . q times the key's scale, and the products with V
 // take fp16 operands, whose rounding (2^-11) is below the output's (2^-8); each
 // kernel says which of them takes the value's scale.  With a bf16 cache
-// probabilities are rounded to bf16, the type of V (tensor products take one type), and
-// O is divided by the sum of the rounded ones (many rows: with the largest of each
-// tile rounded, which 2^-8 of matters); LSE is of the sum before rounding.
+// probabilities are bf16, the type of V (tensor products take one type): few rows take
+// them as the sum of two (2^-16 of each is lost), many rows round once (2^-8) and divide
+// O by the sum with the largest of each tile rounded; LSE is of the sum before.
 // Sums, maxima and scores are fp32.
 #pragma once
 

@@ -4,7 +4,9 @@
 // [1, 2), which keeps its bf16 values exact in fp16 down to 2^-14 of that.  A
 // probability takes its value's scale before it meets the codes of V; the running
 // maximum is taken over log2(probability * value scale), so that this fp16 operand
-// stays in range whatever the scales.
+// stays in range whatever the scales.  Over a bf16 cache a probability is two bf16,
+// its rounding and what that leaves, each with its product with V (12 drafts 51.4 ->
+// 52.4 us; 0.00227 -> 0.00166 off fp64, which is the rounding of O alone).
 #pragma once
 
 #include "attn_tree_work.cuh"
@@ -77,7 +79,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[C::kStages];
   __shared__ uint32_t hidden_all[kWarps][2];
-  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_r[kCodes ? 1 : kWarps][kRows];
+  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -236,11 +238,10 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       }
     }
     float o[kMT][kNT][4], m[kNT][2], l[kNT][2];
-    float lr[kNT][2];  // bf16: the sum of the probabilities as the products take them, by which O is divided
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = lr[nt][0] = lr[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -343,7 +344,6 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             const float a = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - mn);
             m[nt][i] = mn;
             l[nt][i] *= a;
-            lr[nt][i] *= a;
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt) {
               o[mt][nt][i] *= a;
@@ -353,7 +353,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
       }
 #pragma unroll
       for (int ksub = 0; ksub < 2; ++ksub) {
-        uint32_t pb[kNT][2];
+        uint32_t pb[kNT][2], pl[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -367,11 +367,9 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
               w[i] = kCodes ? (x == -INFINITY ? 0.f : pr * vsc[ksub][kh]) : pr;
             }
             const uint32_t both = kCodes ? pack_half(w[0], w[1]) : rows::pack2(w[0], w[1]);
-            if (!kCodes) {
-              lr[nt][0] += __uint_as_float(both << 16);
-              lr[nt][1] += __uint_as_float(both & 0xffff0000u);
-            }
             pb[nt][kh] = transposed(both);
+            if (!kCodes)
+              pl[nt][kh] = transposed(rows::pack2(w[0] - __uint_as_float(both << 16), w[1] - __uint_as_float(both & 0xffff0000u)));
           }
         if (!kCodes) {
 #pragma unroll
@@ -380,7 +378,10 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             const int ch = 2 * mt + ((lane / 8) & 1);
             ldsm4t(va, vt + (ch / 8) * (kFewTile * 128) + swz<128>(16 * ksub + lane % 8 + 8 * (lane / 16), ch % 8));
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma<false>(o[mt][nt], va, pb[nt][0], pb[nt][1]);
+            for (int nt = 0; nt < kNT; ++nt) {
+              mma<false>(o[mt][nt], va, pb[nt][0], pb[nt][1]);
+              mma<false>(o[mt][nt], va, pl[nt][0], pl[nt][1]);
+            }
           }
         } else {
           // lane (n, c): columns 32 g + 4 n .. + 3 of keys 2c, 2c+1, 2c+8, 2c+9; the
@@ -416,22 +417,18 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
-          if (!kCodes) lr[nt][i] += __shfl_xor_sync(0xffffffffu, lr[nt][i], off);
-        }
+        for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
         close_row(m[nt][i], l[nt][i]);
         if (n == 0) {
           sm_m[warp][8 * nt + 2 * c + i] = m[nt][i];
           sm_l[warp][8 * nt + 2 * c + i] = l[nt][i];
-          if (!kCodes) sm_r[warp][8 * nt + 2 * c + i] = l[nt][i] == l[nt][i] ? lr[nt][i] : NAN;
         }
       }
     const bool whole = t_begin == 0 && t_end == wk.tiles;
     const int slot = whole ? -1 : (2 * unit + !first) * w.heads + sub;
     __syncwarp();
     PieceEnd<D, kCodes, kRows> end;
-    end.rows_of(p, sq, h, row0, slot, sm_m[warp], sm_l[warp], kCodes ? sm_l[warp] : sm_r[warp], (uint64_t)hidden[1] << 32 | hidden[0],
+    end.rows_of(p, sq, h, row0, slot, sm_m[warp], sm_l[warp], (uint64_t)hidden[1] << 32 | hidden[0],
                 poison || expired, lane);
 #pragma unroll
     for (int g = 0; g < D / C::kTurn; ++g) {

@@ -141,9 +141,8 @@ struct PieceEnd {
   uint64_t hid[kN];    // new tokens with values that are not finite, seen by the row
   bool live[kN], direct, poison;
 
-  // sm_m, sm_l: maxima and sums; sm_r: the sums of the probabilities as rounded
   __device__ __forceinline__ void rows_of(const Params& p, const Seq& sq, int h, int row0, int slot, const float* sm_m,
-                                          const float* sm_l, const float* sm_r, uint64_t hidden, bool bad, int lane) {
+                                          const float* sm_l, uint64_t hidden, bool bad, int lane) {
     const int M = sq.n * p.G;
     direct = slot < 0;
     poison = bad;
@@ -155,7 +154,7 @@ struct PieceEnd {
       const int tok = (row0 + r) / p.G, head = h * p.G + (row0 + r) - tok * p.G;
       const float m = sm_m[r], l = m == -INFINITY ? 0.f : sm_l[r];
       // a row of NaN sums keeps them; one that saw nothing is 0
-      inv[j] = l != 0.f ? 1.f / sm_r[r] : 0.f;
+      inv[j] = l != 0.f ? 1.f / l : 0.f;
       hid[j] = hidden ? hidden & mask_word(p.mask, sq.q0 + tok, tok) : 0;
       at[j] = direct ? (int64_t)(sq.q0 + tok) * p.Hq + head : (int64_t)slot * kRows + r;
       float lse = l != 0.f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;

@@ -417,7 +417,7 @@ def test_interleaved_without_a_truth_value(dev):
 @pytest.mark.parametrize("splits", [0, 1])
 def test_weights_that_are_rounded_add_up_to_one(dev, d, G, splits):
     """Keys that all hold the same values give back those values: the bf16 probabilities of a bf16 cache
-    are divided by their own sum.  One key takes 0.98 of a row, against a running maximum that an earlier
+    are divided by their own sum (few rows: are two bf16 each).  One key takes 0.98 of a row, against a running maximum that an earlier
     one has set (its weight is no power of two); the rounding of the others, 2^-8 of 0.02, stays under half
     a step of the result (2^-9 of it at least), so it is exact."""
     lens, ns, H = [700, 333], [6, 6], 2
@@ -434,3 +434,18 @@ def test_weights_that_are_rounded_add_up_to_one(dev, d, G, splits):
     o, lse = call(dev, c, q, lens, ns, None, num_splits=splits)
     assert fa.attn_last_device_error() == 0
     assert (o == value).all()
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 2), (128, 1)])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_few_rows_lose_nothing_of_their_weights(dev, d, G, splits):
+    """Up to 8 rows (16 at d = 64) over a bf16 cache take a probability as the sum of two bf16: 2^-8 of 2^-8
+    of it is lost, so O is good to its own rounding and what scores and sums add."""
+    lens, ns, H = [3000, 700, 65], [6, 6, 6], 2
+    c = fill(dev, 710, lens, H, d, 32, False)
+    q = normal(dev, 711, 18, H * G, d, std=1.5)
+    o, lse = (t.cpu().double() for t in call(dev, c, q, lens, ns, None, num_splits=splits))
+    assert fa.attn_last_device_error() == 0
+    wo, wl, A, S = want_of(c, q, lens, ns, None)
+    tol = 2.0 ** -8 * wo.abs() + A * (2.0 ** -16 + 2.0 ** -19 * S[..., None] + 2.0 ** -17)
+    assert ((o - wo).abs() <= tol).all(), ((o - wo).abs() / tol).max()
