@@ -59,7 +59,9 @@ int attn_cache_write(const attn_paged_cache *cache, const void *k, int64_t k_str
 /*
  * attn_cache_read: positions 0 .. cu_seqlens[b+1] - cu_seqlens[b] - 1 of every
  * sequence into the packed rows cu_seqlens[b] .. of k, v [total, H, d] bf16
- * (contiguous), the layout attn_fwd and attn_fwd_decode take.  Codes read back
+ * (contiguous), the layout attn_fwd and attn_fwd_decode take.  (Those have as
+ * many key heads as query heads: heads that queries share are repeated for
+ * them first; attn_fwd_tree reads shared heads as they are.)  Codes read back
  * as bf16(code * scale).  Errors as for attn_cache_write; the rows concerned
  * are not written.
  */
@@ -77,7 +79,9 @@ int attn_cache_read(const attn_paged_cache *cache, void *k, void *v, const int32
  * before it (n_b = 1: decoding).  A row that sees no key gets O = 0 and
  * LSE = -inf; what keys and values hold where a row does not see them,
  * infinities and NaN included, does not reach it.  A query with an infinity or a
- * NaN gives a row of NaN (LSE too) wherever it sees a key.
+ * NaN gives a row of NaN (LSE too) wherever it sees a key.  Over codes, where
+ * more than 16 query rows share a key head, values whose scale is 2^-64 or less
+ * may count as 0 beside scales that are 2^12 times larger and more.
  * q: [total, Hq, d] bf16, token stride in elements (multiple of 8, at least
  * Hq * d); Hq a multiple of cache->H, head h reads key head h / (Hq / H).
  * o: [total, Hq, d] bf16, lse: [total, Hq] fp32, contiguous.  mask: int64

@@ -622,8 +622,9 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k_scale=Non
                stream=None):
     """Reads a paged cache (as for cache_write) back: positions 0 .. of every
     sequence b into the rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of packed bf16
-    k, v [total, H, d], the layout forward() and decode() take.  `total` rows
-    are allocated by torch; rows behind the last sequence are not written."""
+    k, v [total, H, d], the layout forward() and decode() take (which have as many
+    key heads as query heads: repeat_interleave(G, 1) heads that G queries share).
+    `total` rows are allocated by torch; rows behind the last sequence are not written."""
     return _call("cache_read", stream, k_cache.device, k_cache, v_cache, page_table, k_scale, v_scale, cu_seqlens,
                  total)
 

@@ -7,13 +7,13 @@
 // many streams as there are warps.  d / 8 lanes
 // hold a row, eight channels each: 16 bytes of bf16, 8 bytes of codes.  Writing,
 // the row maximum is a shuffle reduction in bf16.  (With 16 codes a lane each 16-byte
-// store fills half a sector: 113 us for the 612 MB of reading back a batch of
-// eight, 99.7 with eight, and 96.5 since runs are shorter.)  Every byte moves once, so HBM bounds both (launch latency for a few
+// store fills half a sector: 113 us against 99.7 for the 612 MB of reading back a
+// batch of eight.)  Every byte moves once, so HBM bounds both (launch latency for a few
 // tokens: runs of one).
 //
 // A CTA first looks for a decrease in the offsets, all of them, with all its threads
-// (one token for 64 sequences 2.65 -> 3.1 us; with each warp looking for itself 3.0, but
-// 30 against 9.3 for 4096 sequences, and 105.9 against 97.9 for the batch of eight).
+// (one token for 64 sequences 2.65 -> 3.1 us, the batch of eight 97.4 -> 98.8; with each
+// warp looking for itself 3.0, but 30 against 9.3 for 4096 sequences, and 105.9).
 #pragma once
 
 #include <climits>

@@ -171,8 +171,8 @@ int check_cache(const attn_paged_cache* c) {
 }
 
 // Tokens a warp writes or reads one after the other, at most: with more the warps'
-// streams lie further apart (reading 98586 e4m3 tokens of 8 heads, d = 128: 109.6,
-// 97.3, 96.5, 99.2 and 99.7 us with 1, 3, 4, 8 and 16; bf16 118.8 with 4, 121.5 with 16).
+// streams lie further apart (reading 98586 e4m3 tokens of 8 heads, d = 128: 100.3, 98.8
+// and 99.9 us with 3, 4 and 8).
 constexpr int kMaxRun = 4;
 
 attn::cache::Pages pages_of(const attn_paged_cache* c) {
@@ -206,7 +206,7 @@ bool few(const Plan& pl) { return pl.rows <= 16; }
 // Few rows: as many persistent warps as fit the SMs; more: a persistent CTA an SM
 // with tcgen05 products.  9 to 16 rows take the former but for a bf16 cache with
 // d = 128, where HBM outruns its arithmetic (us, few : many; 12 rows, 16 sequences of
-// 4096 keys: d = 128 bf16 104 : 82, e4m3 69 : 84, d = 64 50 : 63 and 54 : 75; 16 rows,
+// 4096 keys: d = 128 bf16 104 : 82, e4m3 69 : 84, d = 64 52 : 63 and 54 : 75; 16 rows,
 // 64 sequences of 8192 keys: d = 128 bf16 284 : 254, e4m3 192 : 247).  num_splits caps
 // the pieces of a segment instead.
 Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, bool codes) {

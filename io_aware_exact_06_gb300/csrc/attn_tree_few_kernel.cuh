@@ -38,13 +38,14 @@ constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
 // CTAs per SM.  Two leave a lane 255 registers and DRAM fewer streams; d = 64 codes
 // are bound by their arithmetic and want three (64 ragged sequences of up to 8192
-// keys, one token, 32 + 8 heads, two : three CTAs: d = 128 e4m3 143 : 145 us, bf16
-// 241 : 247, d = 64 bf16 131 : 136, e4m3 142 : 103).
+// keys, one token, 32 + 8 heads, two : three CTAs: d = 128 e4m3 144 : 145 us, bf16
+// 247 : 246, d = 64 bf16 132 : 136, e4m3 142 : 104).
 __host__ __device__ constexpr int few_ctas(int d, bool codes) { return d == 64 && codes ? 3 : 2; }
-// For the registers: d = 128 bf16 does better held to three CTAs' (241 against 243 us,
-// one token for four short sequences 11.8 against 12.5), e4m3 does not (184 : 143).
+// For the registers: d = 128 bf16 does better held to three CTAs' where sequences are
+// short (one token for four of them 12.0 against 12.8 us, the long batch 243 against
+// 241), e4m3 does not (184 : 143).
 __host__ __device__ constexpr int few_bound(int d, bool codes) { return (d == 128) != codes ? 3 : 2; }
-constexpr int kFewRing = 16384;  // bytes of a warp's stages (24576: d = 64 bf16 137 us)
+constexpr int kFewRing = 16384;  // bytes of a warp's stages (24576: d = 64 bf16 135 us against 129)
 
 template <int D, bool kCodes, int kNT>
 struct FewCfg : Row<D, kCodes> {

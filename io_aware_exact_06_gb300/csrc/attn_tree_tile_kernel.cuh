@@ -67,7 +67,10 @@ constexpr int kRing = 8;  // segments whose flags are kept
 constexpr float kPLog2 = 7.f;  // P is stored as fp16(2^7 p), room for 2^kLazy above
 constexpr int kSpread = 12;       // log2
 constexpr int kFar = INT_MAX;     // in place of a tile's F: the scales lie further apart
-constexpr int kScaleFloor = -64;  // exponent of cache_write's smallest scale, a row of zeros: not counted
+// Exponent of cache_write's smallest scale, in most cases a row of zeros': not counted
+// among the scales that may lie far apart.  (Values below 2^-55, its others, count as
+// zeros beside scales that are.)
+constexpr int kScaleFloor = -64;
 
 template <int D, bool kCodes, bool kPair>
 struct BigCfg : Row<D, kCodes> {
