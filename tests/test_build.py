@@ -12,15 +12,14 @@ from io_aware_exact_06_gb300 import build
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def test_the_library_needs_no_torch(tmp_path):
-    """Without torch, and with no module of torch conveniences built, the library is; its calls work."""
+def test_the_library_needs_no_torch():
+    """Without torch the library is built all the same, and its calls work."""
     build.build()
     script = textwrap.dedent(f"""
         import sys
         sys.path.insert(0, {ROOT!r})
         sys.modules["torch"] = None  # import torch raises
         from io_aware_exact_06_gb300 import build
-        build.BINDING = {str(tmp_path / "none.so")!r}
         assert build.build() == build.LIB
         import io_aware_exact_06_gb300 as fa
         assert fa.attn_fwd_tree_workspace(2, 10, 8, 4, 128, 8, 4096, 8) > 0
