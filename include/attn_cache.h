@@ -1,7 +1,9 @@
 /*
  * C ABI of the paged key/value cache on GB300 (sm_103a): writing new tokens
- * into it, reading it back, and attention over it for the newest token or a
- * tree of drafted tokens of every sequence.
+ * into it, reading it back, attention over it for the newest token or a
+ * tree of drafted tokens of every sequence (sequences that share a prefix
+ * included), and its pages between steps: forked, copied, given back, accepted
+ * drafts moved together.
  *
  * The cache holds num_pages pages of page_size token rows.  Position p of
  * sequence b is row p % page_size of page page_table[b][p / page_size].  Keys
@@ -112,6 +114,99 @@ int attn_fwd_tree(const void *q, int64_t q_stride, const attn_paged_cache *cache
 
 size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_new, int max_len,
                                int num_splits);
+
+/*
+ * attn_fwd_prefix: attn_fwd_tree for groups of sequences that share a prefix
+ * (samples of one prompt), whose keys and values are read once for all rows of
+ * the group.  Sequences cu_groups[g] .. cu_groups[g+1]-1 are group g (cu_groups:
+ * int32[groups+1], prefix_lens: int32[groups], on the device); their tables name
+ * the same pages for the first prefix_lens[g] positions, as far as these fill
+ * pages, and those are read by the first sequence's table.  (What follows in a
+ * page that is not filled is each sequence's own.)  A prefix ends before the new
+ * tokens of its sequences.  A sequence in no group shares nothing; groups may be
+ * empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
+ * from its by rounding alone.
+ * max_group >= the new tokens of every group together, max_prefix >= every
+ * prefix_lens[g], at most max_len: they size the launch (close bounds pick the
+ * kernels that fit).
+ * workspace: attn_fwd_prefix_workspace(...) bytes, as for attn_fwd_tree.
+ * Errors in the error word: those of attn_fwd_tree, and ATTN_ERR_SEQLENS where
+ * cu_groups decreases (no row is written), where a group lies outside the batch or
+ * exceeds the bounds (no row of its sequences is), or a prefix reaches into a
+ * sequence's new tokens (no row of that sequence is).  A page of a prefix outside
+ * the cache makes the group's rows NaN.
+ */
+int attn_fwd_prefix(const void *q, int64_t q_stride, const attn_paged_cache *cache,
+                    const int32_t *seqlens, const int32_t *cu_seqlens, const int64_t *mask,
+                    const int32_t *cu_groups, const int32_t *prefix_lens, void *o, float *lse, int B,
+                    int total, int Hq, int max_new, int max_len, int groups, int max_group,
+                    int max_prefix, float scale, int num_splits, void *workspace,
+                    size_t workspace_bytes, attn_stream_t stream);
+
+size_t attn_fwd_prefix_workspace(int B, int total, int Hq, int H, int d, int max_new, int max_len,
+                                 int groups, int max_group, int max_prefix, int num_splits);
+
+/*
+ * attn_cache_fork: the page table of the next batch.  Its row i (of N) goes on
+ * with row parents[i] of the present one (of B; -1: with none) to new_seqlens[i]
+ * positions: a parent named once goes on, one named several times is forked, one
+ * not named is given up; a row may grow, shrink, or end (0).  A row of length n
+ * has ceil(n / page_size) pages; the rest of its table is -1.
+ * refs[page] counts the rows whose tables name the page, 0: it is free.  A row
+ * keeps its parent's pages as far as it needs them and gets free ones behind
+ * them: the lowest-numbered, in the order of the rows and of their positions.
+ * Where it grows into a page that its parent had filled in part, it writes there:
+ * it keeps that page if nobody else has it (no other row before the call; of the
+ * children that have it, all grow and it is the first), else it gets a free one,
+ * and copy_src[i] and copy_dst[i] name the pages to copy (attn_cache_copy, for
+ * each layer's cache); they are -1 elsewhere.  Pages given up may be handed out
+ * by the next call, not by this one.
+ * page_table [B, page_table_stride], page_table_out [N, page_table_stride] (not
+ * the same memory: ATTN_ERR_SHAPE), refs and refs_out [num_pages] (may be the
+ * same), seqlens [B], parents, new_seqlens, copy_src and copy_dst [N], all int32
+ * on the device.  page_size 16, 32, 64, 128 or 256.
+ * workspace: attn_cache_fork_workspace(...) bytes of the caller's device memory,
+ * not initialised, in use until the call's work on stream has finished.
+ * Errors in the error word: ATTN_ERR_SEQLENS (a length below 0 or beyond the
+ * table), ATTN_ERR_INDEX (a parent outside the batch; a page outside the cache or
+ * with a count below 1) and ATTN_ERR_PAGES (fewer free pages than asked for):
+ * nothing changes hands then, refs_out is refs and the rest -1.  A page that a table
+ * names more often than refs counts is reported (ATTN_ERR_INDEX) as its count falls
+ * below 0.
+ */
+int attn_cache_fork(const int32_t *page_table, int page_table_stride, const int32_t *seqlens, int B,
+                    const int32_t *parents, const int32_t *new_seqlens, int N, const int32_t *refs,
+                    int32_t *refs_out, int num_pages, int page_size, int32_t *page_table_out,
+                    int32_t *copy_src, int32_t *copy_dst, void *workspace, size_t workspace_bytes,
+                    attn_stream_t stream);
+
+size_t attn_cache_fork_workspace(int B, int N, int page_table_stride, int num_pages, int page_size);
+
+/*
+ * attn_cache_copy: page src[i] of the cache, all of it, into page dst[i], for the
+ * n pairs in which src[i] is not -1 (int32[n] on the device).  A page may be the
+ * source of many pairs; the target of one, and not a source as well.  The page table
+ * is not read (it may be NULL).  ATTN_ERR_INDEX in the error word: a page outside
+ * the cache; that pair is left out.
+ */
+int attn_cache_copy(const attn_paged_cache *cache, const int32_t *src, const int32_t *dst, int n,
+                    attn_stream_t stream);
+
+/*
+ * attn_cache_compact: the accepted ones of the new tokens of every sequence moved
+ * to the first of their places: new token path[cu_seqlens[b] + j] to place j, for j
+ * below accepted[b] (as attn_verify_drafts returns them; they increase with j).
+ * seqlens as for the attention that wrote them, all new tokens included; the
+ * sequence goes on with seqlens[b] - n_b + accepted[b] positions, and what is behind
+ * them is left as it was.  Two sequences whose new tokens share a page must not both
+ * move in it.
+ * Errors in the error word: ATTN_ERR_SEQLENS as for attn_cache_write; ATTN_ERR_INDEX
+ * (accepted[b] below 0 or above n_b, a path that does not increase or leaves the new
+ * tokens: nothing of that sequence is moved; a page outside the cache: that row is not).
+ */
+int attn_cache_compact(const attn_paged_cache *cache, const int32_t *seqlens, const int32_t *cu_seqlens,
+                       const int32_t *path, const int32_t *accepted, int B, int total,
+                       attn_stream_t stream);
 
 #ifdef __cplusplus
 }

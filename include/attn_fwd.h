@@ -44,7 +44,8 @@ typedef enum {
     ATTN_ERR_ARCH = -9,           /* current device is not sm_103 */
     ATTN_ERR_SCRATCH = -10,       /* attn_fwd_noalloc: problem larger than its fixed scratch;
                                      a caller's workspace missing or too small */
-    ATTN_ERR_INDEX = -11          /* a position or page outside its table (device) */
+    ATTN_ERR_INDEX = -11,         /* a position, page or token outside its table (device) */
+    ATTN_ERR_PAGES = -12          /* fewer free pages than a plan asks for (device) */
 } attn_status;
 
 /*

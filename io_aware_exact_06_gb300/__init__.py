@@ -1,8 +1,8 @@
 """GB300 (sm_103a) fused exact attention: forward and backward.
 
 A thin ctypes binding of the C ABI in ``include/attn_fwd.h``,
-``include/attn_bwd.h``, ``include/attn_fp8.h``, ``include/attn_norm.h`` and
-``include/attn_cache.h`` (the library ``_build/libattn_fwd.so``, built by
+``include/attn_bwd.h``, ``include/attn_fp8.h``, ``include/attn_norm.h``,
+``include/attn_cache.h`` and ``include/attn_verify.h`` (the library ``_build/libattn_fwd.so``, built by
 ``build.py``).  The functions here only
 marshal arguments: every step of the computation runs in the library's CUDA
 kernels.  There is no CPU path: calling the library without it built, or on a
@@ -21,8 +21,11 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_window", "attn_fwd_fp8", "attn_fwd_
            "attn_status_string", "AttnError", "AttnFwdOptions", "lib", "forward", "backward", "decode",
            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace",
            "attn_cache_write", "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace",
+           "attn_fwd_prefix", "attn_fwd_prefix_workspace", "attn_cache_fork", "attn_cache_fork_workspace",
+           "attn_cache_copy", "attn_cache_compact", "attn_verify_drafts",
            "AttnRotary", "AttnPagedCache", "qk_norm_rope", "qk_norm_rope_backward", "cache_write",
-           "cache_read", "tree_decode", "EXPORTED_SYMBOLS"]
+           "cache_read", "tree_decode", "prefix_decode", "cache_fork", "cache_copy", "cache_compact",
+           "verify_drafts", "EXPORTED_SYMBOLS"]
 
 # Every symbol the headers under include/ declare.
 EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_decode", "attn_last_device_error", "attn_last_error_site",
@@ -32,7 +35,10 @@ EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_decode
                     "attn_fwd_fp8", "attn_fwd_fp8_codes",
                     "attn_fp8_quantize_qk", "attn_fp8_quantize_v",
                     "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace",
-                    "attn_cache_write", "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace")
+                    "attn_cache_write", "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace",
+                    "attn_fwd_prefix", "attn_fwd_prefix_workspace", "attn_cache_fork",
+                    "attn_cache_fork_workspace", "attn_cache_copy", "attn_cache_compact",
+                    "attn_verify_drafts")
 
 ATTN_OK = 0
 
@@ -129,6 +135,20 @@ def lib() -> ctypes.CDLL:
         L.attn_fwd_tree.restype = i
         L.attn_fwd_tree_workspace.argtypes = [i] * 8
         L.attn_fwd_tree_workspace.restype = ctypes.c_size_t
+        L.attn_fwd_prefix.argtypes = [vp, i64] + [vp] * 8 + [i] * 8 + [f, i, vp, ctypes.c_size_t, vp]
+        L.attn_fwd_prefix.restype = i
+        L.attn_fwd_prefix_workspace.argtypes = [i] * 11
+        L.attn_fwd_prefix_workspace.restype = ctypes.c_size_t
+        L.attn_cache_fork.argtypes = [vp, i, vp, i, vp, vp, i, vp, vp, i, i, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        L.attn_cache_fork.restype = i
+        L.attn_cache_fork_workspace.argtypes = [i] * 5
+        L.attn_cache_fork_workspace.restype = ctypes.c_size_t
+        L.attn_cache_copy.argtypes = [vp, vp, vp, i, vp]
+        L.attn_cache_copy.restype = i
+        L.attn_cache_compact.argtypes = [vp] * 5 + [i, i, vp]
+        L.attn_cache_compact.restype = i
+        L.attn_verify_drafts.argtypes = [vp, vp, i64, vp, i64, i] + [vp] * 9 + [i, i, i, vp]
+        L.attn_verify_drafts.restype = i
         L.attn_last_device_error.argtypes = [vp]
         L.attn_last_device_error.restype = i
         L.attn_last_error_site.restype = i
@@ -428,6 +448,80 @@ def attn_fwd_tree(q, q_stride: int, cache: AttnPagedCache, seqlens, cu_seqlens, 
     return st
 
 
+def attn_fwd_prefix_workspace(B: int, total: int, Hq: int, H: int, d: int, max_new: int, max_len: int,
+                              groups: int, max_group: int, max_prefix: int, num_splits: int = 0) -> int:
+    """Bytes of workspace attn_fwd_prefix needs."""
+    return int(lib().attn_fwd_prefix_workspace(int(B), int(total), int(Hq), int(H), int(d), int(max_new),
+                                               int(max_len), int(groups), int(max_group), int(max_prefix),
+                                               int(num_splits)))
+
+
+def attn_fwd_prefix(q, q_stride: int, cache: AttnPagedCache, seqlens, cu_seqlens, mask, cu_groups,
+                    prefix_lens, o, lse, B: int, total: int, Hq: int, max_new: int, max_len: int,
+                    groups: int, max_group: int, max_prefix: int, scale: float, num_splits: int = 0,
+                    workspace=None, workspace_bytes: int = 0, stream=None) -> int:
+    """The C call ``attn_fwd_prefix``."""
+    st = lib().attn_fwd_prefix(_ptr(q), int(q_stride), _struct(cache), _ptr(seqlens), _ptr(cu_seqlens),
+                               _ptr(mask), _ptr(cu_groups), _ptr(prefix_lens), _ptr(o), _ptr(lse), int(B),
+                               int(total), int(Hq), int(max_new), int(max_len), int(groups),
+                               int(max_group), int(max_prefix), float(scale), int(num_splits),
+                               _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_prefix")
+    return st
+
+
+def attn_cache_fork_workspace(B: int, N: int, page_table_stride: int, num_pages: int, page_size: int) -> int:
+    """Bytes of workspace attn_cache_fork needs."""
+    return int(lib().attn_cache_fork_workspace(int(B), int(N), int(page_table_stride), int(num_pages),
+                                               int(page_size)))
+
+
+def attn_cache_fork(page_table, page_table_stride: int, seqlens, B: int, parents, new_seqlens, N: int,
+                    refs, refs_out, num_pages: int, page_size: int, page_table_out, copy_src, copy_dst,
+                    workspace=None, workspace_bytes: int = 0, stream=None) -> int:
+    """The C call ``attn_cache_fork``."""
+    st = lib().attn_cache_fork(_ptr(page_table), int(page_table_stride), _ptr(seqlens), int(B),
+                               _ptr(parents), _ptr(new_seqlens), int(N), _ptr(refs), _ptr(refs_out),
+                               int(num_pages), int(page_size), _ptr(page_table_out), _ptr(copy_src),
+                               _ptr(copy_dst), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_fork")
+    return st
+
+
+def attn_cache_copy(cache: AttnPagedCache, src, dst, n: int, stream=None) -> int:
+    """The C call ``attn_cache_copy``."""
+    st = lib().attn_cache_copy(_struct(cache), _ptr(src), _ptr(dst), int(n), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_copy")
+    return st
+
+
+def attn_cache_compact(cache: AttnPagedCache, seqlens, cu_seqlens, path, accepted, B: int, total: int,
+                       stream=None) -> int:
+    """The C call ``attn_cache_compact``."""
+    st = lib().attn_cache_compact(_struct(cache), _ptr(seqlens), _ptr(cu_seqlens), _ptr(path),
+                                  _ptr(accepted), int(B), int(total), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_compact")
+    return st
+
+
+def attn_verify_drafts(tokens, probs, probs_stride: int, draft_probs, draft_stride: int, bf16: bool,
+                       cu_seqlens, mask, u_accept, u_next, seqlens, path, accepted, next_token,
+                       seqlens_out, B: int, total: int, V: int, stream=None) -> int:
+    """The C call ``attn_verify_drafts`` (tensors or addresses; strides in elements)."""
+    st = lib().attn_verify_drafts(_ptr(tokens), _ptr(probs), int(probs_stride), _ptr(draft_probs),
+                                  int(draft_stride), int(bool(bf16)), _ptr(cu_seqlens), _ptr(mask),
+                                  _ptr(u_accept), _ptr(u_next), _ptr(seqlens), _ptr(path),
+                                  _ptr(accepted), _ptr(next_token), _ptr(seqlens_out), int(B), int(total),
+                                  int(V), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_verify_drafts")
+    return st
+
+
 def attn_last_device_error(stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device error status."""
     return lib().attn_last_device_error(_stream(stream))
@@ -554,7 +648,9 @@ def _native():
         loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace", "attn_cache_write",
-            "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace")])
+            "attn_cache_read", "attn_fwd_tree", "attn_fwd_tree_workspace", "attn_fwd_prefix",
+            "attn_fwd_prefix_workspace", "attn_cache_fork", "attn_cache_fork_workspace", "attn_cache_copy",
+            "attn_cache_compact", "attn_verify_drafts")])
         _serve = module
     return _serve
 
@@ -644,3 +740,74 @@ def tree_decode(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, max_new: i
     """
     return _call("tree_decode", stream, q.device, q, k_cache, v_cache, page_table, k_scale, v_scale, seqlens,
                  cu_seqlens, max_new, max_len, mask, scale, num_splits, out, lse)
+
+
+def prefix_decode(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, max_new: int, max_len: int,
+                  cu_groups, prefix_lens, max_group: int, max_prefix: int, mask=None,
+                  scale: float | None = None, k_scale=None, v_scale=None, num_splits: int = 0,
+                  out=None, lse=None, stream=None):
+    """tree_decode for groups of sequences that share a prefix (samples of one prompt):
+    its keys and values are read once for all of a group's rows.
+
+    cu_groups int32 [groups + 1]: sequences cu_groups[g] .. cu_groups[g+1]-1 are group g;
+    prefix_lens int32 [groups]: their page tables name the same pages for that many first
+    positions, as far as these fill pages.  Sequences in no group share nothing.  max_group
+    bounds the new tokens of a group, max_prefix (at most max_len) the prefixes.  The rest,
+    and what is returned, as for tree_decode.
+    """
+    return _call("prefix_decode", stream, q.device, q, k_cache, v_cache, page_table, k_scale, v_scale, seqlens,
+                 cu_seqlens, max_new, max_len, mask, scale, num_splits, out, lse, cu_groups, prefix_lens, max_group,
+                 max_prefix)
+
+
+def cache_fork(page_table, seqlens, parents, new_seqlens, refs, page_size: int, out=None, refs_out=None,
+               stream=None):
+    """The page table of the next batch: row i goes on with row parents[i] of this one
+    (-1: with none) to new_seqlens[i] positions.  A parent named several times is forked,
+    one not named is given up.
+
+    page_table int32 [B, width], seqlens int32 [B], parents, new_seqlens int32 [N], refs
+    int32 [pages]: how many rows name a page (0: it is free).  Returns (out [N, width],
+    refs_out [pages], copy_src [N], copy_dst [N]), allocated by torch when not given;
+    refs_out may be refs, out must not be page_table.  Rows that write into a page which
+    others have get one of their own: copy_src and copy_dst (-1: none) are for cache_copy,
+    once for each layer.  A plan that is not possible is reported on the device
+    (attn_last_device_error: too few free pages, a bad parent, page or length) and changes
+    nothing: refs_out is refs then, the rest -1.
+    """
+    return _call("cache_fork", stream, page_table.device, page_table, seqlens, parents, new_seqlens, refs, page_size,
+                 out, refs_out)
+
+
+def cache_copy(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, stream=None) -> None:
+    """Copies pages src[i] of a paged cache (as for cache_write) to dst[i], int32 [n]; pairs
+    with src -1 are left out.  A page is the target of one pair at most, and then no source."""
+    _call("cache_copy", stream, k_cache.device, k_cache, v_cache, k_scale, v_scale, src, dst)
+
+
+def cache_compact(k_cache, v_cache, page_table, seqlens, cu_seqlens, path, accepted, k_scale=None,
+                  v_scale=None, stream=None) -> None:
+    """Moves the accepted new tokens of every sequence to the first of the new tokens' places
+    in a paged cache (as for cache_write; seqlens with all new tokens): path int32 [total] and
+    accepted int32 [B] as verify_drafts returns them."""
+    _call("cache_compact", stream, k_cache.device, k_cache, v_cache, page_table, k_scale, v_scale, seqlens, cu_seqlens,
+          path, accepted)
+
+
+def verify_drafts(tokens, probs, cu_seqlens, u_accept, u_next, draft_probs=None, mask=None, seqlens=None,
+                  stream=None):
+    """Which drafted tokens the target keeps, and the token behind them, drawn from given
+    random numbers so that they are distributed as the target's own.
+
+    tokens int32 [total]: the new tokens that tree_decode attended to, the first of every
+    sequence accepted already, the others a chain (mask None) or a tree (mask int64 [total]
+    as for tree_decode; a draft's parent is the highest new token before it that it sees).
+    probs [total, V] fp32 or bf16: the target's distribution behind each of them; draft_probs
+    (same type): what its children were drawn from (None: drafts count as certain).
+    u_accept fp32 [total], u_next fp32 [B] in [0, 1).  Returns (path int32 [total]: the
+    accepted tokens' indices in their sequence, then -1; accepted int32 [B]: how many, the
+    first included; next_token int32 [B]; the lengths int32 [B] that remain of seqlens, the
+    new tokens included, or None without it).  Tokens behind the last sequence are padding.
+    """
+    return _call("verify_drafts", stream, tokens.device, tokens, probs, draft_probs, cu_seqlens, mask, u_accept, u_next,
+                 seqlens)

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libattn_fwd.so")
 SOURCES = [os.path.join(CSRC, "attn_fwd.cu"), os.path.join(CSRC, "attn_bwd.cu"),
-           os.path.join(CSRC, "attn_serve.cu")]
+           os.path.join(CSRC, "attn_serve.cu"), os.path.join(CSRC, "attn_prefix.cu"),
+           os.path.join(CSRC, "attn_pages.cu")]
 # the torch conveniences of the norm and cache calls, as a CPython module
 BINDING_SOURCE = os.path.join(CSRC, "serve_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

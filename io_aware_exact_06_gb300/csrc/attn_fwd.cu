@@ -678,6 +678,7 @@ extern "C" int attn_last_device_error(attn_stream_t stream) {
   if (h[0] & attn::kErrSeqlens) return ATTN_ERR_SEQLENS;
   if (h[0] & attn::kErrWorklist) return ATTN_ERR_SHAPE;
   if (h[0] & attn::rows::kBadIndex) return ATTN_ERR_INDEX;
+  if (h[0] & attn::rows::kNoPages) return ATTN_ERR_PAGES;
   return ATTN_OK;
 }
 
@@ -698,7 +699,8 @@ extern "C" const char* attn_status_string(int status) {
     case ATTN_ERR_SEQLENS: return "invalid cu_seqlens";
     case ATTN_ERR_ARCH: return "device is not sm_103";
     case ATTN_ERR_SCRATCH: return "problem larger than the scratch it was given (attn_fwd_noalloc's fixed one, or a workspace)";
-    case ATTN_ERR_INDEX: return "a position or page outside its table";
+    case ATTN_ERR_INDEX: return "a position, page or token outside its table";
+    case ATTN_ERR_PAGES: return "fewer free pages than asked for";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,165 @@
+// Host side of attn_fwd_prefix (include/attn_cache.h): attention over the paged cache
+// for sequences whose first pages are shared.  Two lines of work, one after the other:
+// every group's rows over its shared pages, then every sequence's over its own; a last
+// kernel joins them.  It keeps no workspace in the library.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/attn_cache.h"
+#include "attn_prefix_join.cuh"
+#include "attn_serve_host.h"
+#include "attn_tree_plan.h"
+
+namespace {
+
+using namespace attn_serve;
+
+struct Sizes {
+  int B, total, Hq, H, d, max_new, max_len, groups, max_group, max_prefix, splits;
+};
+
+int check_sizes(const Sizes& z) {
+  const int st = check_tree(z.B, z.total, z.Hq, z.H, z.d, z.max_new, z.max_len, z.splits);
+  if (st != ATTN_OK) return st;
+  if (z.groups < 0 || z.max_group < 0 || z.max_prefix < 0 || z.max_prefix > z.max_len) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+bool empty(const Sizes& z) { return z.B == 0 || z.total == 0 || z.max_new == 0; }
+
+// The line of groups, the line of sequences, and the parts of the workspace: slots of
+// both, and the rows of both that are not cut.
+struct Plans {
+  Plan group, seq;
+  bool any;  // some group may share a page
+  int64_t rows;
+  size_t floats() const { return 2 * (size_t)rows + (any ? tree_rows(group) : 0) + tree_rows(seq); }
+};
+Plans plans(const Sizes& z, int page, bool codes) {
+  Plans x{};
+  x.rows = (int64_t)z.total * z.Hq;
+  const int most = std::min(z.max_group, z.total);
+  x.any = z.groups > 0 && most > 0 && z.max_prefix >= page;
+  if (x.any) x.group = tree_plan(z.groups, z.total, z.Hq, z.H, z.d, most, z.max_prefix, z.splits, codes);
+  x.seq = tree_plan(z.B, z.total, z.Hq, z.H, z.d, z.max_new, z.max_len, z.splits, codes);
+  return x;
+}
+
+template <int D, bool kCodes>
+int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree::Params& pg, const attn::tree::Params& p,
+                  cudaStream_t s) {
+  int st = ATTN_OK;
+  if (x.any && (st = launch_line<D, kCodes, true>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
+  if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
+  const int64_t rows = x.rows;
+  if (x.seq.many || x.group.many)
+    return launch(attn::tree::prefix_join_kernel<D, 8>, rows, 256, 0, s, pg, x.group.work, p, x.seq.work, 1);
+  const int run = (int)std::clamp<int64_t>(rows / (32 * kPlanSms), 1, 8);  // 32 warps an SM at least
+  return launch(attn::tree::prefix_join_kernel<D, 1>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg, x.group.work, p,
+                x.seq.work, run);
+}
+
+}  // namespace
+
+extern "C" size_t attn_fwd_prefix_workspace(int B, int total, int Hq, int H, int d, int max_new, int max_len,
+                                            int groups, int max_group, int max_prefix, int num_splits) {
+  const Sizes z{B, total, Hq, H, d, max_new, max_len, groups, max_group, max_prefix, num_splits};
+  if (check_sizes(z) != ATTN_OK || empty(z)) return 0;
+  size_t most = 0;  // the cache's type and its pages' size are not known here
+  for (bool codes : {false, true}) most = std::max(most, plans(z, 16, codes).floats());
+  return most * (d + 1) * sizeof(float);
+}
+
+extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged_cache* cache, const int32_t* seqlens,
+                               const int32_t* cu_seqlens, const int64_t* mask, const int32_t* cu_groups,
+                               const int32_t* prefix_lens, void* o, float* lse, int B, int total, int Hq, int max_new,
+                               int max_len, int groups, int max_group, int max_prefix, float scale, int num_splits,
+                               void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  if (!cache) return ATTN_ERR_NULL;
+  const int d = cache->d;
+  const Sizes z{B, total, Hq, cache->H, d, max_new, max_len, groups, max_group, max_prefix, num_splits};
+  int st = check_sizes(z);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f) return ATTN_ERR_SCALE;
+  if (empty(z)) return ATTN_OK;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if ((st = check_rows(q, q_stride, Hq, d)) != ATTN_OK) return st;
+  if (!o || !lse || !seqlens || !cu_seqlens || (groups && (!cu_groups || !prefix_lens))) return ATTN_ERR_NULL;
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) || !aligned(mask, 8) ||
+      !aligned(cu_groups, 4) || !aligned(prefix_lens, 4) || !aligned(workspace, 16))
+    return ATTN_ERR_ALIGN;
+  const bool codes = cache->k_scale != nullptr;
+  const Plans x = plans(z, cache->page_size, codes);
+  if (!x.seq.fits || (x.any && !x.group.fits)) return ATTN_ERR_SHAPE;
+  if (x.rows > INT32_MAX) return ATTN_ERR_SHAPE;
+  if (!workspace || workspace_bytes < x.floats() * (d + 1) * sizeof(float)) return ATTN_ERR_SCRATCH;
+
+  const attn::cache::Pages pg = pages_of(cache);
+  attn::tree::Params p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_ts = q_stride;
+  p.lens = seqlens;
+  p.cu = cu_seqlens;
+  p.table = cache->page_table;
+  p.mask = mask;
+  p.v = cache->v;
+  p.kscale = cache->k_scale;
+  p.vscale = cache->v_scale;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.B = B;
+  p.total = total;
+  p.Hq = Hq;
+  p.H = cache->H;
+  p.G = Hq / cache->H;
+  p.stride = cache->page_table_stride;
+  p.pages = cache->num_pages;
+  p.log_page = pg.log_page;
+  p.max_new = max_new;
+  p.max_len = max_len;
+  // scale 0 weighs every key alike; the smallest normal factor does, without 0 * inf
+  p.c = (float)std::max((double)scale * 1.4426950408889634, (double)FLT_MIN);
+  p.groups = cu_groups;
+  p.prefix = prefix_lens;
+  p.n_groups = groups;
+  p.max_group = max_group;
+  p.max_prefix = max_prefix;
+  attn::tree::Params of_groups = p;
+  of_groups.prefixes = true;
+  // rows of D floats first, then their LSE
+  float* at = static_cast<float*>(workspace);
+  float* lse_at = at + x.floats() * d;
+  auto take = [&](size_t rows, float*& o_part, float*& lse_part) {
+    o_part = at, lse_part = lse_at;
+    at += rows * d, lse_at += rows;
+  };
+  take(x.rows, of_groups.o_row, of_groups.lse_row);
+  take(x.rows, p.o_row, p.lse_row);
+  if (x.any) take(tree_rows(x.group), of_groups.o_part, of_groups.lse_part);
+  take(tree_rows(x.seq), p.o_part, p.lse_part);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
+  int dev = 0, sms = 0;
+  if ((st = attn_host::lib_device(&dev, &sms, &p.err)) != ATTN_OK) return st;
+  of_groups.err = p.err;
+  const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
+  CUtensorMap maps[4];
+  for (int i = 0; i < 4; ++i) {
+    if (i < 2 && !x.any) continue;
+    const int box = std::min(cache->page_size,
+                             few(i < 2 ? x.group : x.seq) ? attn::tree::kFewTile : attn::tree::kBigTile);
+    if ((st = attn_host::lib_make_cache_map(&maps[i], i % 2 ? cache->v : cache->k, rows, cache->H, d, codes, box)) != ATTN_OK)
+      return st;
+  }
+  return d == 64 ? codes ? launch_prefix<64, true>(x, maps, of_groups, p, s)
+                         : launch_prefix<64, false>(x, maps, of_groups, p, s)
+         : codes ? launch_prefix<128, true>(x, maps, of_groups, p, s)
+                 : launch_prefix<128, false>(x, maps, of_groups, p, s);
+}

@@ -12,6 +12,7 @@ namespace rows {
 
 constexpr int kBadSeqlens = 2;  // bits of the library's error word
 constexpr int kBadIndex = 8;
+constexpr int kNoPages = 16;
 
 __device__ __forceinline__ void unpack(const uint4& w, float (&f)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};

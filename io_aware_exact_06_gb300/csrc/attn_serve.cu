@@ -11,70 +11,18 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <set>
-#include <utility>
 
 #include "../../include/attn_cache.h"
 #include "../../include/attn_norm.h"
-#include "attn_cache_kernel.cuh"
-#include "attn_host.h"
 #include "attn_norm_kernel.cuh"
-#include "attn_tree_few_kernel.cuh"
-#include "attn_tree_tile_kernel.cuh"
+#include "attn_serve_host.h"
+#include "attn_tree_plan.h"
 
 namespace {
 
-constexpr int kPlanSms = 152;  // GB300: the split rules need no device
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int error_word(int** err) {
-  std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
-  int dev = 0, sms = 0;
-  return attn_host::lib_device(&dev, &sms, err);
-}
-
-// Launch that may overlap the end of the stream's previous kernel (every
-// kernel here waits for it before its first global access).
-template <typename... KArgs, typename... Args>
-int launch(void (*kernel)(KArgs...), int64_t grid, int threads, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e == cudaSuccess ? ATTN_OK : attn_host::lib_cuda_fail(e);
-}
-
-// Raises the dynamic shared-memory limit of a kernel, once per device.  Call
-// with the library lock held.
-int allow_smem(const void* kernel, int bytes) {
-  static std::set<std::pair<int, const void*>> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  if (done.count({dev, kernel})) return ATTN_OK;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  done.insert({dev, kernel});
-  return ATTN_OK;
-}
+using namespace attn_serve;
 
 // ------------------------------------------------------------ norm, rotation --
-int check_rows(const void* x, int64_t stride, int H, int d) {
-  if (H == 0) return ATTN_OK;
-  if (!x) return ATTN_ERR_NULL;
-  if (stride < (int64_t)H * d) return ATTN_ERR_SHAPE;
-  if (!aligned(x, 16) || stride % 8) return ATTN_ERR_ALIGN;
-  return ATTN_OK;
-}
-
 int check_rotary(const attn_rotary* r, int T, int d, attn::norm::Rotary* out) {
   if (!r) return ATTN_ERR_NULL;
   if (r->rot < 0 || r->rot > d || r->rot % 16) return ATTN_ERR_SHAPE;
@@ -112,19 +60,6 @@ int check_norm(int T, int Hq, int Hk, int d, float eps) {
   return ATTN_OK;
 }
 
-// Chunks of H heads of d channels when a warp holds `steps` row groups.
-int64_t chunks_of(int H, int d, int steps) {
-  const int64_t c = (int64_t)(32 / (d / 8)) * steps;
-  return (H + c - 1) / c;
-}
-
-// How many of `most` pieces (chunks of a token, tokens) a warp takes one after
-// the other: as many as leave the GPU's resident warps about four rounds, so
-// that loads run ahead without an uneven end.
-int run_of(int64_t pieces, int64_t most, int warps_per_sm) {
-  return (int)std::clamp<int64_t>(pieces / (4 * (int64_t)kPlanSms * warps_per_sm), 1, most);
-}
-
 // CTAs of the gradient for queries and for keys: two an SM in all, what the
 // kernel's registers allow, in proportion to the heads; fewer when there is
 // less to do.  A run is four chunks at most, so that the warps' streams lie closer
@@ -150,119 +85,13 @@ BwdPlan bwd_plan(int T, int Hq, int Hk, int d) {
   return pl;
 }
 
-// --------------------------------------------------------------------- cache --
-int check_cache(const attn_paged_cache* c) {
-  if (!c) return ATTN_ERR_NULL;
-  if (c->d != 64 && c->d != 128) return ATTN_ERR_HEADDIM;
-  if (c->H < 1 || (int64_t)c->H * c->d > (1 << 20) || c->num_pages < 1 || c->page_table_stride < 1)
-    return ATTN_ERR_SHAPE;
-  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 &&
-      c->page_size != 256)
-    return ATTN_ERR_SHAPE;
-  // rows, and positions of a sequence, are 32-bit numbers
-  if ((int64_t)c->num_pages * c->page_size > INT32_MAX ||
-      (int64_t)c->page_table_stride * c->page_size > INT32_MAX)
-    return ATTN_ERR_SHAPE;
-  if (!c->k || !c->v || !c->page_table || !c->k_scale != !c->v_scale) return ATTN_ERR_NULL;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
-      !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
-    return ATTN_ERR_ALIGN;
-  return ATTN_OK;
-}
-
-// Tokens a warp writes or reads one after the other, at most: with more the warps'
-// streams lie further apart (reading 98586 e4m3 tokens of 8 heads, d = 128: 100.3, 98.8
-// and 99.9 us with 3, 4 and 8).
-constexpr int kMaxRun = 4;
-
-attn::cache::Pages pages_of(const attn_paged_cache* c) {
-  attn::cache::Pages p{};
-  p.k = c->k;
-  p.v = c->v;
-  p.ks = c->k_scale;
-  p.vs = c->v_scale;
-  p.table = c->page_table;
-  p.stride = c->page_table_stride;
-  p.pages = c->num_pages;
-  p.log_page = 4;
-  while ((1 << p.log_page) < c->page_size) ++p.log_page;
-  p.H = c->H;
-  return p;
-}
-
 // ---------------------------------------------------------------------- tree --
-struct Plan {
-  int rows;  // query rows of a segment: 8 or 16 (few rows), 128 or 256
-  attn::tree::Work work;
-  int64_t ctas;
-  int64_t slots;  // parts in the workspace, `rows` rows each
-  bool many;      // eight warps join a row's pieces
-  bool fits;      // the line's tiles are a 32-bit number
-};
-
-bool few(const Plan& pl) { return pl.rows <= 16; }
-
-// Query rows of a segment: the smallest tile that holds max_new * G of them.
-// Few rows: as many persistent warps as fit the SMs; more: a persistent CTA an SM
-// with tcgen05 products.  9 to 16 rows take the former but for a bf16 cache with
-// d = 128, where HBM outruns its arithmetic (us, few : many; 12 rows, 16 sequences of
-// 4096 keys: d = 128 bf16 104 : 82, e4m3 69 : 84, d = 64 52 : 63 and 54 : 75; 16 rows,
-// 64 sequences of 8192 keys: d = 128 bf16 284 : 254, e4m3 192 : 247).  num_splits caps
-// the pieces of a segment instead.
-Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, bool codes) {
-  Plan pl{};
-  const int64_t M = (int64_t)max_new * (Hq / H);
-  constexpr int kBig = attn::tree::kBigRows;
-  pl.rows = M <= 8 ? 8 : M <= 16 && (d == 64 || codes) ? 16 : M <= kBig ? kBig : 2 * kBig;
-  const int64_t T = few(pl) ? attn::tree::kFewTile : attn::tree::kBigTile;
-  const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
-  const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
-  const int64_t segments = (int64_t)B * (H / heads) * ((M + pl.rows - 1) / pl.rows);
-  const int per_cta = few(pl) ? attn::tree::kWarps / heads : 1;
-  pl.work.rows = pl.rows;
-  pl.work.heads = heads;
-  pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
-  pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
-  const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
-  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? attn::tree::few_ctas(d, codes) : 1));
-  pl.work.units = (int)(pl.ctas * per_cta);
-  pl.slots = 2 * (int64_t)pl.work.units * heads;
-  // eight warps to a row where segments are cut into many pieces, and where the
-  // rows leave the SMs idle anyway
-  pl.many = pl.work.units > 32 * segments || (int64_t)total * Hq <= 8 * kPlanSms;
-  pl.fits = (double)segments * (double)tiles <= INT32_MAX;
-  return pl;
-}
-
-size_t tree_rows(const Plan& pl) { return (size_t)pl.slots * pl.rows; }
-size_t tree_bytes(const Plan& pl, int d) { return tree_rows(pl) * (d + 1) * sizeof(float); }
-
-int check_tree(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits) {
-  if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
-  if (B < 0 || total < 0 || Hq < 1 || H < 1 || Hq % H || (int64_t)Hq * d > (1 << 20)) return ATTN_ERR_SHAPE;
-  if (max_new < 0 || max_new > attn::tree::kMaxNew || max_len < max_new || num_splits < 0 || num_splits > 256)
-    return ATTN_ERR_SHAPE;
-  if (max_len > INT32_MAX - 256) return ATTN_ERR_SHAPE;
-  return ATTN_OK;
-}
-
 template <int D, bool kCodes>
 int launch_tree(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                 cudaStream_t s) {
   using namespace attn::tree;
-  constexpr int kTwo = D == 64 || kCodes ? 2 : 1;  // no plan has 16 rows of the other kind
-  auto kernel = pl.rows == 8          ? tree_few_kernel<D, kCodes, 1>
-                : pl.rows == 16       ? tree_few_kernel<D, kCodes, kTwo>
-                : pl.rows == kBigRows ? tree_tile_kernel<D, kCodes, false>
-                                      : tree_tile_kernel<D, kCodes, true>;
-  const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1>::kSmem
-                   : pl.rows == 16       ? FewCfg<D, kCodes, kTwo>::kSmem
-                   : pl.rows == kBigRows ? big_smem<D, kCodes, false>()
-                                         : big_smem<D, kCodes, true>();
-  int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  const int st = launch_line<D, kCodes, false>(pl, mk, mv, p, s);
   if (st != ATTN_OK) return st;
-  if ((st = launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work)) != ATTN_OK)
-    return st;
   const int64_t rows = (int64_t)p.total * p.Hq;
   if (pl.many) return launch(tree_join_kernel<D, 8>, rows, 256, 0, s, p, pl.work, 1);
   const int run = (int)std::clamp<int64_t>(rows / (32 * kPlanSms), 1, 8);  // 32 warps an SM at least

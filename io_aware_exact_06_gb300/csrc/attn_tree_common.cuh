@@ -17,6 +17,12 @@
 // them as the sum of two (2^-16 of each is lost), many rows round once (2^-8) and divide
 // O by the sum with the largest of each tile rounded; LSE is of the sum before.
 // Sums, maxima and scores are fp32.
+//
+// Sequences whose first pages are the same (samples of one prompt) may have those
+// attended to once for all of them: kShared, in two lines of work.  In the first an
+// item is a group, its rows are all its sequences' and its keys the shared pages, every
+// one of them context; in the second an item is a sequence over its other pages.  The
+// rows' two parts meet in the join.
 #pragma once
 
 #include "attn_rows.cuh"
@@ -45,6 +51,12 @@ struct Params {
   int max_new, max_len;
   float c;  // scale * log2 e (at least the smallest normal float)
   int* err;
+  // shared prefixes: offsets of the groups' sequences, their common lengths
+  const int *groups, *prefix;
+  int n_groups, max_group, max_prefix;
+  bool prefixes;    // the line of groups, else that of sequences
+  float* o_row;     // [total * Hq][D], [total * Hq]: this line's rows whose keys lie in one
+  float* lse_row;   // piece (with slots: what is left for the join)
 };
 
 // Bytes of a key's (or value's) row of one head, and how TMA boxes cut it.
@@ -142,18 +154,74 @@ __device__ __forceinline__ uint4 no_infinity(uint4 x) {
   return make_uint4(no_infinity(x.x), no_infinity(x.y), no_infinity(x.z), no_infinity(x.w));
 }
 
-// The rows and keys of a sequence; false if they are not what the caller's
-// bounds allow.
+// The rows and keys of an item of a line: rows q0 .. q0 + n - 1, keys 0 .. len - 1.
+template <bool kShared>
 struct Seq {
   int q0, n, len;
+  __device__ __forceinline__ int drafts() const { return n; }  // the last keys: under the mask
+  __device__ __forceinline__ bool whole() const { return true; }  // its keys are all that its rows see
+  __device__ __forceinline__ int64_t table(const Params& p, int b) const { return (int64_t)b * p.stride; }
 };
-__device__ __forceinline__ bool load_seq(const Params& p, int b, Seq& s) {
+template <>
+struct Seq<true> {
+  int q0, n, len;
+  int masked;    // drafts
+  int at;        // the table's row
+  int page0;     // its first page (-1: a group's, from 0 on)
+  __device__ __forceinline__ int drafts() const { return masked; }
+  __device__ __forceinline__ bool whole() const { return page0 == 0; }
+  __device__ __forceinline__ int64_t table(const Params& p, int) const {
+    return (int64_t)at * p.stride + max(page0, 0);
+  }
+};
+// False if they are not what the caller's bounds allow.
+__device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<false>& s) {
   s.q0 = p.cu[b];
   const int end = p.cu[b + 1];
   s.len = p.lens[b];
   s.n = end - s.q0;
   return s.q0 >= 0 && end >= s.q0 && end <= p.total && s.n <= p.max_new && s.len >= s.n &&
          s.len <= p.max_len && s.len <= (int64_t)p.stride << p.log_page;
+}
+
+// The group of sequence b, or -1: the last whose offset is not above b.
+__device__ __forceinline__ int find_group(const Params& p, int b) {
+  int lo = 0, hi = p.n_groups;  // groups[0 .. lo-1] <= b < groups[hi ..]
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (p.groups[mid] <= b) lo = mid + 1; else hi = mid;
+  }
+  return lo > 0 && b < p.groups[lo] ? lo - 1 : -1;
+}
+// Shared pages of group g; false if its offsets or its prefix are not what the caller's
+// bounds allow (its sequences are refused then).
+__device__ __forceinline__ bool load_group(const Params& p, int g, int& pages) {
+  const int s0 = p.groups[g], s1 = p.groups[g + 1], prefix = p.prefix[g];
+  pages = prefix >> p.log_page;
+  if (s0 < 0 || s1 < s0 || s1 > p.B || prefix < 0 || prefix > p.max_prefix || pages > p.stride) return false;
+  return (int64_t)p.cu[s1] - p.cu[s0] <= p.max_group;
+}
+__device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<true>& s) {
+  int pages = 0;
+  if (p.prefixes) {  // group b
+    if (!load_group(p, b, pages)) return false;
+    s.at = p.groups[b];
+    // (rows of a sequence that is refused are computed and not used)
+    s.q0 = max(p.cu[s.at], 0);
+    s.n = max(min(p.cu[p.groups[b + 1]], p.total) - s.q0, 0);
+    s.len = pages << p.log_page;
+    s.masked = 0;
+    s.page0 = -1;
+    return true;
+  }
+  Seq<false> own{};
+  bool fits = load_seq(p, b, own);
+  const int g = find_group(p, b);
+  if (g >= 0) fits &= load_group(p, g, pages);
+  fits &= (int64_t)pages << p.log_page <= own.len - own.n;
+  s.q0 = own.q0, s.n = s.masked = own.n, s.at = b, s.page0 = pages;
+  s.len = fits ? own.len - (pages << p.log_page) : own.len;
+  return fits;
 }
 
 // Whether new token i (mask word `word`) sees new token t.

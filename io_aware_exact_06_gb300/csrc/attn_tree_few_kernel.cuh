@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return r;
 }
 
-template <int D, bool kCodes, int kNT>
+template <int D, bool kCodes, int kNT, bool kShared>
 __global__ void __launch_bounds__(kFewThreads, few_bound(D, kCodes))
 tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ Params p, const __grid_constant__ Work w) {
@@ -99,7 +99,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   grid_dep_launch();
   const int units = kWarps / w.heads;  // of the CTA
   const int unit = blockIdx.x * units + warp / w.heads, sub = warp % w.heads;
-  Walk wk;
+  Walk<kShared> wk;
   if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) return;
   bool expired = false;  // a wait ran out: nothing more is copied, the rows come out as NaN
 
@@ -108,13 +108,13 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   const int box = min(page, kFewTile);  // rows of one copy
   const int per = kFewTile / box;       // copies per tile (of each matrix)
   const int batch = 32 / per;           // tiles whose page numbers one load fetches
-  Walk fw = wk;                         // runs ahead of wk
+  Walk<kShared> fw = wk;                         // runs ahead of wk
   int f_tile, f_end, f_at = 0, f_head, f_ids, f_next, f_stage = 0;
   bool f_more = true;
   uint32_t bad = 0;  // bit s: the tile in stage s reads a page outside the cache
   auto fetch = [&](int tile) {  // this lane's copy of the `batch` tiles from `tile` on
     const int64_t pos = (int64_t)tile * kFewTile + lane * box;
-    return pos < fw.s.len ? p.table[(int64_t)fw.b * p.stride + (pos >> p.log_page)] : 0;
+    return pos < fw.s.len ? p.table[fw.s.table(p, fw.b) + (pos >> p.log_page)] : 0;
   };
   auto enter = [&]() {
     f_tile = fw.tile;
@@ -181,8 +181,8 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   int stage = 0, parity = 0;
   bool first = true;
   do {
-    const Seq sq = wk.s;
-    const int M = sq.n * p.G, ctx = sq.len - sq.n;
+    const Seq<kShared> sq = wk.s;
+    const int M = sq.n * p.G, ctx = sq.len - sq.drafts();
     const int mtiles = wk.segs / (p.H / w.heads), group = wk.seg / mtiles;
     const int h = group * w.heads + sub, row0 = (wk.seg - group * mtiles) * kRows;
     const int t_begin = wk.tile, t_end = wk.tile + wk.piece();
@@ -319,7 +319,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
               if (kCodes) x *= ksc;
               if (edge) {
                 const int d = key0 + key - ctx;
-                if (d >= sq.n || (d >= 0 && !sees(word[nt][i], d))) x = -INFINITY;
+                if (d >= sq.drafts() || (d >= 0 && !sees(word[nt][i], d))) x = -INFINITY;
               }
               sc[ksub][nt][2 * kh + i] = x;
               // a masked score stays -inf whatever the scale of its key holds

@@ -193,7 +193,7 @@ __device__ __forceinline__ uint32_t half_fma2(uint32_t a, uint32_t b, uint32_t c
 // 2^e for e in -126 .. 127, 0 below.
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(e, 127)) << 23); }
 
-template <int D, bool kCodes, bool kPair>
+template <int D, bool kCodes, bool kPair, bool kShared>
 struct Big {
   using C = BigCfg<D, kCodes, kPair>;
   const Params& p;
@@ -219,14 +219,14 @@ struct Big {
     }
   }
   __device__ __forceinline__ bool aborted() const { return *(volatile int*)&ss.abort != 0; }
-  __device__ __forceinline__ int head(const Walk& k) const { return k.seg / (k.segs / p.H); }
-  __device__ __forceinline__ int row0(const Walk& k) const { return k.seg % (k.segs / p.H) * C::kRows; }
+  __device__ __forceinline__ int head(const Walk<kShared>& k) const { return k.seg / (k.segs / p.H); }
+  __device__ __forceinline__ int row0(const Walk<kShared>& k) const { return k.seg % (k.segs / p.H) * C::kRows; }
 
   // ------------------------------------------------------------- producers --
   // One warp copies the keys (and the scales), another the values, each as far
   // ahead as its stages reach.
   template <bool kKeys>
-  __device__ __forceinline__ void produce(Walk k, const CUtensorMap* map) {
+  __device__ __forceinline__ void produce(Walk<kShared> k, const CUtensorMap* map) {
     constexpr int kN = kKeys ? C::kK : C::kV, kFull = kKeys ? C::bKF : C::bVF, kEmpty = kKeys ? C::bKE : C::bVE;
     constexpr int kElems = kCodes ? C::kBox : C::kBox / 2;
     const int lane = threadIdx.x % 32;
@@ -236,7 +236,7 @@ struct Big {
     int s = 0, round = 0, seg = 0;
     do {
       const int h = head(k), len = k.s.len, end = k.tile + k.piece();
-      const int* table = p.table + (int64_t)k.b * p.stride;
+      const int* table = p.table + k.s.table(p, k.b);
       auto fetch = [&](int tile) {
         const int64_t pos = (int64_t)tile * kBigTile + lane * box;
         return pos < len ? table[pos >> p.log_page] : 0;
@@ -325,7 +325,7 @@ struct Big {
   // or with kPair a key tile of one row tile): S(0), S(1), then for each step j its
   // P V and S(j + 2).  The warp's lanes look at the barriers of a step together: one
   // look is some 200 cycles (370 -> 340 us, and 299 -> 290 in one call).
-  __device__ __forceinline__ void multiply(Walk k) {
+  __device__ __forceinline__ void multiply(Walk<kShared> k) {
     const int lane = threadIdx.x % 32;
     // Values that are the same in every lane, for the compiler to see: descriptors are
     // then made in uniform registers, and products follow each other faster (trees of
@@ -379,13 +379,13 @@ struct Big {
 
   // -------------------------------------------------------------- operands --
   // This thread's query row of the segment (of each of its tiles) into the Q tile.
-  __device__ __forceinline__ void write_query(const Walk& k, int seg) {
+  __device__ __forceinline__ void write_query(const Walk<kShared>& k, int seg) {
 #pragma unroll 1
     for (int i = 0; i < C::kRows / kBigRows; ++i) write_row(k, seg, i);
     fence_async_smem();
     mbar_arrive(bar(C::bQF));
   }
-  __device__ __forceinline__ void write_row(const Walk& k, int seg, int part) {
+  __device__ __forceinline__ void write_row(const Walk<kShared>& k, int seg, int part) {
     const int r = threadIdx.x % 128;
     const int h = head(k), row = row0(k) + part * kBigRows + r, M = k.s.n * p.G;
     const uint32_t to = smem + part * C::kQ1;
@@ -441,13 +441,13 @@ struct Big {
     }
   }
 
-  __device__ __forceinline__ void prepare(Walk k) {
+  __device__ __forceinline__ void prepare(Walk<kShared> k) {
     const int r = threadIdx.x % 128, lane = threadIdx.x % 32;  // thread r: key r of a tile
     int ks = 0, kr = 0, vs = 0, vr = 0, rs = 0, rr = 0, ms = 0, mr = 0, seg = 0, vref = 0, low = 0, tile_parity = 0;
     do {
       if (seg > 0) wait(C::bQE, (seg - 1) & 1);
       write_query(k, seg);
-      const int len = k.s.len, ctx = len - k.s.n, end = k.tile + k.piece();
+      const int len = k.s.len, ctx = len - k.s.drafts(), end = k.tile + k.piece();
       uint32_t* hidden = ss.hidden[seg % kRing];
       for (int t = k.tile; t < end; ++t) {
         const int pos = t * kBigTile + r;
@@ -559,7 +559,7 @@ struct Big {
   }
 
   // --------------------------------------------------------------- softmax --
-  __device__ __forceinline__ void softmax(Walk k, int g) {
+  __device__ __forceinline__ void softmax(Walk<kShared> k, int g) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = 32 * (warp % 4) + lane;
     const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);  // this warp's lanes of TMEM
@@ -568,13 +568,13 @@ struct Big {
     int ms = 0, mr = 0, ks = 0, seg = 0;
     bool firstp = true;
     do {
-      const Seq sq = k.s;
-      const int M = sq.n * p.G, ctx = sq.len - sq.n, r0 = row0(k) + (kPair ? g * kBigRows : 0), h = head(k);
+      const Seq<kShared> sq = k.s;
+      const int M = sq.n * p.G, ctx = sq.len - sq.drafts(), r0 = row0(k) + (kPair ? g * kBigRows : 0), h = head(k);
       const int row = r0 + r, n = k.piece();
       const bool live = row < M, busy = r0 + 32 * (warp % 4) < M;  // the thread; its warp
       const int tok = live ? row / p.G : 0;
       const uint64_t word = (live ? mask_word(p.mask, sq.q0 + tok, tok) : 0) &
-                            (sq.n >= 64 ? ~0ull : (1ull << sq.n) - 1);
+                            (sq.drafts() >= 64 ? ~0ull : (1ull << sq.drafts()) - 1);
       float rc = p.c, m = -INFINITY, l = 0.f, fix = 0.f;
       int vref = 0;
       for (int j = 0; j < n; ++j) {
@@ -645,13 +645,14 @@ struct Big {
         // O's units: 2^(6 - F) of the values, 2^7 of the probabilities (in the sums too)
         const float ua = kCodes ? wa * pow2((kPair ? vref : ss.fend[0][r]) - 6) : wa;
         const float ub = kCodes ? wb * pow2((kPair ? vref : ss.fend[1][r]) - 6) : wb;
-        const bool whole = k.tile == 0 && n == k.tiles;
+        const bool whole = k.tile == 0 && n == k.tiles, direct = whole && sq.whole();
+        float* const part = kShared && whole ? p.o_row : p.o_part;
         const int slot = whole ? -1 : 2 * (int)blockIdx.x + !firstp;
         const int64_t at = whole ? (int64_t)(sq.q0 + tok) * p.Hq + h * p.G + (row - tok * p.G) : (int64_t)slot * C::kRows + (row - row0(k));
         if (live && (kPair || g == 0)) {
           float lse = ls != 0.f ? (mm + lg2(ls) - (kCodes ? kPLog2 : 0.f)) * 0.69314718055994531f : -INFINITY;
-          if (poison) lse = whole ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
-          (whole ? p.lse : p.lse_part)[at] = lse;
+          if (poison) lse = direct ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
+          (direct ? p.lse : kShared && whole ? p.lse_row : p.lse_part)[at] = lse;
         }
 #pragma unroll 1
         for (int col = kPair ? 0 : g * (D / 2); col < (kPair ? D : (g + 1) * (D / 2)); col += 32) {
@@ -668,8 +669,8 @@ struct Big {
             f[i] = inv != 0.f ? f[i] * inv : 0.f;
             if (poison) f[i] = NAN;
           }
-          if (live && hid) add_hidden(f, hid & word, k.b, h, ctx, col);
-          if (live && whole) {
+          if (live && hid) add_hidden(f, hid & word, sq.table(p, k.b), h, ctx, col);
+          if (live && direct) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(p.o + at * D + col + 8 * i) =
@@ -678,7 +679,7 @@ struct Big {
           } else if (live) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(p.o_part + at * D + col + 4 * i) =
+              *reinterpret_cast<float4*>(part + at * D + col + 4 * i) =
                   make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
           }
         }
@@ -691,12 +692,12 @@ struct Big {
   }
 
   // What cleaning took out of the products, for a row that sees it.
-  __device__ __forceinline__ void add_hidden(float (&f)[32], uint64_t todo, int b, int h, int ctx, int col) {
+  __device__ __forceinline__ void add_hidden(float (&f)[32], uint64_t todo, int64_t table, int h, int ctx, int col) {
     while (todo) {
       const int t = __ffsll((long long)todo) - 1;
       todo &= todo - 1;
       const int pos = ctx + t;
-      const int id = p.table[(int64_t)b * p.stride + (pos >> p.log_page)];
+      const int id = p.table[table + (pos >> p.log_page)];
       if ((unsigned)id >= (unsigned)p.pages) continue;
       const int in = pos & ((1 << p.log_page) - 1);
       const int64_t v = ((((int64_t)id << p.log_page) + in) * p.H + h) * D + col;
@@ -892,7 +893,7 @@ struct Big {
   }
 };
 
-template <int D, bool kCodes, bool kPair>
+template <int D, bool kCodes, bool kPair, bool kShared>
 __global__ void __launch_bounds__(kBigThreads, 1)
 tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ Params p, const __grid_constant__ Work w) {
@@ -908,7 +909,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     if (threadIdx.x == 0) atomicOr(p.err, kTimedOut);
     return;
   }
-  Walk k;
+  Walk<kShared> k;
   if (!find_place(p, w, blockIdx.x, blockIdx.x == 0 && warp == 0, k)) return;  // the whole CTA
   auto init = [&](int first, int n, int count) {
     for (int i = 0; i < n; ++i) mbar_init(smem_u32(&ss.bars[first + i]), count);
@@ -941,7 +942,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Big<D, kCodes, kPair> big{p, w, ss, smem_big, smem_u32(smem_big), ss.tmem};
+  Big<D, kCodes, kPair, kShared> big{p, w, ss, smem_big, smem_u32(smem_big), ss.tmem};
   if (warp < 8) {
     regs_inc<kSoftmaxRegs>();
     big.softmax(k, warp / 4);

@@ -32,34 +32,54 @@ struct Work {
   int units;
 };
 
-__device__ __forceinline__ int seq_tiles(const Seq& s, const Work& w) {
+template <bool kShared>
+__device__ __forceinline__ int seq_tiles(const Seq<kShared>& s, const Work& w) {
   return (s.len + (1 << w.log_tile) - 1) >> w.log_tile;  // lengths end 256 below 2^31
 }
-__device__ __forceinline__ int seq_segments(const Params& p, const Seq& s, const Work& w) {
+template <bool kShared>
+__device__ __forceinline__ int seq_segments(const Params& p, const Seq<kShared>& s, const Work& w) {
   return (s.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
 }
-// Tiles of sequence b in the line; 0 if it has no new token, impossible lengths, or is
-// the first and does not begin at 0.  falls is set where the offsets decrease: then they
-// place no row at all (a row could belong to two sequences).
-__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq& s, bool& falls) {
+// Items of the line: sequences, or groups of them.
+template <bool kShared>
+__device__ __forceinline__ int line_items(const Params& p) {
+  return kShared && p.prefixes ? p.n_groups : p.B;
+}
+// Tiles of item b in the line; 0 if it has no new token, impossible lengths, or is
+// the first sequence and does not begin at 0.  falls is set where the offsets decrease:
+// then they place no row at all (a row could belong to two sequences).
+template <bool kShared>
+__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq<kShared>& s,
+                                          bool& falls) {
+  s.q0 = s.n = 0;
   const bool fits = load_seq(p, b, s);
   falls |= (int)((uint32_t)s.q0 + (uint32_t)s.n) < s.q0;
-  if (!fits || (b == 0 && s.q0 != 0)) {
+  if (!fits || (b == 0 && s.q0 != 0 && !(kShared && p.prefixes))) {
     if (report) atomicOr(p.err, rows::kBadSeqlens);
     return 0;
   }
   return seq_segments(p, s, w) * seq_tiles(s, w);  // the whole line is below 2^31 (checked on the host)
+}
+// Whether a warp finds that the groups' offsets decrease, or, for a line of groups, the
+// sequences' (the line of sequences sees those itself).
+__device__ __forceinline__ bool groups_fall(const Params& p, bool report) {
+  const int lane = threadIdx.x % 32;
+  const bool mine = rows::offsets_fall(p.groups, p.n_groups, lane, 32);
+  const bool falls = __any_sync(0xffffffffu, mine);
+  if (falls && report && lane == 0) atomicOr(p.err, rows::kBadSeqlens);
+  return falls || (p.prefixes && __any_sync(0xffffffffu, rows::offsets_fall(p.cu, p.B, lane, 32)));
 }
 __device__ __forceinline__ int share_of(int total, const Work& w) {
   const int even = (total - 1) / w.units + 1;
   return even > w.min_share ? even : w.min_share;
 }
 
-// Where a unit is in the line: sequence b (lengths in s), segment seg of it, tile
+// Where a unit is in the line: item b (lengths in s), segment seg of it, tile
 // of that, and how many tiles of its share are left.
+template <bool kShared>
 struct Walk {
   int b, seg, segs, tile, tiles, left;
-  Seq s;
+  Seq<kShared> s;
   __device__ __forceinline__ void enter(const Params& p, const Work& w) {
     if (load_seq(p, b, s)) {
       segs = seq_segments(p, s, w);
@@ -78,7 +98,7 @@ struct Walk {
     if (++seg < segs) return true;
     seg = 0;
     do {
-      if (++b >= p.B) return false;
+      if (++b >= line_items<kShared>(p)) return false;
       enter(p, w);
     } while (segs == 0 || tiles == 0);
     return true;
@@ -88,10 +108,13 @@ struct Walk {
 // A unit's place in the line, found by each of its warps: lane t sums the tiles
 // of its block of sequences, the sums are scanned, and the lane whose block holds
 // the first tile of the share walks to it.  False: nothing to do.
-__device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool report, Walk& walk) {
-  const int t = threadIdx.x % 32, per = (p.B + 31) / 32;
-  const int b0 = (int)min((int64_t)t * per, (int64_t)p.B), b1 = min(p.B - b0, per) + b0;
-  Seq s{};
+template <bool kShared>
+__device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool report, Walk<kShared>& walk) {
+  const int items = line_items<kShared>(p);
+  const int t = threadIdx.x % 32, per = (items + 31) / 32;
+  const int b0 = (int)min((int64_t)t * per, (int64_t)items), b1 = min(items - b0, per) + b0;
+  if (kShared && groups_fall(p, report)) return false;
+  Seq<kShared> s{};
   int mine = 0;
   bool falls = false;
   for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report, s, falls);
@@ -121,6 +144,11 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   walk.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
   walk.s.n = __shfl_sync(0xffffffffu, s.n, src);
   walk.s.len = __shfl_sync(0xffffffffu, s.len, src);
+  if constexpr (kShared) {
+    walk.s.masked = __shfl_sync(0xffffffffu, s.masked, src);
+    walk.s.at = __shfl_sync(0xffffffffu, s.at, src);
+    walk.s.page0 = __shfl_sync(0xffffffffu, s.page0, src);
+  }
   at = __shfl_sync(0xffffffffu, at, src);
   walk.segs = seq_segments(p, walk.s, w);
   walk.tiles = seq_tiles(walk.s, w);
@@ -131,8 +159,8 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
 }
 
 // The end of a piece: what a warp writes of its kRows query rows, as the result
-// where the piece is the whole segment (slot < 0), else into its slot of the
-// workspace.  Lane i takes columns 4 (i % 8) .. of rows i / 8, i / 8 + 4, ..
+// where the piece is the whole segment (slot < 0; or with shared prefixes into the
+// rows that are kept for the join), else into its slot of the workspace.  Lane i takes columns 4 (i % 8) .. of rows i / 8, i / 8 + 4, ..
 template <int D, bool kCodes, int kRows>
 struct PieceEnd {
   static constexpr int kN = kRows / 4;
@@ -140,11 +168,13 @@ struct PieceEnd {
   float inv[kN];
   uint64_t hid[kN];    // new tokens with values that are not finite, seen by the row
   bool live[kN], direct, poison;
+  float* part;
 
-  __device__ __forceinline__ void rows_of(const Params& p, const Seq& sq, int h, int row0, int slot, const float* sm_m,
+  template <bool kShared>
+  __device__ __forceinline__ void rows_of(const Params& p, const Seq<kShared>& sq, int h, int row0, int slot, const float* sm_m,
                                           const float* sm_l, uint64_t hidden, bool bad, int lane) {
     const int M = sq.n * p.G;
-    direct = slot < 0;
+    direct = slot < 0 && sq.whole();
     poison = bad;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
@@ -155,17 +185,19 @@ struct PieceEnd {
       const float m = sm_m[r], l = m == -INFINITY ? 0.f : sm_l[r];
       // a row of NaN sums keeps them; one that saw nothing is 0
       inv[j] = l != 0.f ? 1.f / l : 0.f;
-      hid[j] = hidden ? hidden & mask_word(p.mask, sq.q0 + tok, tok) : 0;
-      at[j] = direct ? (int64_t)(sq.q0 + tok) * p.Hq + head : (int64_t)slot * kRows + r;
+      hid[j] = hidden ? hidden & mask_word(p.mask, sq.q0 + tok, tok) : 0;  // (none of a prefix)
+      at[j] = slot < 0 ? (int64_t)(sq.q0 + tok) * p.Hq + head : (int64_t)slot * kRows + r;
       float lse = l != 0.f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
       if (poison) lse = direct ? NAN : INFINITY;  // +inf makes the join of the pieces a NaN row
-      if (lane % 8 == 0) (direct ? p.lse : p.lse_part)[at[j]] = lse;
+      part = kShared && slot < 0 ? p.o_row : p.o_part;
+      if (lane % 8 == 0) (direct ? p.lse : kShared && slot < 0 ? p.lse_row : p.lse_part)[at[j]] = lse;
     }
   }
 
   // 32 columns from col0 on; buf[r pad]: the rows' sums
-  __device__ __forceinline__ void columns(const Params& p, const Seq& sq, int b, int h, const float* buf, int pad,
-                                          int col0, int lane) {
+  template <bool kShared>
+  __device__ __forceinline__ void columns(const Params& p, const Seq<kShared>& sq, int b, int h, const float* buf,
+                                          int pad, int col0, int lane) {
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       if (!live[j]) continue;
@@ -178,8 +210,8 @@ struct PieceEnd {
       while (todo) {
         const int t = __ffsll((long long)todo) - 1;
         todo &= todo - 1;
-        const int pos = sq.len - sq.n + t;
-        const int id = p.table[(int64_t)b * p.stride + (pos >> p.log_page)];
+        const int pos = sq.len - sq.drafts() + t;
+        const int id = p.table[sq.table(p, b) + (pos >> p.log_page)];
         if ((unsigned)id >= (unsigned)p.pages) continue;
         const int64_t v = ((((int64_t)id << p.log_page) + (pos & ((1 << p.log_page) - 1))) * p.H + h) * D + col;
 #pragma unroll
@@ -197,7 +229,7 @@ struct PieceEnd {
         *reinterpret_cast<uint2*>(p.o + at[j] * D + col) =
             make_uint2(rows::pack2(f[0], f[1]), rows::pack2(f[2], f[3]));
       else
-        *reinterpret_cast<float4*>(p.o_part + at[j] * D + col) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(part + at[j] * D + col) = make_float4(f[0], f[1], f[2], f[3]);
     }
   }
 };
@@ -218,12 +250,12 @@ tree_join_kernel(const __grid_constant__ Params p, const __grid_constant__ Work 
   grid_dep_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp % kPerRow;
   const int64_t all = (int64_t)p.total * p.Hq, row0 = ((int64_t)blockIdx.x * 8 + warp) / kPerRow * run;
-  Seq sq{};
+  Seq<false> sq{};
   int total = 0, before = 0;
   // The sequence of token t and its place in the line: a lane reads sequences lane,
   // lane + 32, ..  The first that holds t has it.
   auto find = [&](int t) {
-    Seq other;
+    Seq<false> other;
     int n = 0, b = p.B;
     bool falls = false;
     total = before = 0;

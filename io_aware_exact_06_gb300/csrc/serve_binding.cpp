@@ -1,4 +1,4 @@
-// The torch conveniences of include/attn_norm.h and include/attn_cache.h as a
+// The torch conveniences of include/attn_norm.h, attn_cache.h and attn_verify.h as a
 // CPython module: checks of what the C calls cannot see (types, shapes,
 // strides, devices), outputs and workspaces from torch's allocator, the call.
 // These operators run once per layer and step on a few tokens; marshalling
@@ -22,6 +22,7 @@
 
 #include "../../include/attn_cache.h"
 #include "../../include/attn_norm.h"
+#include "../../include/attn_verify.h"
 
 namespace {
 
@@ -33,6 +34,13 @@ struct Calls {
   decltype(&attn_cache_read) cache_read;
   decltype(&attn_fwd_tree) fwd_tree;
   decltype(&attn_fwd_tree_workspace) fwd_tree_workspace;
+  decltype(&attn_fwd_prefix) fwd_prefix;
+  decltype(&attn_fwd_prefix_workspace) fwd_prefix_workspace;
+  decltype(&attn_cache_fork) cache_fork;
+  decltype(&attn_cache_fork_workspace) cache_fork_workspace;
+  decltype(&attn_cache_copy) cache_copy;
+  decltype(&attn_cache_compact) cache_compact;
+  decltype(&attn_verify_drafts) verify_drafts;
 } calls;
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
@@ -155,7 +163,7 @@ PyObject* pack(std::initializer_list<at::Tensor> ts) {
   PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
   if (!r) throw python_error();
   Py_ssize_t i = 0;
-  for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+  for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None));
   return r;
 }
 
@@ -217,10 +225,10 @@ PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// k_cache, v_cache, page_table, k_scale, v_scale
-attn_paged_cache cache_of(PyObject* const* a, int64_t B) {
-  const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache"), &table = tensor(a[2], "page_table");
-  const at::Tensor *ks = optional_tensor(a[3], "k_scale"), *vs = optional_tensor(a[4], "v_scale");
+// The cache without a page table.
+attn_paged_cache pages_of(PyObject* k_cache, PyObject* v_cache, PyObject* k_scale, PyObject* v_scale) {
+  const at::Tensor &k = tensor(k_cache, "k_cache"), &v = tensor(v_cache, "v_cache");
+  const at::Tensor *ks = optional_tensor(k_scale, "k_scale"), *vs = optional_tensor(v_scale, "v_scale");
   TORCH_CHECK_VALUE(!ks == !vs, "k_scale and v_scale go together");
   const at::ScalarType type = k.scalar_type();
   TORCH_CHECK_TYPE(!ks || type == at::kFloat8_e4m3fn || type == at::kByte,
@@ -228,10 +236,8 @@ attn_paged_cache cache_of(PyObject* const* a, int64_t B) {
   TORCH_CHECK_TYPE(ks || type == at::kBFloat16, "a cache without scales must be bf16");
   plain_dims(k, "k_cache", type, 4);
   plain_shape(v, "v_cache", type, k.sizes());
-  plain_shape(table, "page_table", at::kInt, {B, table.dim() == 2 ? table.size(1) : 0});
   const at::Device dev = k.device();
   same_device(v, "v_cache", dev);
-  same_device(table, "page_table", dev);
   attn_paged_cache c{};
   c.k = k.data_ptr();
   c.v = v.data_ptr();
@@ -243,12 +249,21 @@ attn_paged_cache cache_of(PyObject* const* a, int64_t B) {
     c.k_scale = static_cast<float*>(ks->data_ptr());
     c.v_scale = static_cast<float*>(vs->data_ptr());
   }
-  c.page_table = static_cast<const int32_t*>(table.data_ptr());
-  c.page_table_stride = extent(table.size(1), "page_table");
   c.num_pages = extent(k.size(0), "k_cache");
   c.page_size = extent(k.size(1), "k_cache");
   c.H = extent(k.size(2), "k_cache");
   c.d = extent(k.size(3), "k_cache");
+  return c;
+}
+
+// k_cache, v_cache, page_table, k_scale, v_scale
+attn_paged_cache cache_of(PyObject* const* a, int64_t B) {
+  const at::Tensor& table = tensor(a[2], "page_table");
+  attn_paged_cache c = pages_of(a[0], a[1], a[3], a[4]);
+  plain_shape(table, "page_table", at::kInt, {B, table.dim() == 2 ? table.size(1) : 0});
+  same_device(table, "page_table", tensor(a[0], "k_cache").device());
+  c.page_table = static_cast<const int32_t*>(table.data_ptr());
+  c.page_table_stride = extent(table.size(1), "page_table");
   return c;
 }
 
@@ -302,10 +317,10 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, k_cache, v_cache, page_table, k_scale, v_scale, seqlens, cu_seqlens, max_new, max_len, mask, scale, num_splits,
-// out, lse
-PyObject* tree_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  want(n, 15);
+// out, lse; with shared prefixes also cu_groups, prefix_lens, max_group, max_prefix
+template <bool kPrefix>
+PyObject* decode(PyObject* const* a, Py_ssize_t n) {
+  want(n, kPrefix ? 19 : 15);
   const at::Tensor &qt = tensor(a[0], "q"), &lens = tensor(a[6], "seqlens"), &cu = tensor(a[7], "cu_seqlens");
   const attn_paged_cache c = cache_of(a + 1, lens.dim() == 1 ? lens.size(0) : -1);
   const int64_t B = batch_of(lens);
@@ -337,24 +352,179 @@ PyObject* tree_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(l, "lse", dev);
   }
   const int Bi = extent(B, "seqlens");
-  const size_t bytes = calls.fwd_tree_workspace(Bi, q.T, q.H, c.H, c.d, max_new, max_len, splits);
+  const int32_t *lens_p = static_cast<const int32_t*>(lens.data_ptr()), *cu_p = static_cast<const int32_t*>(cu.data_ptr());
+  const int64_t* mask_p = mask ? static_cast<const int64_t*>(mask->data_ptr()) : nullptr;
+  float* l_p = static_cast<float*>(l.data_ptr());
   at::Tensor ws;
-  if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
-  const int st = calls.fwd_tree(q.p, q.stride, &c, static_cast<const int32_t*>(lens.data_ptr()),
-                                static_cast<const int32_t*>(cu.data_ptr()),
-                                mask ? static_cast<const int64_t*>(mask->data_ptr()) : nullptr, o.data_ptr(),
-                                static_cast<float*>(l.data_ptr()), Bi, q.T, q.H, max_new, max_len, scale, splits,
-                                bytes ? ws.data_ptr() : nullptr, bytes, stream_of(dev));
+  int st;
+  if constexpr (kPrefix) {
+    const at::Tensor &groups = tensor(a[15], "cu_groups"), &prefix = tensor(a[16], "prefix_lens");
+    plain_dims(prefix, "prefix_lens", at::kInt, 1);
+    plain_shape(groups, "cu_groups", at::kInt, {prefix.size(0) + 1});
+    same_device(groups, "cu_groups", dev);
+    same_device(prefix, "prefix_lens", dev);
+    const int n_groups = extent(prefix.size(0), "prefix_lens"), max_group = to_int(a[17], "max_group"),
+              max_prefix = to_int(a[18], "max_prefix");
+    const size_t bytes =
+        calls.fwd_prefix_workspace(Bi, q.T, q.H, c.H, c.d, max_new, max_len, n_groups, max_group, max_prefix, splits);
+    if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    st = calls.fwd_prefix(q.p, q.stride, &c, lens_p, cu_p, mask_p, static_cast<const int32_t*>(groups.data_ptr()),
+                          static_cast<const int32_t*>(prefix.data_ptr()), o.data_ptr(), l_p, Bi, q.T, q.H, max_new,
+                          max_len, n_groups, max_group, max_prefix, scale, splits, bytes ? ws.data_ptr() : nullptr, bytes,
+                          stream_of(dev));
+  } else {
+    const size_t bytes = calls.fwd_tree_workspace(Bi, q.T, q.H, c.H, c.d, max_new, max_len, splits);
+    if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    st = calls.fwd_tree(q.p, q.stride, &c, lens_p, cu_p, mask_p, o.data_ptr(), l_p, Bi, q.T, q.H, max_new, max_len, scale,
+                        splits, bytes ? ws.data_ptr() : nullptr, bytes, stream_of(dev));
+  }
   return st != ATTN_OK ? PyLong_FromLong(st) : pack({o, l});
+}
+PyObject* tree_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return decode<false>(a, n);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return decode<true>(a, n);
   END_HANDLE_TH_ERRORS
 }
 
-// Addresses of the library's seven calls, in the order of Calls.
+const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+
+// An int32 vector [length] on the device.
+const at::Tensor& int_vector(PyObject* o, const char* name, int64_t length, const at::Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  plain_shape(t, name, at::kInt, {length});
+  same_device(t, name, dev);
+  return t;
+}
+
+// page_table, seqlens, parents, new_seqlens, refs, page_size, out, refs_out
+PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 8);
+  const at::Tensor &table = tensor(a[0], "page_table"), &parents = tensor(a[2], "parents"), &refs = tensor(a[4], "refs");
+  plain_dims(table, "page_table", at::kInt, 2);
+  plain_dims(parents, "parents", at::kInt, 1);
+  plain_dims(refs, "refs", at::kInt, 1);
+  const at::Device dev = table.device();
+  same_device(parents, "parents", dev);
+  same_device(refs, "refs", dev);
+  const int B = extent(table.size(0), "page_table"), W = extent(table.size(1), "page_table"),
+            N = extent(parents.size(0), "parents"), pages = extent(refs.size(0), "refs"), page = to_int(a[5], "page_size");
+  const at::Tensor &lens = int_vector(a[1], "seqlens", B, dev), &to = int_vector(a[3], "new_seqlens", N, dev);
+  const at::Tensor *og = optional_tensor(a[6], "out"), *rg = optional_tensor(a[7], "refs_out");
+  const c10::cuda::CUDAGuard guard(dev);
+  const at::Tensor out = og ? *og : make({N, W}, at::kInt, dev), now = rg ? *rg : make({pages}, at::kInt, dev);
+  plain_shape(out, "out", at::kInt, {N, W});
+  plain_shape(now, "refs_out", at::kInt, {pages});
+  same_device(out, "out", dev);
+  same_device(now, "refs_out", dev);
+  const at::Tensor src = make({N}, at::kInt, dev), dst = make({N}, at::kInt, dev);
+  const size_t bytes = calls.cache_fork_workspace(B, N, W, pages, page);
+  at::Tensor ws;
+  if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+  const int st = calls.cache_fork(ints(table), W, ints(lens), B, ints(parents), ints(to), N, ints(refs),
+                                  static_cast<int32_t*>(now.data_ptr()), pages, page, static_cast<int32_t*>(out.data_ptr()),
+                                  static_cast<int32_t*>(src.data_ptr()), static_cast<int32_t*>(dst.data_ptr()),
+                                  bytes ? ws.data_ptr() : nullptr, bytes, stream_of(dev));
+  return st != ATTN_OK ? PyLong_FromLong(st) : pack({out, now, src, dst});
+  END_HANDLE_TH_ERRORS
+}
+
+// k_cache, v_cache, k_scale, v_scale, src, dst
+PyObject* cache_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 6);
+  const attn_paged_cache c = pages_of(a[0], a[1], a[2], a[3]);
+  const at::Device dev = tensor(a[0], "k_cache").device();
+  const at::Tensor& src = tensor(a[4], "src");
+  plain_dims(src, "src", at::kInt, 1);
+  same_device(src, "src", dev);
+  const at::Tensor& dst = int_vector(a[5], "dst", src.size(0), dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  return PyLong_FromLong(calls.cache_copy(&c, ints(src), ints(dst), extent(src.size(0), "src"), stream_of(dev)));
+  END_HANDLE_TH_ERRORS
+}
+
+// k_cache, v_cache, page_table, k_scale, v_scale, seqlens, cu_seqlens, path, accepted
+PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 9);
+  const at::Tensor &lens = tensor(a[5], "seqlens"), &path = tensor(a[7], "path");
+  const attn_paged_cache c = cache_of(a, lens.dim() == 1 ? lens.size(0) : -1);
+  const int64_t B = batch_of(lens);
+  plain_dims(path, "path", at::kInt, 1);
+  const at::Device dev = tensor(a[0], "k_cache").device();
+  same_device(lens, "seqlens", dev);
+  same_device(path, "path", dev);
+  const at::Tensor &cu = int_vector(a[6], "cu_seqlens", B + 1, dev), &kept = int_vector(a[8], "accepted", B, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  return PyLong_FromLong(calls.cache_compact(&c, ints(lens), ints(cu), ints(path), ints(kept), extent(B, "seqlens"),
+                                             extent(path.size(0), "path"), stream_of(dev)));
+  END_HANDLE_TH_ERRORS
+}
+
+// tokens, probs, draft_probs, cu_seqlens, mask, u_accept, u_next, seqlens
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 8);
+  const at::Tensor &tokens = tensor(a[0], "tokens"), &probs = tensor(a[1], "probs"), &cu = tensor(a[3], "cu_seqlens"),
+                   &u = tensor(a[5], "u_accept"), &un = tensor(a[6], "u_next");
+  const at::Tensor *draft = optional_tensor(a[2], "draft_probs"), *mask = optional_tensor(a[4], "mask"),
+                   *lens = optional_tensor(a[7], "seqlens");
+  plain_dims(tokens, "tokens", at::kInt, 1);
+  const int64_t T = tokens.size(0);
+  const at::Device dev = tokens.device();
+  const at::ScalarType type = probs.scalar_type();
+  TORCH_CHECK_TYPE(type == at::kFloat || type == at::kBFloat16, "probs must be fp32 or bf16");
+  auto rows = [&](const at::Tensor& t, const char* name) {
+    TORCH_CHECK_TYPE(t.scalar_type() == type, name, " must be ", type);
+    TORCH_CHECK_VALUE(t.is_cuda() && t.dim() == 2 && t.size(0) == T && t.size(1) == probs.size(1), name,
+                      " must be a CUDA tensor [tokens, vocabulary]");
+    TORCH_CHECK_VALUE(t.size(1) >= 1 && (t.size(1) == 1 || t.stride(1) == 1) && (T <= 1 || t.stride(0) >= t.size(1)), name,
+                      ": a row must be contiguous, and rows must not overlap");
+    same_device(t, name, dev);
+    return T > 1 ? t.stride(0) : t.size(1);
+  };
+  const int64_t p_stride = rows(probs, "probs"), q_stride = draft ? rows(*draft, "draft_probs") : 0;
+  plain_dims(cu, "cu_seqlens", at::kInt, 1);
+  TORCH_CHECK_VALUE(cu.size(0) >= 1, "cu_seqlens must hold at least one offset");
+  const int64_t B = cu.size(0) - 1;
+  plain_shape(u, "u_accept", at::kFloat, {T});
+  plain_shape(un, "u_next", at::kFloat, {B});
+  same_device(cu, "cu_seqlens", dev);
+  same_device(u, "u_accept", dev);
+  same_device(un, "u_next", dev);
+  if (mask) {
+    plain_shape(*mask, "mask", at::kLong, {T});
+    same_device(*mask, "mask", dev);
+  }
+  if (lens) int_vector(a[7], "seqlens", B, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  const at::Tensor path = make({T}, at::kInt, dev), kept = make({B}, at::kInt, dev), next = make({B}, at::kInt, dev);
+  at::Tensor to;
+  if (lens) to = make({B}, at::kInt, dev);
+  const int st = calls.verify_drafts(
+      ints(tokens), probs.data_ptr(), p_stride, draft ? draft->data_ptr() : nullptr, q_stride, type == at::kBFloat16, ints(cu),
+      mask ? static_cast<const int64_t*>(mask->data_ptr()) : nullptr, static_cast<const float*>(u.data_ptr()),
+      static_cast<const float*>(un.data_ptr()), lens ? ints(*lens) : nullptr, static_cast<int32_t*>(path.data_ptr()),
+      static_cast<int32_t*>(kept.data_ptr()), static_cast<int32_t*>(next.data_ptr()),
+      lens ? static_cast<int32_t*>(to.data_ptr()) : nullptr, extent(B, "cu_seqlens"), extent(T, "tokens"),
+      extent(probs.size(1), "probs"), stream_of(dev));
+  return st != ATTN_OK ? PyLong_FromLong(st) : pack({path, kept, next, to});
+  END_HANDLE_TH_ERRORS
+}
+
+// Addresses of the library's calls, in the order of Calls.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  want(n, 7);
-  void* p[7];
-  for (int i = 0; i < 7; ++i) {
+  constexpr int kCalls = 14;
+  want(n, kCalls);
+  void* p[kCalls];
+  for (int i = 0; i < kCalls; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) throw python_error();
   }
@@ -365,13 +535,21 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   calls.cache_read = reinterpret_cast<decltype(calls.cache_read)>(p[4]);
   calls.fwd_tree = reinterpret_cast<decltype(calls.fwd_tree)>(p[5]);
   calls.fwd_tree_workspace = reinterpret_cast<decltype(calls.fwd_tree_workspace)>(p[6]);
+  calls.fwd_prefix = reinterpret_cast<decltype(calls.fwd_prefix)>(p[7]);
+  calls.fwd_prefix_workspace = reinterpret_cast<decltype(calls.fwd_prefix_workspace)>(p[8]);
+  calls.cache_fork = reinterpret_cast<decltype(calls.cache_fork)>(p[9]);
+  calls.cache_fork_workspace = reinterpret_cast<decltype(calls.cache_fork_workspace)>(p[10]);
+  calls.cache_copy = reinterpret_cast<decltype(calls.cache_copy)>(p[11]);
+  calls.cache_compact = reinterpret_cast<decltype(calls.cache_compact)>(p[12]);
+  calls.verify_drafts = reinterpret_cast<decltype(calls.verify_drafts)>(p[13]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(bind),       FAST(norm_rope),  FAST(norm_rope_bwd),          FAST(cache_write),
-                         FAST(cache_read), FAST(tree_decode), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(bind),          FAST(norm_rope),     FAST(norm_rope_bwd), FAST(cache_write),
+                         FAST(cache_read),    FAST(tree_decode),   FAST(prefix_decode), FAST(cache_fork),
+                         FAST(cache_copy),    FAST(cache_compact), FAST(verify_drafts), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
