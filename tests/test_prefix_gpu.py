@@ -1,0 +1,272 @@
+"""Attention of new tokens over shared prefixes against fp64: every sequence over
+its own page table.  The kernels and their roundings are those of attention over
+one sequence's pages, and so are the tolerances (tests/test_tree_gpu.py counts
+them); the join of pieces is fp32, inside the 2^-17 A counted for sums there."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import io_aware_exact_06_gb300 as fa
+from tests import serve_ref as ref
+from tests.test_cache_gpu import cu_of, normal
+from tests.test_tree_gpu import check, fill, random_masks, rows_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import __graft_entry__
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+def ints(dev, values):
+    return torch.tensor(values, dtype=torch.int32, device=dev)
+
+
+def share(c, groups, prefix):
+    """The tables of a group's sequences name the first one's pages for the whole pages of the prefix."""
+    for g, p in enumerate(prefix):
+        n = p // c["page"]
+        if groups[g + 1] > groups[g]:
+            c["page_table"][groups[g]:groups[g + 1], :n] = c["page_table"][groups[g], :n].clone()
+    return c
+
+
+def call(dev, c, q, lens, ns, mask, groups, prefix, **kw):
+    cu = [sum(ns[:i]) for i in range(len(ns) + 1)]
+    kw.setdefault("max_new", max(ns))
+    kw.setdefault("max_len", max(lens))
+    kw.setdefault("max_group", max([cu[groups[g + 1]] - cu[groups[g]] for g in range(len(prefix))] + [0]))
+    kw.setdefault("max_prefix", max(prefix + [0]))
+    return fa.prefix_decode(q, c["k_cache"], c["v_cache"], c["page_table"], ints(dev, lens), cu_of(dev, ns),
+                            cu_groups=ints(dev, groups), prefix_lens=ints(dev, prefix),
+                            mask=None if mask is None else mask.to(dev), k_scale=c["k_scale"], v_scale=c["v_scale"], **kw)
+
+
+CASES = [  # lengths, new tokens, groups' offsets, prefixes, Hq, H, d, page, codes, tree, splits
+    ([50, 60], [1, 1], [0, 2], [48], 1, 1, 64, 16, False, False, 0),
+    ([300, 320, 301, 300], [1, 1, 1, 1], [0, 4], [299], 8, 2, 128, 16, False, False, 0),
+    ([300, 320, 301, 300], [1, 1, 1, 1], [0, 4], [299], 16, 4, 128, 64, True, False, 3),
+    ([40, 700, 720, 40, 520, 530], [1, 1, 1, 1, 1, 1], [1, 3, 3, 4, 6], [650, 9, 0, 512], 12, 4, 64, 32, True, False, 0),
+    ([40, 700, 720, 40, 520, 530], [2, 3, 0, 1, 4, 1], [0, 0, 1, 3, 6], [0, 33, 640, 15], 6, 2, 128, 32, False, True, 2),
+    ([1100, 1090, 1030], [5, 31, 3], [0, 3], [1027], 8, 1, 128, 16, False, True, 0),
+    ([1100, 1090, 1030], [5, 31, 3], [0, 3], [1027], 8, 1, 128, 16, True, True, 5),
+    ([900] * 9, [33] * 9, [0, 9], [777], 4, 2, 64, 256, False, True, 0),
+    ([900] * 9, [33] * 9, [0, 9], [777], 4, 2, 128, 128, True, True, 1),
+    ([900] * 9, [33] * 9, [0, 9], [777], 2, 1, 128, 64, False, True, 0),
+    ([600 + b for b in range(70)], [1] * 70, [0, 35, 70], [599, 500], 4, 1, 128, 16, False, False, 0),
+    ([600 + b for b in range(70)], [1] * 70, [0, 35, 70], [599, 500], 4, 1, 64, 16, True, False, 0),
+    ([130] * 40, [2] * 40, [0, 40], [128], 2, 2, 64, 16, False, True, 1),
+    ([2000, 2001], [64, 64], [0, 2], [1900], 5, 1, 128, 16, False, True, 256),
+    ([16 * 9] * 200, [1] * 200, list(range(0, 201, 2)), [16 * (g % 9) for g in range(100)], 3, 1, 128, 16, True, False, 0),
+]
+
+
+@pytest.mark.parametrize("lens,ns,groups,prefix,Hq,H,d,page,codes,tree,splits", CASES)
+def test_against_fp64(dev, lens, ns, groups, prefix, Hq, H, d, page, codes, tree, splits):
+    seed = 300 + len(lens) * 7 + Hq + d
+    c = share(fill(dev, seed, lens, H, d, page, codes), groups, prefix)
+    total = sum(ns)
+    q = normal(dev, seed + 2, total, Hq + 2, d, std=1.5)[:, :Hq]  # a token stride
+    mask = random_masks(seed, ns) if tree else None
+    got = call(dev, c, q, lens, ns, mask, groups, prefix, num_splits=splits)
+    assert fa.attn_last_device_error() == 0
+    check(c, q, lens, ns, mask, got)
+    again = call(dev, c, q, lens, ns, mask, groups, prefix, num_splits=splits)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("B", [2, 40, 90])  # few rows of a group, one tile, several
+def test_peaky_and_flat_scores(dev, codes, B):
+    lens, ns, groups, prefix = [400 + b % 5 for b in range(B)], [1] * B, [0, B], [390]
+    for std in (0.0, 6.0):
+        c = share(fill(dev, 310, lens, 1, 128, 16, codes, std=max(std, 1.0)), groups, prefix)
+        q = normal(dev, 311, B, 4, 128, std=std)
+        check(c, q, lens, ns, None, call(dev, c, q, lens, ns, None, groups, prefix))
+        check(c, q, lens, ns, None, call(dev, c, q, lens, ns, None, groups, prefix, scale=0.0), scale=0.0)
+    assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("B", [3, 60])
+def test_value_scales_of_all_sizes(dev, codes, B):
+    """A prefix whose values differ by many powers of two, from token to token."""
+    from tests.test_cache_gpu import make, put
+    lens, ns, groups, prefix = [310] * B, [1] * B, [0, B], [304]
+    c = make(dev, 320, lens, 1, 128, 16, codes)
+    kv = normal(dev, 321, sum(lens), 2, 128)
+    kv[:, 1] *= torch.exp2(torch.arange(sum(lens), device=dev) % 41 - 20.0)[:, None].to(torch.bfloat16)
+    put(dev, c, kv[:, :1], kv[:, 1:], lens, lens)
+    share(c, groups, prefix)
+    q = normal(dev, 322, B, 4, 128)
+    check(c, q, lens, ns, None, call(dev, c, q, lens, ns, None, groups, prefix))
+    assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("G", [1, 8])
+def test_what_rows_do_not_see_does_not_matter(dev, codes, G):
+    """Drafts hidden from others hold NaN; rows behind a sequence, and pages behind a prefix's last
+    whole one in the first sequence's table, are other sequences' business."""
+    lens, ns, groups, prefix, d = [200 + b for b in range(20)], [6] * 20, [0, 20], [150], 128
+    c = share(fill(dev, 330, lens, 1, d, 16, codes), groups, prefix)
+    table = c["page_table"].cpu()
+    for b in range(20):
+        row = int(ref.row_index(table, 16, b, torch.tensor(lens[b] - 6 + 2)))
+        if codes:
+            c["v_cache"].view(torch.uint8)[row // 16, row % 16] = 0x7f
+        else:
+            c["v_cache"][row // 16, row % 16] = float("nan")
+    mask = torch.tensor([1 | 1 << i for _ in ns for i in range(6)], dtype=torch.int64)
+    q = normal(dev, 331, 120, G, d)
+    got = call(dev, c, q, lens, ns, mask, groups, prefix)
+    assert fa.attn_last_device_error() == 0
+    o, lse = (x.view(20, 6, *x.shape[1:]) for x in got)
+    assert o[:, 2].isnan().all() and o[:, [0, 1, 3, 4, 5]].isfinite().all() and lse.isfinite().all()
+    k, v = rows_of(c)
+    wo, wl, A, S = ref.tree(q.cpu(), k, v, table, 16, lens, [6 * b for b in range(21)], mask, d ** -0.5)
+    keep = [0, 1, 3, 4, 5]
+    off = (o.cpu().double() - wo.view_as(o)).abs()[:, keep]
+    # bf16 of O and of the probabilities, as in test_tree_gpu; scores below 20 in magnitude
+    assert (off <= (2.0 ** -7 * A.view_as(o) + 2.0 ** -12)[:, keep]).all()
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_rows_that_see_the_prefix_alone_or_nothing(dev, codes):
+    lens, ns, groups, prefix = [70, 75, 12], [6, 6, 12], [0, 2, 3], [64, 0]
+    c = share(fill(dev, 340, lens, 2, 64, 16, codes), groups, prefix)
+    # lengths end right behind the prefix: a token without bits sees the prefix alone
+    q = normal(dev, 341, 24, 4, 64)
+    mask = torch.tensor([0, 3] * 6 + [0, 2] * 6, dtype=torch.int64)
+    got = call(dev, c, q, lens, ns, mask, groups, prefix)
+    assert fa.attn_last_device_error() == 0
+    check(c, q, lens, ns, mask, got)
+    assert (got[0][12::2] == 0).all() and (got[1][12::2] == -math.inf).all()
+
+
+def test_without_groups_it_is_tree_decode(dev):
+    lens, ns = [333, 40, 512], [1, 3, 2]
+    for codes in (False, True):
+        c = fill(dev, 350, lens, 2, 128, 16, codes)
+        q = normal(dev, 351, 6, 8, 128)
+        want = fa.tree_decode(q, c["k_cache"], c["v_cache"], c["page_table"], ints(dev, lens), cu_of(dev, ns), 3, 512,
+                              k_scale=c["k_scale"], v_scale=c["v_scale"])
+        for groups, prefix in (([0], []), ([0, 1, 3], [0, 15])):
+            got = call(dev, c, q, lens, ns, None, groups, prefix)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa.attn_last_device_error() == 0
+
+
+def test_padded_batch_and_bounds(dev):
+    lens, ns, groups, prefix = [90, 95, 33, 0], [3, 2, 1, 0], [0, 2], [80]
+    c = share(fill(dev, 360, lens, 2, 128, 32, True), groups, prefix)
+    q = normal(dev, 361, 12, 4, 128)
+    for bounds in (dict(), dict(max_new=64, max_len=5000, max_group=12, max_prefix=4000), dict(max_group=1 << 30)):
+        out = torch.full((12, 4, 128), 7.0, dtype=torch.bfloat16, device=dev)
+        lse = torch.full((12, 4), 7.0, device=dev)
+        call(dev, c, q, lens, ns, None, groups, prefix, out=out, lse=lse, **bounds)
+        assert fa.attn_last_device_error() == 0
+        check(c, q, lens, ns, None, (out, lse))
+        assert (out[6:] == 7).all() and (lse[6:] == 7).all()
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("B", [4, 100])
+def test_a_nan_in_a_prefix_stays_in_its_group(dev, codes, B):
+    lens, ns, groups, prefix = [300] * B, [1] * B, [0, B // 2, B], [256, 128]
+    c = share(fill(dev, 370, lens, 1, 128, 16, codes), groups, prefix)
+    page = int(c["page_table"][0, 3])
+    if codes:
+        c["k_scale"][page, :, 5] = float("nan")
+    else:
+        c["k_cache"][page, 5, :, 7] = float("nan")
+    q = normal(dev, 371, B, 4, 128)
+    o, lse = call(dev, c, q, lens, ns, None, groups, prefix)
+    assert fa.attn_last_device_error() == 0
+    assert o[:B // 2].isnan().all() and lse[:B // 2].isnan().all()
+    assert o[B // 2:].isfinite().all() and lse[B // 2:].isfinite().all()
+
+
+def test_offsets_past_32_bits(dev):
+    pages = 17000
+    for codes in (True, False):
+        lens, ns, groups, prefix, H, d, page = [600, 610], [40, 3], [0, 2], [512], 8, 128, 256
+        c = fill(dev, 380, lens, H, d, page, codes)
+        big = {**c}
+        for n in "kv":
+            for x in ("_cache", "_scale"):
+                if c[n + x] is None:
+                    continue
+                t = c[n + x].view(torch.uint8) if codes and x == "_cache" else c[n + x]
+                wide = torch.empty((pages + t.shape[0], *t.shape[1:]), dtype=t.dtype, device=dev)
+                wide[pages:] = t
+                big[n + x] = wide.view(c[n + x].dtype)
+        big["page_table"] = c["page_table"] + pages
+        share(c, groups, prefix), share(big, groups, prefix)
+        q = normal(dev, 381, 43, 16, d)
+        want, got = (call(dev, x, q, lens, ns, None, groups, prefix) for x in (c, big))
+        assert fa.attn_last_device_error() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del big, got
+        torch.cuda.empty_cache()
+
+
+BAD = ["falling groups", "group below", "group beyond", "long prefix", "negative prefix", "large group", "prefix in drafts",
+       "prefix page", "short sequence", "falling offsets", "first offset"]
+
+
+@pytest.mark.parametrize("what", BAD)
+@pytest.mark.parametrize("G", [2, 40])
+def test_bad_plans_are_reported(dev, what, G):
+    """Sequences that are not concerned are right; the others are not written, or NaN where a page is wrong."""
+    lens, ns, groups, prefix, d = [120, 130, 200, 210, 50], [2, 1, 3, 1, 1], [0, 2, 4], [96, 160], 64
+    c = share(fill(dev, 390, lens, 1, d, 16, True), groups, prefix)
+    q = normal(dev, 391, 8, G, d)
+    good = call(dev, c, q, lens, ns, None, groups, prefix)
+    lens_d, cu, cg, pl, table = ints(dev, lens), cu_of(dev, ns), ints(dev, groups), ints(dev, prefix), c["page_table"].clone()
+    bounds = dict(max_new=3, max_len=210, max_group=4, max_prefix=160)
+    status, ruined = -8, [3, 4, 5, 6]  # the second group's rows
+    if what == "falling groups":
+        cg[1], ruined = 5, list(range(8))
+    elif what == "group below":
+        cg[0], ruined = -1, [0, 1, 2]
+    elif what == "group beyond":
+        cg[2], ruined = 6, [3, 4, 5, 6, 7]
+    elif what == "long prefix":
+        bounds["max_prefix"] = 159
+    elif what == "negative prefix":
+        pl[1] = -1
+    elif what == "large group":
+        bounds["max_group"] = 3
+    elif what == "prefix in drafts":
+        pl[0], ruined = 128, [0, 1, 2]  # beyond the first sequence's 118, and the second's only new token
+    elif what == "prefix page":
+        table[2, 4], status = 1 << 28, -11
+    elif what == "short sequence":
+        lens_d[3], ruined = 150, [6]
+    elif what == "falling offsets":
+        cu[2], ruined = 7, list(range(8))
+    else:
+        cu[0], ruined = 1, [0, 1]
+    out = torch.full((8, G, d), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((8, G), 7.0, device=dev)
+    if what == "prefix in drafts":
+        lens_d[1] = 128
+    fa.prefix_decode(q, c["k_cache"], c["v_cache"], table, lens_d, cu, cu_groups=cg, prefix_lens=pl, k_scale=c["k_scale"],
+                     v_scale=c["v_scale"], out=out, lse=lse, **bounds)
+    assert fa.attn_last_device_error() == status
+    if status == -11:
+        assert out[ruined].isnan().all() and lse[ruined].isnan().all()
+    else:
+        assert (out[ruined] == 7).all() and (lse[ruined] == 7).all()
+    others = [t for t in range(8) if t not in ruined]
+    assert ((out[others].float() - good[0][others].float()).abs() <= 2.0 ** -7).all()
+    assert ((lse[others] - good[1][others]).abs() <= 2.0 ** -14).all()
+    assert fa.attn_last_device_error() == 0
