@@ -1,7 +1,7 @@
 // Host side of attn_fwd_prefix (include/attn_cache.h): attention over the paged cache
 // for sequences whose first pages are shared.  Two lines of work, one after the other:
-// every group's rows over its shared pages, then every sequence's over its own; a last
-// kernel joins them.  It keeps no workspace in the library.
+// every group's rows over its shared pages, then every sequence's over its own.  A first
+// kernel lays them out, a last one joins the rows' parts.  It keeps no workspace in the library.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -13,7 +13,7 @@
 #include <mutex>
 
 #include "../../include/attn_cache.h"
-#include "attn_prefix_join.cuh"
+#include "attn_prefix_kernel.cuh"
 #include "attn_serve_host.h"
 #include "attn_tree_plan.h"
 
@@ -40,8 +40,15 @@ struct Plans {
   Plan group, seq;
   bool any;  // some group may share a page
   int64_t rows;
-  size_t floats() const { return 2 * (size_t)rows + (any ? tree_rows(group) : 0) + tree_rows(seq); }
+  size_t parts() const { return 2 * (size_t)rows + (any ? tree_rows(group) : 0) + tree_rows(seq); }
 };
+// The lines' items and their tiles, in front of the parts.
+size_t plan_bytes(const Sizes& z) {
+  return ((size_t)z.B + z.groups) * sizeof(attn::tree::Item) + 16;
+}
+size_t bytes_of(const Sizes& z, const Plans& x) {
+  return plan_bytes(z) + x.parts() * (z.d + 1) * sizeof(float);
+}
 Plans plans(const Sizes& z, int page, bool codes) {
   Plans x{};
   x.rows = (int64_t)z.total * z.Hq;
@@ -53,9 +60,10 @@ Plans plans(const Sizes& z, int page, bool codes) {
 }
 
 template <int D, bool kCodes>
-int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree::Params& pg, const attn::tree::Params& p,
-                  cudaStream_t s) {
-  int st = ATTN_OK;
+int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree::Plan& plan, const attn::tree::Params& pg,
+                  const attn::tree::Params& p, cudaStream_t s) {
+  int st = launch(attn::tree::prefix_plan_kernel, 1, attn::tree::kPlanThreads, 0, s, plan);
+  if (st != ATTN_OK) return st;
   if (x.any && (st = launch_line<D, kCodes, true>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
@@ -73,8 +81,8 @@ extern "C" size_t attn_fwd_prefix_workspace(int B, int total, int Hq, int H, int
   const Sizes z{B, total, Hq, H, d, max_new, max_len, groups, max_group, max_prefix, num_splits};
   if (check_sizes(z) != ATTN_OK || empty(z)) return 0;
   size_t most = 0;  // the cache's type and its pages' size are not known here
-  for (bool codes : {false, true}) most = std::max(most, plans(z, 16, codes).floats());
-  return most * (d + 1) * sizeof(float);
+  for (bool codes : {false, true}) most = std::max(most, bytes_of(z, plans(z, 16, codes)));
+  return most;
 }
 
 extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged_cache* cache, const int32_t* seqlens,
@@ -99,7 +107,7 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   const Plans x = plans(z, cache->page_size, codes);
   if (!x.seq.fits || (x.any && !x.group.fits)) return ATTN_ERR_SHAPE;
   if (x.rows > INT32_MAX) return ATTN_ERR_SHAPE;
-  if (!workspace || workspace_bytes < x.floats() * (d + 1) * sizeof(float)) return ATTN_ERR_SCRATCH;
+  if (!workspace || workspace_bytes < bytes_of(z, x)) return ATTN_ERR_SCRATCH;
 
   const attn::cache::Pages pg = pages_of(cache);
   attn::tree::Params p{};
@@ -126,16 +134,37 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   p.max_len = max_len;
   // scale 0 weighs every key alike; the smallest normal factor does, without 0 * inf
   p.c = (float)std::max((double)scale * 1.4426950408889634, (double)FLT_MIN);
-  p.groups = cu_groups;
-  p.prefix = prefix_lens;
-  p.n_groups = groups;
-  p.max_group = max_group;
-  p.max_prefix = max_prefix;
+  // the lines, then rows of d floats, then their LSE
+  attn::tree::Plan plan{};
+  plan.lens = seqlens;
+  plan.cu = cu_seqlens;
+  plan.groups = cu_groups;
+  plan.prefix = prefix_lens;
+  plan.group_items = static_cast<attn::tree::Item*>(workspace);
+  plan.seq_items = plan.group_items + groups;
+  plan.lines = reinterpret_cast<int*>(plan.seq_items + B);
+  plan.B = B;
+  plan.total = total;
+  plan.n_groups = groups;
+  plan.H = cache->H;
+  plan.G = p.G;
+  plan.stride = p.stride;
+  plan.log_page = p.log_page;
+  plan.max_new = max_new;
+  plan.max_len = max_len;
+  plan.max_group = max_group;
+  plan.max_prefix = max_prefix;
+  plan.group_work = x.any ? x.group.work : x.seq.work;
+  plan.seq_work = x.seq.work;
+  p.items = plan.seq_items;
+  p.line = plan.lines + 1;
+  p.n_items = B;
   attn::tree::Params of_groups = p;
-  of_groups.prefixes = true;
-  // rows of D floats first, then their LSE
-  float* at = static_cast<float*>(workspace);
-  float* lse_at = at + x.floats() * d;
+  of_groups.items = plan.group_items;
+  of_groups.line = plan.lines;
+  of_groups.n_items = groups;
+  float* at = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(z));
+  float* lse_at = at + x.parts() * d;
   auto take = [&](size_t rows, float*& o_part, float*& lse_part) {
     o_part = at, lse_part = lse_at;
     at += rows * d, lse_at += rows;
@@ -148,7 +177,7 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
   int dev = 0, sms = 0;
   if ((st = attn_host::lib_device(&dev, &sms, &p.err)) != ATTN_OK) return st;
-  of_groups.err = p.err;
+  plan.err = of_groups.err = p.err;
   const int64_t rows = (int64_t)cache->num_pages * cache->page_size;
   CUtensorMap maps[4];
   for (int i = 0; i < 4; ++i) {
@@ -158,8 +187,8 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
     if ((st = attn_host::lib_make_cache_map(&maps[i], i % 2 ? cache->v : cache->k, rows, cache->H, d, codes, box)) != ATTN_OK)
       return st;
   }
-  return d == 64 ? codes ? launch_prefix<64, true>(x, maps, of_groups, p, s)
-                         : launch_prefix<64, false>(x, maps, of_groups, p, s)
-         : codes ? launch_prefix<128, true>(x, maps, of_groups, p, s)
-                 : launch_prefix<128, false>(x, maps, of_groups, p, s);
+  return d == 64 ? codes ? launch_prefix<64, true>(x, maps, plan, of_groups, p, s)
+                         : launch_prefix<64, false>(x, maps, plan, of_groups, p, s)
+         : codes ? launch_prefix<128, true>(x, maps, plan, of_groups, p, s)
+                 : launch_prefix<128, false>(x, maps, plan, of_groups, p, s);
 }

@@ -21,8 +21,9 @@
 // Sequences whose first pages are the same (samples of one prompt) may have those
 // attended to once for all of them: kShared, in two lines of work.  In the first an
 // item is a group, its rows are all its sequences' and its keys the shared pages, every
-// one of them context; in the second an item is a sequence over its other pages.  The
-// rows' two parts meet in the join.
+// one of them context; in the second an item is a sequence over its other pages.  A kernel
+// of its own lays both lines out (attn_prefix_kernel.cuh); the rows' two parts meet in
+// its join.
 #pragma once
 
 #include "attn_rows.cuh"
@@ -51,12 +52,20 @@ struct Params {
   int max_new, max_len;
   float c;  // scale * log2 e (at least the smallest normal float)
   int* err;
-  // shared prefixes: offsets of the groups' sequences, their common lengths
-  const int *groups, *prefix;
-  int n_groups, max_group, max_prefix;
-  bool prefixes;    // the line of groups, else that of sequences
+  // shared prefixes: the line's items, written by the kernel before
+  const struct Item* items;
+  const int* line;  // tiles of the line
+  int n_items;
   float* o_row;     // [total * Hq][D], [total * Hq]: this line's rows whose keys lie in one
   float* lse_row;   // piece (with slots: what is left for the join)
+};
+
+// An item of the line of groups or of sequences.
+struct __align__(16) Item {
+  int q0, n, len, masked;  // rows q0 .. q0 + n - 1, keys 0 .. len - 1, the last `masked` of them drafts
+  int at, page0;           // its row of the page table; its first page there, -1: a group's, from 0 on
+  int first;               // tiles of the line in front of it
+  int group;               // of a sequence, or -1
 };
 
 // Bytes of a key's (or value's) row of one head, and how TMA boxes cut it.
@@ -164,10 +173,7 @@ struct Seq {
 };
 template <>
 struct Seq<true> {
-  int q0, n, len;
-  int masked;    // drafts
-  int at;        // the table's row
-  int page0;     // its first page (-1: a group's, from 0 on)
+  int q0, n, len, masked, at, page0;
   __device__ __forceinline__ int drafts() const { return masked; }
   __device__ __forceinline__ bool whole() const { return page0 == 0; }
   __device__ __forceinline__ int64_t table(const Params& p, int) const {
@@ -184,44 +190,16 @@ __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<false>& s) 
          s.len <= p.max_len && s.len <= (int64_t)p.stride << p.log_page;
 }
 
-// The group of sequence b, or -1: the last whose offset is not above b.
-__device__ __forceinline__ int find_group(const Params& p, int b) {
-  int lo = 0, hi = p.n_groups;  // groups[0 .. lo-1] <= b < groups[hi ..]
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (p.groups[mid] <= b) lo = mid + 1; else hi = mid;
-  }
-  return lo > 0 && b < p.groups[lo] ? lo - 1 : -1;
-}
-// Shared pages of group g; false if its offsets or its prefix are not what the caller's
-// bounds allow (its sequences are refused then).
-__device__ __forceinline__ bool load_group(const Params& p, int g, int& pages) {
-  const int s0 = p.groups[g], s1 = p.groups[g + 1], prefix = p.prefix[g];
-  pages = prefix >> p.log_page;
-  if (s0 < 0 || s1 < s0 || s1 > p.B || prefix < 0 || prefix > p.max_prefix || pages > p.stride) return false;
-  return (int64_t)p.cu[s1] - p.cu[s0] <= p.max_group;
+// Item b; its tiles in front in `first`.
+__device__ __forceinline__ void load_item(const Item* item, Seq<true>& s, int& first, int& group) {
+  const int4 x = reinterpret_cast<const int4*>(item)[0], y = reinterpret_cast<const int4*>(item)[1];
+  s.q0 = x.x, s.n = x.y, s.len = x.z, s.masked = x.w, s.at = y.x, s.page0 = y.y;
+  first = y.z, group = y.w;
 }
 __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<true>& s) {
-  int pages = 0;
-  if (p.prefixes) {  // group b
-    if (!load_group(p, b, pages)) return false;
-    s.at = p.groups[b];
-    // (rows of a sequence that is refused are computed and not used)
-    s.q0 = max(p.cu[s.at], 0);
-    s.n = max(min(p.cu[p.groups[b + 1]], p.total) - s.q0, 0);
-    s.len = pages << p.log_page;
-    s.masked = 0;
-    s.page0 = -1;
-    return true;
-  }
-  Seq<false> own{};
-  bool fits = load_seq(p, b, own);
-  const int g = find_group(p, b);
-  if (g >= 0) fits &= load_group(p, g, pages);
-  fits &= (int64_t)pages << p.log_page <= own.len - own.n;
-  s.q0 = own.q0, s.n = s.masked = own.n, s.at = b, s.page0 = pages;
-  s.len = fits ? own.len - (pages << p.log_page) : own.len;
-  return fits;
+  int first, group;
+  load_item(p.items + b, s, first, group);
+  return true;
 }
 
 // Whether new token i (mask word `word`) sees new token t.

@@ -40,34 +40,17 @@ template <bool kShared>
 __device__ __forceinline__ int seq_segments(const Params& p, const Seq<kShared>& s, const Work& w) {
   return (s.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
 }
-// Items of the line: sequences, or groups of them.
-template <bool kShared>
-__device__ __forceinline__ int line_items(const Params& p) {
-  return kShared && p.prefixes ? p.n_groups : p.B;
-}
-// Tiles of item b in the line; 0 if it has no new token, impossible lengths, or is
-// the first sequence and does not begin at 0.  falls is set where the offsets decrease:
-// then they place no row at all (a row could belong to two sequences).
-template <bool kShared>
-__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq<kShared>& s,
-                                          bool& falls) {
-  s.q0 = s.n = 0;
+// Tiles of sequence b in the line; 0 if it has no new token, impossible lengths, or is
+// the first and does not begin at 0.  falls is set where the offsets decrease: then they
+// place no row at all (a row could belong to two sequences).
+__device__ __forceinline__ int line_tiles(const Params& p, const Work& w, int b, bool report, Seq<false>& s, bool& falls) {
   const bool fits = load_seq(p, b, s);
   falls |= (int)((uint32_t)s.q0 + (uint32_t)s.n) < s.q0;
-  if (!fits || (b == 0 && s.q0 != 0 && !(kShared && p.prefixes))) {
+  if (!fits || (b == 0 && s.q0 != 0)) {
     if (report) atomicOr(p.err, rows::kBadSeqlens);
     return 0;
   }
   return seq_segments(p, s, w) * seq_tiles(s, w);  // the whole line is below 2^31 (checked on the host)
-}
-// Whether a warp finds that the groups' offsets decrease, or, for a line of groups, the
-// sequences' (the line of sequences sees those itself).
-__device__ __forceinline__ bool groups_fall(const Params& p, bool report) {
-  const int lane = threadIdx.x % 32;
-  const bool mine = rows::offsets_fall(p.groups, p.n_groups, lane, 32);
-  const bool falls = __any_sync(0xffffffffu, mine);
-  if (falls && report && lane == 0) atomicOr(p.err, rows::kBadSeqlens);
-  return falls || (p.prefixes && __any_sync(0xffffffffu, rows::offsets_fall(p.cu, p.B, lane, 32)));
 }
 __device__ __forceinline__ int share_of(int total, const Work& w) {
   const int even = (total - 1) / w.units + 1;
@@ -98,7 +81,7 @@ struct Walk {
     if (++seg < segs) return true;
     seg = 0;
     do {
-      if (++b >= line_items<kShared>(p)) return false;
+      if (++b >= (kShared ? p.n_items : p.B)) return false;
       enter(p, w);
     } while (segs == 0 || tiles == 0);
     return true;
@@ -108,13 +91,10 @@ struct Walk {
 // A unit's place in the line, found by each of its warps: lane t sums the tiles
 // of its block of sequences, the sums are scanned, and the lane whose block holds
 // the first tile of the share walks to it.  False: nothing to do.
-template <bool kShared>
-__device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool report, Walk<kShared>& walk) {
-  const int items = line_items<kShared>(p);
-  const int t = threadIdx.x % 32, per = (items + 31) / 32;
-  const int b0 = (int)min((int64_t)t * per, (int64_t)items), b1 = min(items - b0, per) + b0;
-  if (kShared && groups_fall(p, report)) return false;
-  Seq<kShared> s{};
+__device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool report, Walk<false>& walk) {
+  const int t = threadIdx.x % 32, per = (p.B + 31) / 32;
+  const int b0 = (int)min((int64_t)t * per, (int64_t)p.B), b1 = min(p.B - b0, per) + b0;
+  Seq<false> s{};
   int mine = 0;
   bool falls = false;
   for (int b = b0; b < b1; ++b) mine += line_tiles(p, w, b, report, s, falls);
@@ -144,16 +124,40 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   walk.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
   walk.s.n = __shfl_sync(0xffffffffu, s.n, src);
   walk.s.len = __shfl_sync(0xffffffffu, s.len, src);
-  if constexpr (kShared) {
-    walk.s.masked = __shfl_sync(0xffffffffu, s.masked, src);
-    walk.s.at = __shfl_sync(0xffffffffu, s.at, src);
-    walk.s.page0 = __shfl_sync(0xffffffffu, s.page0, src);
-  }
   at = __shfl_sync(0xffffffffu, at, src);
   walk.segs = seq_segments(p, walk.s, w);
   walk.tiles = seq_tiles(walk.s, w);
   walk.seg = at / walk.tiles;
   walk.tile = at - walk.seg * walk.tiles;
+  walk.left = min(share, total - first);
+  return true;
+}
+
+// The same over a line that is laid out: the last item whose first tile is not behind the
+// share's, by 32 probes a step.
+__device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool, Walk<true>& walk) {
+  const int lane = threadIdx.x % 32, total = *p.line;
+  if (total == 0) return false;
+  const int share = share_of(total, w);
+  if ((int64_t)share * unit >= total) return false;
+  const int first = share * unit;
+  int lo = 0, n = p.n_items;  // items 0 .. lo - 1 begin at or in front of it, lo + n .. behind
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int at = lo + (int)min((int64_t)(lane + 1) * step, (int64_t)n);
+    const int cnt = __popc(__ballot_sync(0xffffffffu, p.items[at - 1].first <= first));
+    const int skip = (int)min((int64_t)cnt * step, (int64_t)n);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  lo += __popc(__ballot_sync(0xffffffffu, lane < n && p.items[min(lo + lane, p.n_items - 1)].first <= first));
+  walk.b = lo - 1;  // items without tiles lie in front of it
+  int before, group;
+  load_item(p.items + walk.b, walk.s, before, group);
+  walk.segs = seq_segments(p, walk.s, w);
+  walk.tiles = seq_tiles(walk.s, w);
+  walk.seg = (first - before) / walk.tiles;
+  walk.tile = first - before - walk.seg * walk.tiles;
   walk.left = min(share, total - first);
   return true;
 }
