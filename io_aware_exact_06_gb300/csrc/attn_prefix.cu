@@ -14,6 +14,7 @@
 
 #include "../../include/attn_cache.h"
 #include "attn_prefix_kernel.cuh"
+#include "attn_prefix_rows_kernel.cuh"
 #include "attn_serve_host.h"
 #include "attn_tree_plan.h"
 
@@ -49,14 +50,44 @@ size_t plan_bytes(const Sizes& z) {
 size_t bytes_of(const Sizes& z, const Plans& x) {
   return plan_bytes(z) + x.parts() * (z.d + 1) * sizeof(float);
 }
+// A segment of as many row tiles as CTAs take over the same keys at a time (at most 8),
+// where at least nine tenths of the SMs are busy so: 2048 rows of 8 key heads over 32768 keys
+// read them eight times from HBM else.
+void make_teams(Plan& pl, int64_t tiles) {
+  int team = 1;
+  for (int t = 2; t <= 8 && t <= tiles; ++t) {
+    const double busy = (double)tiles / (double)((tiles + t - 1) / t * t) * (kPlanSms / t * t) / kPlanSms;
+    if (busy >= 0.9) team = t;
+  }
+  pl.work.rows = pl.rows * team;
+  pl.work.units = (int)std::max<int64_t>(1, std::min<int64_t>(pl.ctas, kPlanSms / team));
+  pl.ctas = (int64_t)pl.work.units * team;
+  pl.slots = 2 * pl.ctas;
+}
 Plans plans(const Sizes& z, int page, bool codes) {
   Plans x{};
   x.rows = (int64_t)z.total * z.Hq;
   const int most = std::min(z.max_group, z.total);
   x.any = z.groups > 0 && most > 0 && z.max_prefix >= page;
-  if (x.any) x.group = tree_plan(z.groups, z.total, z.Hq, z.H, z.d, most, z.max_prefix, z.splits, codes);
+  if (x.any) {
+    x.group = tree_plan(z.groups, z.total, z.Hq, z.H, z.d, most, z.max_prefix, z.splits, codes);
+    if (!codes && !few(x.group)) make_teams(x.group, ((int64_t)most * (z.Hq / z.H) + x.group.rows - 1) / x.group.rows);
+  }
   x.seq = tree_plan(z.B, z.total, z.Hq, z.H, z.d, z.max_new, z.max_len, z.splits, codes);
   return x;
+}
+
+// The line of groups: over a bf16 cache many rows have a kernel of their own.
+template <int D, bool kCodes>
+int launch_groups(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
+                  cudaStream_t s) {
+  using namespace attn::tree;
+  if (kCodes || few(pl)) return launch_line<D, kCodes, true>(pl, mk, mv, p, s);
+  auto kernel = pl.rows == kBigRows ? prefix_rows_kernel<D, false> : prefix_rows_kernel<D, true>;
+  const int smem = pl.rows == kBigRows ? RowsCfg<D, false>::kSmem : RowsCfg<D, true>::kSmem;
+  const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (st != ATTN_OK) return st;
+  return launch(kernel, pl.ctas, kRowsThreads, smem, s, mk, mv, p, pl.work);
 }
 
 template <int D, bool kCodes>
@@ -64,7 +95,7 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
                   const attn::tree::Params& p, cudaStream_t s) {
   int st = launch(attn::tree::prefix_plan_kernel, 1, attn::tree::kPlanThreads, 0, s, plan);
   if (st != ATTN_OK) return st;
-  if (x.any && (st = launch_line<D, kCodes, true>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
+  if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
   if (x.seq.many || x.group.many)
