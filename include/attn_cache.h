@@ -166,7 +166,7 @@ size_t attn_fwd_prefix_workspace(int B, int total, int Hq, int H, int d, int max
  * same), seqlens [B], parents, new_seqlens, copy_src and copy_dst [N], all int32
  * on the device.  page_size 16, 32, 64, 128 or 256.
  * workspace: attn_cache_fork_workspace(...) bytes of the caller's device memory,
- * not initialised, in use until the call's work on stream has finished.
+ * 16-byte aligned, not initialised, in use until the call's work on stream has finished.
  * Errors in the error word: ATTN_ERR_SEQLENS (a length below 0 or beyond the
  * table), ATTN_ERR_INDEX (a parent outside the batch; a page outside the cache or
  * with a count below 1) and ATTN_ERR_PAGES (fewer free pages than asked for):

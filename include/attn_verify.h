@@ -32,7 +32,7 @@ extern "C" {
  * child is left, the next token is the first x with w(0) + .. + w(x) > u_next[b] times
  * the sum of w; where that sum is 0, of p.
  * Probabilities are taken between 0 and 1 (NaN: 0).  Tests are made in fp64 and sums in
- * units of 2^-45, exactly: results do not depend on the launch and repeat bit for bit.
+ * units of 2^-43, exactly: results do not depend on the launch and repeat bit for bit.
  * tokens: int32[total]; u_accept: fp32[total], u_next: fp32[B], in [0, 1).
  * path: int32[total], from cu_seqlens[b] on the accepted new tokens, 0 and the accepted
  * drafts (indices within the sequence, increasing), then -1; accepted: int32[B], how

@@ -21,10 +21,12 @@ using namespace attn_serve;
 
 // As launch(), with clusters of `ctas`.
 template <typename... KArgs, typename... Args>
-int launch_clusters(void (*kernel)(KArgs...), int64_t grid, int ctas, int threads, cudaStream_t s, const Args&... args) {
+int launch_clusters(void (*kernel)(KArgs...), int64_t grid, int ctas, int threads, int smem, cudaStream_t s,
+                    const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -38,6 +40,20 @@ int launch_clusters(void (*kernel)(KArgs...), int64_t grid, int ctas, int thread
   return e == cudaSuccess ? ATTN_OK : attn_host::lib_cuda_fail(e);
 }
 
+// Lets a kernel have clusters of more than eight CTAs, once per device.  Call with the
+// library lock held.
+int allow_wide_clusters(const void* kernel) {
+  static std::set<int> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  if (done.count(dev)) return ATTN_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
+  done.insert(dev);
+  return ATTN_OK;
+}
+
 int64_t element_bytes(const attn_paged_cache* c) { return c->k_scale ? 1 : 2; }
 
 bool page_size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
@@ -49,9 +65,9 @@ int check_fork(int B, int N, int W, int pages, int page_size) {
   return ATTN_OK;
 }
 
-// 32-bit words: three for each old row, and the pages that are handed out.
+// 32-bit words: four for each row, old and new, and the pages that are handed out.
 size_t fork_words(int B, int N, int W, int pages) {
-  return 3 * (size_t)B + (size_t)std::min<int64_t>(pages, (int64_t)N * W);
+  return 4 * ((size_t)B + N) + (size_t)std::min<int64_t>(pages, (int64_t)N * W);
 }
 
 }  // namespace
@@ -138,11 +154,12 @@ extern "C" int attn_cache_fork(const int32_t* page_table, int page_table_stride,
     return ATTN_ERR_NULL;
   for (const void* x : {(const void*)refs, (const void*)refs_out, (const void*)page_table, (const void*)seqlens,
                         (const void*)parents, (const void*)new_seqlens, (const void*)page_table_out,
-                        (const void*)copy_src, (const void*)copy_dst, (const void*)workspace})
+                        (const void*)copy_src, (const void*)copy_dst})
     if (!aligned(x, 4)) return ATTN_ERR_ALIGN;
   const uintptr_t from = reinterpret_cast<uintptr_t>(page_table), to = reinterpret_cast<uintptr_t>(page_table_out);
   if (B && N && from < to + (size_t)N * W * 4 && to < from + (size_t)B * W * 4) return ATTN_ERR_SHAPE;  // they overlap
   const size_t words = fork_words(B, N, W, num_pages);
+  if (!aligned(workspace, 16)) return ATTN_ERR_ALIGN;
   if (words && (!workspace || workspace_bytes < words * sizeof(int))) return ATTN_ERR_SCRATCH;
   Fork p{};
   p.table = page_table;
@@ -154,18 +171,28 @@ extern "C" int attn_cache_fork(const int32_t* page_table, int page_table_stride,
   p.out = page_table_out;
   p.src = copy_src;
   p.dst = copy_dst;
-  p.heir = static_cast<int*>(workspace);
+  p.info = static_cast<int4*>(workspace);
+  p.heir = reinterpret_cast<int*>(p.info + N);
   p.writer = p.heir + B;
   p.reader = p.writer + B;
-  p.order = p.reader + B;
+  p.taken = p.reader + B;
+  p.order = p.taken + B;
   p.B = B;
   p.N = N;
   p.W = W;
   p.pages = num_pages;
+  p.vec = aligned(refs, 16) && aligned(refs_out, 16);
   p.log_page = 4;
   while ((1 << p.log_page) < page_size) ++p.log_page;
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
-  return launch_clusters(cache_fork_kernel, kForkCtas, kForkCtas, kForkThreads, reinterpret_cast<cudaStream_t>(stream), p);
+  {
+    std::lock_guard<std::mutex> lock(attn_host::lib_mutex());
+    if ((st = allow_wide_clusters(reinterpret_cast<const void*>(cache_fork_kernel))) != ATTN_OK) return st;
+  }
+  // what is read and written in 32-bit words; a small plan gains nothing from more CTAs (64 rows: 12.3 us
+  // with 8, 14.0 with 16)
+  p.ctas = ((int64_t)B + N) * W + num_pages > (1 << 18) ? kMaxForkCtas : kMaxForkCtas / 2;
+  return launch_clusters(cache_fork_kernel, p.ctas, p.ctas, kForkThreads, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 extern "C" int attn_verify_drafts(const int32_t* tokens, const void* probs, int64_t probs_stride, const void* draft_probs,
@@ -203,19 +230,14 @@ extern "C" int attn_verify_drafts(const int32_t* tokens, const void* probs, int6
   p.B = B;
   p.total = total;
   p.V = V;
-  // CTAs of a sequence: as many as its segments give work, while all of them fit the
+  // CTAs of a sequence: while their warps have more than a segment each, and all fit the
   // GPU at once
   p.ctas = 1;
-  while (p.ctas < kMaxCluster && 2 * p.ctas * kWarps <= (V + kSeg - 1) / kSeg && (int64_t)2 * p.ctas * B <= 4 * kPlanSms)
-    p.ctas *= 2;
+  while (p.ctas < kMaxCluster && p.ctas * kWarps * kSeg < V && (int64_t)2 * p.ctas * B <= 4 * kPlanSms) p.ctas *= 2;
   if ((int64_t)B * p.ctas > INT32_MAX) return ATTN_ERR_SHAPE;
   int st = error_word(&p.err);
   if (st != ATTN_OK) return st;
-  const bool vec = aligned(probs, 16) && probs_stride * size % 16 == 0 && aligned(draft_probs, 16) &&
-                   (!draft_probs || draft_stride * size % 16 == 0);
-  auto kernel = bf16 ? draft_probs ? vec ? verify_kernel<__nv_bfloat16, true, true> : verify_kernel<__nv_bfloat16, true, false>
-                       : vec ? verify_kernel<__nv_bfloat16, false, true> : verify_kernel<__nv_bfloat16, false, false>
-                : draft_probs ? vec ? verify_kernel<float, true, true> : verify_kernel<float, true, false>
-                : vec ? verify_kernel<float, false, true> : verify_kernel<float, false, false>;
-  return launch_clusters(kernel, (int64_t)B * p.ctas, p.ctas, kThreads, reinterpret_cast<cudaStream_t>(stream), p);
+  auto kernel = bf16 ? draft_probs ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>
+                : draft_probs ? verify_kernel<float, true> : verify_kernel<float, false>;
+  return launch_clusters(kernel, (int64_t)B * p.ctas, p.ctas, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }

@@ -161,8 +161,12 @@ struct Fork {
   const int *table, *lens, *parents, *new_lens, *refs;
   int *refs_out, *out, *src, *dst;
   int *heir, *writer, *reader;  // [B] a row's first child, its first that writes to the last page, whether one only reads it
+  int* taken;                   // [B] pages that the first child takes over
+  int4* info;                   // [N] parent; 4 pages kept + 2 (first child) + 1 (copies the last); pages; first request
   int* order;                   // free pages, lowest first, as many as are asked for
   int B, N, W, pages, log_page;
+  bool vec;  // counts lie on multiples of 16 bytes
+  int ctas;  // of the cluster
   int* err;
 };
 
@@ -170,14 +174,16 @@ struct Fork {
 // some hundred kilobytes of integers, and a launch for each step would cost more than
 // the step.  Pages are handed out lowest first, in the order of the rows that ask, and
 // counts only ever add up, so no atomic's order shows in what comes out.
-constexpr int kForkCtas = 8;
+constexpr int kMaxForkCtas = 16;  // of a cluster (not a portable size)
 constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
+constexpr int kAtOnce = 4;  // loads of a lane in flight
 
 struct ForkShared {
-  int64_t free, asks;  // of this CTA's part
+  int free, asks;  // of this CTA's part
   int bad;             // error bits
-  int warp[4 * kForkWarps];
+  int free_of[kForkWarps];
+  int warp[kForkWarps];
 };
 
 // Exclusive place of this thread among the CTA's, from its count; `sum` the CTA's count.
@@ -198,11 +204,6 @@ __device__ __forceinline__ int place_of(int count, int* warps, int& sum) {
   return before + upto - count;
 }
 
-__device__ __forceinline__ int64_t load_cluster64(const void* p, uint32_t rank) {
-  int64_t v;
-  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(map_cluster(smem_u32(p), rank)) : "memory");
-  return v;
-}
 __device__ __forceinline__ int load_cluster32(const void* p, uint32_t rank) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_cluster(smem_u32(p), rank)) : "memory");
@@ -226,21 +227,57 @@ __device__ __forceinline__ NewRow new_row(const Fork& p, int i) {
   return r;
 }
 
+// Counts of pages i .. i + 3 (below hi; 1 behind it).
+__device__ __forceinline__ int4 counts_at(const Fork& p, int i, int hi) {
+  if (p.vec && i + 3 < hi) return *reinterpret_cast<const int4*>(p.refs + i);
+  int4 x = make_int4(1, 1, 1, 1);
+  if (i < hi) x.x = p.refs[i];
+  if (i + 1 < hi) x.y = p.refs[i + 1];
+  if (i + 2 < hi) x.z = p.refs[i + 2];
+  if (i + 3 < hi) x.w = p.refs[i + 3];
+  return x;
+}
+
 __global__ void __launch_bounds__(kForkThreads, 1) cache_fork_kernel(const __grid_constant__ Fork p) {
   __shared__ ForkShared sm;
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint32_t rank = cluster_ctarank();
-  const int thread = (int)rank * kForkThreads + threadIdx.x, all = kForkCtas * kForkThreads;
+  const int thread = (int)rank * kForkThreads + threadIdx.x, all = p.ctas * kForkThreads;
   const int wide = thread / 32, warps = all / 32;
   const int most = p.W << p.log_page;
   if (threadIdx.x == 0) sm.free = sm.asks = sm.bad = 0;
   __syncthreads();
+  // each CTA has a run of the new rows
+  const int run = (p.N + p.ctas - 1) / p.ctas;
+  const int i0 = (int)min((int64_t)rank * run, (int64_t)p.N), i1 = (int)min((int64_t)i0 + run, (int64_t)p.N);
 
   // ------------------------------------------------ is the plan possible? --
   int bad = 0;
-  for (int b = thread; b < p.B; b += all) p.heir[b] = p.writer[b] = INT_MAX, p.reader[b] = 0;
+  for (int b = thread; b < p.B; b += all) p.heir[b] = p.writer[b] = INT_MAX, p.reader[b] = p.taken[b] = 0;
+  for (int i = i0 + (int)threadIdx.x; i < i1; i += kForkThreads) {
+    if (p.parents[i] < -1 || p.parents[i] >= p.B) bad |= rows::kBadIndex;
+    if (p.new_lens[i] < 0 || p.new_lens[i] > most) bad |= rows::kBadSeqlens;
+  }
+  // each warp has a stretch of pages: counts copied, free ones counted
+  const int stretch = ((p.pages + warps - 1) / warps + 127) & ~127;
+  const int lo = (int)min((int64_t)wide * stretch, (int64_t)p.pages), hi = (int)min((int64_t)lo + stretch, (int64_t)p.pages);
+  int mine = 0;
+#pragma unroll 4
+  for (int i = lo + 4 * lane; i < hi; i += 128) {
+    const int4 x = counts_at(p, i, hi);
+    mine += (x.x == 0) + (x.y == 0) + (x.z == 0) + (x.w == 0);
+    if (p.refs_out == p.refs) continue;
+    if (p.vec && i + 3 < hi) {
+      *reinterpret_cast<int4*>(p.refs_out + i) = x;
+    } else {
+      p.refs_out[i] = x.x;
+      if (i + 1 < hi) p.refs_out[i + 1] = x.y;
+      if (i + 2 < hi) p.refs_out[i + 2] = x.z;
+      if (i + 3 < hi) p.refs_out[i + 3] = x.w;
+    }
+  }
   for (int b = wide; b < p.B; b += warps) {
     const int len = p.lens[b];
     if (len < 0 || len > most) {
@@ -248,46 +285,41 @@ __global__ void __launch_bounds__(kForkThreads, 1) cache_fork_kernel(const __gri
       continue;
     }
     const int n = (len + (1 << p.log_page) - 1) >> p.log_page;
-#pragma unroll 4
-    for (int j = lane; j < n; j += 32) {
-      const int page = p.table[(int64_t)b * p.W + j];
-      if ((unsigned)page >= (unsigned)p.pages || p.refs[page] < 1) bad |= rows::kBadIndex;
+    const int* row = p.table + (int64_t)b * p.W;
+    for (int j = lane; j < n; j += 32 * kAtOnce) {
+      int page[kAtOnce], count[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) page[u] = j + 32 * u < n ? row[j + 32 * u] : -1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) count[u] = (unsigned)page[u] < (unsigned)p.pages ? p.refs[page[u]] : 0;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (j + 32 * u < n && count[u] < 1) bad |= rows::kBadIndex;
     }
-  }
-  for (int i = thread; i < p.N; i += all) {
-    if (p.parents[i] < -1 || p.parents[i] >= p.B) bad |= rows::kBadIndex;
-    if (p.new_lens[i] < 0 || p.new_lens[i] > most) bad |= rows::kBadSeqlens;
-  }
-  // the CTA's stretch of pages: counts copied, free ones counted
-  const int stretch = ((p.pages + kForkCtas - 1) / kForkCtas + 3) & ~3;
-  const int lo = (int)min((int64_t)rank * stretch, (int64_t)p.pages), hi = (int)min((int64_t)lo + stretch, (int64_t)p.pages);
-  int mine = 0;
-#pragma unroll 4
-  for (int i = lo + (int)threadIdx.x; i < hi; i += kForkThreads) {
-    const int n = p.refs[i];
-    mine += n == 0;
-    if (p.refs_out != p.refs) p.refs_out[i] = n;
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   bad = __reduce_or_sync(0xffffffffu, bad);
   if (lane == 0) {
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sm.free), (unsigned long long)mine);
+    sm.free_of[warp] = mine;
+    atomicAdd(&sm.free, mine);
     if (bad) atomicOr(&sm.bad, bad);
   }
   cluster_sync();
-  int64_t free_all = 0, free_before = 0;
-  bad = 0;
-  for (int c = 0; c < kForkCtas; ++c) {
-    const int64_t n = load_cluster64(&sm.free, c);
-    free_all += n;
-    if (c < (int)rank) free_before += n;
-    bad |= load_cluster32(&sm.bad, c);
-  }
+  // (counts of pages and of requests are 32-bit numbers, and so are their sums)
+  const bool other = lane < p.ctas;
+  int there = other ? load_cluster32(&sm.free, lane) : 0;
+  const int free_all = __reduce_add_sync(0xffffffffu, there);
+  const int free_before = __reduce_add_sync(0xffffffffu, lane < (int)rank ? there : 0) +
+                          __reduce_add_sync(0xffffffffu, lane < warp ? sm.free_of[lane] : 0);  // of the warp's stretch
+  bad = __reduce_or_sync(0xffffffffu, other ? load_cluster32(&sm.bad, lane) : 0);
 
   // --------------------------------------------------- who writes where? --
+  // (a thread's first row stays in registers)
+  NewRow first{};
   if (!bad)
-    for (int i = thread; i < p.N; i += all) {
+    for (int i = i0 + (int)threadIdx.x; i < i1; i += kForkThreads) {
       const NewRow r = new_row(p, i);
+      if (i == i0 + (int)threadIdx.x) first = r;
       if (r.parent < 0) continue;
       atomicMin(p.heir + r.parent, i);
       if (r.grows)
@@ -298,29 +330,32 @@ __global__ void __launch_bounds__(kForkThreads, 1) cache_fork_kernel(const __gri
   cluster_sync();
   // A row that grows into a page leaves it where nobody else has it, once the first
   // of those that grow has kept it; the others copy it.
-  auto copies = [&](const NewRow& r, int i) {
-    return r.grows && !(p.refs[r.last] == 1 && !__ldcg(p.reader + r.parent) && __ldcg(p.writer + r.parent) == i);
-  };
-  // each CTA asks for a run of rows
-  const int run = (p.N + kForkCtas - 1) / kForkCtas;
-  const int i0 = (int)min((int64_t)rank * run, (int64_t)p.N), i1 = (int)min((int64_t)i0 + run, (int64_t)p.N);
-  int64_t asks = 0;
-  if (!bad)
-    for (int i = i0 + (int)threadIdx.x; i < i1; i += kForkThreads) {
-      const NewRow r = new_row(p, i);
-      const bool c = copies(r, i);
-      asks += r.needs - r.keep + c;
+  int asks = 0;
+  for (int from = i0; from < i1 && !bad; from += kForkThreads) {
+    const int i = from + threadIdx.x;
+    int4 x = make_int4(-1, 0, 0, 0);
+    if (i < i1) {
+      const NewRow r = from == i0 ? first : new_row(p, i);
+      bool c = false, heir = false;
+      if (r.parent >= 0) {
+        const int count = r.grows ? p.refs[r.last] : 1, reader = __ldcg(p.reader + r.parent),
+                  writer = __ldcg(p.writer + r.parent);
+        heir = __ldcg(p.heir + r.parent) == i;
+        c = r.grows && !(count == 1 && !reader && writer == i);
+        if (heir) p.taken[r.parent] = r.keep - c;
+      }
       p.src[i] = c ? r.last : -1;
+      x = make_int4(r.parent, 4 * (r.keep - c) + 2 * heir + c, r.needs, r.needs - r.keep + c);
     }
-  const int asked = __reduce_add_sync(0xffffffffu, (int)asks);  // N W fits 32 bits
-  if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.asks), (unsigned long long)asked);
-  cluster_sync();
-  int64_t asks_all = 0, asks_before = 0;
-  for (int c = 0; c < kForkCtas; ++c) {
-    const int64_t n = load_cluster64(&sm.asks, c);
-    asks_all += n;
-    if (c < (int)rank) asks_before += n;
+    int sum;
+    x.w = asks + place_of(x.w, sm.warp, sum);  // among its CTA's
+    if (i < i1) p.info[i] = x;
+    asks += sum;
   }
+  if (threadIdx.x == 0) sm.asks = asks;
+  cluster_sync();
+  there = other ? load_cluster32(&sm.asks, lane) : 0;
+  const int asks_all = __reduce_add_sync(0xffffffffu, there);
   if (asks_all > free_all) bad |= rows::kNoPages;
   if (bad) {  // nothing changes hands
     if (thread == 0) atomicOr(p.err, bad);
@@ -330,57 +365,60 @@ __global__ void __launch_bounds__(kForkThreads, 1) cache_fork_kernel(const __gri
     return;
   }
   // the lowest free pages, as many as are asked for
-  int64_t at = free_before;
-  for (int from = lo; from < hi && at < asks_all; from += kForkThreads) {
-    const int i = from + threadIdx.x;
-    const bool is = i < hi && p.refs[i] == 0;
-    int sum;
-    const int64_t place = at + place_of(is, sm.warp, sum);
-    if (is && place < asks_all) p.order[place] = i;
-    at += sum;
-  }
-  // every row's first request; kept in dst until the row is written
-  at = asks_before;
-  for (int from = i0; from < i1; from += kForkThreads) {
-    const int i = from + threadIdx.x;
-    int n = 0;
-    if (i < i1) {
-      const NewRow r = new_row(p, i);
-      n = r.needs - r.keep + (p.src[i] >= 0);
+  int at = free_before;
+#pragma unroll 4
+  for (int from = lo; from < hi; from += 128) {
+    if (at >= asks_all) break;  // the same in the whole warp
+    const int i = from + 4 * lane;
+    const int4 x = counts_at(p, i, hi);
+    const int is[4] = {x.x == 0, x.y == 0, x.z == 0, x.w == 0};
+    int place = 0, sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t vote = __ballot_sync(0xffffffffu, is[e]);
+      place += __popc(vote & ((1u << lane) - 1));
+      sum += __popc(vote);
     }
-    int sum;
-    const int64_t place = at + place_of(n, sm.warp, sum);
-    if (i < i1) p.dst[i] = (int)place;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (is[e] && at + place < asks_all) p.order[at + place] = i + e;
+      place += is[e];
+    }
     at += sum;
   }
   cluster_sync();
 
   // --------------------------------------------------------- the new rows --
   for (int i = wide; i < p.N; i += warps) {
-    const NewRow r = new_row(p, i);
-    const int first = __ldcg(p.dst + i);
-    const bool c = __ldcg(p.src + i) >= 0, heir = r.parent >= 0 && __ldcg(p.heir + r.parent) == i;
-    const int held = r.keep - c;  // pages that stay the parent's
-    __syncwarp();
-    for (int j = lane; j < p.W; j += 32) {
-      int page = -1;
-      if (j < held) {
-        page = p.table[(int64_t)r.parent * p.W + j];
-        if (!heir) atomicAdd(p.refs_out + page, 1);
-      } else if (j < r.needs) {
-        page = __ldcg(p.order + first + (j - held));
-        p.refs_out[page] = 1;
-        if (c && j == held) p.dst[i] = page;
+    const int4 x = __ldcg(p.info + i);
+    const bool c = x.y & 1, heir = x.y & 2;
+    const int held = x.y >> 2, needs = x.z;  // pages that stay the parent's, and of the row
+    const int first = x.w + __reduce_add_sync(0xffffffffu, lane < i / run ? there : 0);  // of row i's CTA
+    const int* row = p.table + (int64_t)x.x * p.W;
+    for (int j0 = lane; j0 < p.W; j0 += 32 * kAtOnce) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int j = j0 + 32 * u;
+        page[u] = j < held ? row[j] : j < needs ? __ldcg(p.order + first + (j - held)) : -1;
       }
-      p.out[(int64_t)i * p.W + j] = page;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int j = j0 + 32 * u;
+        if (j < p.W) p.out[(int64_t)i * p.W + j] = page[u];
+        if (j < held) {
+          if (!heir) atomicAdd(p.refs_out + page[u], 1);
+        } else if (j < needs) {
+          p.refs_out[page[u]] = 1;
+          if (c && j == held) p.dst[i] = page[u];
+        }
+      }
     }
     if (!c && lane == 0) p.dst[i] = -1;
   }
   // old rows give up what their first child did not take over
   for (int b = wide; b < p.B; b += warps) {
-    const int heir = __ldcg(p.heir + b);
-    int j = 0;
-    if (heir < p.N) j = new_row(p, heir).keep - (__ldcg(p.src + heir) >= 0);
+    int j = __ldcg(p.taken + b);
     const int n = (p.lens[b] + (1 << p.log_page) - 1) >> p.log_page;
     for (j += lane; j < n; j += 32)
       if (atomicSub(p.refs_out + p.table[(int64_t)b * p.W + j], 1) < 1) atomicOr(p.err, rows::kBadIndex);

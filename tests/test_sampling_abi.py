@@ -102,8 +102,8 @@ def test_fork_refusals(lib, args, status):
 
 
 def test_fork_workspace_size():
-    assert fa.attn_cache_fork_workspace(4, 6, 8, 100, 16) == 4 * (3 * 4 + 48)
-    assert fa.attn_cache_fork_workspace(4, 6, 8, 10, 16) == 4 * (3 * 4 + 10)
+    assert fa.attn_cache_fork_workspace(4, 6, 8, 100, 16) == 4 * (4 * 10 + 48)
+    assert fa.attn_cache_fork_workspace(4, 6, 8, 10, 16) == 4 * (4 * 10 + 10)
     assert fa.attn_cache_fork_workspace(4, 6, 8, 100, 15) == 0
 
 
