@@ -45,7 +45,7 @@ struct Plans {
 };
 // The lines' items and their tiles, in front of the parts.
 size_t plan_bytes(const Sizes& z) {
-  return ((size_t)z.B + z.groups) * sizeof(attn::tree::Item) + 16;
+  return ((size_t)z.B + z.groups) * sizeof(attn::tree::Item) + 32;
 }
 size_t bytes_of(const Sizes& z, const Plans& x) {
   return plan_bytes(z) + x.parts() * (z.d + 1) * sizeof(float);
@@ -98,11 +98,9 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
   if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
-  if (x.seq.many || x.group.many)
-    return launch(attn::tree::prefix_join_kernel<D, 8>, rows, 256, 0, s, pg, x.group.work, p, x.seq.work, 1);
   const int run = (int)std::clamp<int64_t>(rows / (32 * kPlanSms), 1, 8);  // 32 warps an SM at least
-  return launch(attn::tree::prefix_join_kernel<D, 1>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg, x.group.work, p,
-                x.seq.work, run);
+  return launch(attn::tree::prefix_join_kernel<D>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg,
+                x.any ? x.group.work : x.seq.work, p, x.seq.work, run);
 }
 
 }  // namespace
@@ -188,7 +186,7 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   plan.group_work = x.any ? x.group.work : x.seq.work;
   plan.seq_work = x.seq.work;
   p.items = plan.seq_items;
-  p.line = plan.lines + 1;
+  p.line = plan.lines + 4;
   p.n_items = B;
   attn::tree::Params of_groups = p;
   of_groups.items = plan.group_items;

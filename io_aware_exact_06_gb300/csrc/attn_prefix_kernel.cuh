@@ -15,7 +15,7 @@ namespace tree {
 struct Plan {
   const int *lens, *cu, *groups, *prefix;
   Item *group_items, *seq_items;
-  int* lines;  // tiles of both
+  int* lines;  // of both, four words each: as Params::line
   int B, total, n_groups, H, G, stride, log_page;
   int max_new, max_len, max_group, max_prefix;
   Work group_work, seq_work;
@@ -24,73 +24,89 @@ struct Plan {
 
 constexpr int kPlanThreads = 1024;
 
+// Offsets and prefixes as a plan reads them: from shared memory where they fit.
+struct Offsets {
+  const int *cu, *groups, *prefix;
+};
+
 // The group of sequence b, or -1: the last whose offset is not above b.
-__device__ __forceinline__ int find_group(const Plan& p, int b) {
+__device__ __forceinline__ int find_group(const Plan& p, const Offsets& of, int b) {
   int lo = 0, hi = p.n_groups;  // groups[0 .. lo-1] <= b < groups[hi ..]
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (p.groups[mid] <= b) lo = mid + 1; else hi = mid;
+    if (of.groups[mid] <= b) lo = mid + 1; else hi = mid;
   }
-  return lo > 0 && b < p.groups[lo] ? lo - 1 : -1;
+  return lo > 0 && b < of.groups[lo] ? lo - 1 : -1;
 }
 
 // Shared pages of group g; false if its offsets or its prefix are not what the caller's
 // bounds allow (its sequences are refused then).
-__device__ __forceinline__ bool load_group(const Plan& p, int g, int& pages) {
-  const int s0 = p.groups[g], s1 = p.groups[g + 1], prefix = p.prefix[g];
+__device__ __forceinline__ bool load_group(const Plan& p, const Offsets& of, int g, int& pages) {
+  const int s0 = of.groups[g], s1 = of.groups[g + 1], prefix = of.prefix[g];
   pages = prefix >> p.log_page;
   if (s0 < 0 || s1 < s0 || s1 > p.B || prefix < 0 || prefix > p.max_prefix || pages > p.stride) return false;
-  return (int64_t)p.cu[s1] - p.cu[s0] <= p.max_group;
+  return (int64_t)of.cu[s1] - of.cu[s0] <= p.max_group;
 }
 
 // Its rows are all its sequences' (of one that is refused they are computed and not used).
-__device__ __forceinline__ bool group_item(const Plan& p, int g, Item& x) {
+__device__ __forceinline__ bool group_item(const Plan& p, const Offsets& of, int g, Item& x) {
   int pages = 0;
-  if (!load_group(p, g, pages)) return false;
-  x.at = p.groups[g];
-  x.q0 = max(p.cu[x.at], 0);
-  x.n = max(min(p.cu[p.groups[g + 1]], p.total) - x.q0, 0);
+  if (!load_group(p, of, g, pages)) return false;
+  x.at = of.groups[g];
+  x.q0 = max(of.cu[x.at], 0);
+  x.n = max(min(of.cu[of.groups[g + 1]], p.total) - x.q0, 0);
   x.len = pages << p.log_page;
   x.page0 = -1;
   return true;
 }
 
-__device__ __forceinline__ bool seq_item(const Plan& p, int b, Item& x) {
-  const int q0 = p.cu[b], end = p.cu[b + 1], len = p.lens[b];
+__device__ __forceinline__ bool seq_item(const Plan& p, const Offsets& of, int b, int len, Item& x, int& g) {
+  const int q0 = of.cu[b], end = of.cu[b + 1];
   const int64_t n = (int64_t)end - q0;
   bool fits = (b == 0 ? q0 == 0 : q0 >= 0) && n >= 0 && end <= p.total && n <= p.max_new && len >= n && len <= p.max_len &&
               len <= (int64_t)p.stride << p.log_page;
   int pages = 0;
-  x.group = find_group(p, b);
-  if (x.group >= 0) fits &= load_group(p, x.group, pages);
+  g = find_group(p, of, b);
+  if (g >= 0) fits &= load_group(p, of, g, pages);
   if (!fits || (int64_t)pages << p.log_page > len - n) return false;
   x.q0 = q0, x.n = x.masked = (int)n, x.len = len - (pages << p.log_page), x.at = b, x.page0 = pages;
   return true;
 }
 
+// A line whose segments are padded to whole shares has no share with pieces of two of
+// them: the end of one and the beginning of another (queries, the pipeline's filling, the
+// piece's end) cost about what kCross tiles do.  So it is padded where the units then suffice
+// for shares of at most so many tiles more than even ones.
+constexpr int kCross = 4;
+
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Plan p) {
-  __shared__ int warps[kPlanThreads / 32];
+  __shared__ int warps[kPlanThreads / 32], shares[2][kCross + 1];
+  __shared__ int sm_cu[kPlanThreads + 1], sm_groups[kPlanThreads + 1], sm_prefix[kPlanThreads];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (threadIdx.x < 2 * (kCross + 1)) (&shares[0][0])[threadIdx.x] = 0;
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const bool cu_falls = rows::offsets_fall(p.cu, p.B, threadIdx.x, kPlanThreads);
-  const bool falls = __syncthreads_or(cu_falls || rows::offsets_fall(p.groups, p.n_groups, threadIdx.x, kPlanThreads));
+  Offsets of{p.cu, p.groups, p.prefix};
+  const int first_len = (int)threadIdx.x < p.B ? p.lens[threadIdx.x] : 0;
+  if (p.B <= kPlanThreads) {
+    for (int i = threadIdx.x; i <= p.B; i += kPlanThreads) sm_cu[i] = p.cu[i];
+    of.cu = sm_cu;
+  }
+  if (p.n_groups <= kPlanThreads) {
+    for (int i = threadIdx.x; i <= p.n_groups && p.n_groups > 0; i += kPlanThreads) sm_groups[i] = p.groups[i];
+    if ((int)threadIdx.x < p.n_groups) sm_prefix[threadIdx.x] = p.prefix[threadIdx.x];
+    of.groups = sm_groups, of.prefix = sm_prefix;
+  }
+  __syncthreads();
+  const bool cu_falls = rows::offsets_fall(of.cu, p.B, threadIdx.x, kPlanThreads);
+  const bool falls = __syncthreads_or(cu_falls || rows::offsets_fall(of.groups, p.n_groups, threadIdx.x, kPlanThreads));
   bool bad = falls;
   for (int line = 0; line < 2; ++line) {
-    const int items = line ? p.B : p.n_groups;
+    const int items = falls ? 0 : line ? p.B : p.n_groups;
     const Work& w = line ? p.seq_work : p.group_work;
-    int at = 0;
-    for (int from = 0; from < items && !falls; from += kPlanThreads) {
-      const int i = from + threadIdx.x;
-      Item x{};
-      int tiles = 0;
-      if (i < items) {
-        if (line ? seq_item(p, i, x) : group_item(p, i, x))
-          tiles = (x.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads) * ((x.len + (1 << w.log_tile) - 1) >> w.log_tile);
-        else
-          x.n = x.len = 0, bad = true;
-      }
-      int upto = tiles;  // the whole line is below 2^31 (checked on the host)
+    int at = 0, pad = 1;
+    auto scan = [&](int count) {  // place of this thread's count behind those in front; `at` moves on
+      int upto = count;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, upto, off);
@@ -100,16 +116,50 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       if (lane == 31) warps[warp] = upto;
       __syncthreads();
       const int mine = warps[lane];
-      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
-      x.first = at + before + upto - tiles;
+      const int first = at + __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + upto - count;
       at += __reduce_add_sync(0xffffffffu, mine);
+      return first;
+    };
+    for (int from = 0; from < items; from += kPlanThreads) {
+      const int i = from + threadIdx.x;
+      Item x{};
+      int segs = 0, tiles = 0, g = -1;
+      if (i < items) {
+        if (line ? seq_item(p, of, i, from ? p.lens[i] : first_len, x, g) : group_item(p, of, i, x)) {
+          segs = (x.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
+          tiles = (x.len + (1 << w.log_tile) - 1) >> w.log_tile;
+        } else {
+          x.n = x.len = 0, bad = true;
+        }
+      }
+      x.first = scan(segs * tiles);  // the whole line is below 2^31 (checked on the host)
+      if (items <= kPlanThreads && at > 0) {
+        const int even = max((at - 1) / w.units + 1, w.min_share);
+#pragma unroll
+        for (int c = 0; c <= kCross; ++c) {
+          const int mine = tiles > 0 ? min(segs, w.units + 1) * ((tiles - 1) / (even + c) + 1) : 0;
+          const int sum = __reduce_add_sync(0xffffffffu, min(mine, 1 << 20));
+          if (lane == 0 && sum) atomicAdd(&shares[line][c], sum);
+        }
+        __syncthreads();
+        for (int c = kCross; c >= 0; --c)
+          if (shares[line][c] <= w.units) pad = even + c;
+        if (pad > 1) at = 0, x.first = scan(segs * padded(tiles, pad));
+      }
       if (i < items) {
         int4* to = reinterpret_cast<int4*>((line ? p.seq_items : p.group_items) + i);
         to[0] = make_int4(x.q0, x.n, x.len, x.masked);
-        to[1] = make_int4(x.at, x.page0, x.first, x.group);
+        to[1] = make_int4(x.at, x.page0, x.first, 0);
+        if (line && x.page0 > 0) {  // (the groups' items have been written)
+          const int4* of_group = reinterpret_cast<const int4*>(p.group_items + g);
+          const int4 a = of_group[0], b = of_group[1];
+          to[2] = make_int4(a.x, a.y, a.z, b.z);
+        }
       }
     }
-    if (threadIdx.x == 0) p.lines[line] = at;
+    const int share = pad > 1 ? pad : at > 0 ? share_of(at, w) : 1;
+    if (threadIdx.x == 0) *reinterpret_cast<int4*>(p.lines + 4 * line) = make_int4(at, share, pad, 0);
+    __syncthreads();
   }
   if (bad) atomicOr(p.err, rows::kBadSeqlens);
 }
@@ -127,9 +177,10 @@ struct Pieces {
   }
 };
 
-// Row `row` of key head h, of an item (sq) with `before` tiles in front of it of `total`.
-__device__ __forceinline__ Pieces find_pieces(const Params& p, const Work& w, const Seq<true>& sq, int total, int before,
-                                              int h, int row) {
+// Row `row` of key head h, of an item (sq) with `before` tiles in front of it; line as in
+// Params.
+__device__ __forceinline__ Pieces find_pieces(const Params& p, const Work& w, const Seq<true>& sq, int share, int pad,
+                                              int before, int h, int row) {
   Pieces x{};
   const int tiles = seq_tiles(sq, w);
   if (tiles == 0) return x;
@@ -137,7 +188,7 @@ __device__ __forceinline__ Pieces find_pieces(const Params& p, const Work& w, co
   x.sub = h - group * w.heads;
   const int mtiles = (sq.n * p.G + w.rows - 1) / w.rows, mt = row / w.rows;
   x.r = row - mt * w.rows;
-  const int share = share_of(total, w), first = before + (group * mtiles + mt) * tiles;
+  const int first = before + (group * mtiles + mt) * padded(tiles, pad);
   x.c0 = first / share;
   x.n = (first + tiles - 1) / share - x.c0 + 1;
   x.inside = first != x.c0 * share;
@@ -145,46 +196,45 @@ __device__ __forceinline__ Pieces find_pieces(const Params& p, const Work& w, co
   return x;
 }
 
-// A row, (new token, query head), has one warp, or eight (warp k takes pieces k,
-// k + kPerRow, ..); a warp takes `run` rows one after the other, and looks their
-// sequence and group up once for a token.  Weights are e^(LSE - max), as for the pieces
-// of one line.  Rows of a sequence that the attention refused, and rows that the line of
-// sequences wrote as results, are left as they are.
-template <int D, int kPerRow>
-__global__ void __launch_bounds__(256, kPerRow == 1 ? 4 : 3)
+// A row, (new token, query head), has one warp; a warp takes `run` rows one after the
+// other, and looks their sequence up once for a token.  Weights are e^(LSE - max), as for
+// the pieces of one line.  Rows of a sequence that the attention refused, and rows that
+// the line of sequences wrote as results, are left as they are.
+template <int D>
+__global__ void __launch_bounds__(256, 4)
 prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Work wg, const __grid_constant__ Params p,
                    const __grid_constant__ Work w, int run) {
-  constexpr int kPer = D / 32;
-  __shared__ float sm_sum[8], sm_acc[8][D];
+  constexpr int kPer = D / 32, kBatch = 8;  // pieces on their way at a time
   grid_dep_wait();
   grid_dep_launch();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp % kPerRow;
-  const int64_t all = (int64_t)p.total * p.Hq, row0 = ((int64_t)blockIdx.x * 8 + warp) / kPerRow * run;
-  const int total = *p.line, g_total = *pg.line;
-  if (total == 0) return;  // no sequence has rows (offsets that decrease among them)
-  Seq<true> sq{}, gq{};    // the token's sequence, its group
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t all = (int64_t)p.total * p.Hq, row0 = ((int64_t)blockIdx.x * 8 + warp) * run;
+  if (row0 >= all) return;
+  const int4 line = *reinterpret_cast<const int4*>(p.line), g_line = *reinterpret_cast<const int4*>(pg.line);
+  Seq<true> sq{}, gq{};  // the token's sequence, its group
   int before = 0, g_before = 0;
   auto find = [&](int t) {
     const int b = rows::find_sequence(p.cu, p.B, t);
     if (b >= p.B) return false;
-    int group, none;
-    load_item(p.items + b, sq, before, group);
+    load_item(p.items + b, sq, before);
+    const int4 g = reinterpret_cast<const int4*>(p.items + b)[2];
     if (t < sq.q0 || t >= sq.q0 + sq.n) return false;
     gq.n = gq.len = 0;
-    if (sq.page0 > 0) load_item(pg.items + group, gq, g_before, none);
+    if (sq.page0 > 0) gq.q0 = g.x, gq.n = g.y, gq.len = g.z, g_before = g.w;
     return true;
   };
   bool found = false;
   int at = -1;  // the token looked up
   const int64_t end = min(row0 + run, all);
+  if (line.x == 0) return;  // no sequence has rows (offsets that decrease among them)
 #pragma unroll 1
   for (int64_t rowi = row0; rowi < end; ++rowi) {
     const int t = (int)(rowi / p.Hq), head = (int)(rowi - (int64_t)t * p.Hq);
     const int h = head / p.G, g = head - h * p.G;
     if (t != at) found = find(t), at = t;
     if (!found) continue;
-    const Pieces a = find_pieces(pg, wg, gq, g_total, g_before, h, (t - gq.q0) * p.G + g);
-    const Pieces b = find_pieces(p, w, sq, total, before, h, (t - sq.q0) * p.G + g);
+    const Pieces a = find_pieces(pg, wg, gq, g_line.y, g_line.z, g_before, h, (t - gq.q0) * p.G + g);
+    const Pieces b = find_pieces(p, w, sq, line.y, line.z, before, h, (t - sq.q0) * p.G + g);
     if (b.rows && sq.whole()) continue;  // the result
     const int n = a.n + b.n;
     auto part = [&](int c, const float*& o) {  // piece c: its LSE, and where its row is
@@ -194,60 +244,56 @@ prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Wo
       o = (x.rows ? q.o_row : q.o_part) + i * D;
       return (x.rows ? q.lse_row : q.lse_part) + i;
     };
-    constexpr int kBatch = kPerRow == 1 ? 4 : 8;
-    float x[kBatch][kPer], ls[kBatch];
-    auto load = [&](int from) {
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int c = from + j * kPerRow;
-        ls[j] = -INFINITY;
-        if (c >= n) continue;
-        const float* o;
-        ls[j] = *part(c, o);
-        o += lane * kPer;
-        if (kPer == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(o);
-          x[j][0] = y.x, x[j][1] = y.y, x[j][kPer - 2] = y.z, x[j][kPer - 1] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(o);
-          x[j][0] = y.x, x[j][1] = y.y;
-        }
-      }
-    };
-    load(k);
-    float top = -INFINITY;
-    for (int c = lane; c < n; c += 32) {
-      const float* o;
-      top = fmaxf(top, *part(c, o));
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float acc[kPer], sum = 0.f;
+    // 32 pieces at a time: lane c has the weight of piece c
+    float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    for (int c = k;;) {
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      const int here = min(n - c0, 32);
+      const float* o;
+      const float* mine = part(min(c0 + lane, n - 1), o);
+      const uint64_t where = reinterpret_cast<uint64_t>(o);
+      float x[kBatch][kPer];
+      auto load = [&](int from) {
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (ls[j] == -INFINITY) continue;
-        const float wt = __expf(ls[j] - top);  // a NaN stays one: fmaxf has passed it over
-        sum += wt;
+        for (int j = 0; j < kBatch; ++j) {
+          const int c = min(from + j, here - 1);
+          const float* row = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, where, c)) + lane * kPer;
+          if (kPer == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(row);
+            x[j][0] = y.x, x[j][1] = y.y, x[j][kPer - 2] = y.z, x[j][kPer - 1] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(row);
+            x[j][0] = y.x, x[j][1] = y.y;
+          }
+        }
+      };
+      load(0);
+      const float ls = lane < here ? *mine : -INFINITY;
+      float most = ls;  // a NaN is passed over
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wt, x[j][i], acc[i]);
-      }
-      c += kBatch * kPerRow;
-      if (c >= n) break;
-      load(c);
-    }
-    if (kPerRow > 1) {  // the row's warps are the CTA's
-      if (lane == 0) sm_sum[k] = sum;
+      for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+      most = fmaxf(most, top);
+      // (a first +inf, of a row that is to be NaN, makes every weight 0 or NaN)
+      const float shrink = top == -INFINITY ? 0.f : __expf(top - most);
+      float wt = ls == -INFINITY ? 0.f : __expf(ls - most);
+      top = most;
+      sum *= shrink;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sm_acc[k][lane * kPer + i] = acc[i];
-      __syncthreads();
-      if (k != 0) return;  // (run is 1)
-      for (int j = 1; j < kPerRow; ++j) {
-        sum += sm_sum[j];
+      for (int i = 0; i < kPer; ++i) acc[i] *= shrink;
+      const uint32_t some = __ballot_sync(0xffffffffu, ls != -INFINITY);
+      for (int from = 0;;) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += sm_acc[j][lane * kPer + i];
+        for (int j = 0; j < kBatch; ++j) {
+          const float f = __shfl_sync(0xffffffffu, wt, (from + j) & 31);
+          if (from + j >= here || !((some >> (from + j)) & 1)) continue;  // (what an empty piece holds counts for nothing)
+          sum += f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) acc[i] = fmaf(f, x[j][i], acc[i]);
+        }
+        from += kBatch;
+        if (from >= here) break;
+        load(from);
       }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;

@@ -54,6 +54,19 @@ struct RowsCfg {
                        bQF = bOF + 2, bDrain = bQF + 2, kBars = bDrain + 1;
 };
 
+// Rows `step` apart as tokens and heads of a group of G.
+struct Rows {
+  int row, tok, g, step, dtok, dg, G;
+  __device__ __forceinline__ Rows(int G_, int first, int step_) : row(first), step(step_), G(G_) {
+    tok = row / G, g = row - tok * G;
+    dtok = step / G, dg = step - dtok * G;
+  }
+  __device__ __forceinline__ void next() {
+    row += step, tok += dtok, g += dg;
+    if (g >= G) g -= G, ++tok;
+  }
+};
+
 template <int D, bool kPair>
 struct RowsRole {
   using C = RowsCfg<D, kPair>;
@@ -220,26 +233,22 @@ struct RowsRole {
   template <int kThreads>
   __device__ __forceinline__ void load_queries(const Walk<true>& k, int first, uint32_t to, int thread) {
     constexpr int kCh = D / 8, kPer = kBigRows * kCh / kThreads;  // 16-byte chunks of a row, of a thread
+    constexpr int kStep = kThreads / kCh;                         // rows between them
     const int h = head(k), M = k.s.n * p.G, ch = thread % kCh;
+    const Rows from(p.G, first + thread / kCh, kStep);
     const __nv_bfloat16* base = p.q + (int64_t)k.s.q0 * p.q_ts + (int64_t)h * p.G * D + ch * 8;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      uint4 x[kPer / 2];
+    uint4 x[kPer];
+    Rows at = from;
 #pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) {
-        const int row = first + (thread + (half * (kPer / 2) + i) * kThreads) / kCh;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (row < M) {
-          const int tok = row / p.G;
-          x[i] = *reinterpret_cast<const uint4*>(base + tok * p.q_ts + (int64_t)(row - tok * p.G) * D);
-        }
-      }
+    for (int i = 0; i < kPer; ++i, at.next()) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (at.row < M) x[i] = *reinterpret_cast<const uint4*>(base + at.tok * p.q_ts + (int64_t)at.g * D);
+    }
 #pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) {
-        const int r = (thread + (half * (kPer / 2) + i) * kThreads) / kCh;
-        const uint4 y = no_infinity(x[i]);
-        sts128(to + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), y.x, y.y, y.z, y.w);
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const int r = thread / kCh + i * kStep;
+      const uint4 y = no_infinity(x[i]);
+      sts128(to + (ch / 8) * C::kChunk + swz<128>(r, ch % 8), y.x, y.y, y.z, y.w);
     }
     fence_async_smem();
   }
@@ -386,23 +395,19 @@ struct RowsRole {
       const float inv = ls != 0.f ? 1.f / lo : 0.f;
       const int64_t slot = whole ? -1 : (int64_t)(2 * unit + !firstp) * w.rows + first_row % w.rows;
       float* const part = whole ? p.o_row : p.o_part;
-      // rows 4 i + lane / 8 of this warp, where they go
-      auto place = [&](int row) {
-        const int tok = row / p.G;
-        return whole ? (int64_t)(q0 + tok) * p.Hq + h * p.G + (row - tok * p.G)
-                     : slot + (row - first_row);
+      // where a row goes
+      auto place = [&](const Rows& x) {
+        return whole ? (int64_t)(q0 + x.tok) * p.Hq + h * p.G + x.g : slot + (x.row - first_row);
       };
       if (first_row + r < M && (kPair || g == 0)) {
         float lse = ls != 0.f ? ((mm == -INFINITY ? 0.f : mm * c2) + lg2(ls)) * 0.69314718055994531f : -INFINITY;
         if (poison) lse = INFINITY;  // makes the join of the pieces a NaN row
-        (whole ? p.lse_row : p.lse_part)[place(first_row + r)] = lse;
+        (whole ? p.lse_row : p.lse_part)[place(Rows(p.G, first_row + r, 1))] = lse;
       }
-      int64_t to[8];
+      int64_t to[8];  // of rows 4 i + lane / 8 of this warp
+      Rows x(p.G, first_row + 32 * (warp % 4) + lane / 8, 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = first_row + 32 * (warp % 4) + 4 * i + lane / 8;
-        to[i] = row < M ? place(row) * D : -1;
-      }
+      for (int i = 0; i < 8; ++i, x.next()) to[i] = x.row < M ? place(x) * D : -1;
 #pragma unroll 1
       for (int col = kPair ? 0 : g * (D / 2); col < (kPair ? D : (g + 1) * (D / 2)); col += 32) {
         uint32_t xa[32], xb[32];

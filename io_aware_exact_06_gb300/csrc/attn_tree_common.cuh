@@ -54,7 +54,7 @@ struct Params {
   int* err;
   // shared prefixes: the line's items, written by the kernel before
   const struct Item* items;
-  const int* line;  // tiles of the line
+  const int* line;  // tiles of the line, those of a share, what a segment's are padded to a multiple of
   int n_items;
   float* o_row;     // [total * Hq][D], [total * Hq]: this line's rows whose keys lie in one
   float* lse_row;   // piece (with slots: what is left for the join)
@@ -65,7 +65,8 @@ struct __align__(16) Item {
   int q0, n, len, masked;  // rows q0 .. q0 + n - 1, keys 0 .. len - 1, the last `masked` of them drafts
   int at, page0;           // its row of the page table; its first page there, -1: a group's, from 0 on
   int first;               // tiles of the line in front of it
-  int group;               // of a sequence, or -1
+  int none;
+  int4 group;              // of a sequence that shares pages: its group's q0, n, len, first
 };
 
 // Bytes of a key's (or value's) row of one head, and how TMA boxes cut it.
@@ -191,14 +192,14 @@ __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<false>& s) 
 }
 
 // Item b; its tiles in front in `first`.
-__device__ __forceinline__ void load_item(const Item* item, Seq<true>& s, int& first, int& group) {
+__device__ __forceinline__ void load_item(const Item* item, Seq<true>& s, int& first) {
   const int4 x = reinterpret_cast<const int4*>(item)[0], y = reinterpret_cast<const int4*>(item)[1];
   s.q0 = x.x, s.n = x.y, s.len = x.z, s.masked = x.w, s.at = y.x, s.page0 = y.y;
-  first = y.z, group = y.w;
+  first = y.z;
 }
 __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<true>& s) {
-  int first, group;
-  load_item(p.items + b, s, first, group);
+  int first;
+  load_item(p.items + b, s, first);
   return true;
 }
 

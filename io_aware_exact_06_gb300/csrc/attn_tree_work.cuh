@@ -133,12 +133,12 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   return true;
 }
 
+__device__ __forceinline__ int padded(int tiles, int pad) { return pad > 1 ? (tiles + pad - 1) / pad * pad : tiles; }
 // The same over a line that is laid out: the last item whose first tile is not behind the
 // share's, by 32 probes a step.
 __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool, Walk<true>& walk) {
-  const int lane = threadIdx.x % 32, total = *p.line;
+  const int lane = threadIdx.x % 32, total = p.line[0], share = p.line[1], pad = p.line[2];
   if (total == 0) return false;
-  const int share = share_of(total, w);
   if ((int64_t)share * unit >= total) return false;
   const int first = share * unit;
   int lo = 0, n = p.n_items;  // items 0 .. lo - 1 begin at or in front of it, lo + n .. behind
@@ -152,13 +152,15 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   }
   lo += __popc(__ballot_sync(0xffffffffu, lane < n && p.items[min(lo + lane, p.n_items - 1)].first <= first));
   walk.b = lo - 1;  // items without tiles lie in front of it
-  int before, group;
-  load_item(p.items + walk.b, walk.s, before, group);
+  int before;
+  load_item(p.items + walk.b, walk.s, before);
   walk.segs = seq_segments(p, walk.s, w);
   walk.tiles = seq_tiles(walk.s, w);
-  walk.seg = (first - before) / walk.tiles;
-  walk.tile = first - before - walk.seg * walk.tiles;
+  const int room = padded(walk.tiles, pad);
+  walk.seg = (first - before) / room;
+  walk.tile = first - before - walk.seg * room;
   walk.left = min(share, total - first);
+  if (pad > 1) walk.left = min(walk.left, walk.tiles - walk.tile);  // a share lies in one segment
   return true;
 }
 

@@ -160,7 +160,10 @@ def test_without_groups_it_is_tree_decode(dev):
                               k_scale=c["k_scale"], v_scale=c["v_scale"])
         for groups, prefix in (([0], []), ([0, 1, 3], [0, 15])):
             got = call(dev, c, q, lens, ns, None, groups, prefix)
-            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            # keys are cut into other pieces: each is within its own rounding of fp64 (check), so the two
+            # differ by twice that at most, and not bit for bit
+            check(c, q, lens, ns, None, got)
+            check(c, q, lens, ns, None, want)
     assert fa.attn_last_device_error() == 0
 
 
