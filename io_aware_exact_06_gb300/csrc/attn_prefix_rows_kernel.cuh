@@ -160,7 +160,7 @@ struct RowsRole {
   }
 
   // -------------------------------------------------------------- products --
-  __device__ __forceinline__ void scores(int g, int slot) {
+  __device__ __forceinline__ void scores(uint32_t tmem, uint32_t smem, int g, int slot) {
     const uint32_t d = tmem + 128 * g;
     const uint64_t a = make_sdesc(smem + (kPair ? g * C::kMat : 0), 16, 1024, kSwizzle128B);
     const uint64_t b = make_sdesc(smem + C::kOffRing + slot * C::kMat, 16, 1024, kSwizzle128B);
@@ -170,7 +170,7 @@ struct RowsRole {
       mma_ss(d, a + off, b + off, make_idesc_bf16(128, 128, false), kk > 0);
     }
   }
-  __device__ __forceinline__ void values(int g, int slot, bool accumulate) {
+  __device__ __forceinline__ void values(uint32_t tmem, uint32_t smem, int g, int slot, bool accumulate) {
     const uint64_t b = make_sdesc(smem + C::kOffRing + slot * C::kMat, C::kChunk, 1024, kSwizzle128B);
 #pragma unroll
     for (int kk = 0; kk < kBigTile / 16; ++kk)
@@ -179,15 +179,20 @@ struct RowsRole {
   }
   // One thread issues every product, in the order of the steps (a step is a key tile, or
   // with kPair a key tile of one row tile): S(0), S(1), then for each step j its P V and
-  // S(j + 2).
+  // S(j + 2).  The warp's lanes look at a step's barriers side by side, and what descriptors
+  // are made of is the same in every lane for the compiler to see, so that they are made in
+  // uniform registers: this thread is what the others wait for (a pair of tiles of 2048
+  // cycles of products took it 4100 with lane 0 alone).
   __device__ __forceinline__ void multiply(Walk<true> k) {
-    uint32_t ring = 0;  // position of the piece's first keys; values behind their keys
-    uint32_t pcount[2] = {0, 0};
+    const int lane = threadIdx.x % 32;
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uniform(tmem), base = uniform(smem);
+    int kslot = 0, kround = 0, vslot = 1, vround = 0;  // keys and values take slots by turns
+    uint32_t pcount = 0;                               // parity of the groups' next probabilities
     int seg = 0;
-    auto slot = [&](uint32_t pos) { return (int)(pos % C::kStages); };
-    auto wait_full = [&](uint32_t pos) {
-      wait(C::bFull + slot(pos), (pos / C::kStages) & 1);
-      tc_fence_after();
+    auto advance = [](int& slot, int& round) {
+      slot += 2;
+      if (slot >= C::kStages) slot -= C::kStages, ++round;
     };
     do {
       const int tiles = k.piece(), n = kPair ? 2 * tiles : tiles;
@@ -196,36 +201,42 @@ struct RowsRole {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int step = i + g, j = step - 2;
-          const uint32_t kpos = ring + 2 * (kPair ? i / 2 : step), vpos = ring + 2 * (kPair ? j / 2 : j) + 1;
           const bool first = !kPair || g == 0, last = !kPair || g == 1;  // of a key tile
-          if (j >= 0 && j < n) {
-            if (first) wait_full(vpos);
-            if (first && step < n) wait_full(kpos);  // no wait between a group's products
-            wait(C::bPF + g, pcount[g]++ & 1);
-            tc_fence_after();
-            if (!dead) {
-              values(g, slot(vpos), j > 1);
-              if (last) mma_commit(bar(C::bEmpty + slot(vpos)));
-              if (step >= n) mma_commit(bar(C::bOF + g));
+          const bool pv = j >= 0 && j < n, s = step < n;
+          if (!pv && !s) continue;
+          int on = -1, parity = 0;  // what this lane waits for
+          if (lane == 0 && s && first) on = C::bFull + kslot, parity = kround;
+          if (lane == 1 && pv && first) on = C::bFull + vslot, parity = vround;
+          if (lane == 2 && pv) on = C::bPF + g, parity = pcount >> g;
+          if (lane == 3 && s && step < 2) on = C::bQF + g, parity = seg;
+          if (on >= 0) wait(on, parity & 1);
+          dead = __any_sync(0xffffffffu, dead);
+          tc_fence_after();
+          const int ku = uniform(kslot), vu = uniform(vslot);
+          if (lane == 0 && !dead) {
+            if (pv) {
+              values(tm, base, g, vu, j > 1);
+              if (last) mma_commit(bar(C::bEmpty + vu));
+              if (!s) mma_commit(bar(C::bOF + g));
             }
-          }
-          if (step < n) {
-            if (step < 2) wait(C::bQF + g, seg & 1);
-            if (step < 2 && first) wait_full(kpos);
-            tc_fence_after();
-            if (!dead) {
-              scores(g, slot(kpos));
+            if (s) {
+              scores(tm, base, g, ku);
               mma_commit(bar(C::bSF + g));
-              if (last) mma_commit(bar(C::bEmpty + slot(kpos)));
+              if (last) mma_commit(bar(C::bEmpty + ku));
             }
           }
+          __syncwarp();
+          if (pv) pcount ^= 1u << g;
+          if (pv && last) advance(vslot, vround);
+          if (s && last) advance(kslot, kround);
         }
       }
-      ring += 2 * tiles;
       ++seg;
     } while (next(k));
-    mma_commit(bar(C::bDrain));
-    mbar_wait(bar(C::bDrain), 0, 100000000ull);
+    if (lane == 0) {
+      mma_commit(bar(C::bDrain));
+      mbar_wait(bar(C::bDrain), 0, 100000000ull);
+    }
   }
 
   // --------------------------------------------------------------- softmax --
@@ -499,7 +510,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     if (!any) {
     } else if (warp == 8)
       role.produce(k, &map_k, &map_v);
-    else if (warp == 9 && threadIdx.x % 32 == 0)
+    else if (warp == 9)
       role.multiply(k);
     __syncwarp();
   }
