@@ -216,13 +216,11 @@ struct RowsRole {
           if (lane == 0 && !dead) {
             if (pv) {
               values(tm, base, g, vu, j > 1);
-              if (last) mma_commit(bar(C::bEmpty + vu));
               if (!s) mma_commit(bar(C::bOF + g));
             }
             if (s) {
               scores(tm, base, g, ku);
               mma_commit(bar(C::bSF + g));
-              if (last) mma_commit(bar(C::bEmpty + ku));
             }
           }
           __syncwarp();
@@ -272,7 +270,14 @@ struct RowsRole {
     const float c2 = p.c;
     float* turn = reinterpret_cast<float*>(smem_ptr + C::kOffTurn) + warp * 32 * 32;
     uint32_t scount = 0, ocount[2] = {0, 0};
+    uint32_t ring = 0;  // tiles of the pieces before
     int seg = 0;
+    // The slot of a tile's keys (values: 1) is free for this group.  Its scores' barrier tells
+    // so of the keys, and of the values of its tile before, whose product was issued in front
+    // of the scores: commits of their own would cost the issuing thread 130 cycles each.
+    auto release = [&](int j, int values) {
+      if (threadIdx.x % 128 == 0) mbar_arrive(bar(C::bEmpty + (int)((2 * (ring + j) + values) % C::kStages)));
+    };
     const int unit = (int)blockIdx.x / (w.rows / C::kRows);
     auto bring = [&](const Walk<true>& x) {
       if (kPair)
@@ -290,6 +295,8 @@ struct RowsRole {
       for (int j = kPair ? 0 : g; j < n; j += kPair ? 1 : 2) {
         wait(C::bSF + g, scount++ & 1);
         tc_fence_after();
+        release(j, 0);
+        if (j >= (kPair ? 1 : 2)) release(j - (kPair ? 1 : 2), 1);
         const int keys = len - (k.tile + j) * kBigTile;  // of the prefix, from this tile on
         float s[128], top[2];
         auto read = [&]() {
@@ -384,7 +391,11 @@ struct RowsRole {
       const bool whole = k.tile == 0 && n == k.tiles;
       more = next(k);  // k is the next piece's from here on
       if (kPair && more) bring(k);  // the last S product has read this group's queries
-      if (kPair || n > g) wait(C::bOF + g, ocount[g]++ & 1);
+      if (kPair || n > g) {
+        wait(C::bOF + g, ocount[g]++ & 1);
+        release(kPair ? n - 1 : n - 1 - ((n - 1 - g) & 1), 1);
+      }
+      ring += n;
       if (!kPair) {
         if (n > (g ^ 1)) wait(C::bOF + (g ^ 1), ocount[g ^ 1]++ & 1);
         ss.ml[g][r] = make_float2(m, l);
@@ -475,7 +486,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   };
   if (threadIdx.x == 0) {
     init(C::bFull, C::kStages, 1);
-    init(C::bEmpty, C::kStages, 1);
+    init(C::bEmpty, C::kStages, kPair ? 2 : 1);  // groups that take a tile
     init(C::bSF, 2, 1);
     init(C::bPF, 2, 128);
     init(C::bOF, 2, 1);
