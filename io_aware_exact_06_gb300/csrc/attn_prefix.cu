@@ -98,7 +98,8 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
   if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
-  const int run = (int)std::clamp<int64_t>(rows / (32 * kPlanSms), 1, 8);  // 32 warps an SM at least
+  // 32 warps an SM: all rows at once, while a warp has eight at most
+  const int run = (int)std::clamp<int64_t>((rows + 32 * kPlanSms - 1) / (32 * kPlanSms), 1, 8);
   return launch(attn::tree::prefix_join_kernel<D>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg,
                 x.any ? x.group.work : x.seq.work, p, x.seq.work, run);
 }

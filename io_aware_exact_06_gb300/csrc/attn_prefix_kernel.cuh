@@ -22,7 +22,7 @@ struct Plan {
   int* err;
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 
 // Offsets and prefixes as a plan reads them: from shared memory where they fit.
 struct Offsets {
@@ -84,6 +84,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __shared__ int sm_cu[kPlanThreads + 1], sm_groups[kPlanThreads + 1], sm_prefix[kPlanThreads];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x < 2 * (kCross + 1)) (&shares[0][0])[threadIdx.x] = 0;
+  prefetch(threadIdx.x == 0   ? p.cu
+           : threadIdx.x == 1 ? p.lens
+           : threadIdx.x == 2 ? p.groups
+           : threadIdx.x == 3 ? p.prefix
+           : threadIdx.x == 4 ? p.lines
+                              : nullptr);
   grid_dep_wait();
   grid_dep_launch();
   Offsets of{p.cu, p.groups, p.prefix};
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       __syncthreads();
       if (lane == 31) warps[warp] = upto;
       __syncthreads();
-      const int mine = warps[lane];
+      const int mine = lane < kPlanThreads / 32 ? warps[lane] : 0;
       const int first = at + __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + upto - count;
       at += __reduce_add_sync(0xffffffffu, mine);
       return first;
@@ -135,11 +141,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       x.first = scan(segs * tiles);  // the whole line is below 2^31 (checked on the host)
       if (items <= kPlanThreads && at > 0) {
         const int even = max((at - 1) / w.units + 1, w.min_share);
-#pragma unroll
-        for (int c = 0; c <= kCross; ++c) {
-          const int mine = tiles > 0 ? min(segs, w.units + 1) * ((tiles - 1) / (even + c) + 1) : 0;
-          const int sum = __reduce_add_sync(0xffffffffu, min(mine, 1 << 20));
-          if (lane == 0 && sum) atomicAdd(&shares[line][c], sum);
+        if (from + 32 * warp < items) {
+#pragma unroll 1
+          for (int c = 0; c <= kCross; ++c) {
+            const int mine = tiles > 0 ? min(segs, w.units + 1) * ((tiles - 1) / (even + c) + 1) : 0;
+            const int sum = __reduce_add_sync(0xffffffffu, min(mine, 1 << 20));
+            if (lane == 0 && sum) atomicAdd(&shares[line][c], sum);
+          }
         }
         __syncthreads();
         for (int c = kCross; c >= 0; --c)
@@ -205,11 +213,19 @@ __global__ void __launch_bounds__(256, 4)
 prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Work wg, const __grid_constant__ Params p,
                    const __grid_constant__ Work w, int run) {
   constexpr int kPer = D / 32, kBatch = 8;  // pieces on their way at a time
+  prefetch_line(p);
+  if (threadIdx.x >= 32 && threadIdx.x < 40) {
+    const int t = threadIdx.x - 32;
+    prefetch(t == 0 ? (const void*)pg.o_part : t == 1 ? (const void*)pg.lse_part : t == 2 ? (const void*)pg.o_row
+             : t == 3 ? (const void*)pg.lse_row : t == 4 ? (const void*)p.cu : t == 5 ? (const void*)p.lse : nullptr);
+  }
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t all = (int64_t)p.total * p.Hq, row0 = ((int64_t)blockIdx.x * 8 + warp) * run;
-  if (row0 >= all) return;
+  const int all = p.total * p.Hq;  // a 32-bit number (checked on the host)
+  const int64_t row0_64 = ((int64_t)blockIdx.x * 8 + warp) * run;
+  if (row0_64 >= all) return;
+  const int row0 = (int)row0_64;
   const int4 line = *reinterpret_cast<const int4*>(p.line), g_line = *reinterpret_cast<const int4*>(pg.line);
   Seq<true> sq{}, gq{};  // the token's sequence, its group
   int before = 0, g_before = 0;
@@ -224,17 +240,24 @@ prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Wo
     return true;
   };
   bool found = false;
-  int at = -1;  // the token looked up
-  const int64_t end = min(row0 + run, all);
+  int at = -1, head_at = -1;  // the token looked up, the key head whose pieces a and b are
+  Pieces a{}, b{};
+  const int end = (int)min((int64_t)row0 + run, (int64_t)all);
   if (line.x == 0) return;  // no sequence has rows (offsets that decrease among them)
+  int t = row0 / p.Hq, head = row0 - t * p.Hq - 1;
 #pragma unroll 1
-  for (int64_t rowi = row0; rowi < end; ++rowi) {
-    const int t = (int)(rowi / p.Hq), head = (int)(rowi - (int64_t)t * p.Hq);
-    const int h = head / p.G, g = head - h * p.G;
-    if (t != at) found = find(t), at = t;
+  for (int rowi = row0; rowi < end; ++rowi) {
+    if (++head == p.Hq) head = 0, ++t;
+    if (t != at) found = find(t), at = t, head_at = -1;
     if (!found) continue;
-    const Pieces a = find_pieces(pg, wg, gq, g_line.y, g_line.z, g_before, h, (t - gq.q0) * p.G + g);
-    const Pieces b = find_pieces(p, w, sq, line.y, line.z, before, h, (t - sq.q0) * p.G + g);
+    if (head_at < 0 || head >= (head_at + 1) * p.G || (a.n > 0 && a.r + 1 == wg.rows) || b.r + 1 == w.rows) {
+      const int h = head / p.G, g = head - h * p.G;
+      head_at = h;
+      a = find_pieces(pg, wg, gq, g_line.y, g_line.z, g_before, h, (t - gq.q0) * p.G + g);
+      b = find_pieces(p, w, sq, line.y, line.z, before, h, (t - sq.q0) * p.G + g);
+    } else {
+      ++a.r, ++b.r;
+    }
     if (b.rows && sq.whole()) continue;  // the result
     const int n = a.n + b.n;
     auto part = [&](int c, const float*& o) {  // piece c: its LSE, and where its row is
@@ -297,7 +320,7 @@ prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Wo
       }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    __nv_bfloat16* dst = p.o + rowi * D + lane * kPer;
+    __nv_bfloat16* dst = p.o + (int64_t)rowi * D + lane * kPer;
 #pragma unroll
     for (int i = 0; i < kPer; i += 2)
       *reinterpret_cast<uint32_t*>(dst + i) = sum != 0.f ? rows::pack2(acc[i] * inv, acc[i + 1] * inv) : 0u;

@@ -496,6 +496,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     ss.abort = 0;
     for (int i = 0; i < kFlags; ++i) ss.bad[i] = 0;
   }
+  prefetch_line(p);
   grid_dep_wait();
   grid_dep_launch();
   if (smem_u32(smem_rows) & 1023u) {  // the swizzled tiles would be read askew
@@ -504,6 +505,15 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   }
   Walk<true> k;
   if (!find_place(p, w, blockIdx.x / (w.rows / C::kRows), false, k)) return;  // the whole CTA
+  if (threadIdx.x >= 128) {  // queries, one row to a thread
+    const int row = k.seg % (k.segs / p.H) * w.rows + (int)blockIdx.x % (w.rows / C::kRows) * C::kRows + (int)threadIdx.x - 128;
+    if (row < k.s.n * p.G) {
+      const int tok = row / p.G;
+      const __nv_bfloat16* q = p.q + (int64_t)(k.s.q0 + tok) * p.q_ts + (int64_t)(k.seg / (k.segs / p.H) * p.G + row - tok * p.G) * D;
+      prefetch(q);
+      if (D == 128) prefetch(q + 64);
+    }
+  }
   if (warp == 9) {
     tmem_alloc(smem_u32(&ss.tmem), 512);
     tmem_relinquish();

@@ -191,6 +191,26 @@ __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<false>& s) 
          s.len <= p.max_len && s.len <= (int64_t)p.stride << p.log_page;
 }
 
+// What the first loads will want, asked for while the kernel waits for the one before it:
+// each is the head of a chain of dependent loads, and in a buffer of its own.
+__device__ __forceinline__ void prefetch(const void* p) {
+  if (p) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void prefetch_line(const Params& p) {
+  const int t = threadIdx.x;
+  prefetch(t == 0   ? (const void*)p.items
+           : t == 1 ? (const void*)p.line
+           : t == 2 ? (const void*)p.table
+           : t == 3 ? (const void*)p.q
+           : t == 4 ? (const void*)p.o_part
+           : t == 5 ? (const void*)p.lse_part
+           : t == 6 ? (const void*)p.o_row
+           : t == 7 ? (const void*)p.lse_row
+           : t == 8 ? (const void*)p.mask
+           : t == 9 ? (const void*)p.o
+                    : nullptr);
+}
+
 // Item b; its tiles in front in `first`.
 __device__ __forceinline__ void load_item(const Item* item, Seq<true>& s, int& first) {
   const int4 x = reinterpret_cast<const int4*>(item)[0], y = reinterpret_cast<const int4*>(item)[1];

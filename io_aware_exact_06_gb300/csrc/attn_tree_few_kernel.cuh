@@ -95,12 +95,20 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     hidden[0] = hidden[1] = 0;
   }
   __syncwarp();
+  if (kShared) prefetch_line(p);
   grid_dep_wait();
   grid_dep_launch();
   const int units = kWarps / w.heads;  // of the CTA
   const int unit = blockIdx.x * units + warp / w.heads, sub = warp % w.heads;
   Walk<kShared> wk;
   if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) return;
+  if (kShared) {  // the first piece's queries, beside the copies
+    const int r = wk.seg / (wk.segs / (p.H / w.heads)), row = (wk.seg - r * (wk.segs / (p.H / w.heads))) * kRows + lane / 4;
+    if (row < wk.s.n * p.G) {
+      const int tok = row / p.G;
+      prefetch(p.q + (int64_t)(wk.s.q0 + tok) * p.q_ts + (int64_t)((r * w.heads + sub) * p.G + row - tok * p.G) * D + lane % 4 * (D / 4));
+    }
+  }
   bool expired = false;  // a wait ran out: nothing more is copied, the rows come out as NaN
 
   // ------------------------------------------------------- the warp's copies --

@@ -903,6 +903,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   static_assert(big_smem<D, kCodes, kPair>() <= 227 * 1024, "shared memory");
   BigShared& ss = *reinterpret_cast<BigShared*>(smem_big + C::kOffShared);
   const int warp = threadIdx.x / 32;
+  if (kShared) prefetch_line(p);
   grid_dep_wait();
   grid_dep_launch();
   if (smem_u32(smem_big) & 1023u) {  // the swizzled tiles would be read askew
