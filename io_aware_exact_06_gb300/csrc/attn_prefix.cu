@@ -1,7 +1,7 @@
 // Host side of attn_fwd_prefix (include/attn_cache.h): attention over the paged cache
-// for sequences whose first pages are shared.  Two lines of work, one after the other:
-// every group's rows over its shared pages, then every sequence's over its own.  A first
-// kernel lays them out, a last one joins the rows' parts.  It keeps no workspace in the library.
+// for sequences whose first pages are shared.  Two lines of work at a time, each on SMs of
+// its own: every sequence's rows over its own pages, and every group's over its shared
+// ones.  A first kernel lays them out, a last one joins the rows' parts.  It keeps no workspace in the library.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +34,16 @@ int check_sizes(const Sizes& z) {
 }
 
 bool empty(const Sizes& z) { return z.B == 0 || z.total == 0 || z.max_new == 0; }
+
+// What a CTA takes for a tile of a line, in ns (d = 128; measured alone on an SM but for the
+// few-row kernel, which is given 55 GB/s of an SM's share of HBM).
+float tile_cost(const Plan& pl, int d, bool codes, bool rows_kernel) {
+  const float wide = d == 128 ? 1.f : 0.9f;
+  if (few(pl)) return attn::tree::kFewTile * pl.work.heads * 2.f * d * (codes ? 1 : 2) / 55.f;
+  const bool pair = pl.rows > attn::tree::kBigRows;
+  if (rows_kernel) return wide * (pair ? 1700.f : 950.f);
+  return wide * (pair ? 2300.f : 1400.f);
+}
 
 // The line of groups, the line of sequences, and the parts of the workspace: slots of
 // both, and the rows of both that are not cut.
@@ -70,10 +80,10 @@ Plans plans(const Sizes& z, int page, bool codes) {
   const int most = std::min(z.max_group, z.total);
   x.any = z.groups > 0 && most > 0 && z.max_prefix >= page;
   if (x.any) {
-    x.group = tree_plan(z.groups, z.total, z.Hq, z.H, z.d, most, z.max_prefix, z.splits, codes);
+    x.group = tree_plan(z.groups, z.total, z.Hq, z.H, z.d, most, z.max_prefix, z.splits, codes, true);
     if (!codes && !few(x.group)) make_teams(x.group, ((int64_t)most * (z.Hq / z.H) + x.group.rows - 1) / x.group.rows);
   }
-  x.seq = tree_plan(z.B, z.total, z.Hq, z.H, z.d, z.max_new, z.max_len, z.splits, codes);
+  x.seq = tree_plan(z.B, z.total, z.Hq, z.H, z.d, z.max_new, z.max_len, z.splits, codes, true);
   return x;
 }
 
@@ -95,8 +105,10 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
                   const attn::tree::Params& p, cudaStream_t s) {
   int st = launch(attn::tree::prefix_plan_kernel, 1, attn::tree::kPlanThreads, 0, s, plan);
   if (st != ATTN_OK) return st;
-  if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
+  // The second line starts as soon as every CTA of the first runs, without waiting for it
+  // (what it reads was there before the first began), and ends after it.
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
+  if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
   // 32 warps an SM: all rows at once, while a warp has eight at most
   const int run = (int)std::clamp<int64_t>((rows + 32 * kPlanSms - 1) / (32 * kPlanSms), 1, 8);
@@ -186,6 +198,13 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   plan.max_prefix = max_prefix;
   plan.group_work = x.any ? x.group.work : x.seq.work;
   plan.seq_work = x.seq.work;
+  const bool rows_kernel = x.any && !codes && !few(x.group);
+  const int team = rows_kernel ? x.group.work.rows / x.group.rows : 1;
+  auto per_cta = [](const Plan& pl) { return few(pl) ? attn::tree::kSharedWarps / pl.work.heads : 1; };
+  plan.seq_cta = per_cta(x.seq);
+  plan.group_cta = !x.any ? 1 : team > 1 ? -team : per_cta(x.group);
+  plan.seq_cost = tile_cost(x.seq, d, codes, false);
+  plan.group_cost = x.any ? team * tile_cost(x.group, d, codes, rows_kernel) : 0.f;
   p.items = plan.seq_items;
   p.line = plan.lines + 4;
   p.n_items = B;
@@ -193,6 +212,7 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   of_groups.items = plan.group_items;
   of_groups.line = plan.lines;
   of_groups.n_items = groups;
+  of_groups.second = true;
   float* at = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(z));
   float* lse_at = at + x.parts() * d;
   auto take = [&](size_t rows, float*& o_part, float*& lse_part) {

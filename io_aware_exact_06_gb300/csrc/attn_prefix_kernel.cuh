@@ -19,10 +19,13 @@ struct Plan {
   int B, total, n_groups, H, G, stride, log_page;
   int max_new, max_len, max_group, max_prefix;
   Work group_work, seq_work;
+  int group_cta, seq_cta;      // units of a CTA; negative: CTAs of a unit
+  float group_cost, seq_cost;  // of a tile, as time of a CTA
   int* err;
 };
 
 constexpr int kPlanThreads = 256;
+constexpr int kSms = 152;  // GB300
 
 // Offsets and prefixes as a plan reads them: from shared memory where they fit.
 struct Offsets {
@@ -80,7 +83,7 @@ __device__ __forceinline__ bool seq_item(const Plan& p, const Offsets& of, int b
 constexpr int kCross = 4;
 
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Plan p) {
-  __shared__ int warps[kPlanThreads / 32], shares[2][kCross + 1];
+  __shared__ int warps[2][kPlanThreads / 32], shares[2][kCross + 1];
   __shared__ int sm_cu[kPlanThreads + 1], sm_groups[kPlanThreads + 1], sm_prefix[kPlanThreads];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x < 2 * (kCross + 1)) (&shares[0][0])[threadIdx.x] = 0;
@@ -107,67 +110,108 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   const bool cu_falls = rows::offsets_fall(of.cu, p.B, threadIdx.x, kPlanThreads);
   const bool falls = __syncthreads_or(cu_falls || rows::offsets_fall(of.groups, p.n_groups, threadIdx.x, kPlanThreads));
   bool bad = falls;
-  for (int line = 0; line < 2; ++line) {
-    const int items = falls ? 0 : line ? p.B : p.n_groups;
-    const Work& w = line ? p.seq_work : p.group_work;
-    int at = 0, pad = 1;
-    auto scan = [&](int count) {  // place of this thread's count behind those in front; `at` moves on
-      int upto = count;
+  // Places of this thread's counts behind those in front, in both lines; `at` moves on.
+  auto scan = [&](int2 count, int2& at) {
+    int2 upto = count;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += v;
-      }
-      __syncthreads();
-      if (lane == 31) warps[warp] = upto;
-      __syncthreads();
-      const int mine = lane < kPlanThreads / 32 ? warps[lane] : 0;
-      const int first = at + __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + upto - count;
-      at += __reduce_add_sync(0xffffffffu, mine);
-      return first;
-    };
-    for (int from = 0; from < items; from += kPlanThreads) {
-      const int i = from + threadIdx.x;
-      Item x{};
-      int segs = 0, tiles = 0, g = -1;
-      if (i < items) {
-        if (line ? seq_item(p, of, i, from ? p.lens[i] : first_len, x, g) : group_item(p, of, i, x)) {
-          segs = (x.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads);
-          tiles = (x.len + (1 << w.log_tile) - 1) >> w.log_tile;
-        } else {
-          x.n = x.len = 0, bad = true;
-        }
-      }
-      x.first = scan(segs * tiles);  // the whole line is below 2^31 (checked on the host)
-      if (items <= kPlanThreads && at > 0) {
-        const int even = max((at - 1) / w.units + 1, w.min_share);
-        if (from + 32 * warp < items) {
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto.x, off), y = __shfl_up_sync(0xffffffffu, upto.y, off);
+      if (lane >= off) upto.x += x, upto.y += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[0][warp] = upto.x, warps[1][warp] = upto.y;
+    __syncthreads();
+    const bool has = lane < kPlanThreads / 32;
+    const int x = has ? warps[0][lane] : 0, y = has ? warps[1][lane] : 0;
+    const int2 first = make_int2(at.x + __reduce_add_sync(0xffffffffu, lane < warp ? x : 0) + upto.x - count.x,
+                                 at.y + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) + upto.y - count.y);
+    at.x += __reduce_add_sync(0xffffffffu, x), at.y += __reduce_add_sync(0xffffffffu, y);
+    return first;
+  };
+  auto segments = [&](const Item& x, const Work& w) { return (x.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads); };
+  auto tiles_of = [&](const Item& x, const Work& w) { return (x.len + (1 << w.log_tile) - 1) >> w.log_tile; };
+  // Thread i has group i and sequence i, and those kPlanThreads further on.  (Lines of up
+  // to kPlanThreads items may be padded; their items stay in registers.)
+  const int most = max(p.B, p.n_groups);
+  int2 at = make_int2(0, 0), pad = make_int2(1, 1);
+  Item gi{}, si{};
+  int2 segs{}, tiles{}, first{};
+  int g = -1;
+  auto load = [&](int i) {
+    gi = Item{}, si = Item{};
+    segs = tiles = make_int2(0, 0);
+    if (i < p.n_groups) {
+      if (group_item(p, of, i, gi))
+        segs.x = segments(gi, p.group_work), tiles.x = tiles_of(gi, p.group_work);
+      else
+        gi.n = gi.len = 0, bad = true;
+    }
+    if (i < p.B) {
+      if (seq_item(p, of, i, i < kPlanThreads ? first_len : p.lens[i], si, g))
+        segs.y = segments(si, p.seq_work), tiles.y = tiles_of(si, p.seq_work);
+      else
+        si.n = si.len = 0, bad = true;
+    }
+  };
+  for (int from = 0; from < most && !falls; from += kPlanThreads) {  // (the whole lines are below 2^31: checked on the host)
+    load(from + threadIdx.x);
+    scan(make_int2(segs.x * tiles.x, segs.y * tiles.y), at);
+  }
+  // The SMs go to the lines as their tiles cost.
+  const float group_all = at.x * p.group_cost, seq_all = at.y * p.seq_cost;
+  int sms = 0;  // of the line of groups
+  if (at.x > 0) {
+    const int team = max(-p.group_cta, 1);
+    sms = at.y > 0 ? (int)(kSms * (group_all / (group_all + seq_all)) + 0.5f) : kSms;
+    sms = min(max(sms / team * team, team), at.y > 0 ? kSms - 1 : kSms);
+  }
+  auto units_of = [&](int ctas, int per_cta, const Work& w) {
+    return max(1, min(w.units, per_cta < 0 ? ctas / -per_cta : ctas * per_cta));
+  };
+  const int2 units = make_int2(units_of(sms, p.group_cta, p.group_work), units_of(kSms - sms, p.seq_cta, p.seq_work));
+  int2 share = make_int2(at.x > 0 ? max((at.x - 1) / units.x + 1, p.group_work.min_share) : 1,
+                         at.y > 0 ? max((at.y - 1) / units.y + 1, p.seq_work.min_share) : 1);
+  if (most <= kPlanThreads) {
+    if (32 * warp < most) {
 #pragma unroll 1
-          for (int c = 0; c <= kCross; ++c) {
-            const int mine = tiles > 0 ? min(segs, w.units + 1) * ((tiles - 1) / (even + c) + 1) : 0;
-            const int sum = __reduce_add_sync(0xffffffffu, min(mine, 1 << 20));
-            if (lane == 0 && sum) atomicAdd(&shares[line][c], sum);
-          }
-        }
-        __syncthreads();
-        for (int c = kCross; c >= 0; --c)
-          if (shares[line][c] <= w.units) pad = even + c;
-        if (pad > 1) at = 0, x.first = scan(segs * padded(tiles, pad));
-      }
-      if (i < items) {
-        int4* to = reinterpret_cast<int4*>((line ? p.seq_items : p.group_items) + i);
-        to[0] = make_int4(x.q0, x.n, x.len, x.masked);
-        to[1] = make_int4(x.at, x.page0, x.first, 0);
-        if (line && x.page0 > 0) {  // (the groups' items have been written)
-          const int4* of_group = reinterpret_cast<const int4*>(p.group_items + g);
-          const int4 a = of_group[0], b = of_group[1];
-          to[2] = make_int4(a.x, a.y, a.z, b.z);
-        }
+      for (int c = 0; c <= kCross; ++c) {
+        const int x = tiles.x > 0 ? min(segs.x, kSms * 8 + 1) * ((tiles.x - 1) / (share.x + c) + 1) : 0;
+        const int y = tiles.y > 0 ? min(segs.y, kSms * 8 + 1) * ((tiles.y - 1) / (share.y + c) + 1) : 0;
+        const int sx = __reduce_add_sync(0xffffffffu, min(x, 1 << 20)), sy = __reduce_add_sync(0xffffffffu, min(y, 1 << 20));
+        if (lane == 0 && sx) atomicAdd(&shares[0][c], sx);
+        if (lane == 0 && sy) atomicAdd(&shares[1][c], sy);
       }
     }
-    const int share = pad > 1 ? pad : at > 0 ? share_of(at, w) : 1;
-    if (threadIdx.x == 0) *reinterpret_cast<int4*>(p.lines + 4 * line) = make_int4(at, share, pad, 0);
     __syncthreads();
+    for (int c = kCross; c >= 0; --c) {
+      if (shares[0][c] <= units.x) pad.x = share.x + c;
+      if (shares[1][c] <= units.y) pad.y = share.y + c;
+    }
+    if (pad.x > 1) share.x = pad.x;
+    if (pad.y > 1) share.y = pad.y;
+  }
+  at = make_int2(0, 0);
+  for (int from = 0; from < most && !falls; from += kPlanThreads) {
+    const int i = from + threadIdx.x;
+    if (most > kPlanThreads) load(i);
+    first = scan(make_int2(segs.x * padded(tiles.x, pad.x), segs.y * padded(tiles.y, pad.y)), at);
+    auto write = [&](Item* to, const Item& x, int front) {
+      reinterpret_cast<int4*>(to)[0] = make_int4(x.q0, x.n, x.len, x.masked);
+      reinterpret_cast<int4*>(to)[1] = make_int4(x.at, x.page0, front, 0);
+    };
+    if (i < p.n_groups) write(p.group_items + i, gi, first.x);
+    if (i < p.B) write(p.seq_items + i, si, first.y);
+  }
+  __syncthreads();  // all groups are laid out: their sequences' items take them up
+  for (int i = threadIdx.x; i < p.B && !falls; i += kPlanThreads) {
+    if (most > kPlanThreads) load(i);
+    if (si.page0 <= 0) continue;
+    const int4 *of_group = reinterpret_cast<const int4*>(p.group_items + g), a = of_group[0], b = of_group[1];
+    reinterpret_cast<int4*>(p.seq_items + i)[2] = make_int4(a.x, a.y, a.z, b.z);
+  }
+  if (threadIdx.x == 0) {
+    reinterpret_cast<int4*>(p.lines)[0] = make_int4(at.x, share.x, pad.x, 0);
+    reinterpret_cast<int4*>(p.lines)[1] = make_int4(at.y, share.y, pad.y, 0);
   }
   if (bad) atomicOr(p.err, rows::kBadSeqlens);
 }

@@ -52,10 +52,11 @@ struct Params {
   int max_new, max_len;
   float c;  // scale * log2 e (at least the smallest normal float)
   int* err;
-  // shared prefixes: the line's items, written by the kernel before
+  // shared prefixes: the line's items, written by a kernel before
   const struct Item* items;
   const int* line;  // tiles of the line, those of a share, what a segment's are padded to a multiple of
   int n_items;
+  bool second;      // launched beside the other line's kernel, which it waits for at its end
   float* o_row;     // [total * Hq][D], [total * Hq]: this line's rows whose keys lie in one
   float* lse_row;   // piece (with slots: what is left for the join)
 };

@@ -33,6 +33,10 @@ namespace tree {
 // producer warp for the CTA instead spent about 1000 cycles on a 32-key tile's
 // issue, against 365 that HBM needs for the tiles of twelve warps.)
 constexpr int kWarps = 4;     // of a CTA
+// Over shared prefixes a CTA has an SM for itself, so that two lines of work can have SMs
+// of their own at a time.
+constexpr int kSharedWarps = 8;
+__host__ __device__ constexpr int few_warps(bool shared) { return shared ? kSharedWarps : kWarps; }
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
@@ -47,8 +51,9 @@ __host__ __device__ constexpr int few_ctas(int d, bool codes) { return d == 64 &
 __host__ __device__ constexpr int few_bound(int d, bool codes) { return (d == 128) != codes ? 3 : 2; }
 constexpr int kFewRing = 16384;  // bytes of a warp's stages (24576: d = 64 bf16 135 us against 129)
 
-template <int D, bool kCodes, int kNT>
+template <int D, bool kCodes, int kNT, bool kShared>
 struct FewCfg : Row<D, kCodes> {
+  static constexpr int kWarps = few_warps(kShared);
   using Row<D, kCodes>::kRowBytes;
   static constexpr int kMatBytes = kFewTile * kRowBytes;
   static constexpr int kScaleBytes = kCodes ? kFewTile * 4 : 0;
@@ -69,10 +74,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 template <int D, bool kCodes, int kNT, bool kShared>
-__global__ void __launch_bounds__(kFewThreads, few_bound(D, kCodes))
+__global__ void __launch_bounds__(32 * few_warps(kShared), kShared ? 1 : few_bound(D, kCodes))
 tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ Params p, const __grid_constant__ Work w) {
-  using C = FewCfg<D, kCodes, kNT>;
+  using C = FewCfg<D, kCodes, kNT, kShared>;
+  constexpr int kWarps = C::kWarps;
   constexpr int kQ = D / 16;  // k-steps of the score product
   constexpr int kMT = D / 16;  // 16-column tiles of the output
   constexpr int kHH = D / 64;  // 16-byte chunks of a lane's codes
@@ -96,12 +102,15 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   }
   __syncwarp();
   if (kShared) prefetch_line(p);
-  grid_dep_wait();
+  if (!(kShared && p.second)) grid_dep_wait();
   grid_dep_launch();
   const int units = kWarps / w.heads;  // of the CTA
   const int unit = blockIdx.x * units + warp / w.heads, sub = warp % w.heads;
   Walk<kShared> wk;
-  if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) return;
+  if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) {
+    if (kShared && p.second) grid_dep_wait();  // complete only after the other line
+    return;
+  }
   if (kShared) {  // the first piece's queries, beside the copies
     const int r = wk.seg / (wk.segs / (p.H / w.heads)), row = (wk.seg - r * (wk.segs / (p.H / w.heads))) * kRows + lane / 4;
     if (row < wk.s.n * p.G) {
@@ -464,6 +473,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     while (globaltimer_ns() - t0 < 1000000ull) {
     }
   }
+  if (kShared && p.second) grid_dep_wait();
 }
 
 }  // namespace tree

@@ -26,7 +26,8 @@ inline bool few(const Plan& pl) { return pl.rows <= 16; }
 // 4096 keys: d = 128 bf16 104 : 82, e4m3 69 : 84, d = 64 52 : 63 and 54 : 75; 16 rows,
 // 64 sequences of 8192 keys: d = 128 bf16 284 : 254, e4m3 192 : 247).  num_splits caps
 // the pieces of a segment instead.
-inline Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, bool codes) {
+inline Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int max_len, int num_splits, bool codes,
+                      bool shared = false) {
   Plan pl{};
   const int64_t M = (int64_t)max_new * (Hq / H);
   constexpr int kBig = attn::tree::kBigRows;
@@ -35,19 +36,19 @@ inline Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int m
   const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
   const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
   const int64_t segments = (int64_t)B * (H / heads) * ((M + pl.rows - 1) / pl.rows);
-  const int per_cta = few(pl) ? attn::tree::kWarps / heads : 1;
+  const int per_cta = few(pl) ? attn::tree::few_warps(shared) / heads : 1;
   pl.work.rows = pl.rows;
   pl.work.heads = heads;
   pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
   pl.work.min_share = num_splits > 0 ? (int)((tiles + num_splits - 1) / num_splits) : 1;
   const int64_t most = (int64_t)std::min((double)segments * (double)tiles / pl.work.min_share + 1, 1e9);
-  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) ? attn::tree::few_ctas(d, codes) : 1));
+  pl.ctas = std::min<int64_t>((most + per_cta - 1) / per_cta, kPlanSms * (few(pl) && !shared ? attn::tree::few_ctas(d, codes) : 1));
   pl.work.units = (int)(pl.ctas * per_cta);
   pl.slots = 2 * (int64_t)pl.work.units * heads;
   // eight warps to a row where segments are cut into many pieces, and where the
   // rows leave the SMs idle anyway
   pl.many = pl.work.units > 32 * segments || (int64_t)total * Hq <= 8 * kPlanSms;
-  pl.fits = (double)segments * (double)tiles <= INT32_MAX;
+  pl.fits = (double)segments * (double)tiles <= INT32_MAX - (shared ? 1 << 16 : 0);  // (segments may be padded)
   return pl;
 }
 
@@ -73,13 +74,13 @@ int launch_line(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
                 : pl.rows == 16       ? tree_few_kernel<D, kCodes, kTwo, kShared>
                 : pl.rows == kBigRows ? tree_tile_kernel<D, kCodes, false, kShared>
                                       : tree_tile_kernel<D, kCodes, true, kShared>;
-  const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1>::kSmem
-                   : pl.rows == 16       ? FewCfg<D, kCodes, kTwo>::kSmem
+  const int smem = pl.rows == 8          ? FewCfg<D, kCodes, 1, kShared>::kSmem
+                   : pl.rows == 16       ? FewCfg<D, kCodes, kTwo, kShared>::kSmem
                    : pl.rows == kBigRows ? big_smem<D, kCodes, false>()
                                          : big_smem<D, kCodes, true>();
   const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != ATTN_OK) return st;
-  return launch(kernel, pl.ctas, few(pl) ? kFewThreads : kBigThreads, smem, s, mk, mv, p, pl.work);
+  return launch(kernel, pl.ctas, few(pl) ? 32 * few_warps(kShared) : kBigThreads, smem, s, mk, mv, p, pl.work);
 }
 
 }  // namespace attn_serve
