@@ -39,10 +39,10 @@ bool empty(const Sizes& z) { return z.B == 0 || z.total == 0 || z.max_new == 0; 
 // few-row kernel, which is given 55 GB/s of an SM's share of HBM).
 float tile_cost(const Plan& pl, int d, bool codes, bool rows_kernel) {
   const float wide = d == 128 ? 1.f : 0.9f;
-  if (few(pl)) return attn::tree::kFewTile * pl.work.heads * 2.f * d * (codes ? 1 : 2) / 55.f;
+  if (few(pl)) return 2700.f * pl.work.heads / attn::tree::few_warps(true, pl.rows);
   const bool pair = pl.rows > attn::tree::kBigRows;
-  if (rows_kernel) return wide * (pair ? 1700.f : 950.f);
-  return wide * (pair ? 2300.f : 1400.f);
+  if (rows_kernel) return wide * (pair ? 1900.f : 1100.f);
+  return wide * (pair ? 2300.f : 2000.f);
 }
 
 // The line of groups, the line of sequences, and the parts of the workspace: slots of
@@ -200,7 +200,7 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   plan.seq_work = x.seq.work;
   const bool rows_kernel = x.any && !codes && !few(x.group);
   const int team = rows_kernel ? x.group.work.rows / x.group.rows : 1;
-  auto per_cta = [](const Plan& pl) { return few(pl) ? attn::tree::kSharedWarps / pl.work.heads : 1; };
+  auto per_cta = [](const Plan& pl) { return few(pl) ? attn::tree::few_warps(true, pl.rows) / pl.work.heads : 1; };
   plan.seq_cta = per_cta(x.seq);
   plan.group_cta = !x.any ? 1 : team > 1 ? -team : per_cta(x.group);
   plan.seq_cost = tile_cost(x.seq, d, codes, false);

@@ -34,9 +34,8 @@ namespace tree {
 // issue, against 365 that HBM needs for the tiles of twelve warps.)
 constexpr int kWarps = 4;     // of a CTA
 // Over shared prefixes a CTA has an SM for itself, so that two lines of work can have SMs
-// of their own at a time.
-constexpr int kSharedWarps = 8;
-__host__ __device__ constexpr int few_warps(bool shared) { return shared ? kSharedWarps : kWarps; }
+// of their own at a time: as many warps as its registers and shared memory hold.
+__host__ __device__ constexpr int few_warps(bool shared, int rows) { return !shared ? kWarps : rows == 8 ? 12 : 8; }
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
 constexpr int kFewThreads = 32 * kWarps;
@@ -53,7 +52,7 @@ constexpr int kFewRing = 16384;  // bytes of a warp's stages (24576: d = 64 bf16
 
 template <int D, bool kCodes, int kNT, bool kShared>
 struct FewCfg : Row<D, kCodes> {
-  static constexpr int kWarps = few_warps(kShared);
+  static constexpr int kWarps = few_warps(kShared, 8 * kNT);
   using Row<D, kCodes>::kRowBytes;
   static constexpr int kMatBytes = kFewTile * kRowBytes;
   static constexpr int kScaleBytes = kCodes ? kFewTile * 4 : 0;
@@ -74,7 +73,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 template <int D, bool kCodes, int kNT, bool kShared>
-__global__ void __launch_bounds__(32 * few_warps(kShared), kShared ? 1 : few_bound(D, kCodes))
+__global__ void __launch_bounds__(32 * few_warps(kShared, 8 * kNT), kShared ? 1 : few_bound(D, kCodes))
 tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ Params p, const __grid_constant__ Work w) {
   using C = FewCfg<D, kCodes, kNT, kShared>;

@@ -36,7 +36,7 @@ inline Plan tree_plan(int B, int total, int Hq, int H, int d, int max_new, int m
   const int64_t tiles = (std::max<int64_t>(max_len, 1) + T - 1) / T;
   const int heads = !few(pl) ? 1 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;  // of a segment, one a warp
   const int64_t segments = (int64_t)B * (H / heads) * ((M + pl.rows - 1) / pl.rows);
-  const int per_cta = few(pl) ? attn::tree::few_warps(shared) / heads : 1;
+  const int per_cta = few(pl) ? attn::tree::few_warps(shared, pl.rows) / heads : 1;
   pl.work.rows = pl.rows;
   pl.work.heads = heads;
   pl.work.log_tile = few(pl) ? attn::tree::kLogFewTile : attn::tree::kLogBigTile;
@@ -80,7 +80,7 @@ int launch_line(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, co
                                          : big_smem<D, kCodes, true>();
   const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != ATTN_OK) return st;
-  return launch(kernel, pl.ctas, few(pl) ? 32 * few_warps(kShared) : kBigThreads, smem, s, mk, mv, p, pl.work);
+  return launch(kernel, pl.ctas, few(pl) ? 32 * few_warps(kShared, pl.rows) : kBigThreads, smem, s, mk, mv, p, pl.work);
 }
 
 }  // namespace attn_serve
