@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   if (most <= kPlanThreads) {
     if (32 * warp < most) {
 #pragma unroll 1
-      for (int c = 0; c <= kCross; ++c) {
+      for (int c = 0; c <= kCross; c += 2) {
         const int x = tiles.x > 0 ? min(segs.x, kSms * 8 + 1) * ((tiles.x - 1) / (share.x + c) + 1) : 0;
         const int y = tiles.y > 0 ? min(segs.y, kSms * 8 + 1) * ((tiles.y - 1) / (share.y + c) + 1) : 0;
         const int sx = __reduce_add_sync(0xffffffffu, min(x, 1 << 20)), sy = __reduce_add_sync(0xffffffffu, min(y, 1 << 20));
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       }
     }
     __syncthreads();
-    for (int c = kCross; c >= 0; --c) {
+    for (int c = kCross; c >= 0; c -= 2) {
       if (shares[0][c] <= units.x) pad.x = share.x + c;
       if (shares[1][c] <= units.y) pad.y = share.y + c;
     }

@@ -496,16 +496,16 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     ss.abort = 0;
     for (int i = 0; i < kFlags; ++i) ss.bad[i] = 0;
   }
-  if (!p.second) grid_dep_wait();
+  begin_line(p);
   grid_dep_launch();
   if (smem_u32(smem_rows) & 1023u) {  // the swizzled tiles would be read askew
     if (threadIdx.x == 0) atomicOr(p.err, kTimedOut);
-    if (p.second) grid_dep_wait();
+    end_line(p);
     return;
   }
   Walk<true> k;
   if (!find_place(p, w, blockIdx.x / (w.rows / C::kRows), false, k)) {  // the whole CTA
-    if (p.second) grid_dep_wait();  // complete only after the other line
+    end_line(p);
     return;
   }
   if (threadIdx.x >= 128) {  // queries, one row to a thread
@@ -549,7 +549,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     tc_fence_after();
     tmem_dealloc(ss.tmem, 512);
   }
-  if (p.second) grid_dep_wait();
+  end_line(p);
 }
 
 }  // namespace tree

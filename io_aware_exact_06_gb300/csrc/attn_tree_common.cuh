@@ -197,6 +197,19 @@ __device__ __forceinline__ bool load_seq(const Params& p, int b, Seq<false>& s) 
 __device__ __forceinline__ void prefetch(const void* p) {
   if (p) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
+// The start and the end of a line's kernel.  The second line's starts beside the first's:
+// what the kernels before those wrote is in L2 by then (the first has waited for them before
+// it let the second start), and the fence keeps the SM's L1 from answering with what it held
+// of it before.  It completes only after the first line's.
+__device__ __forceinline__ void begin_line(const Params& p) {
+  if (p.second)
+    __threadfence();
+  else
+    grid_dep_wait();
+}
+__device__ __forceinline__ void end_line(const Params& p) {
+  if (p.second) grid_dep_wait();
+}
 __device__ __forceinline__ void prefetch_line(const Params& p) {
   const int t = threadIdx.x;
   prefetch(t == 0   ? (const void*)p.items

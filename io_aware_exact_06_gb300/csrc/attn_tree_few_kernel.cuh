@@ -101,13 +101,16 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
   }
   __syncwarp();
   if (kShared) prefetch_line(p);
-  if (!(kShared && p.second)) grid_dep_wait();
+  if (kShared)
+    begin_line(p);
+  else
+    grid_dep_wait();
   grid_dep_launch();
   const int units = kWarps / w.heads;  // of the CTA
   const int unit = blockIdx.x * units + warp / w.heads, sub = warp % w.heads;
   Walk<kShared> wk;
   if (!find_place(p, w, unit, threadIdx.x < 32 && blockIdx.x == 0, wk)) {
-    if (kShared && p.second) grid_dep_wait();  // complete only after the other line
+    if (kShared) end_line(p);
     return;
   }
   if (kShared) {  // the first piece's queries, beside the copies
@@ -472,7 +475,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     while (globaltimer_ns() - t0 < 1000000ull) {
     }
   }
-  if (kShared && p.second) grid_dep_wait();
+  if (kShared) end_line(p);
 }
 
 }  // namespace tree

@@ -904,16 +904,19 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   BigShared& ss = *reinterpret_cast<BigShared*>(smem_big + C::kOffShared);
   const int warp = threadIdx.x / 32;
   if (kShared) prefetch_line(p);
-  if (!(kShared && p.second)) grid_dep_wait();
+  if (kShared)
+    begin_line(p);
+  else
+    grid_dep_wait();
   grid_dep_launch();
   if (smem_u32(smem_big) & 1023u) {  // the swizzled tiles would be read askew
     if (threadIdx.x == 0) atomicOr(p.err, kTimedOut);
-    if (kShared && p.second) grid_dep_wait();
+    if (kShared) end_line(p);
     return;
   }
   Walk<kShared> k;
   if (!find_place(p, w, blockIdx.x, blockIdx.x == 0 && warp == 0, k)) {  // the whole CTA
-    if (kShared && p.second) grid_dep_wait();  // complete only after the other line
+    if (kShared) end_line(p);
     return;
   }
   auto init = [&](int first, int n, int count) {
@@ -976,7 +979,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     tc_fence_after();
     tmem_dealloc(ss.tmem, 512);
   }
-  if (kShared && p.second) grid_dep_wait();
+  if (kShared) end_line(p);
 }
 
 }  // namespace tree
