@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     at.x += __reduce_add_sync(0xffffffffu, x), at.y += __reduce_add_sync(0xffffffffu, y);
     return first;
   };
-  auto segments = [&](const Item& x, const Work& w) { return (x.n * p.G + w.rows - 1) / w.rows * (p.H / w.heads); };
+  auto segments = [&](const Item& x, const Work& w) {
+    return quotient(x.n * p.G + w.rows - 1, w.rows) * (p.H >> (w.heads / 2));
+  };
   auto tiles_of = [&](const Item& x, const Work& w) { return (x.len + (1 << w.log_tile) - 1) >> w.log_tile; };
   // Thread i has group i and sequence i, and those kPlanThreads further on.  (Lines of up
   // to kPlanThreads items may be padded; their items stay in registers.)
@@ -175,8 +177,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     if (32 * warp < most) {
 #pragma unroll 1
       for (int c = 0; c <= kCross; c += 2) {
-        const int x = tiles.x > 0 ? min(segs.x, kSms * 8 + 1) * ((tiles.x - 1) / (share.x + c) + 1) : 0;
-        const int y = tiles.y > 0 ? min(segs.y, kSms * 8 + 1) * ((tiles.y - 1) / (share.y + c) + 1) : 0;
+        const int x = tiles.x > 0 ? min(segs.x, kSms * 8 + 1) * (quotient(tiles.x - 1, share.x + c) + 1) : 0;
+        const int y = tiles.y > 0 ? min(segs.y, kSms * 8 + 1) * (quotient(tiles.y - 1, share.y + c) + 1) : 0;
         const int sx = __reduce_add_sync(0xffffffffu, min(x, 1 << 20)), sy = __reduce_add_sync(0xffffffffu, min(y, 1 << 20));
         if (lane == 0 && sx) atomicAdd(&shares[0][c], sx);
         if (lane == 0 && sy) atomicAdd(&shares[1][c], sy);
@@ -236,13 +238,13 @@ __device__ __forceinline__ Pieces find_pieces(const Params& p, const Work& w, co
   Pieces x{};
   const int tiles = seq_tiles(sq, w);
   if (tiles == 0) return x;
-  const int group = h / w.heads;
+  const int group = h >> (w.heads / 2);  // 1, 2 or 4 heads
   x.sub = h - group * w.heads;
-  const int mtiles = (sq.n * p.G + w.rows - 1) / w.rows, mt = row / w.rows;
+  const int mtiles = quotient(sq.n * p.G + w.rows - 1, w.rows), mt = quotient(row, w.rows);
   x.r = row - mt * w.rows;
   const int first = before + (group * mtiles + mt) * padded(tiles, pad);
-  x.c0 = first / share;
-  x.n = (first + tiles - 1) / share - x.c0 + 1;
+  x.c0 = quotient(first, share);
+  x.n = quotient(first + tiles - 1, share) - x.c0 + 1;
   x.inside = first != x.c0 * share;
   x.rows = x.n == 1;
   return x;
@@ -288,14 +290,14 @@ prefix_join_kernel(const __grid_constant__ Params pg, const __grid_constant__ Wo
   Pieces a{}, b{};
   const int end = (int)min((int64_t)row0 + run, (int64_t)all);
   if (line.x == 0) return;  // no sequence has rows (offsets that decrease among them)
-  int t = row0 / p.Hq, head = row0 - t * p.Hq - 1;
+  int t = quotient(row0, p.Hq), head = row0 - t * p.Hq - 1;
 #pragma unroll 1
   for (int rowi = row0; rowi < end; ++rowi) {
     if (++head == p.Hq) head = 0, ++t;
     if (t != at) found = find(t), at = t, head_at = -1;
     if (!found) continue;
     if (head_at < 0 || head >= (head_at + 1) * p.G || (a.n > 0 && a.r + 1 == wg.rows) || b.r + 1 == w.rows) {
-      const int h = head / p.G, g = head - h * p.G;
+      const int h = quotient(head, p.G), g = head - h * p.G;
       head_at = h;
       a = find_pieces(pg, wg, gq, g_line.y, g_line.z, g_before, h, (t - gq.q0) * p.G + g);
       b = find_pieces(p, w, sq, line.y, line.z, before, h, (t - sq.q0) * p.G + g);

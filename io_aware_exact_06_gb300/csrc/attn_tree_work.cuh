@@ -133,7 +133,16 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   return true;
 }
 
-__device__ __forceinline__ int padded(int tiles, int pad) { return pad > 1 ? (tiles + pad - 1) / pad * pad : tiles; }
+// n / d for n >= 0, d > 0, by an fp32 reciprocal and its correction: a chain of some ten
+// divisions leads to a row's pieces, and the compiler's takes three times as long.
+__device__ __forceinline__ int quotient(int n, int d) {
+  int q = (int)(__int2float_rn(n) * __frcp_rn(__int2float_rn(d)));
+  int r = n - q * d;
+  if (r < 0) --q, r += d;
+  if (r >= d) ++q, r -= d;
+  return (unsigned)r < (unsigned)d ? q : n / d;  // quotients beyond 2^22 or so
+}
+__device__ __forceinline__ int padded(int tiles, int pad) { return pad > 1 ? quotient(tiles + pad - 1, pad) * pad : tiles; }
 // The same over a line that is laid out: the last item whose first tile is not behind the
 // share's, by 32 probes a step.
 __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool, Walk<true>& walk) {
@@ -157,7 +166,7 @@ __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int u
   walk.segs = seq_segments(p, walk.s, w);
   walk.tiles = seq_tiles(walk.s, w);
   const int room = padded(walk.tiles, pad);
-  walk.seg = (first - before) / room;
+  walk.seg = quotient(first - before, room);
   walk.tile = first - before - walk.seg * room;
   walk.left = min(share, total - first);
   if (pad > 1) walk.left = min(walk.left, walk.tiles - walk.tile);  // a share lies in one segment
