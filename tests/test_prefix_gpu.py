@@ -273,3 +273,48 @@ def test_bad_plans_are_reported(dev, what, G):
     assert ((out[others].float() - good[0][others].float()).abs() <= 2.0 ** -7).all()
     assert ((lse[others] - good[1][others]).abs() <= 2.0 ** -14).all()
     assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_more_groups_and_sequences_than_threads_plan(dev, codes):
+    """700 sequences in groups of two, with empty groups between them and sequences in none."""
+    B, d, page = 700, 64, 16
+    lens = [40 + (7 * b) % 33 for b in range(B)]
+    ns = [b % 3 for b in range(B)]
+    groups, prefix = [5], []
+    for g in range(340):
+        prefix += [16 * (g % 3) + g % 2, 31]
+        groups += [min(5 + 2 * (g + 1), B - 3)] * 2  # the second one is empty
+    c = share(fill(dev, 400, lens, 1, d, page, codes), groups, prefix)
+    q = normal(dev, 401, sum(ns), 3, d)
+    got = call(dev, c, q, lens, ns, None, groups, prefix)
+    assert fa.attn_last_device_error() == 0
+    check(c, q, lens, ns, None, got)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("B,G,d", [(44, 1, 128), (36, 1, 64), (10, 5, 128)])
+def test_many_row_tiles(dev, codes, B, G, d):
+    """9 to 13 row tiles of a group: CTAs beside each other over the same keys, some without a tile."""
+    lens, ns, groups, prefix = [300 + b for b in range(B)], [64] * B, [0, B], [230]
+    c = share(fill(dev, 410, lens, 1, d, 16, codes), groups, prefix)
+    q = normal(dev, 411, 64 * B, G, d)
+    got = call(dev, c, q, lens, ns, None, groups, prefix)
+    assert fa.attn_last_device_error() == 0
+    check(c, q, lens, ns, None, got)
+
+
+def test_infinite_values_in_a_prefix(dev):
+    """An infinite value makes its channel infinite (or NaN, where a probability is the sum of two parts and
+    the second is 0 or negative, as over one sequence's own pages), and no other, also where a tile ends behind
+    the prefix."""
+    for B in (2, 60):
+        lens, ns, groups, prefix, d = [180 + b % 4 for b in range(B)], [1] * B, [0, B], [176], 128
+        c = share(fill(dev, 420, lens, 1, d, 16, False), groups, prefix)
+        c["v_cache"][int(c["page_table"][0, 10]), 15, 0, 9] = float("inf")  # the prefix's last position
+        q = normal(dev, 421, B, 4, d)
+        o, lse = call(dev, c, q, lens, ns, None, groups, prefix)
+        assert fa.attn_last_device_error() == 0
+        assert not o[..., 9].isfinite().any() and lse.isfinite().all()
+        o[..., 9] = 0
+        assert o.isfinite().all()

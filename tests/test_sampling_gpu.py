@@ -198,3 +198,46 @@ def test_streams_by_address(dev):
     s.synchronize()
     assert torch.equal(fork[0], want[4]) and got[0].shape == want[1].shape
     assert fa.attn_last_device_error(s) == 0
+
+
+FIRST = """
+    import sys, torch
+    sys.path.insert(0, "@ROOT@")
+    import io_aware_exact_06_gb300 as fa
+    dev = torch.device("cuda:0")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)
+    table, lens, parents, new, refs = i32(0, 1, 2, -1).view(1, 4), i32(40), i32(0, 0), i32(41, 42), i32(1, 1, 1, 0, 0)
+    kc, vc = torch.randn(2, 5, 16, 1, 64, device=dev).bfloat16()
+    q = torch.randn(2, 4, 64, device=dev).bfloat16()
+    probs = torch.full((2, 50), 0.02, device=dev)
+    cu, groups, prefix, u = i32(0, 1, 2), i32(0, 2), i32(40), torch.rand(2, device=dev)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        t, r, src, dst = fa.cache_fork(table, lens, parents, new, refs, 16)
+        fa.cache_copy(kc, vc, src, dst)
+        o, lse = fa.prefix_decode(q, kc, vc, t, new, cu, 1, 42, groups, prefix, 2, 40)
+        path, kept, nxt, left = fa.verify_drafts(torch.zeros(2, dtype=torch.int32, device=dev), probs, cu, u, u, seqlens=new)
+        fa.cache_compact(kc, vc, t, new, cu, path, kept)
+    g.replay()
+    torch.cuda.synchronize()
+    assert fa.attn_last_device_error() == 0
+    assert t.tolist() == [[0, 1, 2, -1], [0, 1, 3, -1]] and r.tolist() == [2, 2, 1, 1, 0] and kept.tolist() == [1, 1]
+    for b, n in enumerate((41, 42)):
+        rows = t[b].long()[torch.arange(n, device=dev) // 16], torch.arange(n, device=dev) % 16
+        k, v = kc[rows][:, 0].double(), vc[rows][:, 0].double()
+        p = (q[b].double() @ k.T / 8).softmax(-1)
+        assert (o[b].double() - p @ v).abs().max() < 0.03
+    print("ok")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(dev):
+    import os
+    import subprocess
+    import sys
+    import textwrap
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    script = textwrap.dedent(FIRST).replace("@ROOT@", root)
+    out = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0 and "ok" in out.stdout, out.stderr[-2000:]

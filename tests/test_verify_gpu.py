@@ -243,3 +243,27 @@ def test_bad_batches_are_reported(dev, what, V):
     if what.endswith("token"):  # rejected: the token behind it is drawn from the target's rest
         assert got[1][1] == 1 and got[0][4:9].tolist() == [0, -1, -1, -1, -1]
     assert fa.attn_last_device_error() == 0
+
+
+def test_rows_behind_the_batch_stay(dev):
+    """The C call, on the caller's buffers: what belongs to no sequence is left as it was."""
+    s = make(560, [4, 3], 300, torch.float32, True, False)
+    tokens, probs, u = (torch.cat([s[n], s[n][:3]]).to(dev) for n in ("tokens", "probs", "u"))
+    path, kept, nxt = torch.full((10,), 99, dtype=torch.int32, device=dev), *torch.full((2, 3), 99, dtype=torch.int32, device=dev)
+    cu, un = torch.tensor([0, 4, 7], dtype=torch.int32, device=dev), s["u_next"].to(dev)
+    fa.attn_verify_drafts(tokens, probs, 300, None, 0, False, cu, None, u, un, None, path, kept, nxt, None, 2, 10, 300,
+                          torch.cuda.current_stream())
+    assert fa.attn_last_device_error() == 0
+    assert (path[7:] == 99).all() and kept[2] == 99 and nxt[2] == 99 and (path[:7] != 99).all()
+
+
+def test_lengths_in_place(dev):
+    s = make(570, [5, 4], 900, torch.bfloat16, True, True)
+    lens = torch.tensor([80, 70], dtype=torch.int32, device=dev)
+    want = call(dev, s, seqlens=lens.clone())
+    path, (kept, nxt) = torch.empty(9, dtype=torch.int32, device=dev), torch.empty((2, 2), dtype=torch.int32, device=dev)
+    a = {n: s[n].to(dev) for n in ("tokens", "probs", "draft", "mask", "u", "u_next")}
+    fa.attn_verify_drafts(a["tokens"], a["probs"], 900, a["draft"], 900, True, torch.tensor(s["cu"], dtype=torch.int32, device=dev),
+                          a["mask"], a["u"], a["u_next"], lens, path, kept, nxt, lens, 2, 9, 900, torch.cuda.current_stream())
+    assert fa.attn_last_device_error() == 0
+    assert torch.equal(lens, want[3]) and torch.equal(path, want[0]) and torch.equal(nxt, want[2])
