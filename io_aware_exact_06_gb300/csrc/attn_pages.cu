@@ -94,7 +94,8 @@ extern "C" int attn_cache_copy(const attn_paged_cache* cache, const int32_t* src
   p.items = (int64_t)n * p.all;
   p.pages = cache->num_pages;
   if ((st = error_word(&p.err)) != ATTN_OK) return st;
-  const int64_t grid = std::min<int64_t>(p.items, 8 * kPlanSms);
+  // (2000 pages, 541 MB: 89.8 us with 8 CTAs an SM in all, 84.6 with 16, 81.7 with 32)
+  const int64_t grid = std::min<int64_t>(p.items, 32 * kPlanSms);
   return launch(cache_copy_kernel, grid, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }
 
