@@ -418,10 +418,18 @@ __global__ void __launch_bounds__(kForkThreads, 1) cache_fork_kernel(const __gri
   }
   // old rows give up what their first child did not take over
   for (int b = wide; b < p.B; b += warps) {
-    int j = __ldcg(p.taken + b);
-    const int n = (p.lens[b] + (1 << p.log_page) - 1) >> p.log_page;
-    for (j += lane; j < n; j += 32)
-      if (atomicSub(p.refs_out + p.table[(int64_t)b * p.W + j], 1) < 1) atomicOr(p.err, rows::kBadIndex);
+    const int from = __ldcg(p.taken + b), n = (p.lens[b] + (1 << p.log_page) - 1) >> p.log_page;
+    const int* row = p.table + (int64_t)b * p.W;
+    for (int j = from + lane; j < n; j += 32 * kAtOnce) {
+      int page[kAtOnce], count[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) page[u] = j + 32 * u < n ? row[j + 32 * u] : -1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) count[u] = page[u] >= 0 ? atomicSub(p.refs_out + page[u], 1) : 1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (count[u] < 1) atomicOr(p.err, rows::kBadIndex);
+    }
   }
 }
 
