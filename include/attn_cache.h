@@ -162,8 +162,8 @@ size_t attn_fwd_prefix_workspace(int B, int total, int Hq, int H, int d, int max
  * each layer's cache); they are -1 elsewhere.  Pages given up may be handed out
  * by the next call, not by this one.
  * page_table [B, page_table_stride], page_table_out [N, page_table_stride] (not
- * the same memory: ATTN_ERR_SHAPE), refs and refs_out [num_pages] (may be the
- * same), seqlens [B], parents, new_seqlens, copy_src and copy_dst [N], all int32
+ * the same memory: ATTN_ERR_SHAPE), refs and refs_out [num_pages] (the same, or
+ * apart: ATTN_ERR_SHAPE), seqlens [B], parents, new_seqlens, copy_src and copy_dst [N], all int32
  * on the device.  page_size 16, 32, 64, 128 or 256.
  * workspace: attn_cache_fork_workspace(...) bytes of the caller's device memory,
  * 16-byte aligned, not initialised, in use until the call's work on stream has finished.

@@ -157,8 +157,12 @@ extern "C" int attn_cache_fork(const int32_t* page_table, int page_table_stride,
                         (const void*)parents, (const void*)new_seqlens, (const void*)page_table_out,
                         (const void*)copy_src, (const void*)copy_dst})
     if (!aligned(x, 4)) return ATTN_ERR_ALIGN;
-  const uintptr_t from = reinterpret_cast<uintptr_t>(page_table), to = reinterpret_cast<uintptr_t>(page_table_out);
-  if (B && N && from < to + (size_t)N * W * 4 && to < from + (size_t)B * W * 4) return ATTN_ERR_SHAPE;  // they overlap
+  auto overlap = [](const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na && nb && x < y + nb * 4 && y < x + na * 4;
+  };
+  if (overlap(page_table, (size_t)B * W, page_table_out, (size_t)N * W)) return ATTN_ERR_SHAPE;
+  if (refs != refs_out && overlap(refs, num_pages, refs_out, num_pages)) return ATTN_ERR_SHAPE;
   const size_t words = fork_words(B, N, W, num_pages);
   if (!aligned(workspace, 16)) return ATTN_ERR_ALIGN;
   if (words && (!workspace || workspace_bytes < words * sizeof(int))) return ATTN_ERR_SCRATCH;

@@ -101,6 +101,11 @@ def test_fork_refusals(lib, args, status):
     assert fork(lib, **args) == status
 
 
+@pytest.mark.parametrize("shift", [4, -4, 396, -396])
+def test_fork_counts_that_overlap_are_refused(lib, shift):
+    assert fork(lib, refs_out=BUF + shift) == -2
+
+
 def test_fork_workspace_size():
     assert fa.attn_cache_fork_workspace(4, 6, 8, 100, 16) == 4 * (4 * 10 + 48)
     assert fa.attn_cache_fork_workspace(4, 6, 8, 10, 16) == 4 * (4 * 10 + 10)
