@@ -121,10 +121,11 @@ size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_n
  * the group.  Sequences cu_groups[g] .. cu_groups[g+1]-1 are group g (cu_groups:
  * int32[groups+1], prefix_lens: int32[groups], on the device); their tables name
  * the same pages for the first prefix_lens[g] positions, as far as these fill
- * pages, and those are read by the first sequence's table.  (What follows in a
+ * pages, and those are read by the first of these tables.  (What follows in a
  * page that is not filled is each sequence's own.)  A prefix ends before the new
- * tokens of its sequences.  A sequence in no group shares nothing; groups may be
- * empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
+ * tokens of its sequences.  A sequence in no group shares nothing; one without new
+ * tokens has no rows, and neither its table nor its length's place behind the prefix
+ * counts; groups may be empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
  * from its by rounding alone.
  * max_group >= the new tokens of every group together, max_prefix >= every
  * prefix_lens[g], at most max_len: they size the launch (close bounds pick the

@@ -55,9 +55,11 @@ __device__ __forceinline__ bool load_group(const Plan& p, const Offsets& of, int
 __device__ __forceinline__ bool group_item(const Plan& p, const Offsets& of, int g, Item& x) {
   int pages = 0;
   if (!load_group(p, of, g, pages)) return false;
+  const int end = of.groups[g + 1];
   x.at = of.groups[g];
   x.q0 = max(of.cu[x.at], 0);
-  x.n = max(min(of.cu[of.groups[g + 1]], p.total) - x.q0, 0);
+  x.n = max(min(of.cu[end], p.total) - x.q0, 0);
+  while (x.at + 1 < end && of.cu[x.at + 1] == of.cu[x.at]) ++x.at;  // the first with new tokens
   x.len = pages << p.log_page;
   x.page0 = -1;
   return true;
@@ -71,6 +73,7 @@ __device__ __forceinline__ bool seq_item(const Plan& p, const Offsets& of, int b
   int pages = 0;
   g = find_group(p, of, b);
   if (g >= 0) fits &= load_group(p, of, g, pages);
+  if (n == 0) pages = 0;  // no row reads them
   if (!fits || (int64_t)pages << p.log_page > len - n) return false;
   x.q0 = q0, x.n = x.masked = (int)n, x.len = len - (pages << p.log_page), x.at = b, x.page0 = pages;
   return true;

@@ -181,6 +181,20 @@ def test_padded_batch_and_bounds(dev):
 
 
 @pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("G", [2, 40])
+def test_finished_sequences_in_a_group(dev, codes, G):
+    """Places of a batch that hold nothing, a group's first among them: no length, no pages, no new tokens."""
+    lens, ns, groups, prefix = [300, 300, 300, 310, 300, 90], [0, 1, 0, 2, 0, 1], [0, 5, 6], [299, 64]
+    c = share(fill(dev, 335, lens, 1, 128, 16, codes), groups, prefix)
+    for b in (0, 2, 4):
+        lens[b] = 0
+        c["page_table"][b] = -1
+    q = normal(dev, 336, sum(ns), G, 128)
+    check(c, q, lens, ns, None, call(dev, c, q, lens, ns, None, groups, prefix))
+    assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("B", [4, 100])
 def test_a_nan_in_a_prefix_stays_in_its_group(dev, codes, B):
     lens, ns, groups, prefix = [300] * B, [1] * B, [0, B // 2, B], [256, 128]
