@@ -15,6 +15,10 @@
 // A segment is `team` row tiles (pairs of them), and as many CTAs beside each other take
 // one of them each over the same share of the keys, which so come from HBM once: a pair of
 // tiles has 64 KB of them for 1.1 us of products.
+//
+// The chain of a row tile bounds it: S, softmax, P V, and back to S.  A pair of tiles takes
+// 3140 cycles over 128 keys, d = 128, with 2048 of products; 1784 rows over 32768 keys of 8
+// heads 213 us on 136 SMs, 0.64 of their tensor pipe.
 #pragma once
 
 #include "attn_tree_tile_kernel.cuh"

@@ -34,7 +34,8 @@ namespace tree {
 // issue, against 365 that HBM needs for the tiles of twelve warps.)
 constexpr int kWarps = 4;     // of a CTA
 // Over shared prefixes a CTA has an SM for itself, so that two lines of work can have SMs
-// of their own at a time: as many warps as its registers and shared memory hold.
+// of their own at a time: as many warps as its registers and shared memory hold (64 samples
+// with 1024 keys of their own behind 16384: 78 us with 8 warps, 72 with 12).
 __host__ __device__ constexpr int few_warps(bool shared, int rows) { return !shared ? kWarps : rows == 8 ? 12 : 8; }
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
