@@ -125,7 +125,7 @@ size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_n
  * page that is not filled is each sequence's own.)  A prefix ends before the new
  * tokens of its sequences.  A sequence in no group shares nothing; one without new
  * tokens has no rows, and neither its table nor its length's place behind the prefix
- * counts; groups may be empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
+ * counts (nor the prefix of a group without them); groups may be empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
  * from its by rounding alone.
  * max_group >= the new tokens of every group together, max_prefix >= every
  * prefix_lens[g], at most max_len: they size the launch (close bounds pick the

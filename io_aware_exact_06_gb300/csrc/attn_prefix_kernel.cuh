@@ -48,9 +48,10 @@ __device__ __forceinline__ int find_group(const Plan& p, const Offsets& of, int 
 // bounds allow (its sequences are refused then).
 __device__ __forceinline__ bool load_group(const Plan& p, const Offsets& of, int g, int& pages) {
   const int s0 = of.groups[g], s1 = of.groups[g + 1], prefix = of.prefix[g];
-  pages = prefix >> p.log_page;
-  if (s0 < 0 || s1 < s0 || s1 > p.B || prefix < 0 || prefix > p.max_prefix || pages > p.stride) return false;
-  return (int64_t)of.cu[s1] - of.cu[s0] <= p.max_group;
+  if (s0 < 0 || s1 < s0 || s1 > p.B) return false;
+  const int64_t n = (int64_t)of.cu[s1] - of.cu[s0];
+  pages = n > 0 ? prefix >> p.log_page : 0;  // nobody reads them else
+  return n == 0 || (prefix >= 0 && prefix <= p.max_prefix && pages <= p.stride && n <= p.max_group);
 }
 
 // Its rows are all its sequences' (of one that is refused they are computed and not used).

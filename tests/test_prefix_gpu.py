@@ -194,6 +194,15 @@ def test_finished_sequences_in_a_group(dev, codes, G):
     assert fa.attn_last_device_error() == 0
 
 
+def test_groups_without_new_tokens_have_any_prefix(dev):
+    """An empty group, and one whose sequences have all finished: behind the table, below 0."""
+    lens, ns, groups, prefix = [300, 0, 0, 310], [1, 0, 0, 2], [0, 1, 1, 3, 4], [299, 5000, -7, 304]
+    c = share(fill(dev, 337, [300, 300, 300, 310], 2, 64, 16, False), groups, [299, 0, 0, 304])
+    q = normal(dev, 338, sum(ns), 6, 64)
+    check(c, q, lens, ns, None, call(dev, c, q, lens, ns, None, groups, prefix, max_prefix=304))
+    assert fa.attn_last_device_error() == 0
+
+
 @pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("B", [4, 100])
 def test_a_nan_in_a_prefix_stays_in_its_group(dev, codes, B):
