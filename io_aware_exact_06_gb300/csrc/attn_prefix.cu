@@ -110,8 +110,9 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
-  // 32 warps an SM: all rows at once, while a warp has eight at most
-  const int run = (int)std::clamp<int64_t>((rows + 32 * kPlanSms - 1) / (32 * kPlanSms), 1, 8);
+  // 16 warps an SM, as many as the join's registers allow without spills (64 samples 71.5 us with 32
+  // warps, 68.2 with 24, 67.2 with 16): all rows at once, while a warp has eight at most
+  const int run = (int)std::clamp<int64_t>((rows + 16 * kPlanSms - 1) / (16 * kPlanSms), 1, 8);
   return launch(attn::tree::prefix_join_kernel<D>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg,
                 x.any ? x.group.work : x.seq.work, p, x.seq.work, run);
 }

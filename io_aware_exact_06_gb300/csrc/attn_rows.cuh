@@ -44,19 +44,20 @@ __device__ __forceinline__ float row_sum(float x) {
 // The sequence of packed token t: the number of ends cu[1..B] that are <= t,
 // found by the whole warp, 32 probes a step (two dependent loads for up to
 // 1024 sequences).  B when t lies behind the last sequence.  Whatever cu
-// holds, it reads cu[1..B] only.
+// holds, it reads cu[1..B] only; kFresh: from L2.
+template <bool kFresh = false>
 __device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, int t) {
   const int lane = threadIdx.x % 32;
   int lo = 0, n = B;  // the answer lies in [lo, lo + n]
   while (n > 32) {
     const int step = (n + 31) / 32;
     const int at = lo + (int)min((int64_t)(lane + 1) * step, (int64_t)n);  // the end of sequence at - 1
-    const int cnt = __popc(__ballot_sync(0xffffffffu, cu[at] <= t));
+    const int cnt = __popc(__ballot_sync(0xffffffffu, (kFresh ? __ldcg(cu + at) : cu[at]) <= t));
     const int skip = (int)min((int64_t)cnt * step, (int64_t)n);
     lo += skip;
     n = min(step, n - skip);
   }
-  const bool le = lane < n && cu[lo + 1 + lane] <= t;
+  const bool le = lane < n && (kFresh ? __ldcg(cu + lo + 1 + lane) : cu[lo + 1 + lane]) <= t;
   return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 

@@ -144,25 +144,42 @@ __device__ __forceinline__ int quotient(int n, int d) {
 }
 __device__ __forceinline__ int padded(int tiles, int pad) { return pad > 1 ? quotient(tiles + pad - 1, pad) * pad : tiles; }
 // The same over a line that is laid out: the last item whose first tile is not behind the
-// share's, by 32 probes a step.
+// share's, by 32 probes a step, the first of them on their way beside the line's numbers.
 __device__ __forceinline__ bool find_place(const Params& p, const Work& w, int unit, bool, Walk<true>& walk) {
-  const int lane = threadIdx.x % 32, total = p.line[0], share = p.line[1], pad = p.line[2];
+  const int lane = threadIdx.x % 32;
+  const int4 line = *reinterpret_cast<const int4*>(p.line);
+  int lo = 0, n = p.n_items;  // items 0 .. lo - 1 begin at or in front of it, lo + n .. behind
+  int step = (n + 31) / 32, before;
+  const Item* probe = p.items + (int)min((int64_t)(lane + 1) * step, (int64_t)n) - 1;
+  if (p.n_items <= 32)
+    load_item(probe, walk.s, before);
+  else
+    before = probe->first;
+  const int total = line.x, share = line.y, pad = line.z;
   if (total == 0) return false;
   if ((int64_t)share * unit >= total) return false;
   const int first = share * unit;
-  int lo = 0, n = p.n_items;  // items 0 .. lo - 1 begin at or in front of it, lo + n .. behind
-  while (n > 32) {
-    const int step = (n + 31) / 32;
-    const int at = lo + (int)min((int64_t)(lane + 1) * step, (int64_t)n);
-    const int cnt = __popc(__ballot_sync(0xffffffffu, p.items[at - 1].first <= first));
+  for (;;) {
+    const int cnt = __popc(__ballot_sync(0xffffffffu, (int64_t)lane * step < n && before <= first));
     const int skip = (int)min((int64_t)cnt * step, (int64_t)n);
     lo += skip;
     n = min(step, n - skip);
+    if (step == 1 || n == 0) break;
+    step = (n + 31) / 32;
+    before = p.items[lo + min((lane + 1) * step, n) - 1].first;
   }
-  lo += __popc(__ballot_sync(0xffffffffu, lane < n && p.items[min(lo + lane, p.n_items - 1)].first <= first));
   walk.b = lo - 1;  // items without tiles lie in front of it
-  int before;
-  load_item(p.items + walk.b, walk.s, before);
+  if (p.n_items <= 32) {  // a lane has it
+    before = __shfl_sync(0xffffffffu, before, walk.b);
+    walk.s.q0 = __shfl_sync(0xffffffffu, walk.s.q0, walk.b);
+    walk.s.n = __shfl_sync(0xffffffffu, walk.s.n, walk.b);
+    walk.s.len = __shfl_sync(0xffffffffu, walk.s.len, walk.b);
+    walk.s.masked = __shfl_sync(0xffffffffu, walk.s.masked, walk.b);
+    walk.s.at = __shfl_sync(0xffffffffu, walk.s.at, walk.b);
+    walk.s.page0 = __shfl_sync(0xffffffffu, walk.s.page0, walk.b);
+  } else {
+    load_item(p.items + walk.b, walk.s, before);
+  }
   walk.segs = seq_segments(p, walk.s, w);
   walk.tiles = seq_tiles(walk.s, w);
   const int room = padded(walk.tiles, pad);
