@@ -3,6 +3,7 @@ its own page table.  The kernels and their roundings are those of attention over
 one sequence's pages, and so are the tolerances (tests/test_tree_gpu.py counts
 them); the join of pieces is fp32, inside the 2^-17 A counted for sums there."""
 import math
+import random
 
 import pytest
 
@@ -341,3 +342,53 @@ def test_infinite_values_in_a_prefix(dev):
         assert not o[..., 9].isfinite().any() and lse.isfinite().all()
         o[..., 9] = 0
         assert o.isfinite().all()
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("graph", [False, True])
+def test_other_batches_one_behind_the_other(dev, codes, graph):
+    """The same buffers with other offsets, lengths and groups from call to call, nothing waited for between."""
+    rng, B, T, P, S, page, pages = random.Random(7), 30, 3, 500, 70, 16, 1500
+    kind = torch.float8_e4m3fn if codes else torch.bfloat16
+    kc, vc = (normal(dev, 370 + i, pages * page, 2, 128).view(pages, page, 2, 128).to(kind) for i in range(2))
+    scales = {n: torch.full((pages, 2, page), 1.5, device=dev) if codes else None for n in ("k_scale", "v_scale")}
+    batches = []
+    for i in range(12):
+        groups = sorted([0, B] + [rng.randint(0, B) for _ in range(2)])
+        prefix, ns = [rng.randint(0, P) for _ in range(3)], [rng.randint(0, T) for _ in range(B - 1)] + [T]
+        lens, table = [], torch.randint(0, pages, (B, (P + S + T) // page + 2), generator=torch.Generator().manual_seed(i))
+        for k in range(3):
+            for b in range(groups[k], groups[k + 1]):
+                lens.append(prefix[k] + ns[b] + rng.randint(0, S))
+                table[b, :prefix[k] // page] = table[groups[k], :prefix[k] // page]
+        batches.append((normal(dev, 380 + i, B * T, 8, 128), table.to(dev, torch.int32), ints(dev, lens), cu_of(dev, ns),
+                        ints(dev, groups), ints(dev, prefix), sum(ns)))
+    q, table, lens, cu, groups, prefix = bufs = [x.clone() for x in batches[0][:6]]
+    run = lambda: fa.prefix_decode(q, kc, vc, table, lens, cu, T, P + S + T, groups, prefix, B * T, P, **scales)
+
+    def put(batch):
+        for x, y in zip(bufs, batch):
+            x.copy_(y)
+
+    want = []
+    for batch in batches:
+        put(batch)
+        torch.cuda.synchronize()
+        want.append([x[:batch[6]].clone() for x in run()])
+        torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run()
+    got = []
+    for batch in batches * 3:
+        put(batch)
+        if graph:
+            g.replay()
+        else:
+            run()
+            out = run()
+        got.append([x[:batch[6]].clone() for x in out])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for a, b in zip(got, want * 3) for x, y in zip(a, b))
+    assert fa.attn_last_device_error() == 0
