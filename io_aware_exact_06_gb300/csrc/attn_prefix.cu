@@ -22,6 +22,8 @@ namespace {
 
 using namespace attn_serve;
 
+static_assert(attn::tree::kSms == kPlanSms, "the lines' units here, and the SMs that the plan gives them");
+
 struct Sizes {
   int B, total, Hq, H, d, max_new, max_len, groups, max_group, max_prefix, splits;
 };

@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     if (32 * warp < most) {
 #pragma unroll 1
       for (int c = 0; c <= kCross; c += 2) {
-        const int x = tiles.x > 0 ? min(segs.x, kSms * 8 + 1) * (quotient(tiles.x - 1, share.x + c) + 1) : 0;
-        const int y = tiles.y > 0 ? min(segs.y, kSms * 8 + 1) * (quotient(tiles.y - 1, share.y + c) + 1) : 0;
+        // (segments beyond the units need not be counted: they are too many already)
+        const int x = tiles.x > 0 ? min(segs.x, units.x + 1) * (quotient(tiles.x - 1, share.x + c) + 1) : 0;
+        const int y = tiles.y > 0 ? min(segs.y, units.y + 1) * (quotient(tiles.y - 1, share.y + c) + 1) : 0;
         const int sx = __reduce_add_sync(0xffffffffu, min(x, 1 << 20)), sy = __reduce_add_sync(0xffffffffu, min(y, 1 << 20));
         if (lane == 0 && sx) atomicAdd(&shares[0][c], sx);
         if (lane == 0 && sy) atomicAdd(&shares[1][c], sy);

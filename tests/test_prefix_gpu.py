@@ -392,3 +392,18 @@ def test_other_batches_one_behind_the_other(dev, codes, graph):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for a, b in zip(got, want * 3) for x, y in zip(a, b))
     assert fa.attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("H,G,n,codes", [(1825, 1, 300, False), (2001, 8, 70, True), (3001, 1, 20, False)])
+def test_more_heads_than_units(dev, H, G, n, codes, grouped):
+    """Odd head counts above the units of a line: each head is a segment of its own, and every one is computed."""
+    lens, ns, groups, prefix = [n], [1], [0, 1] if grouped else [0], [n - 2] if grouped else []
+    c = fill(dev, 430, lens, H, 64, 16, codes)
+    q = normal(dev, 431, 1, H * G, 64)
+    out = torch.full((1, H * G, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((1, H * G), -77.0, device=dev)  # no row's: scores are below 30, and keys above one
+    call(dev, c, q, lens, ns, None, groups, prefix, out=out, lse=lse)
+    assert fa.attn_last_device_error() == 0
+    assert not (lse == -77.0).any()
+    check(c, q, lens, ns, None, (out, lse))
