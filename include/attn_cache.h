@@ -126,7 +126,9 @@ size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_n
  * tokens of its sequences.  A sequence in no group shares nothing; one without new
  * tokens has no rows, and neither its table nor its length's place behind the prefix
  * counts (nor the prefix of a group without them); groups may be empty, groups may be 0.  Everything else as for attn_fwd_tree; results differ
- * from its by rounding alone.
+ * from its by rounding alone, and where max_new tokens have at most 8 rows a key head (16 with
+ * d = 64) over a bf16 cache both hold a probability as the sum of two bf16, else as one.
+ * Over codes the rows of a group count together for what is said there of more than 16.
  * max_group >= the new tokens of every group together, max_prefix >= every
  * prefix_lens[g], at most max_len: they size the launch (close bounds pick the
  * kernels that fit).

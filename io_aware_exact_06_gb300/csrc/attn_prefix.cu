@@ -39,11 +39,11 @@ bool empty(const Sizes& z) { return z.B == 0 || z.total == 0 || z.max_new == 0; 
 
 // What a CTA takes for a tile of a line, in ns (d = 128; measured alone on an SM but for the
 // few-row kernel, which is given 55 GB/s of an SM's share of HBM).
-float tile_cost(const Plan& pl, int d, bool codes, bool rows_kernel) {
+float tile_cost(const Plan& pl, int d, bool rows_kernel, bool two) {
   const float wide = d == 128 ? 1.f : 0.9f;
   if (few(pl)) return 2700.f * pl.work.heads / attn::tree::few_warps(true, pl.rows);
   const bool pair = pl.rows > attn::tree::kBigRows;
-  if (rows_kernel) return wide * (pair ? 1900.f : 1100.f);
+  if (rows_kernel) return wide * (two ? pair ? 2400.f : 1300.f : pair ? 1900.f : 1100.f);
   return wide * (pair ? 2300.f : 2000.f);
 }
 
@@ -89,13 +89,17 @@ Plans plans(const Sizes& z, int page, bool codes) {
   return x;
 }
 
-// The line of groups: over a bf16 cache many rows have a kernel of their own.
+// The line of groups: over a bf16 cache many rows have a kernel of their own.  `two`:
+// it holds probabilities as the sum of two bf16, as the few-row kernel does, which has
+// these rows over their own keys: a row's weights keep the same bits whether its keys
+// are shared or not.
 template <int D, bool kCodes>
-int launch_groups(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
+int launch_groups(const Plan& pl, bool two, const CUtensorMap& mk, const CUtensorMap& mv, const attn::tree::Params& p,
                   cudaStream_t s) {
   using namespace attn::tree;
   if (kCodes || few(pl)) return launch_line<D, kCodes, true>(pl, mk, mv, p, s);
-  auto kernel = pl.rows == kBigRows ? prefix_rows_kernel<D, false> : prefix_rows_kernel<D, true>;
+  auto kernel = pl.rows == kBigRows ? two ? prefix_rows_kernel<D, false, true> : prefix_rows_kernel<D, false, false>
+                : two               ? prefix_rows_kernel<D, true, true> : prefix_rows_kernel<D, true, false>;
   const int smem = pl.rows == kBigRows ? RowsCfg<D, false>::kSmem : RowsCfg<D, true>::kSmem;
   const int st = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != ATTN_OK) return st;
@@ -110,7 +114,7 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
   // The second line starts as soon as every CTA of the first runs, without waiting for it
   // (what it reads was there before the first began), and ends after it.
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
-  if (x.any && (st = launch_groups<D, kCodes>(x.group, maps[0], maps[1], pg, s)) != ATTN_OK) return st;
+  if (x.any && (st = launch_groups<D, kCodes>(x.group, few(x.seq), maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
   // 16 warps an SM, as many as the join's registers allow without spills (64 samples 71.5 us with 32
   // warps, 68.2 with 24, 67.2 with 16): all rows at once, while a warp has eight at most
@@ -206,8 +210,8 @@ extern "C" int attn_fwd_prefix(const void* q, int64_t q_stride, const attn_paged
   auto per_cta = [](const Plan& pl) { return few(pl) ? attn::tree::few_warps(true, pl.rows) / pl.work.heads : 1; };
   plan.seq_cta = per_cta(x.seq);
   plan.group_cta = !x.any ? 1 : team > 1 ? -team : per_cta(x.group);
-  plan.seq_cost = tile_cost(x.seq, d, codes, false);
-  plan.group_cost = x.any ? team * tile_cost(x.group, d, codes, rows_kernel) : 0.f;
+  plan.seq_cost = tile_cost(x.seq, d, false, false);
+  plan.group_cost = x.any ? team * tile_cost(x.group, d, rows_kernel, few(x.seq)) : 0.f;
   p.items = plan.seq_items;
   p.line = plan.lines + 4;
   p.n_items = B;

@@ -16,8 +16,14 @@
 // one of them each over the same share of the keys, which so come from HBM once: a pair of
 // tiles has 64 KB of them for 1.1 us of products.
 //
-// The chain of a row tile bounds it: S, softmax, P V, and back to S.  A pair of tiles takes
-// 3140 cycles over 128 keys, d = 128, with 2048 of products; 1812 rows over 32768 keys of 8
+// kTwo: a probability is the sum of two bf16, its rounding and what that leaves, each with
+// its product with V, as in attn_tree_few_kernel.cuh; a tile of scores has room for both.  One
+// bf16 in its place, and O divided by the sum with the largest of them as rounded, is what
+// attn_tree_tile_kernel.cuh does for the rows that it has over their own keys.  (64 samples of
+// 16384 keys, one token each: 67.2 us so, 69.9 with two.)
+//
+// The chain of a row tile bounds it: S, softmax, P V, and back to S.  With one bf16 a pair of
+// tiles takes 3140 cycles over 128 keys, d = 128, with 2048 of products; 1812 rows over 32768 keys of 8
 // heads 213 us on 136 SMs, 0.64 of their tensor pipe.
 #pragma once
 
@@ -58,6 +64,11 @@ struct RowsCfg {
                        bQF = bOF + 2, bDrain = bQF + 2, kBars = bDrain + 1;
 };
 
+// What rounding a and b to the bf16 in `as` leaves of them, as bf16.
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t as) {
+  return rows::pack2(a - __uint_as_float(as << 16), b - __uint_as_float(as & 0xffff0000u));
+}
+
 // Rows `step` apart as tokens and heads of a group of G.
 struct Rows {
   int row, tok, g, step, dtok, dg, G;
@@ -71,7 +82,7 @@ struct Rows {
   }
 };
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kTwo>
 struct RowsRole {
   using C = RowsCfg<D, kPair>;
   const Params& p;
@@ -177,9 +188,11 @@ struct RowsRole {
   __device__ __forceinline__ void values(uint32_t tmem, uint32_t smem, int g, int slot, bool accumulate) {
     const uint64_t b = make_sdesc(smem + C::kOffRing + slot * C::kMat, C::kChunk, 1024, kSwizzle128B);
 #pragma unroll
-    for (int kk = 0; kk < kBigTile / 16; ++kk)
-      mma_ts(tmem + 256 + D * g, tmem + 128 * g + 8 * kk, b + (uint64_t)((kk * 2048) >> 4), make_idesc_bf16(128, D, true),
-             kk > 0 || accumulate);
+    for (int part = 0; part < (kTwo ? 2 : 1); ++part)
+#pragma unroll
+      for (int kk = 0; kk < kBigTile / 16; ++kk)
+        mma_ts(tmem + 256 + D * g, tmem + 128 * g + 64 * part + 8 * kk, b + (uint64_t)((kk * 2048) >> 4),
+               make_idesc_bf16(128, D, true), part > 0 || kk > 0 || accumulate);
   }
   // One thread issues every product, in the order of the steps (a step is a key tile, or
   // with kPair a key tile of one row tile): S(0), S(1), then for each step j its P V and
@@ -348,17 +361,17 @@ struct RowsRole {
           m = to;
         }
         const float neg = m == -INFINITY ? 0.f : -m * c2;
-        // O is divided by the sum with the largest probability of each half as rounded
+        // of one part: O is divided by the sum with the largest probability of each half as rounded
         float f = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < (kTwo ? 0 : 2); ++half) {
           const float pm = ex2(fmaf(top[half], c2, neg));
           f += __bfloat162float(__float2bfloat16(pm)) - pm;
         }
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t pw[16];
+          uint32_t pw[16], pr[16];  // probabilities as rounded, and what that leaves of them
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             float e[4];
@@ -370,8 +383,13 @@ struct RowsRole {
             padd(s2, s3, e[2], e[3]);
             pw[i / 2] = rows::pack2(e[0], e[1]);
             pw[i / 2 + 1] = rows::pack2(e[2], e[3]);
+            if (kTwo) {
+              pr[i / 2] = rest_of(e[0], e[1], pw[i / 2]);
+              pr[i / 2 + 1] = rest_of(e[2], e[3], pw[i / 2 + 1]);
+            }
           }
           tmem_st_x16(colS + 16 * q, pw);
+          if (kTwo) tmem_st_x16(colS + 64 + 16 * q, pr);
         }
         l = l * alpha + ((s0 + s1) + (s2 + s3));
         fix = fix * alpha + f;
@@ -475,7 +493,7 @@ struct RowsRole {
   }
 };
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kTwo>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ Params p, const __grid_constant__ Work w) {
@@ -528,7 +546,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  RowsRole<D, kPair> role{p, w, ss, smem_rows, smem_u32(smem_rows), ss.tmem};
+  RowsRole<D, kPair, kTwo> role{p, w, ss, smem_rows, smem_u32(smem_rows), ss.tmem};
   const bool firstp = role.busy(k), any = firstp || role.next(k);
   if (warp < 8) {
     regs_inc<kRowsSoftmaxRegs>();

@@ -407,3 +407,21 @@ def test_more_heads_than_units(dev, H, G, n, codes, grouped):
     assert fa.attn_last_device_error() == 0
     assert not (lse == -77.0).any()
     check(c, q, lens, ns, None, (out, lse))
+
+
+@pytest.mark.parametrize("B", [12, 60, 150])  # one row tile of a group, a pair, several CTAs beside each other
+@pytest.mark.parametrize("d,G", [(64, 16), (128, 5), (128, 8)])
+def test_one_token_rows_lose_nothing_of_their_weights(dev, B, d, G):
+    """A row that attention over its own pages takes with probabilities as the sum of two bf16 (up to 8 rows
+    a key head, 16 at d = 64) has them over a shared prefix too: 2^-8 of 2^-8 of each is lost, so O is good to
+    its own rounding (2^-8) and what scores and sums add, as in tests/test_tree_gpu.py."""
+    lens, ns, groups, prefix = [700 + b % 7 for b in range(B)], [1] * B, [0, B], [696]
+    c = share(fill(dev, 440, lens, 1, d, 16, False), groups, prefix)
+    q = normal(dev, 441, B, G, d, std=1.5)
+    o, lse = (t.cpu().double() for t in call(dev, c, q, lens, ns, None, groups, prefix))
+    assert fa.attn_last_device_error() == 0
+    k, v = rows_of(c)
+    wo, wl, A, S = ref.tree(q.cpu(), k, v, c["page_table"].cpu(), 16, lens, list(range(B + 1)), None, d ** -0.5)
+    tol = 2.0 ** -8 * wo.abs() + A * (2.0 ** -16 + 2.0 ** -19 * S[..., None] + 2.0 ** -17)
+    assert ((o - wo).abs() <= tol).all(), ((o - wo).abs() / tol).max()
+    assert ((lse - wl).abs() <= 2.0 ** -19 * S + 2.0 ** -20 * wl.abs() + 2.0 ** -18).all()
