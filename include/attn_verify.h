@@ -31,15 +31,19 @@ extern "C" {
  * a child is accepted where u z < w(x), else w(x) = 0 and z decreases by it.  Where no
  * child is left, the next token is the first x with w(0) + .. + w(x) > u_next[b] times
  * the sum of w; where that sum is 0, of p.
- * Probabilities are taken between 0 and 1 (NaN: 0).  Tests are made in fp64 and sums in
- * units of 2^-43, exactly: results do not depend on the launch and repeat bit for bit.
+ * Probabilities are taken between 0 and 1 (NaN: 0).  Tests are made in fp64.  In sums, and
+ * in the draw, each entry of w is taken to the nearest multiple of 2^-43 (one of 2^-44 or less
+ * counts as 0, so it is never drawn), and these are added exactly: results do not depend on
+ * the launch and repeat bit for bit.  The tokens are distributed as the target's, to that
+ * rounding and to that of the random numbers, where rows add up to 1; rows are not normed: with
+ * certain drafts z is 1 less what was rejected, whatever the row's sum.
  * tokens: int32[total]; u_accept: fp32[total], u_next: fp32[B], in [0, 1).
  * path: int32[total], from cu_seqlens[b] on the accepted new tokens, 0 and the accepted
  * drafts (indices within the sequence, increasing), then -1; accepted: int32[B], how
  * many; next_token: int32[B]; seqlens (NULL: none) with the new tokens and seqlens_out
  * (may be the same) with the accepted ones, int32[B].  A sequence without new tokens
- * has accepted 0 and next_token -1; next_token is also -1 where a row has no positive
- * entry.  At most 64 new tokens; V at most 262144.
+ * has accepted 0 and next_token -1; next_token is also -1 where a row has no
+ * entry above 2^-44.  At most 64 new tokens; V at most 262144.
  * Errors in the error word: ATTN_ERR_SEQLENS (offsets that decrease, for all sequences;
  * a sequence that begins below 0, the first anywhere but at 0, ends past total, has more
  * than 64 new tokens or is shorter than them: accepted 0, next_token -1, its length as

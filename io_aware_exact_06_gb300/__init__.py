@@ -806,8 +806,10 @@ def verify_drafts(tokens, probs, cu_seqlens, u_accept, u_next, draft_probs=None,
     (same type): what its children were drawn from (None: drafts count as certain).
     u_accept fp32 [total], u_next fp32 [B] in [0, 1).  Returns (path int32 [total]: the
     accepted tokens' indices in their sequence, then -1; accepted int32 [B]: how many, the
-    first included; next_token int32 [B]; the lengths int32 [B] that remain of seqlens, the
-    new tokens included, or None without it).  Tokens behind the last sequence are padding.
+    first included; next_token int32 [B], -1 where a row has no entry above 2^-44; the lengths
+    int32 [B] that remain of seqlens, the new tokens included, or None without it).  Rows should
+    add up to 1; sums and draws take their entries to the nearest multiple of 2^-43.  Tokens
+    behind the last sequence are padding.
     """
     return _call("verify_drafts", stream, tokens.device, tokens, probs, draft_probs, cu_seqlens, mask, u_accept, u_next,
                  seqlens)

@@ -267,3 +267,27 @@ def test_lengths_in_place(dev):
                           a["mask"], a["u"], a["u_next"], lens, path, kept, nxt, lens, 2, 9, 900, torch.cuda.current_stream())
     assert fa.attn_last_device_error() == 0
     assert torch.equal(lens, want[3]) and torch.equal(path, want[0]) and torch.equal(nxt, want[2])
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [300, 40000])
+def test_entries_next_to_the_unit_of_sums(dev, kind, V):
+    """An entry counts as the nearest multiple of 2^-43, one of 2^-44 as 0: in the draw, where a row draws
+    nothing, and where a residual has nothing left and the target's row is drawn from."""
+    above = 2.0 ** -44 * (1 + 2 * torch.finfo(kind).eps)
+    p = torch.zeros(9, V, dtype=torch.float64)
+    q = torch.zeros(9, V, dtype=torch.float64)
+    p[0] = 2.0 ** -44                       # nothing to draw
+    p[1, 5:], p[1, 250], p[1, 290] = 2.0 ** -44, above, above  # two entries, a unit each
+    p[2, 7], p[2, 200], p[2, 299] = 0.75 * 2.0 ** -43, 1.25 * 2.0 ** -43, 1.75 * 2.0 ** -43  # 1, 1 and 2 units
+    for b, left in ((3, 2.0 ** -44), (5, above), (7, 2.0 ** -42)):  # a rejected draft: what the target has beside it
+        p[b, 3], p[b, 260], q[b, 3] = 0.25, left, 0.5
+    s = dict(tokens=torch.full((9,), 3, dtype=torch.int32), probs=p.to(kind), cu=[0, 1, 2, 3, 5, 7, 9], u=torch.full((9,), 0.9),
+             u_next=torch.zeros(6), draft=q.to(kind), mask=None)
+    want = {0.0: [-1, 250, 7, 3, 260, 260],
+            0.5: [-1, 290, 299, 3, 260, 260],    # the first behind half of the units
+            0.26: [-1, 250, 200, 3, 260, 260]}
+    for u, tokens in want.items():
+        got = call(dev, dict(s, u_next=torch.full((6,), u)))
+        assert got[2].tolist() == tokens and got[1].tolist() == [1] * 6
+    assert fa.attn_last_device_error() == 0
