@@ -241,3 +241,21 @@ def test_first_calls_of_a_process_inside_a_capture(dev):
     script = textwrap.dedent(FIRST).replace("@ROOT@", root)
     out = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=600)
     assert out.returncode == 0 and "ok" in out.stdout, out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("codes,d,Hq", [(True, 128, 8), (False, 64, 2), (False, 128, 16)])
+def test_attention_on_a_stream_by_address_is_the_same(dev, codes, d, Hq):
+    r = Round(dev, 770, codes, d, Hq=Hq)
+    q, table = (r.run()[i] for i in (0, 4))  # accepted rows have moved since: the cache as it is now
+    s = torch.cuda.Stream()
+    run = lambda **kw: fa.prefix_decode(q, r.c["k_cache"], r.c["v_cache"], table, r.lens_d, r.cu, max(r.ns), max(r.lens), r.groups_d,
+                                        r.prompts_d, 64, 200, mask=r.mask, k_scale=r.c["k_scale"], v_scale=r.c["v_scale"], **kw)
+    want = run()
+    torch.cuda.synchronize()
+    out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+    torch.cuda.synchronize()
+    got = run(out=out, lse=lse, stream=s.cuda_stream)
+    s.synchronize()
+    assert got[0].data_ptr() == out.data_ptr() and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    check(r.c | {"page_table": table}, q, r.lens, r.ns, r.mask_cpu, (out, lse))
+    assert fa.attn_last_device_error(s) == 0
