@@ -43,14 +43,14 @@ int launch_clusters(void (*kernel)(KArgs...), int64_t grid, int ctas, int thread
 // Lets a kernel have clusters of more than eight CTAs, once per device.  Call with the
 // library lock held.
 int allow_wide_clusters(const void* kernel) {
-  static std::set<int> done;
+  static std::set<std::pair<int, const void*>> done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  if (done.count(dev)) return ATTN_OK;
+  if (done.count({dev, kernel})) return ATTN_OK;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return attn_host::lib_cuda_fail(e);
-  done.insert(dev);
+  done.insert({dev, kernel});
   return ATTN_OK;
 }
 
