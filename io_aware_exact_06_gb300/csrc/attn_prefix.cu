@@ -109,10 +109,13 @@ int launch_groups(const Plan& pl, bool two, const CUtensorMap& mk, const CUtenso
 template <int D, bool kCodes>
 int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree::Plan& plan, const attn::tree::Params& pg,
                   const attn::tree::Params& p, cudaStream_t s) {
+  // No launch may come between these.  The first line waits for the plan before it lets the next kernel
+  // start, and the plan for all that came before it: so the second line may read what those wrote, and write
+  // its parts, beside the first, which it waits for at its end; and the join may read the plan and the
+  // offsets before it waits for both.
   int st = launch(attn::tree::prefix_plan_kernel, 1, attn::tree::kPlanThreads, 0, s, plan);
   if (st != ATTN_OK) return st;
-  // The second line starts as soon as every CTA of the first runs, without waiting for it
-  // (what it reads was there before the first began), and ends after it.
+  // The second line starts as soon as every CTA of the first runs, and ends after it.
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   if (x.any && (st = launch_groups<D, kCodes>(x.group, few(x.seq), maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;

@@ -28,8 +28,9 @@ inline int error_word(int** err) {
   return attn_host::lib_device(&dev, &sms, err);
 }
 
-// Launch that may overlap the end of the stream's previous kernel (every
-// kernel here waits for it before its first global access).
+// Launch that may overlap the end of the stream's previous kernel.  Every kernel here
+// waits for it before its first global access, but for those of attention over shared
+// prefixes behind the plan, which rely on the order of their launches (attn_prefix.cu).
 template <typename... KArgs, typename... Args>
 int launch(void (*kernel)(KArgs...), int64_t grid, int threads, int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg{};

@@ -39,7 +39,6 @@ constexpr int kWarps = 4;     // of a CTA
 __host__ __device__ constexpr int few_warps(bool shared, int rows) { return !shared ? kWarps : rows == 8 ? 12 : 8; }
 constexpr int kFewTile = 32;  // keys per stage
 constexpr int kLogFewTile = 5;
-constexpr int kFewThreads = 32 * kWarps;
 // CTAs per SM.  Two leave a lane 255 registers and DRAM fewer streams; d = 64 codes
 // are bound by their arithmetic and want three (64 ragged sequences of up to 8192
 // keys, one token, 32 + 8 heads, two : three CTAs: d = 128 e4m3 144 : 145 us, bf16
