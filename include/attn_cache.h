@@ -129,6 +129,9 @@ size_t attn_fwd_tree_workspace(int B, int total, int Hq, int H, int d, int max_n
  * from its by rounding alone, and where max_new tokens have at most 8 rows a key head (16 with
  * d = 64) over a bf16 cache both hold a probability as the sum of two bf16, else as one.
  * Over codes the rows of a group count together for what is said there of more than 16.
+ * It has two launches more than attn_fwd_tree, which is faster where little is shared: groups of
+ * less than some eight sequences, or (sequences - groups) * prefix below some 30000 positions (8
+ * sequences: 15 us against 24 with a prefix of 512, 38 against 31 with 8192).
  * max_group >= the new tokens of every group together, max_prefix >= every
  * prefix_lens[g], at most max_len: they size the launch (close bounds pick the
  * kernels that fit).

@@ -37,8 +37,13 @@ int check_sizes(const Sizes& z) {
 
 bool empty(const Sizes& z) { return z.B == 0 || z.total == 0 || z.max_new == 0; }
 
-// What a CTA takes for a tile of a line, in ns (d = 128; measured alone on an SM but for the
-// few-row kernel, which is given 55 GB/s of an SM's share of HBM).
+// What a CTA takes for a tile of a line, in ns: d = 128, measured alone on an SM, but for the
+// few-row kernel, whose constant was fitted to a bf16 cache with d = 128 (two lines that share
+// HBM).  Half the bytes a tile, d = 64 or codes, would do with fewer SMs.  64 samples of 16384
+// keys, up to 1024 of their own, 4 rows a key head, us with 1350, 2000, 2700 and 3600 ns: bf16
+// d = 128 83, 74.5, 74.5, 81, d = 64 54, 57, 62, 68; codes d = 128 66, 70, 73.5, 83, d = 64 56,
+// 60, 62, 70.  The rows kernel with two bf16 a probability (the same case among other calls):
+// 71.0 us with 1900 ns a pair, 70.0 with 2400, 71.2 with 2900.
 float tile_cost(const Plan& pl, int d, bool rows_kernel, bool two) {
   const float wide = d == 128 ? 1.f : 0.9f;
   if (few(pl)) return 2700.f * pl.work.heads / attn::tree::few_warps(true, pl.rows);
@@ -119,8 +124,8 @@ int launch_prefix(const Plans& x, const CUtensorMap (&maps)[4], const attn::tree
   if ((st = launch_line<D, kCodes, true>(x.seq, maps[2], maps[3], p, s)) != ATTN_OK) return st;
   if (x.any && (st = launch_groups<D, kCodes>(x.group, few(x.seq), maps[0], maps[1], pg, s)) != ATTN_OK) return st;
   const int64_t rows = x.rows;
-  // 16 warps an SM, as many as the join's registers allow without spills (64 samples 71.5 us with 32
-  // warps, 68.2 with 24, 67.2 with 16): all rows at once, while a warp has eight at most
+  // 16 warps an SM, as many as the join's registers allow without spills (64 samples, with one bf16 a
+  // probability, 71.5 us with 32 warps, 68.2 with 24, 67.2 with 16): all rows at once, while a warp has eight at most
   const int run = (int)std::clamp<int64_t>((rows + 16 * kPlanSms - 1) / (16 * kPlanSms), 1, 8);
   return launch(attn::tree::prefix_join_kernel<D>, (rows + 8 * run - 1) / (8 * run), 256, 0, s, pg,
                 x.any ? x.group.work : x.seq.work, p, x.seq.work, run);

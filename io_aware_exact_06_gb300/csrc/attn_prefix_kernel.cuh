@@ -11,7 +11,7 @@ namespace tree {
 // Every warp of the kernels behind it needs its place in a line, and every row of the
 // join its sequence and its group: found from offsets, groups and lengths each time, that
 // is a chain of some eight dependent loads and a scan over the batch (64 samples of one
-// prompt, 16384 keys and up to 1024 of their own: 122 us in all so, 103 with this kernel;
+// prompt, 16384 keys and up to 1024 of their own: 122 us in all so, 106 with this kernel;
 // 78 with the lines side by side, which it gives their SMs).  One CTA: 6 us, its chain of
 // loads, scans and barriers.
 struct Plan {

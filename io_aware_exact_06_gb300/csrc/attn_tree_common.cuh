@@ -23,7 +23,8 @@
 // item is a group, its rows are all its sequences' and its keys the shared pages, every
 // one of them context; in the second an item is a sequence over its other pages.  A kernel
 // of its own lays both lines out (attn_prefix_kernel.cuh); the rows' two parts meet in
-// its join.
+// its join.  Rows that are few over their own keys hold probabilities as the sum of two
+// bf16 over a group's as well (attn_prefix_rows_kernel.cuh).
 #pragma once
 
 #include "attn_rows.cuh"
